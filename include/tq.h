@@ -366,6 +366,101 @@ typedef struct {
 tq_status tq_decode_plan(const tq_codebook* book, int batch, int n_q_heads, int n_kv_heads, int max_context,
                          tq_decode_plan_info* info);
 
+/* Token map of one step, built on the device (the write and read paths' slots
+ * and block tables from the sequences' lengths; seo-farm page §4 keeps the
+ * cache in pages).  past_lens, new_lens: device int32 [batch], the tokens of
+ * each sequence already in the cache and the tokens this step adds.
+ * block_table: device int32 [batch][max_blocks], in and out: sequence b's
+ * first ceil(past / block_size) entries are read, the following entries up to
+ * ceil((past + new) / block_size) are written with blocks of the free list
+ * (device int32 [n_free], distinct ids in [0, num_blocks)), taken from its
+ * front in sequence order; other entries are left as they were.  Outputs, all
+ * device: context_lens int32 [batch] (past + new), query_start int32
+ * [batch + 1] (exclusive sums of new_lens, the total last), positions int32
+ * [n_tokens] and slot_mapping int64 [n_tokens] of the step's tokens, sequence
+ * by sequence, and blocks_taken int32 [1], how many free-list entries the step
+ * needs.  n_tokens may exceed the sum of new_lens (a padded batch): the rows
+ * behind the last sequence get position -1 and slot -1, which tq_norm_rope
+ * and tq_quantize_append skip.  Nothing is allocated and no workspace is
+ * needed; a call with the same inputs writes the same outputs.
+ * context_lens must not be past_lens or new_lens, and no output may overlap
+ * an input.  batch is at most 8192 (else TQ_ERR_UNSUPPORTED).
+ * Recorded as device errors: 3 lengths that are negative or beyond max_blocks
+ * * block_size (the sequence counts as empty: context 0, no tokens), 6 the
+ * free list is too short (entries without a block are -1, their tokens' slots
+ * -1), 2 a block id outside the cache (slot -1), 7 the sum of new_lens
+ * exceeds n_tokens (the first n_tokens rows are written).  Asynchronous on
+ * `stream`. */
+tq_status tq_map_tokens(const tq_codebook* book, int batch, const int32_t* past_lens, const int32_t* new_lens,
+                        int32_t* block_table, int max_blocks, int num_blocks, const int32_t* free_blocks, int n_free,
+                        int n_tokens, int32_t* context_lens, int32_t* query_start, int32_t* positions,
+                        int64_t* slot_mapping, int32_t* blocks_taken, void* stream);
+
+/* Head norms of queries and keys and the rotation by position, in one pass:
+ * what a layer's projections go through before the keys are appended
+ * (tq_quantize_append) and the queries attend.  For every token and head
+ * vector x of 128: y = x / sqrt(mean(x^2) + eps) * weight, then the first
+ * rot_dim coordinates are rotated by angle position * inv_freq[j], j <
+ * rot_dim / 2, in pairs (y_j, y_{j + rot_dim/2}), or (y_2j, y_{2j+1}) with
+ * interleaved 1; float32 arithmetic, angles reduced to a turn in 64 bits (at
+ * any position as close as the product in doubles), one rounding to the type
+ * at the end.
+ * q, k: device rows of n_q_heads / n_kv_heads contiguous vectors in `dtype`,
+ * q_stride / k_stride elements from token to token (so slices of one
+ * projection's output are taken as they are); either may be NULL to skip that
+ * tensor.  q_out, k_out: likewise; an output may be its input (same pointer
+ * and stride), any other overlap is not allowed.  Pointers 16-byte aligned,
+ * strides multiples of 16 bytes and at least heads * 128.  q_weight,
+ * k_weight: device [128] in `dtype`, or NULL for no norm on that tensor (a
+ * model that only rotates).  positions: device int32 [n_tokens]; a token with
+ * a negative position is left alone (its output row is not written); NULL
+ * only with rot_dim 0, and then every token is taken.  inv_freq: device double
+ * [rot_dim / 2], radians per position (any frequency scaling is in it).
+ * rot_dim: 0..128; multiples of 16 are built, other even numbers give
+ * TQ_ERR_UNSUPPORTED.  Asynchronous on `stream`. */
+tq_status tq_norm_rope(const tq_codebook* book, const void* q, const void* k, tq_dtype dtype, int n_tokens,
+                       int n_q_heads, int n_kv_heads, int64_t q_stride, int64_t k_stride, const void* q_weight,
+                       const void* k_weight, float eps, const int32_t* positions, const double* inv_freq, int rot_dim,
+                       int interleaved, void* q_out, void* k_out, int64_t q_out_stride, int64_t k_out_stride,
+                       void* stream);
+
+/* Device workspace bytes tq_extend_attention needs for this shape (0 for
+ * invalid arguments). */
+size_t tq_extend_workspace_bytes(const tq_codebook* book, int n_tokens, int batch, int n_q_heads, int n_kv_heads,
+                                 int max_context);
+
+/* Attention of several new tokens per sequence over the packed cache: a
+ * prompt chunk on whatever is cached before it, or the verification of
+ * drafted tokens.  The method is that of tq_decode_attention (甲子光年 article
+ * §2 第二階段 for the score estimate, seo-farm page §4 and §2); the new tokens'
+ * own keys and values are read from the cache too, so they are appended
+ * first.
+ * q: device [n_tokens][n_q_heads][128] in `dtype`, the batch's new tokens one
+ * sequence after another; query_start: device int32 [batch + 1], sequence b's
+ * rows are query_start[b] .. query_start[b + 1] - 1 (non-decreasing, from 0,
+ * at most n_tokens).  context_lens: device int32 [batch], tokens of the
+ * sequence in the cache, its new ones included: with n new tokens, token i of
+ * the sequence sits at position context - n + i and sees positions 0 up to
+ * its own.  A token that sees nothing (more new tokens than context) gets a
+ * zero row; a sequence may have no new tokens.  Query head h reads KV head
+ * h / (n_q_heads / n_kv_heads), any whole ratio.  out: device bf16
+ * [n_tokens][n_q_heads][128]; rows behind query_start[batch] are left as they
+ * were.  The scores' operands are rounded to fp16 (queries scaled by a power
+ * of two, unit-norm keys), softmax weights and value levels to bf16;
+ * everything is summed in float32 and rounded to bf16 once at the end.
+ * cache, block_table, max_blocks, max_context and scale as in
+ * tq_decode_attention (max_context bounds every context_lens[b]).  workspace:
+ * device scratch of tq_extend_workspace_bytes bytes, 256-byte aligned, not
+ * used by any concurrent call.  Device errors: 2 a block id out of range (its
+ * tokens are skipped), 3 a context length or query_start out of range (rows
+ * of that sequence are zero where query_start places them inside n_tokens,
+ * else left as they were), 4 as elsewhere.  PolarQuant handles are not built
+ * (TQ_ERR_UNSUPPORTED).  Asynchronous on `stream`. */
+tq_status tq_extend_attention(const tq_codebook* book, const void* q, tq_dtype dtype, int n_tokens, int batch,
+                              int n_q_heads, int n_kv_heads, const tq_cache_view* cache, const int32_t* block_table,
+                              int max_blocks, const int32_t* query_start, const int32_t* context_lens, int max_context,
+                              float scale, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronise `stream`, then return (and clear) the first device-side error
  * code recorded since the last call: 0 none, 1 slot out of range in
  * quantize-append, 2 block id out of range in decode, 3 context length out of
@@ -373,7 +468,8 @@ tq_status tq_decode_plan(const tq_codebook* book, int batch, int n_q_heads, int 
  * early; its outputs are incomplete), 5 a merge found the partials of a
  * (sequence, KV head) missing or out of range (after a code 4 in the same
  * call, or tq_decode_finish without tq_decode_partials; those outputs are
- * zero).  Returns TQ_ERR_DEVICE when *code != 0. */
+ * zero), 6 and 7 the token map's free list or row count too small.  Returns
+ * TQ_ERR_DEVICE when *code != 0. */
 tq_status tq_get_last_device_error(const tq_codebook* book, void* stream, int* code);
 
 /* A test aid for the bounded waits, off by default: while enabled on a

@@ -28,6 +28,7 @@ EXPORTED = ("tq_codebook_build", "tq_codebook_destroy", "tq_codebook_levels", "t
             "tq_decode_step_prepare", "tq_decode_prepare", "tq_decode_partials", "tq_decode_finish",
             "tq_decode_attention_static", "tq_decode_kernel_kind", "tq_decode_plan", "tq_debug_withhold_commit",
             "tq_decode_parts_workspace_bytes", "tq_decode_attention_parts",
+            "tq_map_tokens", "tq_norm_rope", "tq_extend_workspace_bytes", "tq_extend_attention",
             "tq_get_last_device_error",
             "tq_status_string")
 
@@ -110,11 +111,18 @@ def load():
     lib.tq_decode_parts_workspace_bytes.restype = sz
     lib.tq_decode_attention_parts.argtypes = [ctypes.POINTER(tq_context_part), ctypes.POINTER(tq_context_part), vp,
                                               i32, i32, i32, i32, ctypes.c_float, vp, vp, sz, vp]
+    lib.tq_map_tokens.argtypes = [vp, i32, vp, vp, vp, i32, i32, vp, i32, i32, vp, vp, vp, vp, vp, vp]
+    lib.tq_norm_rope.argtypes = [vp, vp, vp, i32, i32, i32, i32, ctypes.c_int64, ctypes.c_int64, vp, vp,
+                                 ctypes.c_float, vp, vp, i32, i32, vp, vp, ctypes.c_int64, ctypes.c_int64, vp]
+    lib.tq_extend_workspace_bytes.argtypes = [vp, i32, i32, i32, i32, i32]
+    lib.tq_extend_workspace_bytes.restype = sz
+    lib.tq_extend_attention.argtypes = [vp, vp, i32, i32, i32, i32, i32, ctypes.POINTER(tq_cache_view), vp, i32, vp,
+                                        vp, i32, ctypes.c_float, vp, vp, sz, vp]
     lib.tq_get_last_device_error.argtypes = [vp, vp, ctypes.POINTER(i32)]
     lib.tq_status_string.argtypes = [i32]
     lib.tq_status_string.restype = ctypes.c_char_p
     for name in EXPORTED:
-        if name not in ("tq_decode_workspace_bytes", "tq_decode_step_host_workspace_bytes", "tq_status_string"):
+        if not name.endswith("workspace_bytes") and name != "tq_status_string":
             getattr(lib, name).restype = i32
     _LIB = lib
     return lib
@@ -141,6 +149,14 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _book_stream(book, stream):
+    """As _stream, the default being the current stream of the handle's device."""
+    if stream is None and book.device >= 0:
+        import torch
+        return torch.cuda.current_stream(book.device).cuda_stream if torch.cuda.is_available() else None
+    return _stream(stream)
 
 
 class Codebook:
@@ -370,3 +386,36 @@ def tq_decode_attention_parts(first, second, q, dtype, batch, n_q_heads, n_kv_he
     _check(load().tq_decode_attention_parts(ctypes.byref(first), ctypes.byref(second), _ptr(q), dtype, batch,
                                             n_q_heads, n_kv_heads, scale, _ptr(out), _ptr(workspace),
                                             workspace_bytes, _stream(stream)), "tq_decode_attention_parts")
+
+
+def tq_map_tokens(book, batch, past_lens, new_lens, block_table, max_blocks, num_blocks, free_blocks, n_free, n_tokens,
+                  context_lens, query_start, positions, slot_mapping, blocks_taken, stream=None):
+    """Context lengths, query starts, positions, slots and fresh block table
+    entries of one step, on the device."""
+    _check(load().tq_map_tokens(book.handle, batch, _ptr(past_lens), _ptr(new_lens), _ptr(block_table), max_blocks,
+                                num_blocks, _ptr(free_blocks), n_free, n_tokens, _ptr(context_lens),
+                                _ptr(query_start), _ptr(positions), _ptr(slot_mapping), _ptr(blocks_taken),
+                                _book_stream(book, stream)), "tq_map_tokens")
+
+
+def tq_norm_rope(book, q, k, dtype, n_tokens, n_q_heads, n_kv_heads, q_stride, k_stride, q_weight, k_weight, eps,
+                 positions, inv_freq, rot_dim, interleaved, q_out, k_out, q_out_stride, k_out_stride, stream=None):
+    """Head norms of queries and keys and their rotation by position; strides
+    in elements from token to token."""
+    _check(load().tq_norm_rope(book.handle, _ptr(q), _ptr(k), dtype, n_tokens, n_q_heads, n_kv_heads, q_stride,
+                               k_stride, _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions), _ptr(inv_freq),
+                               rot_dim, int(interleaved), _ptr(q_out), _ptr(k_out), q_out_stride, k_out_stride,
+                               _book_stream(book, stream)), "tq_norm_rope")
+
+
+def tq_extend_workspace_bytes(book, n_tokens, batch, n_q_heads, n_kv_heads, max_context):
+    return load().tq_extend_workspace_bytes(book.handle, n_tokens, batch, n_q_heads, n_kv_heads, max_context)
+
+
+def tq_extend_attention(book, q, dtype, n_tokens, batch, n_q_heads, n_kv_heads, view, block_table, max_blocks,
+                        query_start, context_lens, max_context, scale, out, workspace, workspace_bytes, stream=None):
+    """Attention of each sequence's last new tokens over its packed context."""
+    _check(load().tq_extend_attention(book.handle, _ptr(q), dtype, n_tokens, batch, n_q_heads, n_kv_heads,
+                                      ctypes.byref(view), _ptr(block_table), max_blocks, _ptr(query_start),
+                                      _ptr(context_lens), max_context, scale, _ptr(out), _ptr(workspace),
+                                      workspace_bytes, _book_stream(book, stream)), "tq_extend_attention")

@@ -41,5 +41,10 @@ def allocate_workspace(book, batch, n_q_heads, max_context, device="cuda"):
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), nbytes
 
 
+def allocate_extend_workspace(book, n_tokens, batch, n_q_heads, n_kv_heads, max_context, device="cuda"):
+    nbytes = binding.tq_extend_workspace_bytes(book, n_tokens, batch, n_q_heads, n_kv_heads, max_context)
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), nbytes
+
+
 def cache_bytes_per_token_head(book):
     return sum(binding.tq_cache_field_bytes(book).values())

@@ -574,6 +574,30 @@ tq_status decode_args(const tq_codebook* book, int stages, const void* q, tq_dty
   return TQ_OK;
 }
 
+// The cache and handle fields of an extend's launch arguments.
+void fill_cache_args(const tq_codebook* book, const tq_cache_view* cache, tq::DecodeArgs* a) {
+  a->k_codes = static_cast<const uint8_t*>(cache->k_codes);
+  a->k_qjl = book->cfg.qjl_m > 0 ? static_cast<const uint8_t*>(cache->k_qjl) : nullptr;
+  a->k_norm = cache->k_norm;
+  a->k_rnorm = book->cfg.qjl_m > 0 ? cache->k_rnorm : nullptr;
+  a->v_codes = static_cast<const uint8_t*>(cache->v_codes);
+  a->v_norm = cache->v_norm;
+  a->norm16 = book->norm16;
+  a->num_blocks = cache->num_blocks;
+  a->block_size = book->cfg.block_size;
+  a->k_bits = book->k_mse_bits;
+  a->v_bits = book->v_bits;
+  a->qjl_m = book->cfg.qjl_m;
+  a->qjl_coef = book->cfg.qjl_m > 0 ? static_cast<float>(std::sqrt(M_PI / 2.0) / book->cfg.qjl_m) : 0.f;
+  a->R = book->d_R;
+  a->Rt = book->d_Rt;
+  a->Spt = book->d_Spt;
+  a->St = book->d_St;
+  a->tables = book->d_tables;
+  a->error = book->d_error;
+  a->num_sms = book->num_sms;
+}
+
 tq_status launched(cudaError_t err) { return err == cudaSuccess ? TQ_OK : TQ_ERR_CUDA; }
 
 }  // namespace
@@ -916,6 +940,154 @@ tq_status tq_decode_plan(const tq_codebook* book, int batch, int n_q_heads, int 
   info->merge_ctas = !tc ? (n_vec + 1) / 2
                          : info->merge_in_partials ? 0 : tq::tc_merge_per_head(a) ? n_vec : batch * n_kv_heads;
   return TQ_OK;
+}
+
+tq_status tq_map_tokens(const tq_codebook* book, int batch, const int32_t* past_lens, const int32_t* new_lens,
+                        int32_t* block_table, int max_blocks, int num_blocks, const int32_t* free_blocks, int n_free,
+                        int n_tokens, int32_t* context_lens, int32_t* query_start, int32_t* positions,
+                        int64_t* slot_mapping, int32_t* blocks_taken, void* stream) {
+  if (!valid_device_handle(book) || batch < 0 || max_blocks <= 0 || num_blocks <= 0 || n_free < 0 || n_tokens < 0) {
+    return TQ_ERR_INVALID_ARG;
+  }
+  if (query_start == nullptr || blocks_taken == nullptr) return TQ_ERR_INVALID_ARG;
+  if (batch > 0 && (!past_lens || !new_lens || !block_table || !context_lens)) return TQ_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!positions || !slot_mapping)) return TQ_ERR_INVALID_ARG;
+  if (n_free > 0 && !free_blocks) return TQ_ERR_INVALID_ARG;
+  // (every CTA reads the lengths while the first one writes the contexts)
+  if (batch > 0 && (context_lens == past_lens || context_lens == new_lens)) return TQ_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0) return TQ_ERR_INVALID_ARG;
+  if (static_cast<long long>(max_blocks) * book->cfg.block_size > (1ll << 31) - 1) return TQ_ERR_INVALID_ARG;
+  if (batch > tq::kMapMaxBatch) return TQ_ERR_UNSUPPORTED;
+  tq::TokenMapArgs a{};
+  a.batch = batch;
+  a.past_lens = past_lens;
+  a.new_lens = new_lens;
+  a.block_table = block_table;
+  a.max_blocks = max_blocks;
+  a.num_blocks = num_blocks;
+  a.block_size = book->cfg.block_size;
+  a.free_blocks = free_blocks;
+  a.n_free = n_free;
+  a.n_tokens = n_tokens;
+  a.context_lens = context_lens;
+  a.query_start = query_start;
+  a.positions = positions;
+  a.slot_mapping = slot_mapping;
+  a.blocks_taken = blocks_taken;
+  a.error = book->d_error;
+  DeviceGuard guard(book->device);
+  return launched(tq::launch_token_map(a, static_cast<cudaStream_t>(stream)));
+}
+
+tq_status tq_norm_rope(const tq_codebook* book, const void* q, const void* k, tq_dtype dtype, int n_tokens,
+                       int n_q_heads, int n_kv_heads, int64_t q_stride, int64_t k_stride, const void* q_weight,
+                       const void* k_weight, float eps, const int32_t* positions, const double* inv_freq, int rot_dim,
+                       int interleaved, void* q_out, void* k_out, int64_t q_out_stride, int64_t k_out_stride,
+                       void* stream) {
+  if (!valid_device_handle(book) || n_tokens < 0) return TQ_ERR_INVALID_ARG;
+  if (dtype != TQ_BF16 && dtype != TQ_FP32) return TQ_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !std::isfinite(eps) || (interleaved != 0 && interleaved != 1)) return TQ_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim > tq::kDim || rot_dim % 2 != 0) return TQ_ERR_INVALID_ARG;
+  if (rot_dim > 0 && (inv_freq == nullptr || (reinterpret_cast<uintptr_t>(inv_freq) & 7u) != 0)) {
+    return TQ_ERR_INVALID_ARG;
+  }
+  if (n_tokens > 0 && q == nullptr && k == nullptr) return TQ_ERR_INVALID_ARG;
+  const int64_t vec = dtype == TQ_BF16 ? 8 : 4;   // elements of a 16-byte access
+  struct Side {
+    const void *x, *w, *out;
+    int64_t stride, out_stride;
+    int heads;
+  };
+  for (const Side& t : {Side{q, q_weight, q_out, q_stride, q_out_stride, n_q_heads},
+                        Side{k, k_weight, k_out, k_stride, k_out_stride, n_kv_heads}}) {
+    if (t.x == nullptr) continue;
+    if (t.heads <= 0 || t.heads > (1 << 20) || t.out == nullptr) return TQ_ERR_INVALID_ARG;
+    if (!aligned16(t.x) || !aligned16(t.out) || !aligned16(t.w)) return TQ_ERR_INVALID_ARG;
+    const int64_t row = static_cast<int64_t>(t.heads) * tq::kDim;
+    if (t.stride < row || t.out_stride < row || t.stride % vec != 0 || t.out_stride % vec != 0) {
+      return TQ_ERR_INVALID_ARG;
+    }
+    if (t.x == t.out && t.stride != t.out_stride) return TQ_ERR_INVALID_ARG;
+  }
+  if (n_tokens > 0 && rot_dim > 0 && positions == nullptr) return TQ_ERR_INVALID_ARG;
+  if (rot_dim % 16 != 0) return TQ_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return TQ_OK;
+  tq::NormRopeArgs a{};
+  a.q = q;
+  a.k = k;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.q_out_stride = q_out_stride;
+  a.k_out_stride = k_out_stride;
+  a.n_tokens = n_tokens;
+  a.n_q = q != nullptr ? n_q_heads : 0;
+  a.n_kv = k != nullptr ? n_kv_heads : 0;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.rot_dim = rot_dim;
+  a.interleaved = interleaved;
+  DeviceGuard guard(book->device);
+  return launched(tq::launch_norm_rope(a, dtype == TQ_BF16, book->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t tq_extend_workspace_bytes(const tq_codebook* book, int n_tokens, int batch, int n_q_heads, int n_kv_heads,
+                                 int max_context) {
+  if (!valid_device_handle(book) || n_tokens <= 0 || batch <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 ||
+      n_q_heads % n_kv_heads != 0 || max_context < 0) {
+    return 0;
+  }
+  return tq::extend_workspace_bytes(n_tokens, batch, n_q_heads, n_kv_heads, max_context, book->num_sms);
+}
+
+tq_status tq_extend_attention(const tq_codebook* book, const void* q, tq_dtype dtype, int n_tokens, int batch,
+                              int n_q_heads, int n_kv_heads, const tq_cache_view* cache, const int32_t* block_table,
+                              int max_blocks, const int32_t* query_start, const int32_t* context_lens, int max_context,
+                              float scale, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!valid_device_handle(book) || n_tokens < 0 || batch < 0 || n_q_heads <= 0 || n_kv_heads <= 0 ||
+      n_q_heads % n_kv_heads != 0 || max_context < 0 || max_blocks <= 0) {
+    return TQ_ERR_INVALID_ARG;
+  }
+  if (dtype != TQ_BF16 && dtype != TQ_FP32) return TQ_ERR_INVALID_ARG;
+  if (!valid_cache(book, cache) || cache->n_kv_heads != n_kv_heads) return TQ_ERR_INVALID_ARG;
+  if (!(scale >= 0.f) || !std::isfinite(scale)) return TQ_ERR_INVALID_ARG;
+  if (block_table == nullptr && static_cast<long long>(batch) * max_blocks > cache->num_blocks) {
+    return TQ_ERR_INVALID_ARG;
+  }
+  if (static_cast<long long>(n_tokens) * n_q_heads > (1ll << 31) - 1) return TQ_ERR_INVALID_ARG;
+  const bool any = n_tokens > 0 && batch > 0;
+  if (any && (!q || !aligned16(q) || !out || !aligned16(out) || !query_start || !context_lens)) {
+    return TQ_ERR_INVALID_ARG;
+  }
+  if (book->polar) return TQ_ERR_UNSUPPORTED;     // (PolarQuant records: decode one token at a time)
+  if (!any) return TQ_OK;
+  const size_t need = tq_extend_workspace_bytes(book, n_tokens, batch, n_q_heads, n_kv_heads, max_context);
+  if (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) {
+    return TQ_ERR_WORKSPACE;
+  }
+  tq::ExtendArgs a{};
+  tq::DecodeArgs& d = a.d;
+  d.q = q;
+  d.batch = batch;
+  d.n_q = n_q_heads;
+  d.n_kv = n_kv_heads;
+  d.group = n_q_heads / n_kv_heads;
+  fill_cache_args(book, cache, &d);
+  d.block_table = block_table;
+  d.max_blocks = max_blocks;
+  d.context_lens = context_lens;
+  d.max_context = max_context;
+  d.scale = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(book->cfg.d));
+  a.n_tokens = n_tokens;
+  a.query_start = query_start;
+  a.out = out;
+  a.q_bf16 = dtype == TQ_BF16;
+  DeviceGuard guard(book->device);
+  return launched(tq::launch_extend(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 tq_status tq_debug_withhold_commit(tq_codebook* book, int enable) {

@@ -10,7 +10,9 @@
 namespace tq {
 
 // Error codes a kernel records in the handle's error word.
-enum DeviceError : int { kErrSlot = 1, kErrBlock = 2, kErrContext = 3, kErrTimeout = 4, kErrPartials = 5 };
+enum DeviceError : int {
+  kErrSlot = 1, kErrBlock = 2, kErrContext = 3, kErrTimeout = 4, kErrPartials = 5, kErrNoBlock = 6, kErrTokens = 7
+};
 
 struct QuantizeArgs {
   const void* x;          // [n_tokens][n_kv][128], bf16 or fp32
@@ -201,5 +203,57 @@ cudaError_t launch_decode_finish(const DecodeArgs& args, cudaStream_t stream, bo
 // The merge over the partials of two parts of every sequence's context (two
 // caches, each with its own handle and workspace; the same R), into first.out.
 cudaError_t launch_decode_finish_parts(const DecodeArgs& first, const DecodeArgs& second, cudaStream_t stream);
+
+// Token map of one step (token_map.cu): prefix sums over the batch give every
+// new token its sequence, position and slot and every sequence its blocks.
+struct TokenMapArgs {
+  int batch;
+  const int32_t* past_lens;   // [batch]
+  const int32_t* new_lens;    // [batch]
+  int32_t* block_table;       // [batch][max_blocks], fresh entries written
+  int max_blocks, num_blocks, block_size;
+  const int32_t* free_blocks; // [n_free]
+  int n_free;
+  int n_tokens;               // capacity of positions / slot_mapping
+  int32_t* context_lens;      // [batch]
+  int32_t* query_start;       // [batch + 1]
+  int32_t* positions;         // [n_tokens]
+  int64_t* slot_mapping;      // [n_tokens]
+  int32_t* blocks_taken;      // [1]
+  int* error;
+};
+constexpr int kMapMaxBatch = 8192;   // the starts of a batch are held in shared memory
+cudaError_t launch_token_map(const TokenMapArgs& args, cudaStream_t stream);
+
+// Head norms and rotation by position (norm_rope.cu).
+struct NormRopeArgs {
+  const void* q;              // token rows of n_q heads, q_stride elements apart
+  const void* k;
+  void* q_out;
+  void* k_out;
+  long long q_stride, k_stride, q_out_stride, k_out_stride;
+  int n_tokens, n_q, n_kv;    // (an absent tensor has no heads)
+  const void* q_weight;       // [128] of the vectors' type; null: no norm
+  const void* k_weight;
+  float eps;
+  const int32_t* positions;   // [n_tokens]; negative: the token is left alone
+  const double* inv_freq;     // [rot_dim / 2], radians per position
+  int rot_dim, interleaved;
+  int group_tokens;           // set by the launcher
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& args, bool bf16, int num_sms, cudaStream_t stream);
+
+// Attention of several new tokens per sequence over the packed cache
+// (extend.cu).  The cache, scale and table fields of `d` are as in a decode;
+// its q and out are indexed by token here.
+struct ExtendArgs {
+  DecodeArgs d;
+  int n_tokens;
+  const int32_t* query_start; // [batch + 1]
+  void* out;                  // bf16 [n_tokens][n_q][128]
+  bool q_bf16;
+};
+size_t extend_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms);
+cudaError_t launch_extend(const ExtendArgs& args, void* workspace, cudaStream_t stream);
 
 }  // namespace tq
