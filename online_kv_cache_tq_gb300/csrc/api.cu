@@ -8,6 +8,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
@@ -80,10 +81,12 @@ void free_device(tq_codebook* b) {
   cudaFree(b->d_Spt);
   cudaFree(b->d_St);
   cudaFree(b->d_rot_tc);
+  cudaFree(b->d_rot_f16);
   cudaFree(b->d_tables);
   cudaFree(b->d_error);
   b->d_R = b->d_Rt = b->d_Spt = b->d_St = nullptr;
   b->d_rot_tc = nullptr;
+  b->d_rot_f16 = nullptr;
   b->d_tables = nullptr;
   b->d_error = nullptr;
 }
@@ -143,6 +146,32 @@ bool walsh_coefficients(const std::vector<double>& levels, int bits, float* out)
   return ok;
 }
 
+uint16_t fp16_bits(double x) {
+  const __half h = __float2half_rn(static_cast<float>(x));
+  uint16_t out;
+  std::memcpy(&out, &h, sizeof(out));
+  return out;
+}
+
+// The multi-token attention's operand images (see kExtendImage* in kernels.h):
+// R and S with their rows in the order the kernel expands a key's coordinates,
+// then R^T, each 128 x 128 fp16 in the 128-byte swizzled K-major layout.
+std::vector<uint16_t> extend_images(const tq::HostTables& h) {
+  constexpr int d = tq::kDim;
+  std::vector<uint16_t> img(3 * d * d, 0);
+  const int m = static_cast<int>(h.S.size()) / d;
+  for (int r = 0; r < d; ++r) {
+    const int src = (r & ~31) | tq::expanded_bit(r & 31);
+    for (int c = 0; c < d; ++c) {
+      const size_t at = tq::swizzled_f16(r, c);
+      img[at] = fp16_bits(h.R[src * d + c]);
+      img[d * d + at] = fp16_bits(src < m ? h.S[src * d + c] : 0.0);
+      img[2 * d * d + at] = fp16_bits(h.R[c * d + r]);
+    }
+  }
+  return img;
+}
+
 tq_status upload_tables(tq_codebook* b) {
   const int d = b->cfg.d;
   const int m = b->cfg.qjl_m;
@@ -186,6 +215,7 @@ tq_status upload_tables(tq_codebook* b) {
   if (err == cudaSuccess) err = upload(&b->d_Spt, Spt);
   if (err == cudaSuccess) err = upload(&b->d_St, St);
   if (err == cudaSuccess) err = upload(&b->d_rot_tc, tc);
+  if (err == cudaSuccess) err = upload(&b->d_rot_f16, extend_images(h));
   if (err == cudaSuccess) err = upload(&b->d_tables, tv);
   if (err == cudaSuccess) err = upload(&b->d_error, zero);
   if (err == cudaSuccess) err = cudaDeviceGetAttribute(&b->num_sms, cudaDevAttrMultiProcessorCount, b->device);
@@ -1041,7 +1071,7 @@ size_t tq_extend_workspace_bytes(const tq_codebook* book, int n_tokens, int batc
       n_q_heads % n_kv_heads != 0 || max_context < 0) {
     return 0;
   }
-  return tq::extend_workspace_bytes(n_tokens, batch, n_q_heads, n_kv_heads, max_context, book->num_sms);
+  return tq::extend_workspace_bytes(batch, book->num_sms);
 }
 
 tq_status tq_extend_attention(const tq_codebook* book, const void* q, tq_dtype dtype, int n_tokens, int batch,
@@ -1086,6 +1116,7 @@ tq_status tq_extend_attention(const tq_codebook* book, const void* q, tq_dtype d
   a.query_start = query_start;
   a.out = out;
   a.q_bf16 = dtype == TQ_BF16;
+  a.images = reinterpret_cast<const uint4*>(book->d_rot_f16);
   DeviceGuard guard(book->device);
   return launched(tq::launch_extend(a, workspace, static_cast<cudaStream_t>(stream)));
 }

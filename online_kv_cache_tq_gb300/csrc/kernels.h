@@ -244,16 +244,34 @@ struct NormRopeArgs {
 cudaError_t launch_norm_rope(const NormRopeArgs& args, bool bf16, int num_sms, cudaStream_t stream);
 
 // Attention of several new tokens per sequence over the packed cache
-// (extend.cu).  The cache, scale and table fields of `d` are as in a decode;
-// its q and out are indexed by token here.
+// (extend_tc.cu).  The cache, scale and table fields of `d` are as in a
+// decode; its q is indexed by token here.
+//
+// Expansion order: a 32-bit word of a bit plane holds the bits of 32
+// coordinates (or tokens); the kernel expands it eight at a time, chunk i
+// taking bits i, i + 4, .., i + 28, so element c of the expanded 32 is bit
+// expanded_bit(c).
+__host__ __device__ constexpr int expanded_bit(int c) { return (c & 7) * 4 + (c >> 3); }
+// Element (row, column) of a 128 x 128 fp16 operand: two 64-column K blocks
+// of 16 KB, rows of 128 bytes, 16-byte chunks swizzled by the row.
+__host__ __device__ constexpr int swizzled_f16(int row, int col) {
+  return (col >> 6) * 8192 + row * 64 + ((((col >> 3) & 7) ^ (row & 7)) << 3) + (col & 7);
+}
+constexpr int kExtendImageBytes = kDim * kDim * 2;   // R, S (rows in expansion order), R^T: one image each
+
 struct ExtendArgs {
   DecodeArgs d;
   int n_tokens;
   const int32_t* query_start; // [batch + 1]
   void* out;                  // bf16 [n_tokens][n_q][128]
   bool q_bf16;
+  const uint4* images;        // the three images, in that order
+  // workspace regions
+  long long* ws_first;        // [batch + 1]: key tiles of the work items before the sequence's first
+  int4* ws_seq;               // [batch]: first row, new tokens, context of a sequence (checked)
+  float* ws_part;             // partial outputs of the split work items
 };
-size_t extend_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms);
+size_t extend_workspace_bytes(int batch, int num_sms);
 cudaError_t launch_extend(const ExtendArgs& args, void* workspace, cudaStream_t stream);
 
 }  // namespace tq

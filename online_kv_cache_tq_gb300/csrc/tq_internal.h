@@ -69,6 +69,7 @@ struct tq_codebook {
   float* d_Spt;       // [d][m] S' transposed (column k of S' is row k)
   float* d_St;        // [d][m] S transposed: S q = S' R q for a query q
   uint16_t* d_rot_tc; // bf16 hi/lo operand images for the tensor-core quantizer
+  uint16_t* d_rot_f16; // fp16 operand images for the multi-token attention (kernels.h)
   tq::DeviceTables* d_tables;
   int* d_error;       // first device-side error code, 0 when none
   int num_sms;
