@@ -161,11 +161,11 @@ std::vector<uint16_t> extend_images(const tq::HostTables& h) {
   std::vector<uint16_t> img(3 * d * d, 0);
   const int m = static_cast<int>(h.S.size()) / d;
   for (int r = 0; r < d; ++r) {
-    const int src = (r & ~31) | tq::expanded_bit(r & 31);
+    const int src = (r & ~31) | tq::expanded_bit(r & 31), sgn = (r & ~31) | tq::expanded_sign(r & 31);
     for (int c = 0; c < d; ++c) {
       const size_t at = tq::swizzled_f16(r, c);
       img[at] = fp16_bits(h.R[src * d + c]);
-      img[d * d + at] = fp16_bits(src < m ? h.S[src * d + c] : 0.0);
+      img[d * d + at] = fp16_bits(sgn < m ? h.S[sgn * d + c] : 0.0);
       img[2 * d * d + at] = fp16_bits(h.R[c * d + r]);
     }
   }

@@ -196,7 +196,17 @@ __device__ __forceinline__ long long run_length(long long total, int ctas) { ret
 
 // ---- expansion of packed bits ------------------------------------------------
 
-__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+template <int OFFSET>
+__device__ __forceinline__ void store16(uint32_t saddr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0 + %5], {%1, %2, %3, %4};"
+               ::"r"(saddr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "n"(OFFSET)
+               : "memory");
+}
+__device__ __forceinline__ float4 load16(uint32_t saddr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(saddr));
+  return v;
+}
 
 // The 16-bit patterns of a codebook's levels as byte tables: low and high
 // bytes of levels 0..7 (for 16 levels, of the eight positive ones; the sign is
@@ -221,60 +231,70 @@ __device__ __forceinline__ LevelBytes level_bytes(const float* levels, int bits)
   return t;
 }
 
+// The bits i, i + 4, .., i + 28 of a plane word, each moved to bit `to` of its nibble.
+__device__ __forceinline__ uint32_t every_fourth(uint32_t w, int i, int to) {
+  return (i >= to ? w >> (i - to) : w << (to - i)) & (0x11111111u << to);
+}
+
 // Chunk i (bits i, i + 4, .., i + 28) of one plane word per code bit, as eight
 // 16-bit levels.  A code of up to three bits selects bytes from the tables
 // directly; with four the magnitude is the low three bits, inverted when the
 // top bit is clear, and a clear top bit sets the sign.
 template <int BITS>
-__device__ __forceinline__ uint4 expand8(const uint32_t* w, int i, const LevelBytes& t) {
+__device__ __forceinline__ uint4 expand8(const uint32_t (&w)[BITS], int i, const LevelBytes& t) {
   constexpr int kMag = BITS == 4 ? 3 : BITS;
-  uint32_t sel = (w[0] >> i) & 0x11111111u;
-  if constexpr (kMag > 1) sel |= ((w[1] >> i) & 0x11111111u) << 1;
-  if constexpr (kMag > 2) sel |= ((w[2] >> i) & 0x11111111u) << 2;
+  uint32_t sel = every_fourth(w[0], i, 0);
+  if constexpr (kMag > 1) sel |= every_fourth(w[1], i, 1);
+  if constexpr (kMag > 2) sel |= every_fourth(w[2], i, 2);
+  uint32_t top = 0;
+  if constexpr (BITS == 4) top = every_fourth(w[3], i, 0);
   uint32_t out[4];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t s = h ? sel >> 16 : sel;
-    const uint32_t lo = byte_perm(t.lo[0], t.lo[1], s);
-    uint32_t hi = byte_perm(t.hi[0], t.hi[1], s);
-    if constexpr (BITS == 4) {
-      const uint32_t top = (w[3] >> (i + 16 * h)) & 0x1111u;
-      hi ^= byte_perm(0x00000080u, 0u, top);
-    }
-    out[2 * h] = byte_perm(lo, hi, 0x5140);
-    out[2 * h + 1] = byte_perm(lo, hi, 0x7362);
+    const uint32_t lo = __byte_perm(t.lo[0], t.lo[1], h ? sel >> 16 : sel);
+    uint32_t hi = __byte_perm(t.hi[0], t.hi[1], h ? sel >> 16 : sel);
+    if constexpr (BITS == 4) hi ^= __byte_perm(0x00000080u, 0u, h ? top >> 16 : top);
+    out[2 * h] = __byte_perm(lo, hi, 0x5140);
+    out[2 * h + 1] = __byte_perm(lo, hi, 0x7362);
   }
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-template <int BITS>
-__device__ __forceinline__ void expand32(uint8_t* row, int swz, int chunk0, const uint32_t* planes, const LevelBytes& t) {
-  uint32_t w[BITS];
+// Shared addresses of chunks 0..3 of a row's first K block (swizzled); the
+// row's other chunks follow: ^ 64 bytes for chunks 4..7, + 16 KB per block.
+struct RowChunks {
+  uint32_t at[4];
+};
+__device__ __forceinline__ RowChunks row_chunks(uint32_t operand, int row) {
+  RowChunks r;
 #pragma unroll
-  for (int p = 0; p < BITS; ++p) w[p] = planes[p];
+  for (int i = 0; i < 4; ++i) r.at[i] = operand + row * 128 + ((i ^ (row & 7)) << 4);
+  return r;
+}
+__device__ __forceinline__ void next_word(RowChunks& r, int w) {   // from word w of a row to word w + 1
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.at[i] = (r.at[i] ^ 64) + (w & 1) * kBlockBytes;
+}
+
+// One word per plane (32 coordinates or tokens) into four chunks of a row.
+template <int BITS, int OFFSET>
+__device__ __forceinline__ void expand32(const RowChunks& r, uint32_t (&w)[BITS], const LevelBytes& t) {
   if constexpr (BITS == 4) {
 #pragma unroll
     for (int p = 0; p < 3; ++p) w[p] = w[p] ^ ~w[3];
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(row + (((chunk0 + i) ^ swz) << 4)) = expand8<BITS>(w, i, t);
-}
-
-__device__ __forceinline__ void expand32_bits(int bits, uint8_t* row, int swz, int chunk0, const uint32_t* planes,
-                                              const LevelBytes& t) {
-  if (bits == 2) expand32<2>(row, swz, chunk0, planes, t);
-  else if (bits == 3) expand32<3>(row, swz, chunk0, planes, t);
-  else if (bits == 1) expand32<1>(row, swz, chunk0, planes, t);
-  else expand32<4>(row, swz, chunk0, planes, t);
+  for (int i = 0; i < 4; ++i) store16<OFFSET>(r.at[i], expand8<BITS>(w, i, t));
 }
 
 // ---- products ----------------------------------------------------------------
 
 // D (+)= A B^T over `steps` K steps of 16: A in tensor memory (8 columns a
 // step), B in shared memory K blocks of 64 columns.
-__device__ __forceinline__ void product(uint32_t d, uint32_t a_tmem, uint32_t b_smem, int steps, uint32_t idesc,
-                                        bool accumulate) {
-  for (int ks = 0; ks < steps; ++ks)
+template <int STEPS>
+__device__ __forceinline__ void product(uint32_t d, uint32_t a_tmem, uint32_t b_smem, uint32_t idesc, bool accumulate) {
+#pragma unroll
+  for (int ks = 0; ks < STEPS; ++ks)
     ptx::mma_bf16_tmem_a(d, a_tmem + 8 * ks, ptx::desc_k_sw128(b_smem + (ks >> 2) * kBlockBytes + (ks & 3) * 32), idesc,
                          accumulate || ks > 0);
 }
@@ -354,13 +374,38 @@ __device__ __forceinline__ void load_query8(const ExtendArgs& a, long long at, f
   }
 }
 
-// Physical block of the cache at position pos of sequence b; -1 (recorded)
-// when the table's entry is outside the cache.
-__device__ __forceinline__ long long block_at(const DecodeArgs& d, int b, int pos) {
-  const int col = pos / d.block_size;
-  const long long blk = d.block_table ? d.block_table[static_cast<long long>(b) * d.max_blocks + col]
-                                      : static_cast<long long>(b) * d.max_blocks + col;
-  if (blk >= 0 && blk < d.num_blocks) return blk;
+// Walks the cache blocks under 32-token groups of a sequence, 128 tokens at a
+// time (a block holds whole groups), with the block table entry read one step
+// ahead.
+struct Cursor {
+  int pos, col, off;         // of the group that `id` belongs to
+  int id;
+};
+__device__ __forceinline__ int table_entry(const DecodeArgs& d, const Item& it, int pos, int col) {
+  if (pos >= it.seq.z) return -1;
+  return d.block_table ? __ldg(d.block_table + static_cast<long long>(it.b) * d.max_blocks + col)
+                       : it.b * d.max_blocks + col;
+}
+__device__ __forceinline__ void start_cursor(const DecodeArgs& d, const Item& it, int pos, Cursor& c) {
+  c.pos = pos;
+  c.col = pos / d.block_size;
+  c.off = pos - c.col * d.block_size;
+  c.id = table_entry(d, it, c.pos, c.col);
+}
+__device__ __forceinline__ void advance(const DecodeArgs& d, const Item& it, Cursor& c) {
+  c.pos += kTile;
+  c.off += kTile;
+  while (c.off >= d.block_size) {
+    c.off -= d.block_size;
+    ++c.col;
+  }
+  c.id = table_entry(d, it, c.pos, c.col);
+}
+// Row of (block, KV head) in the cache, -1 behind the context and (recorded)
+// for an entry outside the cache.
+__device__ __forceinline__ long long cache_row(const DecodeArgs& d, const Item& it, const Cursor& c) {
+  if (c.pos >= it.seq.z) return -1;
+  if (c.id >= 0 && c.id < d.num_blocks) return static_cast<long long>(c.id) * d.n_kv + it.kvh;
   atomicCAS(d.error, 0, kErrBlock);
   return -1;
 }
@@ -371,23 +416,24 @@ struct Barriers {
 };
 
 // Packed key of one token on its way into the ring.
+template <int KB>
 struct RawKey {
-  uint4 planes[4], qjl;
+  uint4 planes[KB], qjl;
   float norm, rnorm;
   bool valid;
 };
 
-__device__ __forceinline__ void load_key(const DecodeArgs& d, const Item& it, int pos, RawKey& k) {
+// Token `token` (0..31) of the group under the cursor.
+template <int KB>
+__device__ __forceinline__ void load_key(const DecodeArgs& d, const Item& it, const Cursor& c, int token, RawKey<KB>& k) {
   k.valid = false;
   k.norm = k.rnorm = 0.f;
-  if (pos >= it.seq.z) return;
-  const long long blk = block_at(d, it.b, pos);
-  if (blk < 0) return;
-  const long long row = (blk * d.n_kv + it.kvh) * d.block_size + pos % d.block_size;
-  const uint4* const codes = reinterpret_cast<const uint4*>(d.k_codes + row * (d.k_bits * 16));
+  const long long blk = cache_row(d, it, c);
+  if (blk < 0 || c.pos + token >= it.seq.z) return;
+  const long long row = blk * d.block_size + c.off + token;
+  const uint4* const codes = reinterpret_cast<const uint4*>(d.k_codes + row * (KB * 16));
 #pragma unroll
-  for (int p = 0; p < 4; ++p)
-    if (p < d.k_bits) k.planes[p] = __ldg(codes + p);
+  for (int p = 0; p < KB; ++p) k.planes[p] = __ldg(codes + p);
   k.norm = load_norm(d.k_norm, row, d.norm16);
   if (d.k_qjl != nullptr) {
     k.qjl = __ldg(reinterpret_cast<const uint4*>(d.k_qjl + row * 16));
@@ -398,30 +444,56 @@ __device__ __forceinline__ void load_key(const DecodeArgs& d, const Item& it, in
 
 // Value bits of one coordinate over the tile's 128 tokens, and the norm of
 // the token whose factor this thread writes.
+template <int VB>
 struct RawValue {
-  uint32_t words[4][4];      // [plane][32-token group]
+  uint32_t words[VB][4];     // [plane][32-token group]
   float norm;
 };
 
-__device__ __forceinline__ void load_value(const DecodeArgs& d, const Item& it, int tile0, int dim, int token,
-                                           RawValue& v) {
-  v.norm = 0.f;
+// Lane l of the warp has the cursor of group l & 3; `group` is the one whose
+// norms this warp reads.  Blocks of a multiple of 128 (64) tokens give a
+// thread's words in one 16-byte (two 8-byte) loads per plane.
+template <int VB>
+__device__ __forceinline__ void load_value(const DecodeArgs& d, const Item& it, const Cursor& c, int dim, int group,
+                                           int token, RawValue<VB>& v) {
+  const long long row = cache_row(d, it, c);
+  const int words = d.block_size / 32;            // of one plane and coordinate
+  const long long base = row < 0 ? -1 : row * (VB * 128ll * words) + c.off / 32;
+  const uint32_t* const codes = reinterpret_cast<const uint32_t*>(d.v_codes) + dim * words;
+  const int plane = 128 * words;
+  long long at[4];
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int pos = tile0 + 32 * g;               // (a block holds whole groups of 32)
-    const long long blk = pos < it.seq.z ? block_at(d, it.b, pos) : -1;
-    const int off = pos % d.block_size;
+  for (int g = 0; g < 4; ++g) at[g] = __shfl_sync(0xffffffffu, base, g);
+  const long long norm_row = __shfl_sync(0xffffffffu, row, group);
+  const int norm_off = __shfl_sync(0xffffffffu, c.off, group), norm_pos = __shfl_sync(0xffffffffu, c.pos, group);
+  if (words % 4 == 0) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p)
-      if (p < d.v_bits)
-        v.words[p][g] = blk < 0 ? 0u
-                                : __ldg(reinterpret_cast<const uint32_t*>(d.v_codes) +
-                                        transposed_word(blk, it.kvh, d.n_kv, d.v_bits, p, dim, d.block_size, off));
-    if (g == token >> 5 && blk >= 0 && tile0 + token < it.seq.z)
-      v.norm = load_norm(d.v_norm, (blk * d.n_kv + it.kvh) * d.block_size + off + (token & 31), d.norm16);
+    for (int p = 0; p < VB; ++p) {
+        const uint4 w = at[0] < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>(codes + at[0] + p * plane));
+        v.words[p][0] = w.x, v.words[p][1] = w.y, v.words[p][2] = w.z, v.words[p][3] = w.w;
+      }
+  } else if (words % 2 == 0) {
+#pragma unroll
+    for (int p = 0; p < VB; ++p) {
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+          const uint2 w = at[g] < 0 ? make_uint2(0, 0) : __ldg(reinterpret_cast<const uint2*>(codes + at[g] + p * plane));
+          v.words[p][g] = w.x, v.words[p][g + 1] = w.y;
+        }
+      }
+  } else {
+#pragma unroll
+    for (int p = 0; p < VB; ++p) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) v.words[p][g] = at[g] < 0 ? 0u : __ldg(codes + at[g] + p * plane);
+      }
   }
+  v.norm = norm_row < 0 || norm_pos + token >= it.seq.z
+               ? 0.f
+               : load_norm(d.v_norm, norm_row * d.block_size + norm_off + token, d.norm16);
 }
 
+template <int KB, int VB>
 __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers bar;
@@ -505,7 +577,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       int e = exponent_of(biggest);
       if (biggest == 0.f || (e >= -8 && e < 10)) e = 0;
       const float down = exp2_int(-e), factor = exp2_int(e);
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < 4; ++h) {
         uint32_t w[16];
 #pragma unroll
@@ -524,7 +596,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       if (!ok) break;
       ptx::tc_fence_after();
       float2 len2 = make_float2(0.f, 0.f);        // |R q|^2, |S q|^2
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < 8; ++h) {
         if (h < 4 || qjl) {
           uint32_t x[32], w[16];
@@ -554,8 +626,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
         if (!ok) break;
         ptx::tc_fence_after();
         const uint32_t s_addr = lane_addr + (sb ? kS1 : kS0);
-        const float* const kf = key_factor + rg * kTile;
-        const float* const vf = value_factor + rg * kTile;
+        const uint32_t kf = ptx::smem_u32(key_factor + rg * kTile), vf = ptx::smem_u32(value_factor + rg * kTile);
         const uint32_t all = valid_s[rg][0] & valid_s[rg][1] & valid_s[rg][2] & valid_s[rg][3];
         float top_bound = 0.f;                    // |score| <= |R q| |n c| + |S q| |n rho signs|
 #pragma unroll
@@ -564,14 +635,14 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
         const bool usual = t > t0 && e == 0 && seen >= (t + 1) * kTile && all == 0xffffffffu && top_bound <= ref + kRaise;
         if (__all_sync(0xffffffffu, usual)) {
           const uint64_t minus = pair(-ref, -ref);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t x[32], w[16];
             ptx::tmem_ld32(s_addr + 32 * c, x);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const float4 f = *reinterpret_cast<const float4*>(kf + 32 * c + 4 * k);
-              const float4 g = *reinterpret_cast<const float4*>(vf + 32 * c + 4 * k);
+              const float4 f = load16(kf + 128 * c + 16 * k);
+              const float4 g = load16(vf + 128 * c + 16 * k);
               const float2 z0 = unpair(fma2(pair(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])),
                                             pair(f.x, f.y), minus));
               const float2 z1 = unpair(fma2(pair(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])),
@@ -588,21 +659,26 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
           // hidden positions, a scaled query, or scores that may pass the
           // reference: the tile's maximum first
           const int here = min(kTile, max(0, seen - t * kTile));
-          uint32_t mask[4];
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
+          auto mask_of = [&](int g) {
             const int n = min(32, max(0, here - 32 * g));
-            mask[g] = (n == 32 ? 0xffffffffu : (1u << n) - 1u) & valid_s[rg][g];
-          }
+            return (n == 32 ? 0xffffffffu : (1u << n) - 1u) & valid_s[rg][g];
+          };
           float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
+            const uint32_t mask = mask_of(c);
             uint32_t x[32];
             ptx::tmem_ld32(s_addr + 32 * c, x);
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (mask[c] & (1u << expanded_bit(k)))
-                top = fmaxf(top, __uint_as_float(x[k]) * kf[32 * c + k] * factor);
+            for (int k = 0; k < 8; ++k) {
+              const float4 f = load16(kf + 128 * c + 16 * k);
+              const float fk[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float s = __uint_as_float(x[4 * k + q]) * fk[q] * factor;
+                top = mask & (1u << expanded_bit(4 * k + q)) ? fmaxf(top, s) : top;
+              }
+            }
           }
           const bool raise = top > ref + kRaise || (ref == -INFINITY && top > ref);
           if (__any_sync(0xffffffffu, raise)) {
@@ -614,7 +690,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
               if (!ok) break;
               ptx::tc_fence_after();
               sum2 = mul2(sum2, pair(scale, scale));
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < 4; ++c) {
                 uint32_t x[32];
                 ptx::tmem_ld32(lane_addr + kO + 32 * c, x);
@@ -626,23 +702,26 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
           }
           const float shift = ref == -INFINITY ? 0.f : ref;
           float sum = 0.f;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
+            const uint32_t mask = mask_of(c);
             uint32_t x[32], w[16];
             ptx::tmem_ld32(s_addr + 32 * c, x);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float p[2];
+            for (int k = 0; k < 8; ++k) {
+              const float4 f = load16(kf + 128 * c + 16 * k);
+              const float4 g = load16(vf + 128 * c + 16 * k);
+              const float fk[4] = {f.x, f.y, f.z, f.w}, gk[4] = {g.x, g.y, g.z, g.w};
+              float p[4];
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const int k2 = 2 * k + q;
-                const bool on = mask[c] & (1u << expanded_bit(k2));
-                const float s = __uint_as_float(x[k2]) * kf[32 * c + k2] * factor;
-                p[q] = on ? exp2_fast(s - shift) : 0.f;
+              for (int q = 0; q < 4; ++q) {
+                const bool on = mask & (1u << expanded_bit(4 * k + q));
+                p[q] = on ? exp2_fast(__uint_as_float(x[4 * k + q]) * fk[q] * factor - shift) : 0.f;
                 sum += p[q];
-                p[q] = on ? p[q] * vf[32 * c + k2] : 0.f;
+                p[q] = on ? p[q] * gk[q] : 0.f;
               }
-              w[k] = pack_bf16(p[0], p[1]);
+              w[2 * k] = pack_bf16(p[0], p[1]);
+              w[2 * k + 1] = pack_bf16(p[2], p[3]);
             }
             tmem_st16(s_addr + 16 * c, w);
           }
@@ -662,7 +741,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       const float sum = halves.x + halves.y;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;       // (a NaN in a visible token shows)
       float top = 0.f;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t x[32];
         ptx::tmem_ld32(lane_addr + kO + 32 * c, x);
@@ -671,7 +750,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       }
       const int eo = exponent_of(top);
       const float out_down = inv * exp2_int(-eo), out_up = exp2_int(eo);
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t x[32], w[16];
         ptx::tmem_ld32(lane_addr + kO + 32 * c, x);
@@ -693,7 +772,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
         part[kTile * kDim + 2 * tid] = sum == 0.f ? -INFINITY : ref;
         part[kTile * kDim + 2 * tid + 1] = sum;
       }
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t x[32];
         ptx::tmem_ld32(lane_addr + kS1 + 32 * c, x);
@@ -720,11 +799,10 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
     }
   } else if (warp < 8) {
     // ---------------- keys ----------------
-    const int row = tid - kSoftThreads;           // row of the tile: token (row & ~31) + expanded_bit(row & 31)
-    const int token = (row & ~31) | expanded_bit(row & 31);
-    const LevelBytes lev = level_bytes<false>(d.tables->k_levels, d.k_bits);
+    const int row = tid - kSoftThreads;           // row of the tile: token expanded_bit(lane) of the warp's group
+    const LevelBytes lev = level_bytes<false>(d.tables->k_levels, KB);
     float biggest = 0.f;                          // the outermost level
-    for (int i = 0; i < (1 << d.k_bits); ++i) biggest = fmaxf(biggest, fabsf(d.tables->k_levels[i]));
+    for (int i = 0; i < (1 << KB); ++i) biggest = fmaxf(biggest, fabsf(d.tables->k_levels[i]));
     const float to_log2 = d.scale * 1.4426950408889634f;
     int kc = 0, jt = 0;                           // ring entries, key tiles so far
     auto image = [&](int first, int count) {      // operand images as a ring entry
@@ -741,42 +819,48 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
     };
     while (ok && pos < end) {
       const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
-      RawKey next;
-      load_key(d, it, t0 * kTile + token, next);
+      Cursor c;
+      RawKey<KB> next;
+      start_cursor(d, it, t0 * kTile + (row & ~31), c);
+      load_key(d, it, c, expanded_bit(lane), next);
+      advance(d, it, c);
       ok = image(0, qjl ? 2 : 1);
       for (int t = t0; ok && t < t1; ++t, ++jt, ++kc) {
-        const RawKey k = next;
-        if (t + 1 < t1) load_key(d, it, (t + 1) * kTile + token, next);
+        RawKey<KB> k = next;
+        if (t + 1 < t1) {
+          load_key(d, it, c, expanded_bit(lane), next);
+          advance(d, it, c);
+        }
         const int s = kc & 1, rg = jt & (kRing - 1);
         ok = __all_sync(0xffffffffu, TQ_WAIT(bar.k_empty[s], ((kc >> 1) & 1) ^ 1));
         if (!ok) break;
-        uint8_t* const base = smem + kKey0 + s * kKeyBytes + row * 128;
-        const int swz = row & 7;
-        const uint32_t* const pl = reinterpret_cast<const uint32_t*>(k.planes);
-#pragma unroll
+        // 32 coordinates a turn, the words of a plane rotating through .x: a
+        // short loop, so that the three roles' code stays in the first-level
+        // instruction cache
+        RowChunks at = row_chunks(ptx::smem_u32(smem + kKey0 + s * kKeyBytes), row);
+        const float rho = qjl && k.norm > 0.f ? k.rnorm * d.qjl_coef / k.norm : 0.f;
+        const uint32_t minus_rho = __half_as_ushort(__float2half_rn(rho)) * 0x00010001u ^ 0x80008000u;
+#pragma unroll 1
         for (int w = 0; w < 4; ++w) {
-          const uint32_t planes[4] = {pl[w], pl[4 + w], pl[8 + w], pl[12 + w]};
-          expand32_bits(d.k_bits, base + (w >> 1) * kBlockBytes, swz, (w & 1) * 4, planes, lev);
-        }
-        float rho = 0.f;
-        if (qjl) {
-          rho = k.norm > 0.f ? k.rnorm * d.qjl_coef / k.norm : 0.f;
-          const uint32_t pos16 = __half_as_ushort(__float2half_rn(rho));
-          const uint32_t lo = (pos16 & 255u) * 0x01010101u;
-          const uint32_t hi_tab = ((pos16 >> 8) ^ 0x80u) | (pos16 & 0xff00u);   // byte 0: -rho, byte 1: rho
-          const uint32_t qw[4] = {k.qjl.x, k.qjl.y, k.qjl.z, k.qjl.w};
+          uint32_t planes[KB];
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint8_t* const blk = base + (2 + (w >> 1)) * kBlockBytes;
+          for (int p = 0; p < KB; ++p) {
+            planes[p] = k.planes[p].x;
+            k.planes[p].x = k.planes[p].y, k.planes[p].y = k.planes[p].z, k.planes[p].z = k.planes[p].w;
+          }
+          expand32<KB, 0>(at, planes, lev);
+          if (qjl) {
+            const uint32_t bits = k.qjl.x;
+            k.qjl.x = k.qjl.y, k.qjl.y = k.qjl.z, k.qjl.z = k.qjl.w;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t sel = (qw[w] >> i) & 0x11111111u;
-              const uint32_t h0 = byte_perm(hi_tab, 0u, sel), h1 = byte_perm(hi_tab, 0u, sel >> 16);
-              *reinterpret_cast<uint4*>(blk + ((((w & 1) * 4 + i) ^ swz) << 4)) =
-                  make_uint4(byte_perm(lo, h0, 0x5140), byte_perm(lo, h0, 0x7362), byte_perm(lo, h1, 0x5140),
-                             byte_perm(lo, h1, 0x7362));
+            for (int i = 0; i < 4; ++i) {         // a set bit clears the sign of -rho
+              uint32_t out[4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h) out[h] = ((bits << (15 - 4 * i - h)) & 0x80008000u) ^ minus_rho;
+              store16<2 * kBlockBytes>(at.at[i], make_uint4(out[0], out[1], out[2], out[3]));
             }
           }
+          next_word(at, w);
         }
         const float f = k.valid ? k.norm * to_log2 : 0.f;
         key_factor[rg * kTile + row] = f;
@@ -807,24 +891,36 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
   } else if (warp < kMmaWarp) {
     // ---------------- values ----------------
     const int dim = tid - kSoftThreads - kKeyThreads;
-    const int token = (dim & ~31) | expanded_bit(dim & 31);   // whose factor this thread writes, at column dim
-    const LevelBytes lev = level_bytes<true>(d.tables->v_levels, d.v_bits);
+    const int token = expanded_bit(lane);         // of the warp's group: whose factor this thread writes, at column dim
+    const LevelBytes lev = level_bytes<true>(d.tables->v_levels, VB);
     int jt = 0;
     while (ok && pos < end) {
       const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
-      RawValue next;
-      load_value(d, it, t0 * kTile, dim, token, next);
+      Cursor c;
+      RawValue<VB> next;
+      start_cursor(d, it, t0 * kTile + 32 * (lane & 3), c);
+      load_value(d, it, c, dim, dim >> 5, token, next);
+      advance(d, it, c);
       for (int t = t0; t < t1; ++t, ++jt) {
-        const RawValue v = next;
-        if (t + 1 < t1) load_value(d, it, (t + 1) * kTile, dim, token, next);
+        RawValue<VB> v = next;
+        if (t + 1 < t1) {
+          load_value(d, it, c, dim, dim >> 5, token, next);
+          advance(d, it, c);
+        }
         const int s = jt & 1, rg = jt & (kRing - 1);
-        ok = TQ_WAIT(bar.v_empty[s], ((jt >> 1) & 1) ^ 1);
+        ok = __all_sync(0xffffffffu, TQ_WAIT(bar.v_empty[s], ((jt >> 1) & 1) ^ 1));
         if (!ok) break;
-        uint8_t* const base = smem + kValue0 + s * kValueBytes + dim * 128;
-#pragma unroll
+        RowChunks at = row_chunks(ptx::smem_u32(smem + kValue0 + s * kValueBytes), dim);
+#pragma unroll 1
         for (int g = 0; g < 4; ++g) {
-          const uint32_t planes[4] = {v.words[0][g], v.words[1][g], v.words[2][g], v.words[3][g]};
-          expand32_bits(d.v_bits, base + (g >> 1) * kBlockBytes, dim & 7, (g & 1) * 4, planes, lev);
+          uint32_t planes[VB];
+#pragma unroll
+          for (int p = 0; p < VB; ++p) {
+            planes[p] = v.words[p][0];
+            v.words[p][0] = v.words[p][1], v.words[p][1] = v.words[p][2], v.words[p][2] = v.words[p][3];
+          }
+          expand32<VB, 0>(at, planes, lev);
+          next_word(at, g);
         }
         value_factor[rg * kTile + dim] = v.norm;
         ptx::fence_async_shared();
@@ -833,7 +929,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       pos += t1 - t0;
       if (pos < end) next_item(a, it);
     }
-  } else if (lane == 0) {
+  } else if (ptx::elect_one()) {
     // ---------------- products ----------------
     int kc = 0, jt = 0;
     for (int seg = 0; ok && pos < end; ++seg) {
@@ -843,8 +939,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       ok = TQ_WAIT(bar.k_full[kc & 1], (kc >> 1) & 1) && TQ_WAIT(bar.q_raw, seg & 1);
       if (!ok) break;
       ptx::tc_fence_after();
-      product(tmem + kS0, tmem + kS1, key_stage(kc), 8, kIdescF16, false);
-      if (qjl) product(tmem + kO, tmem + kS1, key_stage(kc) + 2 * kBlockBytes, 8, kIdescF16, false);
+      product<8>(tmem + kS0, tmem + kS1, key_stage(kc), kIdescF16, false);
+      if (qjl) product<8>(tmem + kO, tmem + kS1, key_stage(kc) + 2 * kBlockBytes, kIdescF16, false);
       ptx::mma_commit(&bar.k_empty[kc & 1]);
       ptx::mma_commit(&bar.rotated);
       ++kc;
@@ -856,7 +952,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
         // its columns held the weights of tile j - 2
         if (!first_two && !TQ_WAIT(bar.v_empty[j & 1], ((j - 2) >> 1) & 1)) return false;
         ptx::tc_fence_after();
-        product(tmem + (j & 1 ? kS1 : kS0), tmem + kQ, key_stage(kc), qjl ? 16 : 8, kIdescF16, false);
+        if (qjl) product<16>(tmem + (j & 1 ? kS1 : kS0), tmem + kQ, key_stage(kc), kIdescF16, false);
+        else product<8>(tmem + (j & 1 ? kS1 : kS0), tmem + kQ, key_stage(kc), kIdescF16, false);
         ptx::mma_commit(&bar.k_empty[kc & 1]);
         ptx::mma_commit(&bar.s_full[j & 1]);
         ptx::mbar_arrive(&bar.s_full[j & 1]);
@@ -871,15 +968,15 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
         ok = ok && TQ_WAIT(bar.v_full[s], ph) && TQ_WAIT(bar.p_full[s], ph);
         if (!ok) break;
         ptx::tc_fence_after();
-        product(tmem + kO, tmem + (s ? kS1 : kS0), ptx::smem_u32(smem + kValue0 + s * kValueBytes), 8, kIdescBf16,
-                t > t0);
+        product<8>(tmem + kO, tmem + (s ? kS1 : kS0), ptx::smem_u32(smem + kValue0 + s * kValueBytes), kIdescBf16,
+                   t > t0);
         ptx::mma_commit(&bar.v_empty[s]);
       }
       // R^T out
       ok = ok && TQ_WAIT(bar.k_full[kc & 1], (kc >> 1) & 1) && TQ_WAIT(bar.o_raw, seg & 1);
       if (!ok) break;
       ptx::tc_fence_after();
-      product(tmem + kS1, tmem + kS0, key_stage(kc), 8, kIdescF16, false);
+      product<8>(tmem + kS1, tmem + kS0, key_stage(kc), kIdescF16, false);
       ptx::mma_commit(&bar.k_empty[kc & 1]);
       ptx::mma_commit(&bar.turned);
       ++kc;
@@ -944,6 +1041,37 @@ __global__ void __launch_bounds__(32 * kJoinWarps) extend_join_kernel(ExtendArgs
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
+template <int KB, int VB>
+cudaError_t launch_bits(const ExtendArgs& a, int ctas, cudaStream_t stream) {
+  const cudaError_t err =
+      cudaFuncSetAttribute(extend_kernel<KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (err != cudaSuccess) return err;
+  extend_kernel<KB, VB><<<ctas, kExtThreads, kSmemBytes, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int KB>
+cudaError_t launch_keys(const ExtendArgs& a, int ctas, cudaStream_t stream) {
+  switch (a.d.v_bits) {
+    case 1: return launch_bits<KB, 1>(a, ctas, stream);
+    case 2: return launch_bits<KB, 2>(a, ctas, stream);
+    case 3: return launch_bits<KB, 3>(a, ctas, stream);
+    default: return launch_bits<KB, 4>(a, ctas, stream);
+  }
+}
+
+// One build per pair of bit widths: a role's loop then fits the instruction
+// cache (with the widths chosen inside the loops every role ran at a quarter
+// of its speed, waiting for instructions).
+cudaError_t launch_main(const ExtendArgs& a, int ctas, cudaStream_t stream) {
+  switch (a.d.k_bits) {
+    case 1: return launch_keys<1>(a, ctas, stream);
+    case 2: return launch_keys<2>(a, ctas, stream);
+    case 3: return launch_keys<3>(a, ctas, stream);
+    default: return launch_keys<4>(a, ctas, stream);
+  }
+}
+
 constexpr size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
@@ -961,10 +1089,9 @@ cudaError_t launch_extend(const ExtendArgs& args, void* workspace, cudaStream_t 
   a.ws_part = reinterpret_cast<float*>(reinterpret_cast<char*>(a.ws_seq) +
                                        align256(static_cast<size_t>(a.d.batch) * sizeof(int4)));
   const int ctas = a.d.num_sms;
-  cudaError_t err = cudaFuncSetAttribute(extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (err != cudaSuccess) return err;
   extend_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
-  extend_kernel<<<ctas, kExtThreads, kSmemBytes, stream>>>(a);
+  const cudaError_t err = launch_main(a, ctas, stream);
+  if (err != cudaSuccess) return err;
   if (ctas > 1) extend_join_kernel<<<dim3(ctas - 1, kTile / kJoinWarps), 32 * kJoinWarps, 0, stream>>>(a, ctas);
   return cudaGetLastError();
 }

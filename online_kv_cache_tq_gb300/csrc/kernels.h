@@ -251,7 +251,9 @@ cudaError_t launch_norm_rope(const NormRopeArgs& args, bool bf16, int num_sms, c
 // coordinates (or tokens); the kernel expands it eight at a time, chunk i
 // taking bits i, i + 4, .., i + 28, so element c of the expanded 32 is bit
 // expanded_bit(c).
+// The sketch's sign bits are expanded in pairs (j, j + 16) instead.
 __host__ __device__ constexpr int expanded_bit(int c) { return (c & 7) * 4 + (c >> 3); }
+__host__ __device__ constexpr int expanded_sign(int c) { return (c & 1) * 16 + (c >> 1); }
 // Element (row, column) of a 128 x 128 fp16 operand: two 64-column K blocks
 // of 16 KB, rows of 128 bytes, 16-byte chunks swizzled by the row.
 __host__ __device__ constexpr int swizzled_f16(int row, int col) {
