@@ -34,8 +34,10 @@
 // multiply-add, an exponential, a sum, a product and a conversion per score.
 // Tiles with hidden positions take a second path that masks.
 //
-// Thirteen warps: 0-3 softmax (a thread per row), 4-7 keys (a thread per
-// token), 8-11 values (a thread per coordinate), 12 issues the products.
+// Twenty-five warps: 0-7 softmax (two threads per row, 64 columns each), 8-15
+// keys (two threads per token), 16-23 values (two threads per coordinate), 24
+// issues the products.  With half as many, each role's chain of dependent
+// instructions was longer than the products it feeds.
 // Tensor memory: two score tiles of 128 columns (weights overwrite them),
 // the output, the query operand.
 #include <cuda_bf16.h>
@@ -48,10 +50,10 @@ namespace tq {
 namespace {
 
 constexpr int kTile = 128;                        // rows of a row tile, tokens of a key tile
-constexpr int kSoftThreads = 128;
-constexpr int kKeyThreads = 128;
-constexpr int kValueThreads = 128;
-constexpr int kMmaWarp = 12;
+constexpr int kSoftThreads = 256;
+constexpr int kKeyThreads = 256;
+constexpr int kValueThreads = 256;
+constexpr int kMmaWarp = 24;
 constexpr int kExtThreads = kSoftThreads + kKeyThreads + kValueThreads + 32;
 constexpr int kBlockBytes = kTile * 128;          // a 64-column K block of a 128-row operand
 constexpr int kKeyBytes = 4 * kBlockBytes;
@@ -261,7 +263,7 @@ __device__ __forceinline__ uint4 expand8(const uint32_t (&w)[BITS], int i, const
 }
 
 // Shared addresses of chunks 0..3 of a row's first K block (swizzled); the
-// row's other chunks follow: ^ 64 bytes for chunks 4..7, + 16 KB per block.
+// row's other chunks follow: ^ 64 bytes for chunks 4..7.
 struct RowChunks {
   uint32_t at[4];
 };
@@ -271,9 +273,8 @@ __device__ __forceinline__ RowChunks row_chunks(uint32_t operand, int row) {
   for (int i = 0; i < 4; ++i) r.at[i] = operand + row * 128 + ((i ^ (row & 7)) << 4);
   return r;
 }
-__device__ __forceinline__ void next_word(RowChunks& r, int w) {   // from word w of a row to word w + 1
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r.at[i] = (r.at[i] ^ 64) + (w & 1) * kBlockBytes;
+__device__ __forceinline__ RowChunks second_word(const RowChunks& r) {   // chunks 4..7
+  return RowChunks{{r.at[0] ^ 64, r.at[1] ^ 64, r.at[2] ^ 64, r.at[3] ^ 64}};
 }
 
 // One word per plane (32 coordinates or tokens) into four chunks of a row.
@@ -287,15 +288,28 @@ __device__ __forceinline__ void expand32(const RowChunks& r, uint32_t (&w)[BITS]
   for (int i = 0; i < 4; ++i) store16<OFFSET>(r.at[i], expand8<BITS>(w, i, t));
 }
 
+// A word of sketch signs: a set bit clears the sign of -rho.
+template <int OFFSET>
+__device__ __forceinline__ void expand_signs(const RowChunks& r, uint32_t bits, uint32_t minus_rho) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t out[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) out[h] = ((bits << (15 - 4 * i - h)) & 0x80008000u) ^ minus_rho;
+    store16<OFFSET>(r.at[i], make_uint4(out[0], out[1], out[2], out[3]));
+  }
+}
+
 // ---- products ----------------------------------------------------------------
 
-// D (+)= A B^T over `steps` K steps of 16: A in tensor memory (8 columns a
-// step), B in shared memory K blocks of 64 columns.
+// D (+)= A B^T over STEPS K steps of 16, issued by one lane: A in tensor
+// memory (8 columns a step), B in shared memory K blocks of 64 columns (a step
+// is 32 bytes, a block 16 KB: 2 and 1024 in the descriptor's units).
 template <int STEPS>
-__device__ __forceinline__ void product(uint32_t d, uint32_t a_tmem, uint32_t b_smem, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void product(uint32_t d, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
 #pragma unroll
   for (int ks = 0; ks < STEPS; ++ks)
-    ptx::mma_bf16_tmem_a(d, a_tmem + 8 * ks, ptx::desc_k_sw128(b_smem + (ks >> 2) * kBlockBytes + (ks & 3) * 32), idesc,
+    ptx::mma_bf16_tmem_a(d, a_tmem + 8 * ks, b_desc + (ks >> 2) * (kBlockBytes / 16) + (ks & 3) * 2, idesc,
                          accumulate || ks > 0);
 }
 
@@ -342,12 +356,32 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+// ptx::tmem_ld16 in two steps, so that a load runs while the columns before it are worked on.
+__device__ __forceinline__ void tmem_ld16_start(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+      :
       : "memory");
 }
 
@@ -413,84 +447,77 @@ __device__ __forceinline__ long long cache_row(const DecodeArgs& d, const Item& 
 struct Barriers {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
   uint64_t q_raw, rotated, q_full, o_raw, turned, drain;
+  uint64_t rows[4];          // the two warps that share 32 rows
 };
 
-// Packed key of one token on its way into the ring.
+// Half of a packed key (64 coordinates) on its way into the ring.
 template <int KB>
 struct RawKey {
-  uint4 planes[KB], qjl;
+  uint2 planes[KB], qjl;
   float norm, rnorm;
   bool valid;
 };
 
 // Token `token` (0..31) of the group under the cursor.
 template <int KB>
-__device__ __forceinline__ void load_key(const DecodeArgs& d, const Item& it, const Cursor& c, int token, RawKey<KB>& k) {
+__device__ __forceinline__ void load_key(const DecodeArgs& d, const Item& it, const Cursor& c, int token, int half,
+                                         RawKey<KB>& k) {
   k.valid = false;
   k.norm = k.rnorm = 0.f;
   const long long blk = cache_row(d, it, c);
   if (blk < 0 || c.pos + token >= it.seq.z) return;
   const long long row = blk * d.block_size + c.off + token;
-  const uint4* const codes = reinterpret_cast<const uint4*>(d.k_codes + row * (KB * 16));
+  const uint2* const codes = reinterpret_cast<const uint2*>(d.k_codes + row * (KB * 16)) + half;
 #pragma unroll
-  for (int p = 0; p < KB; ++p) k.planes[p] = __ldg(codes + p);
+  for (int p = 0; p < KB; ++p) k.planes[p] = __ldg(codes + 2 * p);
   k.norm = load_norm(d.k_norm, row, d.norm16);
   if (d.k_qjl != nullptr) {
-    k.qjl = __ldg(reinterpret_cast<const uint4*>(d.k_qjl + row * 16));
+    k.qjl = __ldg(reinterpret_cast<const uint2*>(d.k_qjl + row * 16) + half);
     k.rnorm = load_norm(d.k_rnorm, row, d.norm16);
   }
   k.valid = true;
 }
 
-// Value bits of one coordinate over the tile's 128 tokens, and the norm of
-// the token whose factor this thread writes.
+// Value bits of one coordinate over two of the tile's 32-token groups, and the
+// norm of the token whose factor this thread writes.
 template <int VB>
 struct RawValue {
-  uint32_t words[VB][4];     // [plane][32-token group]
+  uint32_t words[VB][2];     // [plane][group]
   float norm;
 };
 
-// Lane l of the warp has the cursor of group l & 3; `group` is the one whose
-// norms this warp reads.  Blocks of a multiple of 128 (64) tokens give a
-// thread's words in one 16-byte (two 8-byte) loads per plane.
+// Lane l of the warp has the cursor of the first or second of the thread's two
+// groups (l & 1); `mine` is the one whose norms this warp reads (-1: neither).
+// Blocks of a multiple of 64 tokens give both words of a plane in one load.
 template <int VB>
-__device__ __forceinline__ void load_value(const DecodeArgs& d, const Item& it, const Cursor& c, int dim, int group,
+__device__ __forceinline__ void load_value(const DecodeArgs& d, const Item& it, const Cursor& c, int dim, int mine,
                                            int token, RawValue<VB>& v) {
   const long long row = cache_row(d, it, c);
   const int words = d.block_size / 32;            // of one plane and coordinate
   const long long base = row < 0 ? -1 : row * (VB * 128ll * words) + c.off / 32;
   const uint32_t* const codes = reinterpret_cast<const uint32_t*>(d.v_codes) + dim * words;
   const int plane = 128 * words;
-  long long at[4];
-#pragma unroll
-  for (int g = 0; g < 4; ++g) at[g] = __shfl_sync(0xffffffffu, base, g);
-  const long long norm_row = __shfl_sync(0xffffffffu, row, group);
-  const int norm_off = __shfl_sync(0xffffffffu, c.off, group), norm_pos = __shfl_sync(0xffffffffu, c.pos, group);
-  if (words % 4 == 0) {
+  const long long at0 = __shfl_sync(0xffffffffu, base, 0), at1 = __shfl_sync(0xffffffffu, base, 1);
+  if (words % 2 == 0) {
 #pragma unroll
     for (int p = 0; p < VB; ++p) {
-        const uint4 w = at[0] < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>(codes + at[0] + p * plane));
-        v.words[p][0] = w.x, v.words[p][1] = w.y, v.words[p][2] = w.z, v.words[p][3] = w.w;
-      }
-  } else if (words % 2 == 0) {
-#pragma unroll
-    for (int p = 0; p < VB; ++p) {
-#pragma unroll
-        for (int g = 0; g < 4; g += 2) {
-          const uint2 w = at[g] < 0 ? make_uint2(0, 0) : __ldg(reinterpret_cast<const uint2*>(codes + at[g] + p * plane));
-          v.words[p][g] = w.x, v.words[p][g + 1] = w.y;
-        }
-      }
+      const uint2 w = at0 < 0 ? make_uint2(0, 0) : __ldg(reinterpret_cast<const uint2*>(codes + at0 + p * plane));
+      v.words[p][0] = w.x, v.words[p][1] = w.y;
+    }
   } else {
 #pragma unroll
     for (int p = 0; p < VB; ++p) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) v.words[p][g] = at[g] < 0 ? 0u : __ldg(codes + at[g] + p * plane);
-      }
+      v.words[p][0] = at0 < 0 ? 0u : __ldg(codes + at0 + p * plane);
+      v.words[p][1] = at1 < 0 ? 0u : __ldg(codes + at1 + p * plane);
+    }
   }
-  v.norm = norm_row < 0 || norm_pos + token >= it.seq.z
-               ? 0.f
-               : load_norm(d.v_norm, norm_row * d.block_size + norm_off + token, d.norm16);
+  v.norm = 0.f;
+  if (mine >= 0) {
+    const long long norm_row = __shfl_sync(0xffffffffu, row, mine);
+    const int norm_off = __shfl_sync(0xffffffffu, c.off, mine), norm_pos = __shfl_sync(0xffffffffu, c.pos, mine);
+    if (norm_row >= 0 && norm_pos + token < it.seq.z)
+      v.norm = load_norm(d.v_norm, norm_row * d.block_size + norm_off + token, d.norm16);
+  }
 }
 
 template <int KB, int VB>
@@ -500,6 +527,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
   __shared__ uint32_t tmem_s;
   __shared__ int abort_s;
   __shared__ Item item_s;
+  __shared__ float swap_s[2][2][kTile];           // what the two threads of a row tell each other
   __shared__ float2 reach_s[kRing][4];            // per 32 tokens of a tile: bounds of the longest scaled key halves
   __shared__ uint32_t valid_s[kRing][4];          // tokens of a tile, by expanded column
 
@@ -529,6 +557,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
     ptx::mbar_init(&bar.o_raw, kSoftThreads);
     ptx::mbar_init(&bar.turned, 1);
     ptx::mbar_init(&bar.drain, 1);
+    for (int w = 0; w < 4; ++w) ptx::mbar_init(&bar.rows[w], 64);
     ptx::fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -550,44 +579,61 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
   bool ok = true;
 #define TQ_WAIT(b, ph) ptx::wait_bar(&(b), (ph), abort, d.error, kErrTimeout)
 
-  if (warp < 4) {
+  if (warp < 8) {
     // ---------------- softmax ----------------
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const int quarter = warp & 3, half = warp >> 2;
+    const int row = quarter * 32 + lane;          // tensor-memory lane; columns 64 half .. + 63
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    int swaps = 0;
+    // the other thread of the row: its value of `mine`
+    auto swap = [&](float mine, float* theirs) {
+      float(*const buf)[kTile] = swap_s[swaps & 1];
+      buf[half][row] = mine;
+      ptx::mbar_arrive(&bar.rows[quarter]);
+      const bool done = __all_sync(0xffffffffu, TQ_WAIT(bar.rows[quarter], swaps & 1));
+      *theirs = buf[half ^ 1][row];
+      ++swaps;
+      return done;
+    };
     int jt = 0;                                   // key tiles so far
     for (int seg = 0; pos < end; ++seg) {
       const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
       const int n_rows = it.seq.y * d.group;
-      const int r = it.i * kTile + tid;
+      const int r = it.i * kTile + row;
       const bool live = r < n_rows;
       const int tok = (live ? r : n_rows - 1) / d.group;
       const long long vec = (static_cast<long long>(it.seq.x) + tok) * d.n_q + it.kvh * d.group + r - tok * d.group;
       const int seen = max(0, it.seq.z - it.seq.y + tok + 1);     // positions this row sees
+      float other;
 
       // the query: fp16, scaled by a power of two if it is outside the range
       float biggest = 0.f;
       if (live) {
 #pragma unroll 4
-        for (int c = 0; c < kDim; c += 8) {
+        for (int c = 0; c < 64; c += 8) {
           float v[8];
-          load_query8(a, vec * kDim + c, v);
+          load_query8(a, vec * kDim + 64 * half + c, v);
 #pragma unroll
           for (int k = 0; k < 8; ++k) biggest = fmaxf(biggest, fabsf(v[k]));
         }
       }
+      ok = swap(biggest, &other);
+      if (!ok) break;
+      biggest = fmaxf(biggest, other);
       int e = exponent_of(biggest);
       if (biggest == 0.f || (e >= -8 && e < 10)) e = 0;
       const float down = exp2_int(-e), factor = exp2_int(e);
 #pragma unroll 1
       for (int h = 0; h < 4; ++h) {
-        uint32_t w[16];
+        uint32_t w[8];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          if (live) load_query8(a, vec * kDim + 32 * h + 8 * c, v);
+          if (live) load_query8(a, vec * kDim + 64 * half + 16 * h + 8 * c, v);
 #pragma unroll
           for (int k = 0; k < 4; ++k) w[4 * c + k] = pack_f16(v[2 * k] * down, v[2 * k + 1] * down);
         }
-        tmem_st16(lane_addr + kS1 + 16 * h, w);
+        ptx::tmem_st8(lane_addr + kS1 + 32 * half + 8 * h, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
       }
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
@@ -597,24 +643,30 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       ptx::tc_fence_after();
       float2 len2 = make_float2(0.f, 0.f);        // |R q|^2, |S q|^2
 #pragma unroll 1
-      for (int h = 0; h < 8; ++h) {
-        if (h < 4 || qjl) {
-          uint32_t x[32], w[16];
-          ptx::tmem_ld32(lane_addr + (h < 4 ? kS0 + 32 * h : kO + 32 * (h - 4)), x);
+      for (int h = 0; h < (qjl ? 8 : 4); ++h) {
+        uint32_t x[16];
+        ptx::tmem_ld16(lane_addr + (h < 4 ? kS0 : kO) + 64 * half + 16 * (h & 3), x);
+        uint32_t w[8];
+        float sum = 0.f;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float u = __uint_as_float(x[2 * k]), v = __uint_as_float(x[2 * k + 1]);
-            float& sum = h < 4 ? len2.x : len2.y;
-            sum = fmaf(u, u, fmaf(v, v, sum));
-            w[k] = pack_f16(u, v);
-          }
-          tmem_st16(lane_addr + kQ + 16 * h, w);
+        for (int k = 0; k < 8; ++k) {
+          const float u = __uint_as_float(x[2 * k]), v = __uint_as_float(x[2 * k + 1]);
+          sum = fmaf(u, u, fmaf(v, v, sum));
+          w[k] = pack_f16(u, v);
         }
+        (h < 4 ? len2.x : len2.y) += sum;
+        ptx::tmem_st8(lane_addr + kQ + 16 * (h & 4) + 32 * half + 8 * (h & 3), w[0], w[1], w[2], w[3], w[4], w[5], w[6],
+                      w[7]);
       }
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       ptx::mbar_arrive(&bar.q_full);
-      const float len_r = sqrtf(len2.x) * factor * 1.01f, len_s = sqrtf(len2.y) * factor * 1.01f;   // (operands' roundings)
+      ok = swap(len2.x, &other);
+      if (!ok) break;
+      const float len_r = sqrtf(len2.x + other) * factor * 1.01f;    // (1.01: the operands' roundings)
+      ok = swap(len2.y, &other);
+      if (!ok) break;
+      const float len_s = sqrtf(len2.y + other) * factor * 1.01f;
 
       float ref = -INFINITY;
       uint64_t sum2 = 0;                          // (two fp32 zeros)
@@ -625,27 +677,34 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t s_addr = lane_addr + (sb ? kS1 : kS0);
-        const uint32_t kf = ptx::smem_u32(key_factor + rg * kTile), vf = ptx::smem_u32(value_factor + rg * kTile);
+        // this thread's 64 scores; their weights go to the first 32 of the columns
+        const uint32_t s_addr = lane_addr + (sb ? kS1 : kS0) + 64 * half;
+        const uint32_t kf = ptx::smem_u32(key_factor + rg * kTile + 64 * half);
+        const uint32_t vf = ptx::smem_u32(value_factor + rg * kTile + 64 * half);
         const uint32_t all = valid_s[rg][0] & valid_s[rg][1] & valid_s[rg][2] & valid_s[rg][3];
         float top_bound = 0.f;                    // |score| <= |R q| |n c| + |S q| |n rho signs|
 #pragma unroll
         for (int g = 0; g < 4; ++g)
           top_bound = fmaxf(top_bound, fmaf(len_r, reach_s[rg][g].x, len_s * reach_s[rg][g].y));
+        // (the same for both threads of a row)
         const bool usual = t > t0 && e == 0 && seen >= (t + 1) * kTile && all == 0xffffffffu && top_bound <= ref + kRaise;
         if (__all_sync(0xffffffffu, usual)) {
           const uint64_t minus = pair(-ref, -ref);
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[32], w[16];
-            ptx::tmem_ld32(s_addr + 32 * c, x);
+          uint32_t x[2][16];
+          tmem_ld16_start(s_addr, x[0]);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float4 f = load16(kf + 128 * c + 16 * k);
-              const float4 g = load16(vf + 128 * c + 16 * k);
-              const float2 z0 = unpair(fma2(pair(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])),
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld16_wait(x[c & 1]);
+            if (c < 3) tmem_ld16_start(s_addr + 16 * (c + 1), x[(c + 1) & 1]);
+            const uint32_t(&y)[16] = x[c & 1];
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float4 f = load16(kf + 64 * c + 16 * k);
+              const float4 g = load16(vf + 64 * c + 16 * k);
+              const float2 z0 = unpair(fma2(pair(__uint_as_float(y[4 * k]), __uint_as_float(y[4 * k + 1])),
                                             pair(f.x, f.y), minus));
-              const float2 z1 = unpair(fma2(pair(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])),
+              const float2 z1 = unpair(fma2(pair(__uint_as_float(y[4 * k + 2]), __uint_as_float(y[4 * k + 3])),
                                             pair(f.z, f.w), minus));
               const uint64_t p0 = pair(exp2_fast(z0.x), exp2_fast(z0.y)), p1 = pair(exp2_fast(z1.x), exp2_fast(z1.y));
               sum2 = add2(sum2, add2(p0, p1));
@@ -653,33 +712,39 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
               w[2 * k] = pack_bf16(w0.x, w0.y);
               w[2 * k + 1] = pack_bf16(w1.x, w1.y);
             }
-            tmem_st16(s_addr + 16 * c, w);
+            ptx::tmem_st8(s_addr + 8 * c, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
           }
         } else {
           // hidden positions, a scaled query, or scores that may pass the
           // reference: the tile's maximum first
           const int here = min(kTile, max(0, seen - t * kTile));
-          auto mask_of = [&](int g) {
+          auto mask_of = [&](int g) {             // visible tokens of group g
             const int n = min(32, max(0, here - 32 * g));
             return (n == 32 ? 0xffffffffu : (1u << n) - 1u) & valid_s[rg][g];
           };
           float top = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t mask = mask_of(c);
-            uint32_t x[32];
-            ptx::tmem_ld32(s_addr + 32 * c, x);
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t mask = mask_of(2 * half + c);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float4 f = load16(kf + 128 * c + 16 * k);
-              const float fk[4] = {f.x, f.y, f.z, f.w};
+            for (int h = 0; h < 2; ++h) {
+              uint32_t y[16];
+              ptx::tmem_ld16(s_addr + 32 * c + 16 * h, y);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float s = __uint_as_float(x[4 * k + q]) * fk[q] * factor;
-                top = mask & (1u << expanded_bit(4 * k + q)) ? fmaxf(top, s) : top;
+              for (int k = 0; k < 4; ++k) {
+                const float4 f = load16(kf + 128 * c + 64 * h + 16 * k);
+                const float fk[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const float s = __uint_as_float(y[4 * k + q]) * fk[q] * factor;
+                  top = mask & (1u << expanded_bit(16 * h + 4 * k + q)) ? fmaxf(top, s) : top;
+                }
               }
             }
           }
+          ok = swap(top, &other);
+          if (!ok) break;
+          top = fmaxf(top, other);
           const bool raise = top > ref + kRaise || (ref == -INFINITY && top > ref);
           if (__any_sync(0xffffffffu, raise)) {
             const float scale = raise ? exp2_fast(ref - top) : 1.f;
@@ -691,39 +756,43 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
               ptx::tc_fence_after();
               sum2 = mul2(sum2, pair(scale, scale));
 #pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                uint32_t x[32];
-                ptx::tmem_ld32(lane_addr + kO + 32 * c, x);
+              for (int c = 0; c < 8; ++c) {
+                const uint32_t at = lane_addr + kO + 64 * half + 8 * c;
+                uint32_t y[8];
+                tmem_ld8(at, y);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * scale);
-                ptx::tmem_st32(lane_addr + kO + 32 * c, x);
+                for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * scale);
+                ptx::tmem_st8(at, y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]);
               }
             }
           }
           const float shift = ref == -INFINITY ? 0.f : ref;
           float sum = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t mask = mask_of(c);
-            uint32_t x[32], w[16];
-            ptx::tmem_ld32(s_addr + 32 * c, x);
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t mask = mask_of(2 * half + c);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float4 f = load16(kf + 128 * c + 16 * k);
-              const float4 g = load16(vf + 128 * c + 16 * k);
-              const float fk[4] = {f.x, f.y, f.z, f.w}, gk[4] = {g.x, g.y, g.z, g.w};
-              float p[4];
+            for (int h = 0; h < 2; ++h) {
+              uint32_t y[16], w[8];
+              ptx::tmem_ld16(s_addr + 32 * c + 16 * h, y);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const bool on = mask & (1u << expanded_bit(4 * k + q));
-                p[q] = on ? exp2_fast(__uint_as_float(x[4 * k + q]) * fk[q] * factor - shift) : 0.f;
-                sum += p[q];
-                p[q] = on ? p[q] * gk[q] : 0.f;
+              for (int k = 0; k < 4; ++k) {
+                const float4 f = load16(kf + 128 * c + 64 * h + 16 * k);
+                const float4 g = load16(vf + 128 * c + 64 * h + 16 * k);
+                const float fk[4] = {f.x, f.y, f.z, f.w}, gk[4] = {g.x, g.y, g.z, g.w};
+                float p[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const bool on = mask & (1u << expanded_bit(16 * h + 4 * k + q));
+                  p[q] = on ? exp2_fast(__uint_as_float(y[4 * k + q]) * fk[q] * factor - shift) : 0.f;
+                  sum += p[q];
+                  p[q] = on ? p[q] * gk[q] : 0.f;
+                }
+                w[2 * k] = pack_bf16(p[0], p[1]);
+                w[2 * k + 1] = pack_bf16(p[2], p[3]);
               }
-              w[2 * k] = pack_bf16(p[0], p[1]);
-              w[2 * k + 1] = pack_bf16(p[2], p[3]);
+              ptx::tmem_st8(s_addr + 16 * c + 8 * h, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
             }
-            tmem_st16(s_addr + 16 * c, w);
           }
           sum2 = add2(sum2, pair(sum, 0.f));
         }
@@ -734,30 +803,35 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       if (!ok) break;
 
       // output: divided by the sum, turned back by R^T
+      const float2 parts = unpair(sum2);
+      ok = swap(parts.x + parts.y, &other);
+      if (!ok) break;
+      // (both threads add in the same order)
+      const float sum = half == 0 ? (parts.x + parts.y) + other : other + (parts.x + parts.y);
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;       // (a NaN in a visible token shows)
       ok = __all_sync(0xffffffffu, TQ_WAIT(bar.v_empty[(jt - 1) & 1], ((jt - 1) >> 1) & 1));
       if (!ok) break;
       ptx::tc_fence_after();
-      const float2 halves = unpair(sum2);
-      const float sum = halves.x + halves.y;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;       // (a NaN in a visible token shows)
       float top = 0.f;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
-        uint32_t x[32];
-        ptx::tmem_ld32(lane_addr + kO + 32 * c, x);
+        uint32_t y[16];
+        ptx::tmem_ld16(lane_addr + kO + 64 * half + 16 * c, y);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) top = fmaxf(top, fabsf(__uint_as_float(x[k]) * inv));
+        for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(__uint_as_float(y[k]) * inv));
       }
-      const int eo = exponent_of(top);
+      ok = swap(top, &other);
+      if (!ok) break;
+      const int eo = exponent_of(fmaxf(top, other));
       const float out_down = inv * exp2_int(-eo), out_up = exp2_int(eo);
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
-        uint32_t x[32], w[16];
-        ptx::tmem_ld32(lane_addr + kO + 32 * c, x);
+        uint32_t y[16], w[8];
+        ptx::tmem_ld16(lane_addr + kO + 64 * half + 16 * c, y);
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          w[k] = pack_f16(__uint_as_float(x[2 * k]) * out_down, __uint_as_float(x[2 * k + 1]) * out_down);
-        tmem_st16(lane_addr + kS0 + 16 * c, w);
+        for (int k = 0; k < 8; ++k)
+          w[k] = pack_f16(__uint_as_float(y[2 * k]) * out_down, __uint_as_float(y[2 * k + 1]) * out_down);
+        ptx::tmem_st8(lane_addr + kS0 + 32 * half + 8 * c, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
       }
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
@@ -768,38 +842,40 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       const bool whole = t0 == 0 && t1 == it.tiles;
       // a run's first item may have begun in the run before, its last may go on
       float* const part = a.ws_part + (2ll * blockIdx.x + (t0 == 0 ? 1 : 0)) * kExtPart;
-      if (!whole) {
-        part[kTile * kDim + 2 * tid] = sum == 0.f ? -INFINITY : ref;
-        part[kTile * kDim + 2 * tid + 1] = sum;
+      if (!whole && half == 0) {
+        part[kTile * kDim + 2 * row] = sum == 0.f ? -INFINITY : ref;
+        part[kTile * kDim + 2 * row + 1] = sum;
       }
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
-        uint32_t x[32];
-        ptx::tmem_ld32(lane_addr + kS1 + 32 * c, x);
+        uint32_t y[16];
+        ptx::tmem_ld16(lane_addr + kS1 + 64 * half + 16 * c, y);
         if (live && whole) {
-          uint4* const dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + vec * kDim + 32 * c);
+          uint4* const dst =
+              reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + vec * kDim + 64 * half + 16 * c);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 2; ++k) {
             uint32_t w[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              w[q] = pack_bf16(__uint_as_float(x[8 * k + 2 * q]) * out_up, __uint_as_float(x[8 * k + 2 * q + 1]) * out_up);
+              w[q] = pack_bf16(__uint_as_float(y[8 * k + 2 * q]) * out_up, __uint_as_float(y[8 * k + 2 * q + 1]) * out_up);
             dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else if (live) {
-          float4* const dst = reinterpret_cast<float4*>(part + tid * kDim + 32 * c);
+          float4* const dst = reinterpret_cast<float4*>(part + row * kDim + 64 * half + 16 * c);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[k] = make_float4(__uint_as_float(x[4 * k]) * out_up, __uint_as_float(x[4 * k + 1]) * out_up,
-                                 __uint_as_float(x[4 * k + 2]) * out_up, __uint_as_float(x[4 * k + 3]) * out_up);
+          for (int k = 0; k < 4; ++k)
+            dst[k] = make_float4(__uint_as_float(y[4 * k]) * out_up, __uint_as_float(y[4 * k + 1]) * out_up,
+                                 __uint_as_float(y[4 * k + 2]) * out_up, __uint_as_float(y[4 * k + 3]) * out_up);
         }
       }
       pos += t1 - t0;
       if (pos < end) next_item(a, it);
     }
-  } else if (warp < 8) {
+  } else if (warp < 16) {
     // ---------------- keys ----------------
-    const int row = tid - kSoftThreads;           // row of the tile: token expanded_bit(lane) of the warp's group
+    const int row = (tid - kSoftThreads) & (kTile - 1);   // row of the tile: token expanded_bit(lane) of the warp's group
+    const int half = (tid - kSoftThreads) / kTile;        // coordinates 64 half .. + 63 of both operand halves
     const LevelBytes lev = level_bytes<false>(d.tables->k_levels, KB);
     float biggest = 0.f;                          // the outermost level
     for (int i = 0; i < (1 << KB); ++i) biggest = fmaxf(biggest, fabsf(d.tables->k_levels[i]));
@@ -811,7 +887,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       uint4* const dst = reinterpret_cast<uint4*>(smem + kKey0 + s * kKeyBytes);
       if (!__all_sync(0xffffffffu, TQ_WAIT(bar.k_empty[s], ((kc >> 1) & 1) ^ 1))) return false;
 #pragma unroll 8
-      for (int i = row; i < count * (kExtendImageBytes / 16); i += kKeyThreads) dst[i] = __ldg(src + i);
+      for (int i = tid - kSoftThreads; i < count * (kExtendImageBytes / 16); i += kKeyThreads) dst[i] = __ldg(src + i);
       ptx::fence_async_shared();
       ptx::mbar_arrive(&bar.k_full[s]);
       ++kc;
@@ -822,64 +898,45 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       Cursor c;
       RawKey<KB> next;
       start_cursor(d, it, t0 * kTile + (row & ~31), c);
-      load_key(d, it, c, expanded_bit(lane), next);
+      load_key(d, it, c, expanded_bit(lane), half, next);
       advance(d, it, c);
       ok = image(0, qjl ? 2 : 1);
       for (int t = t0; ok && t < t1; ++t, ++jt, ++kc) {
-        RawKey<KB> k = next;
+        const RawKey<KB> k = next;
         if (t + 1 < t1) {
-          load_key(d, it, c, expanded_bit(lane), next);
+          load_key(d, it, c, expanded_bit(lane), half, next);
           advance(d, it, c);
         }
         const int s = kc & 1, rg = jt & (kRing - 1);
         ok = __all_sync(0xffffffffu, TQ_WAIT(bar.k_empty[s], ((kc >> 1) & 1) ^ 1));
         if (!ok) break;
-        // 32 coordinates a turn, the words of a plane rotating through .x: a
-        // short loop, so that the three roles' code stays in the first-level
-        // instruction cache
-        RowChunks at = row_chunks(ptx::smem_u32(smem + kKey0 + s * kKeyBytes), row);
-        const float rho = qjl && k.norm > 0.f ? k.rnorm * d.qjl_coef / k.norm : 0.f;
+        const RowChunks at = row_chunks(ptx::smem_u32(smem + kKey0 + s * kKeyBytes) + half * kBlockBytes, row);
+        const float rho = qjl && k.norm > 0.f ? __fdividef(k.rnorm * d.qjl_coef, k.norm) : 0.f;
         const uint32_t minus_rho = __half_as_ushort(__float2half_rn(rho)) * 0x00010001u ^ 0x80008000u;
-#pragma unroll 1
-        for (int w = 0; w < 4; ++w) {
-          uint32_t planes[KB];
+        {
+          uint32_t lo[KB], hi[KB];
 #pragma unroll
-          for (int p = 0; p < KB; ++p) {
-            planes[p] = k.planes[p].x;
-            k.planes[p].x = k.planes[p].y, k.planes[p].y = k.planes[p].z, k.planes[p].z = k.planes[p].w;
-          }
-          expand32<KB, 0>(at, planes, lev);
-          if (qjl) {
-            const uint32_t bits = k.qjl.x;
-            k.qjl.x = k.qjl.y, k.qjl.y = k.qjl.z, k.qjl.z = k.qjl.w;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {         // a set bit clears the sign of -rho
-              uint32_t out[4];
-#pragma unroll
-              for (int h = 0; h < 4; ++h) out[h] = ((bits << (15 - 4 * i - h)) & 0x80008000u) ^ minus_rho;
-              store16<2 * kBlockBytes>(at.at[i], make_uint4(out[0], out[1], out[2], out[3]));
-            }
-          }
-          next_word(at, w);
+          for (int p = 0; p < KB; ++p) lo[p] = k.planes[p].x, hi[p] = k.planes[p].y;
+          expand32<KB, 0>(at, lo, lev);
+          expand32<KB, 0>(second_word(at), hi, lev);
         }
-        const float f = k.valid ? k.norm * to_log2 : 0.f;
-        key_factor[rg * kTile + row] = f;
-        // bounds of |n scale c| and |n scale rho signs|, and the tokens that exist
-        const float root = 11.3137085f;           // sqrt(128)
-        float reach_c = fabsf(f) * biggest * root, reach_q = fabsf(f) * rho * root;
-        if (!(reach_c < INFINITY)) reach_c = INFINITY;
-        if (!(reach_q < INFINITY)) reach_q = INFINITY;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          reach_c = fmaxf(reach_c, __shfl_xor_sync(0xffffffffu, reach_c, o));
-          reach_q = fmaxf(reach_q, __shfl_xor_sync(0xffffffffu, reach_q, o));
+        if (qjl) {
+          expand_signs<2 * kBlockBytes>(at, k.qjl.x, minus_rho);
+          expand_signs<2 * kBlockBytes>(second_word(at), k.qjl.y, minus_rho);
         }
-        // bit of the token within its 32: lane c holds token bit expanded_bit(c)
-        uint32_t bit = k.valid ? 1u << expanded_bit(lane) : 0u;
-        bit = __reduce_or_sync(0xffffffffu, bit);
-        if (lane == 0) {
-          valid_s[rg][row >> 5] = bit;
-          reach_s[rg][row >> 5] = make_float2(reach_c, reach_q);
+        if (half == 0) {
+          const float f = k.valid ? k.norm * to_log2 : 0.f;
+          key_factor[rg * kTile + row] = f;
+          // bounds of |n scale c| and |n scale rho signs| (as bits: not negative), and the tokens that exist
+          const float root = 11.3137085f;         // sqrt(128)
+          const float reach_c = fabsf(f) * biggest * root, reach_q = fabsf(f) * rho * root;
+          const unsigned bits_c = __reduce_max_sync(0xffffffffu, __float_as_uint(reach_c) & 0x7fffffffu);
+          const unsigned bits_q = __reduce_max_sync(0xffffffffu, __float_as_uint(reach_q) & 0x7fffffffu);
+          const unsigned bit = __reduce_or_sync(0xffffffffu, k.valid ? 1u << expanded_bit(lane) : 0u);
+          if (lane == 0) {
+            valid_s[rg][row >> 5] = bit;
+            reach_s[rg][row >> 5] = make_float2(__uint_as_float(bits_c), __uint_as_float(bits_q));
+          }
         }
         ptx::fence_async_shared();
         ptx::mbar_arrive(&bar.k_full[s]);
@@ -890,101 +947,119 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
     }
   } else if (warp < kMmaWarp) {
     // ---------------- values ----------------
-    const int dim = tid - kSoftThreads - kKeyThreads;
-    const int token = expanded_bit(lane);         // of the warp's group: whose factor this thread writes, at column dim
+    const int dim = (tid - kSoftThreads - kKeyThreads) & (kTile - 1);
+    const int half = (tid - kSoftThreads - kKeyThreads) / kTile;   // 32-token groups 2 half and 2 half + 1
+    // the first two warps of a half write its 64 factors, by expanded column
+    const int mine = dim < 64 ? dim >> 5 : -1;
     const LevelBytes lev = level_bytes<true>(d.tables->v_levels, VB);
     int jt = 0;
     while (ok && pos < end) {
       const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
       Cursor c;
       RawValue<VB> next;
-      start_cursor(d, it, t0 * kTile + 32 * (lane & 3), c);
-      load_value(d, it, c, dim, dim >> 5, token, next);
+      start_cursor(d, it, t0 * kTile + 64 * half + 32 * (lane & 1), c);
+      load_value(d, it, c, dim, mine, expanded_bit(lane), next);
       advance(d, it, c);
       for (int t = t0; t < t1; ++t, ++jt) {
-        RawValue<VB> v = next;
+        const RawValue<VB> v = next;
         if (t + 1 < t1) {
-          load_value(d, it, c, dim, dim >> 5, token, next);
+          load_value(d, it, c, dim, mine, expanded_bit(lane), next);
           advance(d, it, c);
         }
         const int s = jt & 1, rg = jt & (kRing - 1);
         ok = __all_sync(0xffffffffu, TQ_WAIT(bar.v_empty[s], ((jt >> 1) & 1) ^ 1));
         if (!ok) break;
-        RowChunks at = row_chunks(ptx::smem_u32(smem + kValue0 + s * kValueBytes), dim);
-#pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
-          uint32_t planes[VB];
+        const RowChunks at = row_chunks(ptx::smem_u32(smem + kValue0 + s * kValueBytes) + half * kBlockBytes, dim);
+        uint32_t lo[VB], hi[VB];
 #pragma unroll
-          for (int p = 0; p < VB; ++p) {
-            planes[p] = v.words[p][0];
-            v.words[p][0] = v.words[p][1], v.words[p][1] = v.words[p][2], v.words[p][2] = v.words[p][3];
-          }
-          expand32<VB, 0>(at, planes, lev);
-          next_word(at, g);
-        }
-        value_factor[rg * kTile + dim] = v.norm;
+        for (int p = 0; p < VB; ++p) lo[p] = v.words[p][0], hi[p] = v.words[p][1];
+        expand32<VB, 0>(at, lo, lev);
+        expand32<VB, 0>(second_word(at), hi, lev);
+        if (mine >= 0) value_factor[rg * kTile + 64 * half + dim] = v.norm;
         ptx::fence_async_shared();
         ptx::mbar_arrive(&bar.v_full[s]);
       }
       pos += t1 - t0;
       if (pos < end) next_item(a, it);
     }
-  } else if (ptx::elect_one()) {
+  } else {
     // ---------------- products ----------------
+    // the whole warp walks the tiles and waits; an elected lane issues
+#define TQ_WARP_WAIT(b, ph) __all_sync(0xffffffffu, TQ_WAIT(b, ph))
+    const uint64_t key_desc = ptx::desc_k_sw128(ptx::smem_u32(smem + kKey0));
+    const uint64_t value_desc = ptx::desc_k_sw128(ptx::smem_u32(smem + kValue0));
     int kc = 0, jt = 0;
-    for (int seg = 0; ok && pos < end; ++seg) {
-      const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
-      auto key_stage = [&](int c) { return ptx::smem_u32(smem + kKey0 + (c & 1) * kKeyBytes); };
-      // R q and S q
-      ok = TQ_WAIT(bar.k_full[kc & 1], (kc >> 1) & 1) && TQ_WAIT(bar.q_raw, seg & 1);
-      if (!ok) break;
-      ptx::tc_fence_after();
-      product<8>(tmem + kS0, tmem + kS1, key_stage(kc), kIdescF16, false);
-      if (qjl) product<8>(tmem + kO, tmem + kS1, key_stage(kc) + 2 * kBlockBytes, kIdescF16, false);
-      ptx::mma_commit(&bar.k_empty[kc & 1]);
-      ptx::mma_commit(&bar.rotated);
-      ++kc;
-      ok = TQ_WAIT(bar.q_full, seg & 1);
-      if (!ok) break;
-      // scores of tile t (number j of the CTA) run while the softmax works on tile t - 1
-      auto scores = [&](int j, bool first_two) {
-        if (!TQ_WAIT(bar.k_full[kc & 1], (kc >> 1) & 1)) return false;
-        // its columns held the weights of tile j - 2
-        if (!first_two && !TQ_WAIT(bar.v_empty[j & 1], ((j - 2) >> 1) & 1)) return false;
+    auto key_stage = [&](int c) { return key_desc + (c & 1) * (kKeyBytes / 16); };
+    // scores of the CTA's key tile j, which run while the softmax works on tile j - 1
+    auto scores = [&](int j, bool first_two) {
+      if (!TQ_WARP_WAIT(bar.k_full[kc & 1], (kc >> 1) & 1)) return false;
+      // the columns held the weights of tile j - 2
+      if (!first_two && !TQ_WARP_WAIT(bar.v_empty[j & 1], ((j - 2) >> 1) & 1)) return false;
+      if (ptx::elect_one()) {
         ptx::tc_fence_after();
         if (qjl) product<16>(tmem + (j & 1 ? kS1 : kS0), tmem + kQ, key_stage(kc), kIdescF16, false);
         else product<8>(tmem + (j & 1 ? kS1 : kS0), tmem + kQ, key_stage(kc), kIdescF16, false);
-        ptx::mma_commit(&bar.k_empty[kc & 1]);
         ptx::mma_commit(&bar.s_full[j & 1]);
+        ptx::mma_commit(&bar.k_empty[kc & 1]);
         ptx::mbar_arrive(&bar.s_full[j & 1]);
-        ++kc;
-        return true;
-      };
+      }
+      __syncwarp();
+      ++kc;
+      return true;
+    };
+    for (int seg = 0; ok && pos < end; ++seg) {
+      const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
+      // R q and S q
+      ok = TQ_WARP_WAIT(bar.k_full[kc & 1], (kc >> 1) & 1) && TQ_WARP_WAIT(bar.q_raw, seg & 1);
+      if (!ok) break;
+      if (ptx::elect_one()) {
+        ptx::tc_fence_after();
+        product<8>(tmem + kS0, tmem + kS1, key_stage(kc), kIdescF16, false);
+        if (qjl) product<8>(tmem + kO, tmem + kS1, key_stage(kc) + 2 * (kBlockBytes / 16), kIdescF16, false);
+        ptx::mma_commit(&bar.rotated);
+        ptx::mma_commit(&bar.k_empty[kc & 1]);
+      }
+      __syncwarp();
+      ++kc;
+      ok = TQ_WARP_WAIT(bar.q_full, seg & 1);
+      if (!ok) break;
       ok = scores(jt, true);
       for (int t = t0; ok && t < t1; ++t, ++jt) {
         if (t + 1 < t1) ok = scores(jt + 1, t == t0);
         const int s = jt & 1;
         const uint32_t ph = (jt >> 1) & 1;
-        ok = ok && TQ_WAIT(bar.v_full[s], ph) && TQ_WAIT(bar.p_full[s], ph);
+        ok = ok && TQ_WARP_WAIT(bar.v_full[s], ph) && TQ_WARP_WAIT(bar.p_full[s], ph);
         if (!ok) break;
-        ptx::tc_fence_after();
-        product<8>(tmem + kO, tmem + (s ? kS1 : kS0), ptx::smem_u32(smem + kValue0 + s * kValueBytes), kIdescBf16,
-                   t > t0);
-        ptx::mma_commit(&bar.v_empty[s]);
+        if (ptx::elect_one()) {
+          ptx::tc_fence_after();
+          // (the weights of columns 64 .. 127 start 64 tensor-memory columns on)
+          const uint32_t w = tmem + (s ? kS1 : kS0);
+          const uint64_t v = value_desc + s * (kValueBytes / 16);
+          product<4>(tmem + kO, w, v, kIdescBf16, t > t0);
+          product<4>(tmem + kO, w + 64, v + kBlockBytes / 16, kIdescBf16, true);
+          ptx::mma_commit(&bar.v_empty[s]);
+        }
+        __syncwarp();
       }
       // R^T out
-      ok = ok && TQ_WAIT(bar.k_full[kc & 1], (kc >> 1) & 1) && TQ_WAIT(bar.o_raw, seg & 1);
+      ok = ok && TQ_WARP_WAIT(bar.k_full[kc & 1], (kc >> 1) & 1) && TQ_WARP_WAIT(bar.o_raw, seg & 1);
       if (!ok) break;
-      ptx::tc_fence_after();
-      product<8>(tmem + kS1, tmem + kS0, key_stage(kc), kIdescF16, false);
-      ptx::mma_commit(&bar.k_empty[kc & 1]);
-      ptx::mma_commit(&bar.turned);
+      if (ptx::elect_one()) {
+        ptx::tc_fence_after();
+        product<8>(tmem + kS1, tmem + kS0, key_stage(kc), kIdescF16, false);
+        ptx::mma_commit(&bar.turned);
+        ptx::mma_commit(&bar.k_empty[kc & 1]);
+      }
+      __syncwarp();
       ++kc;
       pos += t1 - t0;
       if (pos < end) next_item(a, it);
     }
-    ptx::mma_commit(&bar.drain);                  // nothing is in flight when the CTA ends
-    ptx::drain_bar(&bar.drain, 0);
+    if (ptx::elect_one()) {
+      ptx::mma_commit(&bar.drain);                // nothing is in flight when the CTA ends
+      ptx::drain_bar(&bar.drain, 0);
+    }
+#undef TQ_WARP_WAIT
   }
 #undef TQ_WAIT
   __syncwarp();
