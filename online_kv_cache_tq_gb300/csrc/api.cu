@@ -153,20 +153,21 @@ uint16_t fp16_bits(double x) {
   return out;
 }
 
-// The multi-token attention's operand images (see kExtendImage* in kernels.h):
-// R and S with their rows in the order the kernel expands a key's coordinates,
-// then R^T, each 128 x 128 fp16 in the 128-byte swizzled K-major layout.
+// The multi-token attention's operand images (see kExtendImages in kernels.h),
+// each 128 x 128 fp16 in the 128-byte swizzled K-major layout.
 std::vector<uint16_t> extend_images(const tq::HostTables& h) {
   constexpr int d = tq::kDim;
-  std::vector<uint16_t> img(3 * d * d, 0);
+  std::vector<uint16_t> img(tq::kExtendImages * d * d, 0);
   const int m = static_cast<int>(h.S.size()) / d;
   for (int r = 0; r < d; ++r) {
     const int src = (r & ~31) | tq::expanded_bit(r & 31), sgn = (r & ~31) | tq::expanded_sign(r & 31);
     for (int c = 0; c < d; ++c) {
-      const size_t at = tq::swizzled_f16(r, c);
+      const size_t at = tq::swizzled_f16(r, c), turned = tq::swizzled_f16(c, r);
       img[at] = fp16_bits(h.R[src * d + c]);
       img[d * d + at] = fp16_bits(sgn < m ? h.S[sgn * d + c] : 0.0);
       img[2 * d * d + at] = fp16_bits(h.R[c * d + r]);
+      img[3 * d * d + turned] = img[at];
+      img[4 * d * d + turned] = img[d * d + at];
     }
   }
   return img;
@@ -1071,7 +1072,7 @@ size_t tq_extend_workspace_bytes(const tq_codebook* book, int n_tokens, int batc
       n_q_heads % n_kv_heads != 0 || max_context < 0) {
     return 0;
   }
-  return tq::extend_workspace_bytes(batch, book->num_sms);
+  return tq::extend_workspace_bytes(n_tokens, batch, n_q_heads, n_kv_heads, max_context, book->num_sms);
 }
 
 tq_status tq_extend_attention(const tq_codebook* book, const void* q, tq_dtype dtype, int n_tokens, int batch,

@@ -1,0 +1,224 @@
+// Attention of several new tokens per sequence over the packed cache: the
+// plan, the workspace, the two forms' launches and the join of split rows.
+//
+// A sequence takes one of two forms.  The narrow form (extend_tc.cu) expands
+// packed key tiles on the way into its products and needs no other memory;
+// its score product has 256 columns with the sketch, and every row tile of 128
+// expands its key tiles again.  The wide form (extend_wide.cu) expands and
+// turns back a sequence's keys and values once, into the workspace, for row
+// tiles of 256 and score products of 128 columns.
+#include "extend_common.cuh"
+
+namespace tq {
+namespace {
+
+// Rows (new tokens x query heads of the group) from which a sequence takes the
+// wide form, and most expanded tiles that a workspace holds (2 GiB).
+constexpr int kWideFrom = 512;
+constexpr long long kTileCap = 1 << 15;
+
+// One CTA checks the lengths, chooses the forms and forms the prefix sums of
+// key tiles and expanded tiles, a warp per sequence.
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
+
+// Inclusive sum over the CTA's threads.
+__device__ __forceinline__ long long plan_scan(long long v, long long* warp_s) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  if (lane == 31) warp_s[warp] = v;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) v += warp_s[w];
+  __syncthreads();
+  return v;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(ExtendArgs a) {
+  __shared__ long long narrow_s[kPlanThreads], wide_s[kPlanThreads];
+  __shared__ int4 seq_s[kPlanThreads];
+  __shared__ long long warp_s[kPlanWarps];
+  __shared__ long long last_s[3];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = a.d.group;
+  long long base_n = 0, base_w = 0, base_e = 0, asked = 0;
+  for (int b0 = 0; b0 < a.d.batch; b0 += kPlanThreads) {
+    const int nb = min(kPlanThreads, a.d.batch - b0);
+    for (int k = warp; k < nb; k += kPlanWarps) {
+      const int b = b0 + k;
+      int s0 = a.query_start[b], s1 = a.query_start[b + 1], ctx = a.d.context_lens[b];
+      const bool rows_ok = s0 >= 0 && s0 <= s1 && s1 <= a.n_tokens;
+      const bool ctx_ok = ctx >= 0 && ctx <= a.d.max_context &&
+                          ctx <= static_cast<long long>(a.d.max_blocks) * a.d.block_size;
+      if (lane == 0 && (!rows_ok || !ctx_ok)) atomicCAS(a.d.error, 0, kErrContext);
+      if (!rows_ok) s0 = s1 = 0;
+      if (!ctx_ok) ctx = 0;
+      const int n = s1 - s0;
+      const bool eligible = a.tile_cap > 0 && static_cast<long long>(n) * group >= kWideFrom;
+      long long narrow = 0, wide = 0;
+      for (int i = lane; i < row_tiles(kNarrowRows, n, group); i += 32) narrow += key_tiles(i, kNarrowRows, n, ctx, group);
+      if (eligible)
+        for (int i = lane; i < row_tiles(kWideRows, n, group); i += 32) wide += key_tiles(i, kWideRows, n, ctx, group);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) {
+        narrow += __shfl_xor_sync(0xffffffffu, narrow, d);
+        wide += __shfl_xor_sync(0xffffffffu, wide, d);
+      }
+      if (lane == 0) {
+        narrow_s[k] = narrow * a.d.n_kv;
+        wide_s[k] = wide * a.d.n_kv;
+        // (at least one tile: rows that see nothing are given one)
+        seq_s[k] = make_int4(s0, n, ctx, eligible ? max(1, (ctx + kTile - 1) / kTile) : 0);
+      }
+    }
+    __syncthreads();
+    const bool here = tid < nb;
+    int4 seq = here ? seq_s[tid] : make_int4(0, 0, 0, 0);
+    // expanded tiles asked for up to and with this sequence; it is wide if they fit
+    const long long want = static_cast<long long>(seq.w) * a.d.n_kv;
+    const long long upto = asked + plan_scan(want, warp_s);
+    const bool wide = want > 0 && upto <= a.tile_cap;
+    const long long n_tiles = here && !wide ? narrow_s[tid] : 0, w_tiles = wide ? wide_s[tid] : 0;
+    const long long e_tiles = wide ? want : 0;
+    const long long n_upto = base_n + plan_scan(n_tiles, warp_s), w_upto = base_w + plan_scan(w_tiles, warp_s);
+    const long long e_upto = base_e + plan_scan(e_tiles, warp_s);
+    if (here) {
+      a.narrow.first[b0 + tid] = n_upto - n_tiles;
+      a.wide.first[b0 + tid] = w_upto - w_tiles;
+      a.ws_expand[b0 + tid] = e_upto - e_tiles;
+      seq.w = wide ? static_cast<int>(e_upto - e_tiles) : -1;
+      a.ws_seq[b0 + tid] = seq;
+    }
+    if (tid == kPlanThreads - 1) {
+      last_s[0] = n_upto;
+      last_s[1] = w_upto;
+      last_s[2] = e_upto;
+      warp_s[0] = upto;
+    }
+    __syncthreads();
+    base_n = last_s[0];
+    base_w = last_s[1];
+    base_e = last_s[2];
+    asked = warp_s[0];
+    __syncthreads();
+  }
+  if (tid == 0) {
+    a.narrow.first[a.d.batch] = base_n;
+    a.wide.first[a.d.batch] = base_w;
+    a.ws_expand[a.d.batch] = base_e;
+  }
+}
+
+// Joins the partial outputs of a split row tile: sum_s l_s 2^{m_s - M} o_s / sum_s l_s 2^{m_s - M}.
+// blockIdx.x + 1 is a run's number; the block works if that run's beginning is
+// the first cut inside its item.  A warp per row, four coordinates a lane.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps) extend_join_kernel(ExtendArgs a, int ctas) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int narrow_blocks = kNarrowRows / kJoinWarps;
+  const ExtendForm f = blockIdx.y < narrow_blocks ? a.narrow : a.wide;
+  const long long total = f.first[a.d.batch];
+  const long long per = run_length(total, ctas);
+  const long long cut = (blockIdx.x + 1) * per;
+  if (cut >= total) return;
+  const Item it = find_item(a, f, cut);
+  const long long start = cut - it.tile;          // the item's first key tile
+  if (it.tile == 0 || start < cut - per) return;  // no cut here, or an earlier one inside the item
+  const int c0 = static_cast<int>(start / per);   // runs c0 .. c1 hold it
+  const int c1 = static_cast<int>((start + it.tiles - 1) / per);
+  const int n_rows = it.seq.y * a.d.group;
+  const int row = (blockIdx.y < narrow_blocks ? blockIdx.y : blockIdx.y - narrow_blocks) * kJoinWarps + warp;
+  const int r = it.i * f.rows + row;
+  if (r >= n_rows) return;
+  // (the run that holds key tile 0 wrote its second slot, the others their first)
+  auto part = [&](int c) { return f.part + (2ll * c + (c == c0 ? 1 : 0)) * part_floats(f.rows); };
+  const int stats = f.rows * kDim + 2 * row;
+  float top = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part(c)[stats]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float weight = 0.f;
+  for (int c = c0; c <= c1; ++c) {
+    const float* const p = part(c);
+    const float l = p[stats + 1];
+    if (l == 0.f) continue;
+    const float w = l * exp2_fast(p[stats] - top);
+    const float4 o = reinterpret_cast<const float4*>(p + row * kDim)[lane];
+    acc.x = fmaf(w, o.x, acc.x);
+    acc.y = fmaf(w, o.y, acc.y);
+    acc.z = fmaf(w, o.z, acc.z);
+    acc.w = fmaf(w, o.w, acc.w);
+    weight += w;
+  }
+  const float inv = weight == 0.f ? 0.f : 1.f / weight;
+  const int tok = r / a.d.group;
+  const long long vec = (static_cast<long long>(it.seq.x) + tok) * a.d.n_q + it.kvh * a.d.group + r - tok * a.d.group;
+  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + vec * kDim)[lane] =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+}
+
+constexpr size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Layout {
+  size_t first, wide_first, expand, seq, part, wide_part, meta, tiles, total;
+  int tile_cap;
+};
+
+// The wide form's regions are there only if some sequence can have the rows
+// for it; then as many expanded tiles as that many sequences can need.
+Layout layout(int n_tokens, int batch, int group, int n_kv, int max_context, int num_sms) {
+  Layout l;
+  const long long wide = static_cast<long long>(n_tokens) * group / kWideFrom;
+  const long long sequences = wide < batch ? wide : batch;
+  const long long context_tiles = max_context > kTile ? (static_cast<long long>(max_context) + kTile - 1) / kTile : 1;
+  long long cap = context_tiles > kTileCap / n_kv ? (sequences > 0 ? kTileCap : 0) : sequences * context_tiles * n_kv;
+  if (cap > kTileCap) cap = kTileCap;
+  l.tile_cap = static_cast<int>(cap);
+  const size_t sums = align256((static_cast<size_t>(batch) + 1) * sizeof(long long));
+  l.first = 0;
+  l.wide_first = sums;
+  l.expand = 2 * sums;
+  l.seq = 3 * sums;
+  l.part = l.seq + align256(static_cast<size_t>(batch) * sizeof(int4));
+  l.wide_part = l.part + align256(2 * static_cast<size_t>(num_sms) * part_floats(kNarrowRows) * sizeof(float));
+  l.meta = l.wide_part +
+           (cap > 0 ? align256(2 * static_cast<size_t>(num_sms) * part_floats(kWideRows) * sizeof(float)) : 0);
+  l.tiles = l.meta + align256(static_cast<size_t>(cap) * sizeof(TileMeta));
+  l.total = l.tiles + static_cast<size_t>(cap) * kTileImageBytes;
+  return l;
+}
+
+}  // namespace
+
+size_t extend_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms) {
+  return layout(n_tokens, batch, n_q / n_kv, n_kv, max_context, num_sms).total;
+}
+
+cudaError_t launch_extend(const ExtendArgs& args, void* workspace, cudaStream_t stream) {
+  ExtendArgs a = args;
+  char* const ws = static_cast<char*>(workspace);
+  const int ctas = a.d.num_sms;
+  const Layout l = layout(a.n_tokens, a.d.batch, a.d.group, a.d.n_kv, a.d.max_context, ctas);
+  a.narrow = ExtendForm{kNarrowRows, reinterpret_cast<long long*>(ws + l.first), reinterpret_cast<float*>(ws + l.part)};
+  a.wide = ExtendForm{kWideRows, reinterpret_cast<long long*>(ws + l.wide_first),
+                      reinterpret_cast<float*>(ws + l.wide_part)};
+  a.ws_expand = reinterpret_cast<long long*>(ws + l.expand);
+  a.ws_seq = reinterpret_cast<int4*>(ws + l.seq);
+  a.ws_meta = reinterpret_cast<TileMeta*>(ws + l.meta);
+  a.ws_tiles = reinterpret_cast<uint8_t*>(ws + l.tiles);
+  a.tile_cap = l.tile_cap;
+  extend_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+  cudaError_t err = cudaGetLastError();
+  if (err == cudaSuccess && a.tile_cap > 0) err = launch_extend_wide(a, ctas, stream);
+  if (err == cudaSuccess) err = launch_extend_narrow(a, ctas, stream);
+  if (err != cudaSuccess || ctas < 2) return err;
+  const int row_blocks = (kNarrowRows + (a.tile_cap > 0 ? kWideRows : 0)) / kJoinWarps;
+  extend_join_kernel<<<dim3(ctas - 1, row_blocks), 32 * kJoinWarps, 0, stream>>>(a, ctas);
+  return cudaGetLastError();
+}
+
+}  // namespace tq

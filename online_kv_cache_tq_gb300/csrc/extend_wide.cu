@@ -1,0 +1,585 @@
+// The wide form of the multi-token attention: sequences with many rows.
+//
+// extend_expand_kernel turns every key tile (128 tokens of a KV head) of such
+// a sequence into two operands, once: the keys back in the original space,
+//   k_t = R^T c[code_t] + rho_t S^T (2 bits_t - 1)       (unit norm, fp16),
+// a product on the tensor cores of the expanded bits with R^T and S^T, and the
+// values n^v_t c^v[code_t] (rotated space, bf16).  They are stored in the
+// swizzled layout the products read, 64 KB a tile, so that a tile is two bulk
+// copies later.  Per token and KV head this costs 98 K operations and writes
+// 520 bytes; it saves every row tile the expansion and half of the score
+// product (128 columns in place of 256 with the sketch).
+//
+// extend_wide_kernel then works on row tiles of 256: two products of 128 rows
+// take turns, so that the softmax of one runs under the products of the other.
+//   scores  [128 x 128] = q k^T, fp16, queries in shared memory as they come
+//           (scaled by a power of two outside 2^-8 .. 2^10);
+//   output  [128 x 128] += p v, bf16, weights in tensor memory over the scores;
+// the last step turns the output back by R^T.  The softmax is that of the
+// narrow form (extend_tc.cu: its reference, and when a tile may skip the
+// search for its maximum).  The bound of the loop is the tensor cores: 2048
+// cycles of products for 256 x 128 scores, plus twice the time from a
+// product's end to the issue of the one that overwrites its operand.
+//
+// Eighteen warps: 0-7 and 8-15 the softmax of the two row tiles (two threads
+// per row), 16 issues the products, 17 copies tiles.
+#include "extend_common.cuh"
+
+namespace tq {
+namespace {
+
+#define TQ_WAIT(b, ph) ptx::wait_bar(&(b), (ph), abort, d.error, kErrTimeout)
+#define TQ_WARP_WAIT(b, ph) __all_sync(0xffffffffu, TQ_WAIT(b, ph))
+
+// ---- expansion -----------------------------------------------------------------
+
+constexpr int kExpandThreads = 256;
+constexpr int kExpandKey0 = 2 * kExtendImageBytes;
+constexpr int kExpandSmem = kExpandKey0 + 4 * kBlockBytes + 1024;     // (1024: alignment)
+
+template <int KB, int VB>
+__global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(ExtendArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t done;
+  __shared__ uint32_t tmem_s;
+  __shared__ int abort_s;
+  __shared__ float factor_s[kTile], norm_s[kTile], square_s[2][kTile], reach_s[4];
+  __shared__ uint32_t valid_s[4];
+  uint8_t* const smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  const DecodeArgs& d = a.d;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* const abort = &abort_s;
+  const long long total = a.ws_expand[d.batch];
+  if (blockIdx.x >= total) return;                // (the whole CTA)
+  if (tid == 0) {
+    abort_s = 0;
+    ptx::mbar_init(&done, 1);
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0) {
+    ptx::tmem_alloc(&tmem_s, 128);
+    ptx::tmem_relinquish();
+  }
+  const bool qjl = d.k_qjl != nullptr;
+  {                                               // R^T and S^T
+    const uint4* const src = a.images + 3 * (kExtendImageBytes / 16);
+    uint4* const dst = reinterpret_cast<uint4*>(smem);
+#pragma unroll 8
+    for (int i = tid; i < 2 * (kExtendImageBytes / 16); i += kExpandThreads) dst[i] = __ldg(src + i);
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_s;
+  const int row = tid & (kTile - 1), half = tid / kTile;   // key row or value coordinate; half of the other side
+  const LevelBytes key_levels = level_bytes<false>(d.tables->k_levels, KB);
+  const LevelBytes value_levels = level_bytes<false>(d.tables->v_levels, VB);
+  const float to_log2 = d.scale * 1.4426950408889634f;
+  uint32_t phase = 0;
+  for (long long g = blockIdx.x; g < total; g += gridDim.x, phase ^= 1) {
+    int lo = 0, hi = d.batch;                     // the last sequence whose tiles start at or before g
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.ws_expand[mid] <= g) lo = mid;
+      else hi = mid;
+    }
+    Item it{};
+    it.b = lo;
+    it.seq = a.ws_seq[lo];
+    const int tiles = max(1, (it.seq.z + kTile - 1) / kTile), local = static_cast<int>(g - a.ws_expand[lo]);
+    it.kvh = local / tiles;
+    const int pos0 = (local - it.kvh * tiles) * kTile;
+    uint8_t* const out = a.ws_tiles + g * kTileImageBytes;
+    TileMeta* const meta = a.ws_meta + g;
+
+    Cursor kc, vc;
+    RawKey<KB> k;
+    RawValue<VB> v;
+    start_cursor(d, it, pos0 + (row & ~31), kc);
+    start_cursor(d, it, pos0 + 64 * half + 32 * (lane & 1), vc);
+    load_key(d, it, kc, expanded_bit(lane), half, k);
+    // (the first two warps of a half read its 64 value norms, by expanded column)
+    const int mine = row < 64 ? row >> 5 : -1;
+    load_value(d, it, vc, row, mine, expanded_bit(lane), v);
+    {
+      const RowChunks at = row_chunks(ptx::smem_u32(smem + kExpandKey0) + half * kBlockBytes, row);
+      uint32_t w0[KB], w1[KB];
+#pragma unroll
+      for (int p = 0; p < KB; ++p) w0[p] = k.planes[p].x, w1[p] = k.planes[p].y;
+      expand32<KB, 0>(at, w0, key_levels);
+      expand32<KB, 0>(second_word(at), w1, key_levels);
+      if (qjl) {
+        const float rho = k.norm > 0.f ? __fdividef(k.rnorm * d.qjl_coef, k.norm) : 0.f;
+        const uint32_t minus_rho = __half_as_ushort(__float2half_rn(rho)) * 0x00010001u ^ 0x80008000u;
+        expand_signs<2 * kBlockBytes>(at, k.qjl.x, minus_rho);
+        expand_signs<2 * kBlockBytes>(second_word(at), k.qjl.y, minus_rho);
+      }
+    }
+    if (half == 0) {
+      const unsigned bit = __reduce_or_sync(0xffffffffu, k.valid ? 1u << expanded_bit(lane) : 0u);
+      factor_s[row] = k.valid ? k.norm * to_log2 : 0.f;
+      if (lane == 0) valid_s[warp] = bit;
+    }
+    if (mine >= 0) norm_s[64 * half + row] = v.norm;
+    ptx::fence_async_shared();
+    __syncthreads();
+    if (warp == 0 && ptx::elect_one()) {
+      ptx::tc_fence_after();
+      const uint64_t keys = ptx::desc_k_sw128(ptx::smem_u32(smem + kExpandKey0));
+      const uint64_t turn = ptx::desc_k_sw128(ptx::smem_u32(smem));
+#pragma unroll
+      for (int ks = 0; ks < 16; ++ks) {
+        const uint64_t off = (ks >> 2) * (kBlockBytes / 16) + (ks & 3) * 2;
+        if (ks < 8 || qjl) ptx::mma_bf16(tmem, keys + off, turn + off, kIdescF16, ks > 0);
+      }
+      ptx::mma_commit(&done);
+    }
+    __syncwarp();
+    // the values, under the product
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      uint32_t planes[VB];
+#pragma unroll
+      for (int p = 0; p < VB; ++p) planes[p] = v.words[p][w];
+      if constexpr (VB == 4) {
+#pragma unroll
+        for (int p = 0; p < 3; ++p) planes[p] = planes[p] ^ ~planes[3];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 levels = expand8<VB>(planes, i, value_levels);
+        const uint32_t l[4] = {levels.x, levels.y, levels.z, levels.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&l[e]));
+          const float2 n = *reinterpret_cast<const float2*>(&norm_s[64 * half + 32 * w + 8 * i + 2 * e]);
+          o[e] = pack_bf16(f.x * n.x, f.y * n.y);
+        }
+        *reinterpret_cast<uint4*>(out + kExtendImageBytes + half * kBlockBytes + row * 128 +
+                                  (((4 * w + i) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    const bool ok = TQ_WAIT(done, phase);
+    if (__syncthreads_or(!ok)) break;
+    ptx::tc_fence_after();
+    {
+      const int r = (warp & 3) * 32 + lane, h = warp >> 2;   // tensor-memory lane, columns 64 h .. + 63
+      float square = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t y[16], w[8];
+        ptx::tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 64 * h + 16 * c, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float f0 = __uint_as_float(y[2 * e]), f1 = __uint_as_float(y[2 * e + 1]);
+          square = fmaf(f0, f0, fmaf(f1, f1, square));
+          w[e] = pack_f16(f0, f1);
+        }
+        uint8_t* const dst = out + h * kBlockBytes + r * 128;
+        *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+      square_s[h][r] = square;
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (tid < kTile) {
+      const float f = factor_s[tid];
+      meta->key_factor[tid] = f;
+      const float reach = fabsf(f) * sqrtf(square_s[0][tid] + square_s[1][tid]);
+      const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(reach) & 0x7fffffffu);   // (not negative)
+      if (lane == 0) {
+        reach_s[warp] = __uint_as_float(bits);
+        meta->valid[warp] = valid_s[warp];
+      }
+    }
+    __syncthreads();
+    if (tid == 0) {
+      // (a NaN has the largest bits, and takes the path that looks at every score)
+      unsigned bits = 0;
+      for (int w = 0; w < 4; ++w) bits = max(bits, __float_as_uint(reach_s[w]));
+      meta->reach = __uint_as_float(bits);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) ptx::tmem_dealloc(tmem, 128);
+}
+
+// ---- attention -------------------------------------------------------------------
+
+constexpr int kSoftThreads = 512;
+constexpr int kMmaWarp = 16;
+constexpr int kCopyWarp = 17;
+constexpr int kWideThreads = kSoftThreads + 64;
+constexpr int kImage = kExtendImageBytes;
+constexpr int kQuery0 = 0;                        // two row tiles
+constexpr int kKey0 = 2 * kImage;                 // two stages
+constexpr int kValue0 = 4 * kImage;               // two stages
+constexpr int kMeta0 = 6 * kImage;                // four
+constexpr int kRing = 4;
+constexpr int kWideSmem = kMeta0 + kRing * static_cast<int>(sizeof(TileMeta)) + 1024;   // (1024: alignment)
+static_assert(sizeof(TileMeta) % 16 == 0, "bulk copies are multiples of 16 bytes");
+constexpr uint32_t kS = 0, kO = 256;              // tensor-memory columns, 128 for each row tile
+
+struct WideBarriers {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_full[2], added[2], o_raw[2], turned[2];   // by row tile
+  uint64_t q_full, drain;
+  uint64_t rows[8];          // the two warps that share 32 rows
+};
+
+__global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ WideBarriers bar;
+  __shared__ uint32_t tmem_s;
+  __shared__ int abort_s;
+  __shared__ Item item_s;
+  __shared__ float swap_s[2][2][kWideRows];       // what the two threads of a row tell each other
+  uint8_t* const smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  const DecodeArgs& d = a.d;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* const abort = &abort_s;
+  const long long total = a.wide.first[d.batch];
+  const long long per = run_length(total, gridDim.x);
+  const long long begin = blockIdx.x * per, end = begin + per < total ? begin + per : total;
+  if (begin >= end) return;                       // (the whole CTA)
+
+  if (tid == 0) {
+    abort_s = 0;
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(&bar.k_full[s], 1);
+      ptx::mbar_init(&bar.k_empty[s], 1);
+      ptx::mbar_init(&bar.v_full[s], 1);
+      ptx::mbar_init(&bar.v_empty[s], 1);
+      ptx::mbar_init(&bar.s_full[s], 2);          // the product's completion and the issuer itself
+      ptx::mbar_init(&bar.p_full[s], kSoftThreads / 2);
+      ptx::mbar_init(&bar.added[s], 1);
+      ptx::mbar_init(&bar.o_raw[s], kSoftThreads / 2);
+      ptx::mbar_init(&bar.turned[s], 1);
+    }
+    ptx::mbar_init(&bar.q_full, kSoftThreads);
+    ptx::mbar_init(&bar.drain, 1);
+    for (int w = 0; w < 8; ++w) ptx::mbar_init(&bar.rows[w], 64);
+    ptx::fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(&tmem_s, 512);
+    ptx::tmem_relinquish();
+  }
+  if (warp == 0) {
+    const Item it = find_item(a, a.wide, begin);
+    if (lane == 0) item_s = it;
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_s;
+  Item it = item_s;
+  long long pos = begin;
+  bool ok = true;
+
+  if (warp < 16) {
+    // ---------------- softmax ----------------
+    const int x = warp >> 3, quarter = warp & 3, half = (warp >> 2) & 1;
+    const int row = quarter * 32 + lane;          // of row tile x: tensor-memory lane; columns 64 half .. + 63
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t s_addr = lane_addr + kS + 128 * x + 64 * half, o_addr = lane_addr + kO + 128 * x + 64 * half;
+    uint64_t* const pair_bar = &bar.rows[4 * x + quarter];
+    int swaps = 0;
+    auto swap = [&](float mine, float* theirs) {  // the other thread of the row: its value of `mine`
+      float(*const buf)[kWideRows] = swap_s[swaps & 1];
+      buf[half][kTile * x + row] = mine;
+      ptx::mbar_arrive(pair_bar);
+      const bool done = TQ_WARP_WAIT(*pair_bar, swaps & 1);
+      *theirs = buf[half ^ 1][kTile * x + row];
+      ++swaps;
+      return done;
+    };
+    int jt = 0;                                   // key tiles so far
+    for (int seg = 0; pos < end; ++seg) {
+      const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
+      const int n_rows = it.seq.y * d.group;
+      const int r = it.i * kWideRows + kTile * x + row;
+      const bool live = r < n_rows;
+      const int tok = (live ? r : n_rows - 1) / d.group;
+      const long long vec = (static_cast<long long>(it.seq.x) + tok) * d.n_q + it.kvh * d.group + r - tok * d.group;
+      const int seen = max(0, it.seq.z - it.seq.y + tok + 1);     // positions this row sees
+      float other, biggest = 0.f, square = 0.f;
+      if (live) {
+#pragma unroll 4
+        for (int c = 0; c < 64; c += 8) {
+          float v[8];
+          load_query8(a, vec * kDim + 64 * half + c, v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            biggest = fmaxf(biggest, fabsf(v[k]));
+            square = fmaf(v[k], v[k], square);
+          }
+        }
+      }
+      ok = swap(biggest, &other);
+      if (!ok) break;
+      biggest = fmaxf(biggest, other);
+      int e = exponent_of(biggest);
+      if (biggest == 0.f || (e >= -8 && e < 10)) e = 0;
+      const float down = exp2_int(-e), factor = exp2_int(e);
+      uint8_t* const q_row = smem + kQuery0 + x * kImage + half * kBlockBytes + row * 128;
+#pragma unroll 2
+      for (int c = 0; c < 8; ++c) {
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (live) load_query8(a, vec * kDim + 64 * half + 8 * c, v);
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = pack_f16(v[2 * k] * down, v[2 * k + 1] * down);
+        *reinterpret_cast<uint4*>(q_row + ((c ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      ptx::fence_async_shared();
+      ptx::mbar_arrive(&bar.q_full);
+      ok = swap(square, &other);
+      if (!ok) break;
+      const float len = sqrtf(square + other) * 1.01f;      // (1.01: the operands' roundings)
+
+      float ref = -INFINITY;
+      uint64_t sum2 = 0;                          // (two fp32 zeros)
+      for (int t = t0; t < t1; ++t, ++jt) {
+        ok = TQ_WARP_WAIT(bar.s_full[x], jt & 1);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const TileMeta* const meta = reinterpret_cast<const TileMeta*>(smem + kMeta0) + (jt & (kRing - 1));
+        const uint32_t kf = ptx::smem_u32(meta->key_factor + 64 * half);
+        const uint32_t all = meta->valid[0] & meta->valid[1] & meta->valid[2] & meta->valid[3];
+        // (the same for both threads of a row)
+        const bool usual =
+            t > t0 && e == 0 && seen >= (t + 1) * kTile && all == 0xffffffffu && len * meta->reach <= ref + kRaise;
+        if (__all_sync(0xffffffffu, usual)) {
+          weigh_usual<false>(s_addr, kf, 0, ref, sum2);
+        } else {
+          // hidden positions, a scaled query, or scores that may pass the
+          // reference: the tile's maximum first
+          const int here = min(kTile, max(0, seen - t * kTile));
+          float top = masked_top(s_addr, kf, factor, meta->valid, here, half);
+          ok = swap(top, &other);
+          if (!ok) break;
+          top = fmaxf(top, other);
+          const bool raise = top > ref + kRaise || (ref == -INFINITY && top > ref);
+          if (__any_sync(0xffffffffu, raise)) {
+            const float scale = raise ? exp2_fast(ref - top) : 1.f;
+            if (raise) ref = top;
+            if (t > t0) {
+              // the output so far, once the product before has added to it
+              ok = TQ_WARP_WAIT(bar.added[x], (jt - 1) & 1);
+              if (!ok) break;
+              ptx::tc_fence_after();
+              sum2 = mul2(sum2, pair(scale, scale));
+              scale_output(o_addr, scale);
+            }
+          }
+          const float shift = ref == -INFINITY ? 0.f : ref;
+          const float sum = weigh_masked<false>(s_addr, kf, 0, factor, shift, meta->valid, here, half);
+          sum2 = add2(sum2, pair(sum, 0.f));
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&bar.p_full[x]);
+      }
+      if (!ok) break;
+
+      // output: divided by the sum, turned back by R^T
+      const float2 parts = unpair(sum2);
+      ok = swap(parts.x + parts.y, &other);
+      if (!ok) break;
+      const float sum = (parts.x + parts.y) + other;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;       // (a NaN in a visible token shows)
+      ok = TQ_WARP_WAIT(bar.added[x], (jt - 1) & 1);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const float top = largest_output(o_addr, inv);
+      ok = swap(top, &other);
+      if (!ok) break;
+      const int eo = exponent_of(fmaxf(top, other));
+      output_operand(o_addr, lane_addr + kS + 128 * x + 32 * half, inv * exp2_int(-eo));
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(&bar.o_raw[x]);
+      ok = TQ_WARP_WAIT(bar.turned[x], seg & 1);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const bool whole = t0 == 0 && t1 == it.tiles;
+      // a run's first item may have begun in the run before, its last may go on
+      float* const part = a.wide.part + (2ll * blockIdx.x + (t0 == 0 ? 1 : 0)) * part_floats(kWideRows);
+      const int part_row = kTile * x + row;
+      if (!whole && half == 0) {
+        part[kWideRows * kDim + 2 * part_row] = sum == 0.f ? -INFINITY : ref;
+        part[kWideRows * kDim + 2 * part_row + 1] = sum;
+      }
+      store_output(o_addr, exp2_int(eo), static_cast<__nv_bfloat16*>(a.out) + vec * kDim + 64 * half,
+                   whole ? nullptr : part + part_row * kDim + 64 * half, live);
+      ptx::tc_fence_before();
+      pos += t1 - t0;
+      if (pos < end) next_item(a, a.wide, it);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------- products ----------------
+    // the whole warp walks the tiles and waits; an elected lane issues
+    const uint64_t query_desc = ptx::desc_k_sw128(ptx::smem_u32(smem + kQuery0));
+    const uint64_t key_desc = ptx::desc_k_sw128(ptx::smem_u32(smem + kKey0));
+    const uint64_t value_desc = ptx::desc_k_sw128(ptx::smem_u32(smem + kValue0));
+    int kc = 0, jt = 0;                           // key ring entries, key tiles so far
+    auto scores = [&](int x, bool last) {         // of row tile x against the key ring's next entry
+      if (ptx::elect_one()) {
+        ptx::tc_fence_after();
+        const uint64_t q = query_desc + x * (kImage / 16), k = key_desc + (kc & 1) * (kImage / 16);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          const uint64_t off = (ks >> 2) * (kBlockBytes / 16) + (ks & 3) * 2;
+          ptx::mma_bf16(tmem + kS + 128 * x, q + off, k + off, kIdescF16, ks > 0);
+        }
+        ptx::mma_commit(&bar.s_full[x]);
+        if (last) ptx::mma_commit(&bar.k_empty[kc & 1]);
+        ptx::mbar_arrive(&bar.s_full[x]);
+      }
+      __syncwarp();
+    };
+    for (int seg = 0; ok && pos < end; ++seg) {
+      const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
+      ok = TQ_WARP_WAIT(bar.q_full, seg & 1) && TQ_WARP_WAIT(bar.k_full[kc & 1], (kc >> 1) & 1);
+      if (!ok) break;
+      scores(0, false);
+      scores(1, true);
+      ++kc;
+      for (int t = t0; ok && t < t1; ++t, ++jt) {
+        ok = TQ_WARP_WAIT(bar.v_full[jt & 1], (jt >> 1) & 1);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          ok = ok && TQ_WARP_WAIT(bar.p_full[x], jt & 1);
+          if (!ok) break;
+          if (ptx::elect_one()) {
+            ptx::tc_fence_after();
+            // (the weights of columns 64 .. 127 start 64 tensor-memory columns on)
+            const uint32_t o = tmem + kO + 128 * x, w = tmem + kS + 128 * x;
+            const uint64_t v = value_desc + (jt & 1) * (kImage / 16);
+            product<4>(o, w, v, kIdescBf16, t > t0);
+            product<4>(o, w + 64, v + kBlockBytes / 16, kIdescBf16, true);
+            ptx::mma_commit(&bar.added[x]);
+            if (x == 1) ptx::mma_commit(&bar.v_empty[jt & 1]);
+          }
+          __syncwarp();
+          if (t + 1 < t1) {
+            // the next scores take the columns of the weights just read
+            if (x == 0) ok = TQ_WARP_WAIT(bar.k_full[kc & 1], (kc >> 1) & 1);
+            ok = ok && TQ_WARP_WAIT(bar.added[x], jt & 1);
+            if (!ok) break;
+            scores(x, x == 1);
+            if (x == 1) ++kc;
+          }
+        }
+      }
+      // R^T out
+      ok = ok && TQ_WARP_WAIT(bar.k_full[kc & 1], (kc >> 1) & 1);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        ok = ok && TQ_WARP_WAIT(bar.o_raw[x], seg & 1);
+        if (!ok) break;
+        if (ptx::elect_one()) {
+          ptx::tc_fence_after();
+          product<8>(tmem + kO + 128 * x, tmem + kS + 128 * x, key_desc + (kc & 1) * (kImage / 16), kIdescF16, false);
+          ptx::mma_commit(&bar.turned[x]);
+          if (x == 1) ptx::mma_commit(&bar.k_empty[kc & 1]);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      ++kc;
+      pos += t1 - t0;
+      if (pos < end) next_item(a, a.wide, it);
+    }
+    if (ptx::elect_one()) {
+      ptx::mma_commit(&bar.drain);                // nothing is in flight when the CTA ends
+      ptx::drain_bar(&bar.drain, 0);
+    }
+  } else if (lane == 0) {
+    // ---------------- copies ----------------
+    int kc = 0, jt = 0;
+    while (ok && pos < end) {
+      const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
+      const long long first = it.seq.w + static_cast<long long>(it.kvh) * max(1, (it.seq.z + kTile - 1) / kTile);
+      for (int t = t0; t < t1; ++t, ++jt, ++kc) {
+        const uint8_t* const src = a.ws_tiles + (first + t) * kTileImageBytes;
+        const int s = kc & 1, vs = jt & 1;
+        ok = TQ_WAIT(bar.k_empty[s], ((kc >> 1) & 1) ^ 1);
+        if (!ok) break;
+        ptx::mbar_arrive_expect_tx(&bar.k_full[s], kImage + sizeof(TileMeta));
+        ptx::bulk_load(smem + kKey0 + s * kImage, src, kImage, &bar.k_full[s]);
+        ptx::bulk_load(smem + kMeta0 + (jt & (kRing - 1)) * sizeof(TileMeta), a.ws_meta + first + t, sizeof(TileMeta),
+                       &bar.k_full[s]);
+        ok = TQ_WAIT(bar.v_empty[vs], ((jt >> 1) & 1) ^ 1);
+        if (!ok) {
+          ++kc;
+          break;
+        }
+        ptx::mbar_arrive_expect_tx(&bar.v_full[vs], kImage);
+        ptx::bulk_load(smem + kValue0 + vs * kImage, src + kImage, kImage, &bar.v_full[vs]);
+      }
+      if (!ok) break;
+      const int s = kc & 1;
+      ok = TQ_WAIT(bar.k_empty[s], ((kc >> 1) & 1) ^ 1);
+      if (!ok) break;
+      ptx::mbar_arrive_expect_tx(&bar.k_full[s], kImage);
+      ptx::bulk_load(smem + kKey0 + s * kImage, a.images + 2 * (kImage / 16), kImage, &bar.k_full[s]);
+      ++kc;
+      pos += t1 - t0;
+      if (pos < end) next_item(a, a.wide, it);
+    }
+    if (*abort) {                                 // copies in flight land before the CTA ends
+      for (int c = kc > 1 ? kc - 2 : 0; c < kc; ++c) ptx::drain_bar(&bar.k_full[c & 1], (c >> 1) & 1);
+      for (int j = jt > 1 ? jt - 2 : 0; j < jt; ++j) ptx::drain_bar(&bar.v_full[j & 1], (j >> 1) & 1);
+    }
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int KB, int VB>
+cudaError_t expand_bits(const ExtendArgs& a, int ctas, cudaStream_t stream) {
+  const cudaError_t err =
+      cudaFuncSetAttribute(extend_expand_kernel<KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmem);
+  if (err != cudaSuccess) return err;
+  extend_expand_kernel<KB, VB><<<ctas, kExpandThreads, kExpandSmem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int KB>
+cudaError_t expand_keys(const ExtendArgs& a, int ctas, cudaStream_t stream) {
+  switch (a.d.v_bits) {
+    case 1: return expand_bits<KB, 1>(a, ctas, stream);
+    case 2: return expand_bits<KB, 2>(a, ctas, stream);
+    case 3: return expand_bits<KB, 3>(a, ctas, stream);
+    default: return expand_bits<KB, 4>(a, ctas, stream);
+  }
+}
+
+cudaError_t expand(const ExtendArgs& a, int ctas, cudaStream_t stream) {
+  switch (a.d.k_bits) {
+    case 1: return expand_keys<1>(a, ctas, stream);
+    case 2: return expand_keys<2>(a, ctas, stream);
+    case 3: return expand_keys<3>(a, ctas, stream);
+    default: return expand_keys<4>(a, ctas, stream);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_extend_wide(const ExtendArgs& a, int ctas, cudaStream_t stream) {
+  cudaError_t err = expand(a, ctas, stream);
+  if (err != cudaSuccess) return err;
+  err = cudaFuncSetAttribute(extend_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem);
+  if (err != cudaSuccess) return err;
+  extend_wide_kernel<<<ctas, kWideThreads, kWideSmem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace tq

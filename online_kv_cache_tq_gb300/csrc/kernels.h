@@ -244,7 +244,7 @@ struct NormRopeArgs {
 cudaError_t launch_norm_rope(const NormRopeArgs& args, bool bf16, int num_sms, cudaStream_t stream);
 
 // Attention of several new tokens per sequence over the packed cache
-// (extend_tc.cu).  The cache, scale and table fields of `d` are as in a
+// (extend.cu).  The cache, scale and table fields of `d` are as in a
 // decode; its q is indexed by token here.
 //
 // Expansion order: a 32-bit word of a bit plane holds the bits of 32
@@ -259,7 +259,30 @@ __host__ __device__ constexpr int expanded_sign(int c) { return (c & 1) * 16 + (
 __host__ __device__ constexpr int swizzled_f16(int row, int col) {
   return (col >> 6) * 8192 + row * 64 + ((((col >> 3) & 7) ^ (row & 7)) << 3) + (col & 7);
 }
-constexpr int kExtendImageBytes = kDim * kDim * 2;   // R, S (rows in expansion order), R^T: one image each
+// Operand images of a handle, each 128 x 128 fp16: R and S with their rows in
+// expansion order, R^T, then R^T and S^T with their columns in that order.
+constexpr int kExtendImages = 5;
+constexpr int kExtendImageBytes = kDim * kDim * 2;
+
+// One of the two forms of the attention: the rows of its row tiles, the key
+// tiles of its work items before each sequence's first ([batch + 1]), and the
+// partial outputs of the row tiles that its CTAs' runs cut.
+struct ExtendForm {
+  int rows;
+  long long* first;
+  float* part;
+};
+constexpr int kNarrowRows = 128, kWideRows = 256;
+
+// A key tile expanded for the wide form: the keys (R^T c + rho S^T signs,
+// fp16) and the values (n c, bf16, rotated) as swizzled 128 x 128 operands.
+constexpr int kTileImageBytes = 2 * kExtendImageBytes;
+struct __align__(16) TileMeta {
+  float key_factor[kDim];     // n scale log2(e) by operand row; 0 where there is no token
+  uint32_t valid[4];          // tokens there are, by group of 32
+  float reach;                // largest |factor key|
+  float pad[3];
+};
 
 struct ExtendArgs {
   DecodeArgs d;
@@ -267,13 +290,18 @@ struct ExtendArgs {
   const int32_t* query_start; // [batch + 1]
   void* out;                  // bf16 [n_tokens][n_q][128]
   bool q_bf16;
-  const uint4* images;        // the three images, in that order
+  const uint4* images;
   // workspace regions
-  long long* ws_first;        // [batch + 1]: key tiles of the work items before the sequence's first
-  int4* ws_seq;               // [batch]: first row, new tokens, context of a sequence (checked)
-  float* ws_part;             // partial outputs of the split work items
+  int4* ws_seq;               // [batch]: first row, new tokens, context (checked), first expanded tile or -1
+  ExtendForm narrow, wide;
+  long long* ws_expand;       // [batch + 1]: expanded tiles before the sequence's first
+  uint8_t* ws_tiles;          // [tile_cap][kTileImageBytes]
+  TileMeta* ws_meta;          // [tile_cap]
+  int tile_cap;               // 0: no sequence takes the wide form
 };
-size_t extend_workspace_bytes(int batch, int num_sms);
+size_t extend_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms);
 cudaError_t launch_extend(const ExtendArgs& args, void* workspace, cudaStream_t stream);
+cudaError_t launch_extend_narrow(const ExtendArgs& args, int ctas, cudaStream_t stream);   // (extend_tc.cu)
+cudaError_t launch_extend_wide(const ExtendArgs& args, int ctas, cudaStream_t stream);     // (extend_wide.cu)
 
 }  // namespace tq
