@@ -113,13 +113,13 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(ExtendArgs a)
 }
 
 // Joins the partial outputs of a split row tile: sum_s l_s 2^{m_s - M} o_s / sum_s l_s 2^{m_s - M}.
-// blockIdx.x + 1 is a run's number; the block works if that run's beginning is
-// the first cut inside its item.  A warp per row, four coordinates a lane.
+// Block x works if the beginning of run x + 1 is the first cut inside its
+// item.  A warp per row, four coordinates a lane; four blocks share a tile.
 constexpr int kJoinWarps = 8;
+constexpr int kJoinSplit = 4;
 __global__ void __launch_bounds__(32 * kJoinWarps) extend_join_kernel(ExtendArgs a, int ctas) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int narrow_blocks = kNarrowRows / kJoinWarps;
-  const ExtendForm f = blockIdx.y < narrow_blocks ? a.narrow : a.wide;
+  const ExtendForm f = blockIdx.z == 0 ? a.narrow : a.wide;
   const long long total = f.first[a.d.batch];
   const long long per = run_length(total, ctas);
   const long long cut = (blockIdx.x + 1) * per;
@@ -129,36 +129,34 @@ __global__ void __launch_bounds__(32 * kJoinWarps) extend_join_kernel(ExtendArgs
   if (it.tile == 0 || start < cut - per) return;  // no cut here, or an earlier one inside the item
   const int c0 = static_cast<int>(start / per);   // runs c0 .. c1 hold it
   const int c1 = static_cast<int>((start + it.tiles - 1) / per);
-  const int n_rows = it.seq.y * a.d.group;
-  const int row = (blockIdx.y < narrow_blocks ? blockIdx.y : blockIdx.y - narrow_blocks) * kJoinWarps + warp;
-  const int r = it.i * f.rows + row;
-  if (r >= n_rows) return;
+  const int rows = min(f.rows, it.seq.y * a.d.group - it.i * f.rows);
   // (the run that holds key tile 0 wrote its second slot, the others their first)
   auto part = [&](int c) { return f.part + (2ll * c + (c == c0 ? 1 : 0)) * part_floats(f.rows); };
-  const int stats = f.rows * kDim + 2 * row;
-  float top = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part(c)[stats]);
+  for (int row = blockIdx.y * kJoinWarps + warp; row < rows; row += kJoinSplit * kJoinWarps) {
+    const int stats = f.rows * kDim + 2 * row;
+    float top = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part(c)[stats]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float weight = 0.f;
-  for (int c = c0; c <= c1; ++c) {
-    const float* const p = part(c);
-    const float l = p[stats + 1];
-    if (l == 0.f) continue;
-    const float w = l * exp2_fast(p[stats] - top);
-    const float4 o = reinterpret_cast<const float4*>(p + row * kDim)[lane];
-    acc.x = fmaf(w, o.x, acc.x);
-    acc.y = fmaf(w, o.y, acc.y);
-    acc.z = fmaf(w, o.z, acc.z);
-    acc.w = fmaf(w, o.w, acc.w);
-    weight += w;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float weight = 0.f;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+      const float* const p = part(c);
+      const float2 ml = *reinterpret_cast<const float2*>(p + stats);
+      const float4 o = reinterpret_cast<const float4*>(p + row * kDim)[lane];
+      const float w = ml.y == 0.f ? 0.f : ml.y * exp2_fast(ml.x - top);
+      if (w == 0.f) continue;                     // (a run that saw nothing left no output)
+      acc.x = fmaf(w, o.x, acc.x);
+      acc.y = fmaf(w, o.y, acc.y);
+      acc.z = fmaf(w, o.z, acc.z);
+      acc.w = fmaf(w, o.w, acc.w);
+      weight += w;
+    }
+    const float inv = weight == 0.f ? 0.f : 1.f / weight;
+    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row_vector(a, it, it.i * f.rows + row) * kDim)[lane] =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
   }
-  const float inv = weight == 0.f ? 0.f : 1.f / weight;
-  const int tok = r / a.d.group;
-  const long long vec = (static_cast<long long>(it.seq.x) + tok) * a.d.n_q + it.kvh * a.d.group + r - tok * a.d.group;
-  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + vec * kDim)[lane] =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
 constexpr size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -216,8 +214,7 @@ cudaError_t launch_extend(const ExtendArgs& args, void* workspace, cudaStream_t 
   if (err == cudaSuccess && a.tile_cap > 0) err = launch_extend_wide(a, ctas, stream);
   if (err == cudaSuccess) err = launch_extend_narrow(a, ctas, stream);
   if (err != cudaSuccess || ctas < 2) return err;
-  const int row_blocks = (kNarrowRows + (a.tile_cap > 0 ? kWideRows : 0)) / kJoinWarps;
-  extend_join_kernel<<<dim3(ctas - 1, row_blocks), 32 * kJoinWarps, 0, stream>>>(a, ctas);
+  extend_join_kernel<<<dim3(ctas - 1, kJoinSplit, a.tile_cap > 0 ? 2 : 1), 32 * kJoinWarps, 0, stream>>>(a, ctas);
   return cudaGetLastError();
 }
 

@@ -312,6 +312,12 @@ __device__ __forceinline__ void load_query8(const ExtendArgs& a, long long at, f
   }
 }
 
+// Vector (token x query head) of row r of an item's sequence and KV head.
+__device__ __forceinline__ long long row_vector(const ExtendArgs& a, const Item& it, int r) {
+  const int tok = r / a.d.group;
+  return (static_cast<long long>(it.seq.x) + tok) * a.d.n_q + it.kvh * a.d.group + r - tok * a.d.group;
+}
+
 // Walks the cache blocks under 32-token groups of a sequence, 128 tokens at a
 // time (a block holds whole groups), with the block table entry read one step
 // ahead.
@@ -423,7 +429,7 @@ __device__ __forceinline__ void load_value(const DecodeArgs& d, const Item& it, 
 // addresses of the columns' key and value factors; VF: whether weights are
 // multiplied by a value factor (else the values are scaled already).
 
-// No score hidden, none that may pass the reference by 2^kRaise: one pass.
+// No score hidden, none that may pass the reference by 2^kRaise.
 template <bool VF>
 __device__ __forceinline__ void weigh_usual(uint32_t s, uint32_t kf, uint32_t vf, float ref, uint64_t& sum2) {
   const uint64_t minus = pair(-ref, -ref);
@@ -463,7 +469,27 @@ __device__ __forceinline__ uint32_t visible(const uint32_t* valid, int here, int
   return (n == 32 ? 0xffffffffu : (1u << n) - 1u) & valid[g];
 }
 
-// Hidden positions or a scaled query: the largest visible score first.
+// The largest of the thread's scores.
+__device__ __forceinline__ float plain_top(uint32_t s, uint32_t kf) {
+  float top = -INFINITY;
+  uint32_t x[2][16];
+  tmem_ld16_start(s, x[0]);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    tmem_ld16_wait(x[c & 1]);
+    if (c < 3) tmem_ld16_start(s + 16 * (c + 1), x[(c + 1) & 1]);
+    const uint32_t(&y)[16] = x[c & 1];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 f = load16(kf + 64 * c + 16 * k);
+      top = fmaxf(fmaxf(top, __uint_as_float(y[4 * k]) * f.x), __uint_as_float(y[4 * k + 1]) * f.y);
+      top = fmaxf(fmaxf(top, __uint_as_float(y[4 * k + 2]) * f.z), __uint_as_float(y[4 * k + 3]) * f.w);
+    }
+  }
+  return top;
+}
+
+// The same of the visible scores, or of a scaled query.
 __device__ __forceinline__ float masked_top(uint32_t s, uint32_t kf, float factor, const uint32_t* valid, int here,
                                             int half) {
   float top = -INFINITY;
@@ -558,13 +584,29 @@ __device__ __forceinline__ void output_operand(uint32_t o, uint32_t dst, float s
   }
 }
 
-// The turned output's 64 columns to the bf16 output row, or as fp32 to a partial.
-__device__ __forceinline__ void store_output(uint32_t o, float scale, __nv_bfloat16* out, float* part, bool live) {
+// The turned output's 64 columns, as fp32 to a partial.
+__device__ __forceinline__ void store_partial(uint32_t o, float scale, float* part, bool live) {
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t y[16];
     ptx::tmem_ld16(o + 16 * c, y);
-    if (live && part == nullptr) {
+    if (live) {
+      float4* const dst = reinterpret_cast<float4*>(part + 16 * c);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        dst[k] = make_float4(__uint_as_float(y[4 * k]) * scale, __uint_as_float(y[4 * k + 1]) * scale,
+                             __uint_as_float(y[4 * k + 2]) * scale, __uint_as_float(y[4 * k + 3]) * scale);
+    }
+  }
+}
+
+// The same as bf16 to the output row.
+__device__ __forceinline__ void store_row(uint32_t o, float scale, __nv_bfloat16* out, bool live) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t y[16];
+    ptx::tmem_ld16(o + 16 * c, y);
+    if (live) {
       uint4* const dst = reinterpret_cast<uint4*>(out + 16 * c);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -574,13 +616,20 @@ __device__ __forceinline__ void store_output(uint32_t o, float scale, __nv_bfloa
           w[q] = pack_bf16(__uint_as_float(y[8 * k + 2 * q]) * scale, __uint_as_float(y[8 * k + 2 * q + 1]) * scale);
         dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-    } else if (live) {
-      float4* const dst = reinterpret_cast<float4*>(part + 16 * c);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        dst[k] = make_float4(__uint_as_float(y[4 * k]) * scale, __uint_as_float(y[4 * k + 1]) * scale,
-                             __uint_as_float(y[4 * k + 2]) * scale, __uint_as_float(y[4 * k + 3]) * scale);
     }
+  }
+}
+
+// The same as bf16 into eight swizzled 16-byte chunks of a row in shared memory.
+__device__ __forceinline__ void output_rows(uint32_t o, float scale, uint8_t* dst, int row) {
+#pragma unroll 2
+  for (int c = 0; c < 4; ++c) {
+    uint32_t y[16], w[8];
+    ptx::tmem_ld16(o + 16 * c, y);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = pack_bf16(__uint_as_float(y[2 * k]) * scale, __uint_as_float(y[2 * k + 1]) * scale);
+    *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 

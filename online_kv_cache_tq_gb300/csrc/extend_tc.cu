@@ -230,15 +230,13 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
 #pragma unroll
         for (int g = 0; g < 4; ++g)
           top_bound = fmaxf(top_bound, fmaf(len_r, reach_s[rg][g].x, len_s * reach_s[rg][g].y));
-        // (the same for both threads of a row)
-        const bool usual = t > t0 && e == 0 && seen >= (t + 1) * kTile && all == 0xffffffffu && top_bound <= ref + kRaise;
-        if (__all_sync(0xffffffffu, usual)) {
-          weigh_usual<true>(s_addr, kf, vf, ref, sum2);
-        } else {
-          // hidden positions, a scaled query, or scores that may pass the
-          // reference: the tile's maximum first
-          const int here = min(kTile, max(0, seen - t * kTile));
-          float top = masked_top(s_addr, kf, factor, valid_s[rg], here, half);
+        // (both the same for the two threads of a row, and so for their warps)
+        const bool mask = __any_sync(0xffffffffu, e != 0 || seen < (t + 1) * kTile || all != 0xffffffffu);
+        const bool search = __any_sync(0xffffffffu, !(ref > -INFINITY && top_bound <= ref + kRaise));
+        const int here = min(kTile, max(0, seen - t * kTile));
+        if (search) {
+          // no reference yet, or scores that may pass it: the tile's maximum first
+          float top = mask ? masked_top(s_addr, kf, factor, valid_s[rg], here, half) : plain_top(s_addr, kf);
           ok = swap(top, &other);
           if (!ok) break;
           top = fmaxf(top, other);
@@ -255,10 +253,10 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
               scale_output(lane_addr + kO + 64 * half, scale);
             }
           }
-          const float shift = ref == -INFINITY ? 0.f : ref;
-          const float sum = weigh_masked<true>(s_addr, kf, vf, factor, shift, valid_s[rg], here, half);
-          sum2 = add2(sum2, pair(sum, 0.f));
         }
+        const float shift = ref == -INFINITY ? 0.f : ref;
+        if (mask) sum2 = add2(sum2, pair(weigh_masked<true>(s_addr, kf, vf, factor, shift, valid_s[rg], here, half), 0.f));
+        else weigh_usual<true>(s_addr, kf, vf, shift, sum2);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar.p_full[sb]);
@@ -294,8 +292,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
         part[kTile * kDim + 2 * row] = sum == 0.f ? -INFINITY : ref;
         part[kTile * kDim + 2 * row + 1] = sum;
       }
-      store_output(lane_addr + kS1 + 64 * half, out_up, static_cast<__nv_bfloat16*>(a.out) + vec * kDim + 64 * half,
-                   whole ? nullptr : part + row * kDim + 64 * half, live);
+      if (whole) store_row(lane_addr + kS1 + 64 * half, out_up, static_cast<__nv_bfloat16*>(a.out) + vec * kDim + 64 * half, live);
+      else store_partial(lane_addr + kS1 + 64 * half, out_up, part + row * kDim + 64 * half, live);
       pos += t1 - t0;
       if (pos < end) next_item(a, a.narrow, it);
     }

@@ -224,6 +224,7 @@ constexpr uint32_t kS = 0, kO = 256;              // tensor-memory columns, 128 
 struct WideBarriers {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2], added[2], o_raw[2], turned[2];   // by row tile
+  uint64_t shared[2];        // the eight warps of a row tile, for what they leave in shared memory
   uint64_t q_full, drain;
   uint64_t rows[8];          // the two warps that share 32 rows
 };
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
   __shared__ int abort_s;
   __shared__ Item item_s;
   __shared__ float swap_s[2][2][kWideRows];       // what the two threads of a row tell each other
+  __shared__ float2 query_s[kWideRows];           // length and exponent of a row's query
   uint8_t* const smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   const DecodeArgs& d = a.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -256,6 +258,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
       ptx::mbar_init(&bar.added[s], 1);
       ptx::mbar_init(&bar.o_raw[s], kSoftThreads / 2);
       ptx::mbar_init(&bar.turned[s], 1);
+      ptx::mbar_init(&bar.shared[s], kSoftThreads / 2);
     }
     ptx::mbar_init(&bar.q_full, kSoftThreads);
     ptx::mbar_init(&bar.drain, 1);
@@ -294,6 +297,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
       ++swaps;
       return done;
     };
+    int meetings = 0;
+    auto together = [&]() {                       // all eight warps of the row tile
+      ptx::mbar_arrive(&bar.shared[x]);
+      return TQ_WARP_WAIT(bar.shared[x], meetings++ & 1);
+    };
+    // rows copy_row, copy_row + 2, .. + 14 and 16 bytes of each, for copies between memory and shared memory
+    const int copy_row = 16 * (warp & 7) + (lane >> 4), copy_chunk = lane & 15;
+    uint8_t* const copy_base = smem + kQuery0 + x * kImage + (copy_chunk >> 3) * kBlockBytes;
     int jt = 0;                                   // key tiles so far
     for (int seg = 0; pos < end; ++seg) {
       const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
@@ -301,42 +312,57 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
       const int r = it.i * kWideRows + kTile * x + row;
       const bool live = r < n_rows;
       const int tok = (live ? r : n_rows - 1) / d.group;
-      const long long vec = (static_cast<long long>(it.seq.x) + tok) * d.n_q + it.kvh * d.group + r - tok * d.group;
       const int seen = max(0, it.seq.z - it.seq.y + tok + 1);     // positions this row sees
-      float other, biggest = 0.f, square = 0.f;
-      if (live) {
-#pragma unroll 4
-        for (int c = 0; c < 64; c += 8) {
-          float v[8];
-          load_query8(a, vec * kDim + 64 * half + c, v);
+      float other;
+      // The queries, sixteen lanes to a row (whole lines, and a row's largest
+      // coordinate and length in four shuffles): fp16, scaled by a power of
+      // two if outside the range, swizzled.
+#pragma unroll 1
+      for (int k0 = 0; k0 < 8; k0 += 4) {
+        float v[4][8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            biggest = fmaxf(biggest, fabsf(v[k]));
-            square = fmaf(v[k], v[k], square);
+        for (int k = 0; k < 4; ++k) {
+          const int rr = it.i * kWideRows + kTile * x + copy_row + 2 * (k0 + k);
+          if (rr < n_rows) {
+            load_query8(a, row_vector(a, it, rr) * kDim + copy_chunk * 8, v[k]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[k][q] = 0.f;
           }
         }
-      }
-      ok = swap(biggest, &other);
-      if (!ok) break;
-      biggest = fmaxf(biggest, other);
-      int e = exponent_of(biggest);
-      if (biggest == 0.f || (e >= -8 && e < 10)) e = 0;
-      const float down = exp2_int(-e), factor = exp2_int(e);
-      uint8_t* const q_row = smem + kQuery0 + x * kImage + half * kBlockBytes + row * 128;
-#pragma unroll 2
-      for (int c = 0; c < 8; ++c) {
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (live) load_query8(a, vec * kDim + 64 * half + 8 * c, v);
-        uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = pack_f16(v[2 * k] * down, v[2 * k + 1] * down);
-        *reinterpret_cast<uint4*>(q_row + ((c ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int k = 0; k < 4; ++k) {
+          const int qr = copy_row + 2 * (k0 + k);
+          float biggest = 0.f, square = 0.f;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            biggest = fmaxf(biggest, fabsf(v[k][q]));
+            square = fmaf(v[k][q], v[k][q], square);
+          }
+#pragma unroll
+          for (int o = 1; o < 16; o <<= 1) {
+            biggest = fmaxf(biggest, __shfl_xor_sync(0xffffffffu, biggest, o));
+            square += __shfl_xor_sync(0xffffffffu, square, o);
+          }
+          int qe = exponent_of(biggest);
+          if (biggest == 0.f || (qe >= -8 && qe < 10)) qe = 0;
+          const float down = exp2_int(-qe);
+          if (copy_chunk == 0) query_s[kTile * x + qr] = make_float2(sqrtf(square), static_cast<float>(qe));
+          uint32_t w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) w[q] = pack_f16(v[k][2 * q] * down, v[k][2 * q + 1] * down);
+          *reinterpret_cast<uint4*>(copy_base + qr * 128 + (((copy_chunk & 7) ^ (qr & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
       ptx::fence_async_shared();
       ptx::mbar_arrive(&bar.q_full);
-      ok = swap(square, &other);
+      ok = together();
       if (!ok) break;
-      const float len = sqrtf(square + other) * 1.01f;      // (1.01: the operands' roundings)
+      const float2 query = query_s[kTile * x + row];
+      const float len = query.x * 1.01f;          // (1.01: the operands' roundings)
+      const int e = static_cast<int>(query.y);
+      const float factor = exp2_int(e);
 
       float ref = -INFINITY;
       uint64_t sum2 = 0;                          // (two fp32 zeros)
@@ -347,16 +373,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         const TileMeta* const meta = reinterpret_cast<const TileMeta*>(smem + kMeta0) + (jt & (kRing - 1));
         const uint32_t kf = ptx::smem_u32(meta->key_factor + 64 * half);
         const uint32_t all = meta->valid[0] & meta->valid[1] & meta->valid[2] & meta->valid[3];
-        // (the same for both threads of a row)
-        const bool usual =
-            t > t0 && e == 0 && seen >= (t + 1) * kTile && all == 0xffffffffu && len * meta->reach <= ref + kRaise;
-        if (__all_sync(0xffffffffu, usual)) {
-          weigh_usual<false>(s_addr, kf, 0, ref, sum2);
-        } else {
-          // hidden positions, a scaled query, or scores that may pass the
-          // reference: the tile's maximum first
-          const int here = min(kTile, max(0, seen - t * kTile));
-          float top = masked_top(s_addr, kf, factor, meta->valid, here, half);
+        // (both the same for the two threads of a row, and so for their warps)
+        const bool mask = __any_sync(0xffffffffu, e != 0 || seen < (t + 1) * kTile || all != 0xffffffffu);
+        const bool search = __any_sync(0xffffffffu, !(ref > -INFINITY && len * meta->reach <= ref + kRaise));
+        const int here = min(kTile, max(0, seen - t * kTile));
+        if (search) {
+          // no reference yet, or scores that may pass it: the tile's maximum first
+          float top = mask ? masked_top(s_addr, kf, factor, meta->valid, here, half) : plain_top(s_addr, kf);
           ok = swap(top, &other);
           if (!ok) break;
           top = fmaxf(top, other);
@@ -373,10 +396,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
               scale_output(o_addr, scale);
             }
           }
-          const float shift = ref == -INFINITY ? 0.f : ref;
-          const float sum = weigh_masked<false>(s_addr, kf, 0, factor, shift, meta->valid, here, half);
-          sum2 = add2(sum2, pair(sum, 0.f));
         }
+        const float shift = ref == -INFINITY ? 0.f : ref;
+        if (mask) sum2 = add2(sum2, pair(weigh_masked<false>(s_addr, kf, 0, factor, shift, meta->valid, here, half), 0.f));
+        else weigh_usual<false>(s_addr, kf, 0, shift, sum2);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar.p_full[x]);
@@ -411,8 +434,21 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         part[kWideRows * kDim + 2 * part_row] = sum == 0.f ? -INFINITY : ref;
         part[kWideRows * kDim + 2 * part_row + 1] = sum;
       }
-      store_output(o_addr, exp2_int(eo), static_cast<__nv_bfloat16*>(a.out) + vec * kDim + 64 * half,
-                   whole ? nullptr : part + part_row * kDim + 64 * half, live);
+      if (!whole) {
+        store_partial(o_addr, exp2_int(eo), part + part_row * kDim + 64 * half, live);
+      } else {
+        // bf16 rows through the queries' place in shared memory, to leave in whole lines
+        output_rows(o_addr, exp2_int(eo), smem + kQuery0 + x * kImage + half * kBlockBytes + row * 128, row);
+        ok = together();
+        if (!ok) break;
+#pragma unroll 4
+        for (int k = 0; k < 8; ++k) {
+          const int qr = copy_row + 2 * k, rr = it.i * kWideRows + kTile * x + qr;
+          if (rr < n_rows)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row_vector(a, it, rr) * kDim + copy_chunk * 8) =
+                *reinterpret_cast<const uint4*>(copy_base + qr * 128 + (((copy_chunk & 7) ^ (qr & 7)) << 4));
+        }
+      }
       ptx::tc_fence_before();
       pos += t1 - t0;
       if (pos < end) next_item(a, a.wide, it);
