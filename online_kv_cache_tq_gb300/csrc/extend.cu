@@ -18,7 +18,7 @@ constexpr int kWideFrom = 512;
 constexpr long long kTileCap = 1 << 15;
 
 // One CTA checks the lengths, chooses the forms and forms the prefix sums of
-// key tiles and expanded tiles, a warp per sequence.
+// units of work and expanded tiles, a warp per sequence.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
@@ -59,9 +59,10 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(ExtendArgs a)
       const int n = s1 - s0;
       const bool eligible = a.tile_cap > 0 && static_cast<long long>(n) * group >= kWideFrom;
       long long narrow = 0, wide = 0;
-      for (int i = lane; i < row_tiles(kNarrowRows, n, group); i += 32) narrow += key_tiles(i, kNarrowRows, n, ctx, group);
+      for (int i = lane; i < row_tiles(kNarrowRows, n, group); i += 32) narrow += kNarrowCost + key_tiles(i, kNarrowRows, n, ctx, group);
       if (eligible)
-        for (int i = lane; i < row_tiles(kWideRows, n, group); i += 32) wide += key_tiles(i, kWideRows, n, ctx, group);
+        for (int i = lane; i < row_tiles(kWideRows, n, group); i += 32)
+          wide += kWideCost + key_tiles(i, kWideRows, n, ctx, group);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) {
         narrow += __shfl_xor_sync(0xffffffffu, narrow, d);
@@ -124,11 +125,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) extend_join_kernel(ExtendArgs
   const long long per = run_length(total, ctas);
   const long long cut = (blockIdx.x + 1) * per;
   if (cut >= total) return;
-  const Item it = find_item(a, f, cut);
-  const long long start = cut - it.tile;          // the item's first key tile
-  if (it.tile == 0 || start < cut - per) return;  // no cut here, or an earlier one inside the item
-  const int c0 = static_cast<int>(start / per);   // runs c0 .. c1 hold it
-  const int c1 = static_cast<int>((start + it.tiles - 1) / per);
+  int offset;
+  const Item it = find_item(a, f, cut, &offset);
+  const long long first = cut - offset + f.cost;  // unit of the item's first key tile
+  if (cut <= first || cut - per > first) return;  // no key tile before the cut, or an earlier cut among them
+  const int c0 = static_cast<int>(first / per);   // runs c0 .. c1 hold it
+  const int c1 = static_cast<int>((first + it.tiles - 1) / per);
   const int rows = min(f.rows, it.seq.y * a.d.group - it.i * f.rows);
   // (the run that holds key tile 0 wrote its second slot, the others their first)
   auto part = [&](int c) { return f.part + (2ll * c + (c == c0 ? 1 : 0)) * part_floats(f.rows); };
@@ -201,8 +203,9 @@ cudaError_t launch_extend(const ExtendArgs& args, void* workspace, cudaStream_t 
   char* const ws = static_cast<char*>(workspace);
   const int ctas = a.d.num_sms;
   const Layout l = layout(a.n_tokens, a.d.batch, a.d.group, a.d.n_kv, a.d.max_context, ctas);
-  a.narrow = ExtendForm{kNarrowRows, reinterpret_cast<long long*>(ws + l.first), reinterpret_cast<float*>(ws + l.part)};
-  a.wide = ExtendForm{kWideRows, reinterpret_cast<long long*>(ws + l.wide_first),
+  a.narrow = ExtendForm{kNarrowRows, kNarrowCost, reinterpret_cast<long long*>(ws + l.first),
+                        reinterpret_cast<float*>(ws + l.part)};
+  a.wide = ExtendForm{kWideRows, kWideCost, reinterpret_cast<long long*>(ws + l.wide_first),
                       reinterpret_cast<float*>(ws + l.wide_part)};
   a.ws_expand = reinterpret_cast<long long*>(ws + l.expand);
   a.ws_seq = reinterpret_cast<int4*>(ws + l.seq);

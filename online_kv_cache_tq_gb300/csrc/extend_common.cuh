@@ -33,15 +33,26 @@ __device__ __forceinline__ int row_tiles(int rows, int n_new, int group) {
   return static_cast<int>((static_cast<long long>(n_new) * group + rows - 1) / rows);
 }
 
-// A work item: a row tile of a sequence and KV head, and a key tile in it.
+// A work item: a row tile of a sequence and KV head.
 struct Item {
   int b, kvh, i;       // sequence, KV head, row tile
-  int tile, tiles;     // current key tile, key tiles of the item
+  int tiles;           // its key tiles
   int4 seq;            // first row, new tokens, context, first expanded tile
 };
 
-// The item of form `f` that holds key tile `pos` (found by a whole warp).
-__device__ __forceinline__ Item find_item(const ExtendArgs& a, const ExtendForm& f, long long pos) {
+// A CTA's run of work.  Work is counted in units: an item has f.cost units for
+// its beginning and end, then one per key tile, so that many short items weigh
+// what they take.  Every CTA has an equal run of units; what it works on is
+// the key tiles among them.
+struct Run {
+  long long pos, end;  // units
+  int offset;          // of pos in the item
+  Item it;
+};
+__device__ __forceinline__ long long run_length(long long total, int ctas) { return (total + ctas - 1) / ctas; }
+
+// The item of form `f` that holds unit `pos`, and the offset in it (found by a whole warp).
+__device__ __forceinline__ Item find_item(const ExtendArgs& a, const ExtendForm& f, long long pos, int* offset) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = a.d.batch;                     // the last sequence that starts at or before pos
   while (hi - lo > 1) {
@@ -58,10 +69,12 @@ __device__ __forceinline__ Item find_item(const ExtendArgs& a, const ExtendForm&
   rem -= it.kvh * per_head;
   const int mt = row_tiles(f.rows, it.seq.y, a.d.group);
   it.i = 0;
-  it.tile = it.tiles = 0;
+  it.tiles = 0;
+  *offset = 0;
   for (int i0 = 0; i0 < mt; i0 += 32) {
     const int nt = i0 + lane < mt ? key_tiles(i0 + lane, f.rows, it.seq.y, it.seq.z, a.d.group) : 0;
-    long long upto = nt;
+    const long long units = i0 + lane < mt ? nt + f.cost : 0;
+    long long upto = units;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const long long o = __shfl_up_sync(0xffffffffu, upto, d);
@@ -72,7 +85,7 @@ __device__ __forceinline__ Item find_item(const ExtendArgs& a, const ExtendForm&
       const int src = __ffs(past) - 1;
       it.i = i0 + src;
       it.tiles = __shfl_sync(0xffffffffu, nt, src);
-      it.tile = static_cast<int>(rem - __shfl_sync(0xffffffffu, upto - nt, src));
+      *offset = static_cast<int>(rem - __shfl_sync(0xffffffffu, upto - units, src));
       break;
     }
     rem -= __shfl_sync(0xffffffffu, upto, 31);
@@ -81,7 +94,6 @@ __device__ __forceinline__ Item find_item(const ExtendArgs& a, const ExtendForm&
 }
 
 __device__ __forceinline__ void next_item(const ExtendArgs& a, const ExtendForm& f, Item& it) {
-  it.tile = 0;
   if (++it.i >= row_tiles(f.rows, it.seq.y, a.d.group)) {
     it.i = 0;
     if (++it.kvh >= a.d.n_kv) {
@@ -95,9 +107,26 @@ __device__ __forceinline__ void next_item(const ExtendArgs& a, const ExtendForm&
   it.tiles = key_tiles(it.i, f.rows, it.seq.y, it.seq.z, a.d.group);
 }
 
-// Key tiles of every CTA's run, and floats of a partial output: the rows'
-// outputs, then their (reference, sum).
-__device__ __forceinline__ long long run_length(long long total, int ctas) { return (total + ctas - 1) / ctas; }
+// The run's next segment: key tiles t0 .. t1 - 1 of r.it.  `end_segment` moves behind it.
+__device__ __forceinline__ bool next_segment(const ExtendArgs& a, const ExtendForm& f, Run& r, int& t0, int& t1) {
+  while (r.pos < r.end) {
+    const long long left = r.end - r.pos;
+    const int units = f.cost + r.it.tiles;
+    const int upto = left < units - r.offset ? r.offset + static_cast<int>(left) : units;
+    t0 = max(0, r.offset - f.cost);
+    t1 = max(0, upto - f.cost);
+    if (t0 < t1) return true;
+    r.pos += upto - r.offset;                     // (the run ends before the item's first key tile)
+  }
+  return false;
+}
+__device__ __forceinline__ void end_segment(const ExtendArgs& a, const ExtendForm& f, Run& r, int t1) {
+  r.pos += f.cost + t1 - r.offset;
+  r.offset = 0;
+  if (r.pos < r.end) next_item(a, f, r.it);
+}
+
+// Floats of a partial output: the rows' outputs, then their (reference, sum).
 __host__ __device__ constexpr int part_floats(int rows) { return rows * (kDim + 2); }
 
 // ---- expansion of packed bits ------------------------------------------------
@@ -316,6 +345,23 @@ __device__ __forceinline__ void load_query8(const ExtendArgs& a, long long at, f
 __device__ __forceinline__ long long row_vector(const ExtendArgs& a, const Item& it, int r) {
   const int tok = r / a.d.group;
   return (static_cast<long long>(it.seq.x) + tok) * a.d.n_q + it.kvh * a.d.group + r - tok * a.d.group;
+}
+
+// Brings the query rows of the run's next item to L2 while a segment that ends
+// with key tile t1 is worked on: they come from far memory, and a segment
+// begins with them.
+__device__ __forceinline__ void prefetch_queries(const ExtendArgs& a, const ExtendForm& f, const Run& r, int t1, int t,
+                                                 int threads) {
+  if (r.pos + f.cost + t1 - r.offset >= r.end) return;
+  Item it = r.it;
+  next_item(a, f, it);
+  const int lines = a.q_bf16 ? 2 : 4;             // of 128 bytes
+  const int rows = min(f.rows, it.seq.y * a.d.group - it.i * f.rows);
+  for (int k = t; k < rows * lines; k += threads) {
+    const long long vec = row_vector(a, it, it.i * f.rows + k / lines);
+    const char* const p = static_cast<const char*>(a.d.q) + (vec * lines + k % lines) * 128;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+  }
 }
 
 // Walks the cache blocks under 32-token groups of a sequence, 128 tokens at a
@@ -560,14 +606,19 @@ __device__ __forceinline__ void scale_output(uint32_t o, float scale) {
   }
 }
 
+// The largest of 64 columns of the output.  (A bound from the values' norms
+// would save this pass, but a huge value that a row does not see would push
+// the row's output out of fp16's range.)
 __device__ __forceinline__ float largest_output(uint32_t o, float inv) {
   float top = 0.f;
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t y[16];
-    ptx::tmem_ld16(o + 16 * c, y);
+  uint32_t x[2][16];
+  tmem_ld16_start(o, x[0]);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(__uint_as_float(y[k]) * inv));
+  for (int c = 0; c < 4; ++c) {
+    tmem_ld16_wait(x[c & 1]);
+    if (c < 3) tmem_ld16_start(o + 16 * (c + 1), x[(c + 1) & 1]);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(__uint_as_float(x[c & 1][k]) * inv));
   }
   return top;
 }

@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
   __shared__ uint32_t tmem_s;
   __shared__ int abort_s;
   __shared__ Item item_s;
+  __shared__ int offset_s;
   __shared__ float swap_s[2][2][kTile];           // what the two threads of a row tell each other
   __shared__ float2 reach_s[kRing][4];            // per 32 tokens of a tile: bounds of the longest scaled key halves
   __shared__ uint32_t valid_s[kRing][4];          // tokens of a tile, by expanded column
@@ -82,8 +83,10 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
   volatile int* const abort = &abort_s;
   const long long total = a.narrow.first[d.batch];
   const long long per = run_length(total, gridDim.x);
-  const long long begin = blockIdx.x * per, end = begin + per < total ? begin + per : total;
-  if (begin >= end) return;                       // (the whole CTA)
+  Run run;
+  run.pos = blockIdx.x * per;
+  run.end = run.pos + per < total ? run.pos + per : total;
+  if (run.pos >= run.end) return;                 // (the whole CTA)
 
   if (tid == 0) {
     abort_s = 0;
@@ -109,17 +112,23 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
     ptx::tmem_relinquish();
   }
   if (warp == 0) {
-    const Item it = find_item(a, a.narrow, begin);
-    if (lane == 0) item_s = it;
+    int offset;
+    const Item it = find_item(a, a.narrow, run.pos, &offset);
+    if (lane == 0) {
+      item_s = it;
+      offset_s = offset;
+    }
   }
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_s;
-  Item it = item_s;
+  run.it = item_s;
+  run.offset = offset_s;
+  const Item& it = run.it;
+  int t0, t1;                                     // key tiles of the current segment
   const bool qjl = d.k_qjl != nullptr;
   float* const key_factor = reinterpret_cast<float*>(smem + kFactor0);
   float* const value_factor = key_factor + kRing * kTile;
-  long long pos = begin;
   bool ok = true;
 #define TQ_WAIT(b, ph) ptx::wait_bar(&(b), (ph), abort, d.error, kErrTimeout)
 
@@ -140,8 +149,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       return done;
     };
     int jt = 0;                                   // key tiles so far
-    for (int seg = 0; pos < end; ++seg) {
-      const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
+    for (int seg = 0; next_segment(a, a.narrow, run, t0, t1); ++seg) {
       const int n_rows = it.seq.y * d.group;
       const int r = it.i * kTile + row;
       const bool live = r < n_rows;
@@ -294,8 +302,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       }
       if (whole) store_row(lane_addr + kS1 + 64 * half, out_up, static_cast<__nv_bfloat16*>(a.out) + vec * kDim + 64 * half, live);
       else store_partial(lane_addr + kS1 + 64 * half, out_up, part + row * kDim + 64 * half, live);
-      pos += t1 - t0;
-      if (pos < end) next_item(a, a.narrow, it);
+      end_segment(a, a.narrow, run, t1);
     }
   } else if (warp < 16) {
     // ---------------- keys ----------------
@@ -318,14 +325,14 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       ++kc;
       return true;
     };
-    while (ok && pos < end) {
-      const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
+    while (ok && next_segment(a, a.narrow, run, t0, t1)) {
       Cursor c;
       RawKey<KB> next;
       start_cursor(d, it, t0 * kTile + (row & ~31), c);
       load_key(d, it, c, expanded_bit(lane), half, next);
       advance(d, it, c);
       ok = image(0, qjl ? 2 : 1);
+      prefetch_queries(a, a.narrow, run, t1, tid - kSoftThreads, kKeyThreads);
       for (int t = t0; ok && t < t1; ++t, ++jt, ++kc) {
         const RawKey<KB> k = next;
         if (t + 1 < t1) {
@@ -367,8 +374,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
         ptx::mbar_arrive(&bar.k_full[s]);
       }
       ok = ok && image(2, 1);
-      pos += t1 - t0;
-      if (pos < end) next_item(a, a.narrow, it);
+      end_segment(a, a.narrow, run, t1);
     }
   } else if (warp < kMmaWarp) {
     // ---------------- values ----------------
@@ -378,8 +384,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
     const int mine = dim < 64 ? dim >> 5 : -1;
     const LevelBytes lev = level_bytes<true>(d.tables->v_levels, VB);
     int jt = 0;
-    while (ok && pos < end) {
-      const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
+    while (ok && next_segment(a, a.narrow, run, t0, t1)) {
       Cursor c;
       RawValue<VB> next;
       start_cursor(d, it, t0 * kTile + 64 * half + 32 * (lane & 1), c);
@@ -404,8 +409,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
         ptx::fence_async_shared();
         ptx::mbar_arrive(&bar.v_full[s]);
       }
-      pos += t1 - t0;
-      if (pos < end) next_item(a, a.narrow, it);
+      end_segment(a, a.narrow, run, t1);
     }
   } else {
     // ---------------- products ----------------
@@ -432,8 +436,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       ++kc;
       return true;
     };
-    for (int seg = 0; ok && pos < end; ++seg) {
-      const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
+    for (int seg = 0; ok && next_segment(a, a.narrow, run, t0, t1); ++seg) {
       // R q and S q
       ok = TQ_WARP_WAIT(bar.k_full[kc & 1], (kc >> 1) & 1) && TQ_WARP_WAIT(bar.q_raw, seg & 1);
       if (!ok) break;
@@ -477,8 +480,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       }
       __syncwarp();
       ++kc;
-      pos += t1 - t0;
-      if (pos < end) next_item(a, a.narrow, it);
+      end_segment(a, a.narrow, run, t1);
     }
     if (ptx::elect_one()) {
       ptx::mma_commit(&bar.drain);                // nothing is in flight when the CTA ends

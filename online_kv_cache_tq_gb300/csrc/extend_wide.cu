@@ -74,8 +74,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
   const LevelBytes key_levels = level_bytes<false>(d.tables->k_levels, KB);
   const LevelBytes value_levels = level_bytes<false>(d.tables->v_levels, VB);
   const float to_log2 = d.scale * 1.4426950408889634f;
-  uint32_t phase = 0;
-  for (long long g = blockIdx.x; g < total; g += gridDim.x, phase ^= 1) {
+  // (the first two warps of a half read its 64 value norms, by expanded column)
+  const int mine = row < 64 ? row >> 5 : -1;
+  RawKey<KB> next_key;
+  RawValue<VB> next_value;
+  auto load_tile = [&](long long g) {             // the packed words of tile g
     int lo = 0, hi = d.batch;                     // the last sequence whose tiles start at or before g
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -88,18 +91,20 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
     const int tiles = max(1, (it.seq.z + kTile - 1) / kTile), local = static_cast<int>(g - a.ws_expand[lo]);
     it.kvh = local / tiles;
     const int pos0 = (local - it.kvh * tiles) * kTile;
-    uint8_t* const out = a.ws_tiles + g * kTileImageBytes;
-    TileMeta* const meta = a.ws_meta + g;
-
     Cursor kc, vc;
-    RawKey<KB> k;
-    RawValue<VB> v;
     start_cursor(d, it, pos0 + (row & ~31), kc);
     start_cursor(d, it, pos0 + 64 * half + 32 * (lane & 1), vc);
-    load_key(d, it, kc, expanded_bit(lane), half, k);
-    // (the first two warps of a half read its 64 value norms, by expanded column)
-    const int mine = row < 64 ? row >> 5 : -1;
-    load_value(d, it, vc, row, mine, expanded_bit(lane), v);
+    load_key(d, it, kc, expanded_bit(lane), half, next_key);
+    load_value(d, it, vc, row, mine, expanded_bit(lane), next_value);
+  };
+  load_tile(blockIdx.x);
+  uint32_t phase = 0;
+  for (long long g = blockIdx.x; g < total; g += gridDim.x, phase ^= 1) {
+    uint8_t* const out = a.ws_tiles + g * kTileImageBytes;
+    TileMeta* const meta = a.ws_meta + g;
+    const RawKey<KB> k = next_key;
+    const RawValue<VB> v = next_value;
+    if (g + gridDim.x < total) load_tile(g + gridDim.x);
     {
       const RowChunks at = row_chunks(ptx::smem_u32(smem + kExpandKey0) + half * kBlockBytes, row);
       uint32_t w0[KB], w1[KB];
@@ -200,6 +205,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
       for (int w = 0; w < 4; ++w) bits = max(bits, __float_as_uint(reach_s[w]));
       meta->reach = __uint_as_float(bits);
     }
+    __syncthreads();                              // (the next tile overwrites what was read)
   }
   __syncthreads();
   if (warp == 0) ptx::tmem_dealloc(tmem, 128);
@@ -235,6 +241,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
   __shared__ uint32_t tmem_s;
   __shared__ int abort_s;
   __shared__ Item item_s;
+  __shared__ int offset_s;
   __shared__ float swap_s[2][2][kWideRows];       // what the two threads of a row tell each other
   __shared__ float2 query_s[kWideRows];           // length and exponent of a row's query
   uint8_t* const smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -243,8 +250,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
   volatile int* const abort = &abort_s;
   const long long total = a.wide.first[d.batch];
   const long long per = run_length(total, gridDim.x);
-  const long long begin = blockIdx.x * per, end = begin + per < total ? begin + per : total;
-  if (begin >= end) return;                       // (the whole CTA)
+  Run run;
+  run.pos = blockIdx.x * per;
+  run.end = run.pos + per < total ? run.pos + per : total;
+  if (run.pos >= run.end) return;                 // (the whole CTA)
 
   if (tid == 0) {
     abort_s = 0;
@@ -270,14 +279,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
     ptx::tmem_relinquish();
   }
   if (warp == 0) {
-    const Item it = find_item(a, a.wide, begin);
-    if (lane == 0) item_s = it;
+    int offset;
+    const Item it = find_item(a, a.wide, run.pos, &offset);
+    if (lane == 0) {
+      item_s = it;
+      offset_s = offset;
+    }
   }
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_s;
-  Item it = item_s;
-  long long pos = begin;
+  run.it = item_s;
+  run.offset = offset_s;
+  const Item& it = run.it;
+  int t0, t1;                                     // key tiles of the current segment
   bool ok = true;
 
   if (warp < 16) {
@@ -306,8 +321,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
     const int copy_row = 16 * (warp & 7) + (lane >> 4), copy_chunk = lane & 15;
     uint8_t* const copy_base = smem + kQuery0 + x * kImage + (copy_chunk >> 3) * kBlockBytes;
     int jt = 0;                                   // key tiles so far
-    for (int seg = 0; pos < end; ++seg) {
-      const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
+    for (int seg = 0; next_segment(a, a.wide, run, t0, t1); ++seg) {
       const int n_rows = it.seq.y * d.group;
       const int r = it.i * kWideRows + kTile * x + row;
       const bool live = r < n_rows;
@@ -450,8 +464,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         }
       }
       ptx::tc_fence_before();
-      pos += t1 - t0;
-      if (pos < end) next_item(a, a.wide, it);
+      end_segment(a, a.wide, run, t1);
     }
   } else if (warp == kMmaWarp) {
     // ---------------- products ----------------
@@ -475,8 +488,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
       }
       __syncwarp();
     };
-    for (int seg = 0; ok && pos < end; ++seg) {
-      const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
+    for (int seg = 0; ok && next_segment(a, a.wide, run, t0, t1); ++seg) {
       ok = TQ_WARP_WAIT(bar.q_full, seg & 1) && TQ_WARP_WAIT(bar.k_full[kc & 1], (kc >> 1) & 1);
       if (!ok) break;
       scores(0, false);
@@ -525,47 +537,52 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
       }
       if (!ok) break;
       ++kc;
-      pos += t1 - t0;
-      if (pos < end) next_item(a, a.wide, it);
+      end_segment(a, a.wide, run, t1);
     }
     if (ptx::elect_one()) {
       ptx::mma_commit(&bar.drain);                // nothing is in flight when the CTA ends
       ptx::drain_bar(&bar.drain, 0);
     }
-  } else if (lane == 0) {
+  } else {
     // ---------------- copies ----------------
+    // the whole warp walks the segments and waits; lane 0 copies
     int kc = 0, jt = 0;
-    while (ok && pos < end) {
-      const int t0 = it.tile, t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + (end - pos)));
+    while (ok && next_segment(a, a.wide, run, t0, t1)) {
       const long long first = it.seq.w + static_cast<long long>(it.kvh) * max(1, (it.seq.z + kTile - 1) / kTile);
       for (int t = t0; t < t1; ++t, ++jt, ++kc) {
         const uint8_t* const src = a.ws_tiles + (first + t) * kTileImageBytes;
         const int s = kc & 1, vs = jt & 1;
-        ok = TQ_WAIT(bar.k_empty[s], ((kc >> 1) & 1) ^ 1);
+        ok = TQ_WARP_WAIT(bar.k_empty[s], ((kc >> 1) & 1) ^ 1);
         if (!ok) break;
-        ptx::mbar_arrive_expect_tx(&bar.k_full[s], kImage + sizeof(TileMeta));
-        ptx::bulk_load(smem + kKey0 + s * kImage, src, kImage, &bar.k_full[s]);
-        ptx::bulk_load(smem + kMeta0 + (jt & (kRing - 1)) * sizeof(TileMeta), a.ws_meta + first + t, sizeof(TileMeta),
-                       &bar.k_full[s]);
-        ok = TQ_WAIT(bar.v_empty[vs], ((jt >> 1) & 1) ^ 1);
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(&bar.k_full[s], kImage + sizeof(TileMeta));
+          ptx::bulk_load(smem + kKey0 + s * kImage, src, kImage, &bar.k_full[s]);
+          ptx::bulk_load(smem + kMeta0 + (jt & (kRing - 1)) * sizeof(TileMeta), a.ws_meta + first + t, sizeof(TileMeta),
+                         &bar.k_full[s]);
+        }
+        ok = TQ_WARP_WAIT(bar.v_empty[vs], ((jt >> 1) & 1) ^ 1);
         if (!ok) {
           ++kc;
           break;
         }
-        ptx::mbar_arrive_expect_tx(&bar.v_full[vs], kImage);
-        ptx::bulk_load(smem + kValue0 + vs * kImage, src + kImage, kImage, &bar.v_full[vs]);
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(&bar.v_full[vs], kImage);
+          ptx::bulk_load(smem + kValue0 + vs * kImage, src + kImage, kImage, &bar.v_full[vs]);
+        }
+        if (t == t0) prefetch_queries(a, a.wide, run, t1, lane, 32);
       }
       if (!ok) break;
       const int s = kc & 1;
-      ok = TQ_WAIT(bar.k_empty[s], ((kc >> 1) & 1) ^ 1);
+      ok = TQ_WARP_WAIT(bar.k_empty[s], ((kc >> 1) & 1) ^ 1);
       if (!ok) break;
-      ptx::mbar_arrive_expect_tx(&bar.k_full[s], kImage);
-      ptx::bulk_load(smem + kKey0 + s * kImage, a.images + 2 * (kImage / 16), kImage, &bar.k_full[s]);
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(&bar.k_full[s], kImage);
+        ptx::bulk_load(smem + kKey0 + s * kImage, a.images + 2 * (kImage / 16), kImage, &bar.k_full[s]);
+      }
       ++kc;
-      pos += t1 - t0;
-      if (pos < end) next_item(a, a.wide, it);
+      end_segment(a, a.wide, run, t1);
     }
-    if (*abort) {                                 // copies in flight land before the CTA ends
+    if (*abort && lane == 0) {                    // copies in flight land before the CTA ends
       for (int c = kc > 1 ? kc - 2 : 0; c < kc; ++c) ptx::drain_bar(&bar.k_full[c & 1], (c >> 1) & 1);
       for (int j = jt > 1 ? jt - 2 : 0; j < jt; ++j) ptx::drain_bar(&bar.v_full[j & 1], (j >> 1) & 1);
     }

@@ -264,15 +264,17 @@ __host__ __device__ constexpr int swizzled_f16(int row, int col) {
 constexpr int kExtendImages = 5;
 constexpr int kExtendImageBytes = kDim * kDim * 2;
 
-// One of the two forms of the attention: the rows of its row tiles, the key
-// tiles of its work items before each sequence's first ([batch + 1]), and the
+// One of the two forms of the attention: the rows of its row tiles, what an
+// item costs besides its key tiles (in key tiles), the units of work (cost and
+// key tiles of the items) before each sequence's first ([batch + 1]), and the
 // partial outputs of the row tiles that its CTAs' runs cut.
 struct ExtendForm {
-  int rows;
+  int rows, cost;
   long long* first;
   float* part;
 };
 constexpr int kNarrowRows = 128, kWideRows = 256;
+constexpr int kNarrowCost = 3, kWideCost = 6;
 
 // A key tile expanded for the wide form: the keys (R^T c + rho S^T signs,
 // fp16) and the values (n c, bf16, rotated) as swizzled 128 x 128 operands.
