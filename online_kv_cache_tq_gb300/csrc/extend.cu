@@ -114,36 +114,27 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(ExtendArgs a)
 }
 
 // Joins the partial outputs of a split row tile: sum_s l_s 2^{m_s - M} o_s / sum_s l_s 2^{m_s - M}.
-// Block x works if the beginning of run x + 1 is the first cut inside its
-// item.  A warp per row, four coordinates a lane; four blocks share a tile.
+// Block x joins the item that run x begins and does not end.  A warp per row,
+// four coordinates a lane.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinSplit = 4;
-__global__ void __launch_bounds__(32 * kJoinWarps) extend_join_kernel(ExtendArgs a, int ctas) {
+constexpr int kJoinSplit = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps) extend_join_kernel(ExtendArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const ExtendForm f = blockIdx.z == 0 ? a.narrow : a.wide;
-  const long long total = f.first[a.d.batch];
-  const long long per = run_length(total, ctas);
-  const long long cut = (blockIdx.x + 1) * per;
-  if (cut >= total) return;
-  int offset;
-  const Item it = find_item(a, f, cut, &offset);
-  const long long first = cut - offset + f.cost;  // unit of the item's first key tile
-  if (cut <= first || cut - per > first) return;  // no key tile before the cut, or an earlier cut among them
-  const int c0 = static_cast<int>(first / per);   // runs c0 .. c1 hold it
-  const int c1 = static_cast<int>((first + it.tiles - 1) / per);
-  const int rows = min(f.rows, it.seq.y * a.d.group - it.i * f.rows);
+  const CutItem cut = f.cuts[blockIdx.x];
+  const int c0 = blockIdx.x;
   // (the run that holds key tile 0 wrote its second slot, the others their first)
   auto part = [&](int c) { return f.part + (2ll * c + (c == c0 ? 1 : 0)) * part_floats(f.rows); };
-  for (int row = blockIdx.y * kJoinWarps + warp; row < rows; row += kJoinSplit * kJoinWarps) {
+  for (int row = blockIdx.y * kJoinWarps + warp; row < cut.rows; row += kJoinSplit * kJoinWarps) {
     const int stats = f.rows * kDim + 2 * row;
     float top = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part(c)[stats]);
+    for (int c = c0 + lane; c <= cut.last; c += 32) top = fmaxf(top, part(c)[stats]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float weight = 0.f;
 #pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
+    for (int c = c0; c <= cut.last; ++c) {
       const float* const p = part(c);
       const float2 ml = *reinterpret_cast<const float2*>(p + stats);
       const float4 o = reinterpret_cast<const float4*>(p + row * kDim)[lane];
@@ -156,7 +147,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) extend_join_kernel(ExtendArgs
       weight += w;
     }
     const float inv = weight == 0.f ? 0.f : 1.f / weight;
-    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row_vector(a, it, it.i * f.rows + row) * kDim)[lane] =
+    const long long vec = row_vector(a, cut.row0, cut.kvh, cut.i * f.rows + row);
+    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + vec * kDim)[lane] =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
   }
 }
@@ -164,7 +156,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) extend_join_kernel(ExtendArgs
 constexpr size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Layout {
-  size_t first, wide_first, expand, seq, part, wide_part, meta, tiles, total;
+  size_t first, wide_first, expand, seq, cuts, part, wide_part, meta, tiles, total;
   int tile_cap;
 };
 
@@ -183,7 +175,8 @@ Layout layout(int n_tokens, int batch, int group, int n_kv, int max_context, int
   l.wide_first = sums;
   l.expand = 2 * sums;
   l.seq = 3 * sums;
-  l.part = l.seq + align256(static_cast<size_t>(batch) * sizeof(int4));
+  l.cuts = l.seq + align256(static_cast<size_t>(batch) * sizeof(int4));
+  l.part = l.cuts + align256(2 * static_cast<size_t>(num_sms) * sizeof(CutItem));
   l.wide_part = l.part + align256(2 * static_cast<size_t>(num_sms) * part_floats(kNarrowRows) * sizeof(float));
   l.meta = l.wide_part +
            (cap > 0 ? align256(2 * static_cast<size_t>(num_sms) * part_floats(kWideRows) * sizeof(float)) : 0);
@@ -204,20 +197,23 @@ cudaError_t launch_extend(const ExtendArgs& args, void* workspace, cudaStream_t 
   const int ctas = a.d.num_sms;
   const Layout l = layout(a.n_tokens, a.d.batch, a.d.group, a.d.n_kv, a.d.max_context, ctas);
   a.narrow = ExtendForm{kNarrowRows, kNarrowCost, reinterpret_cast<long long*>(ws + l.first),
-                        reinterpret_cast<float*>(ws + l.part)};
+                        reinterpret_cast<float*>(ws + l.part), reinterpret_cast<CutItem*>(ws + l.cuts)};
   a.wide = ExtendForm{kWideRows, kWideCost, reinterpret_cast<long long*>(ws + l.wide_first),
-                      reinterpret_cast<float*>(ws + l.wide_part)};
+                      reinterpret_cast<float*>(ws + l.wide_part), reinterpret_cast<CutItem*>(ws + l.cuts) + ctas};
   a.ws_expand = reinterpret_cast<long long*>(ws + l.expand);
   a.ws_seq = reinterpret_cast<int4*>(ws + l.seq);
   a.ws_meta = reinterpret_cast<TileMeta*>(ws + l.meta);
   a.ws_tiles = reinterpret_cast<uint8_t*>(ws + l.tiles);
   a.tile_cap = l.tile_cap;
+  a.group_shift = 0;
+  while ((1 << a.group_shift) < a.d.group) ++a.group_shift;
+  a.group_mul = static_cast<uint32_t>(((1ull << (31 + a.group_shift)) + a.d.group - 1) / a.d.group);
   extend_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
   cudaError_t err = cudaGetLastError();
   if (err == cudaSuccess && a.tile_cap > 0) err = launch_extend_wide(a, ctas, stream);
   if (err == cudaSuccess) err = launch_extend_narrow(a, ctas, stream);
   if (err != cudaSuccess || ctas < 2) return err;
-  extend_join_kernel<<<dim3(ctas - 1, kJoinSplit, a.tile_cap > 0 ? 2 : 1), 32 * kJoinWarps, 0, stream>>>(a, ctas);
+  extend_join_kernel<<<dim3(ctas, kJoinSplit, a.tile_cap > 0 ? 2 : 1), 32 * kJoinWarps, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

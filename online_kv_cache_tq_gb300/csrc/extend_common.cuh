@@ -126,6 +126,25 @@ __device__ __forceinline__ void end_segment(const ExtendArgs& a, const ExtendFor
   if (r.pos < r.end) next_item(a, f, r.it);
 }
 
+// What run blockIdx.x leaves for the join: the item it begins and does not
+// end, if any (one thread, before the run is walked; `any`: the run has work).
+__device__ __forceinline__ void write_cut(const ExtendArgs& a, const ExtendForm& f, Run r, long long per, bool any) {
+  CutItem cut{0, 0, 0, 0, 0};
+  int t0, t1;
+  while (any && next_segment(a, f, r, t0, t1)) {
+    if (t0 == 0 && t1 < r.it.tiles) {
+      const long long first = r.pos - r.offset + f.cost;        // unit of its first key tile
+      cut.row0 = r.it.seq.x;
+      cut.kvh = r.it.kvh;
+      cut.i = r.it.i;
+      cut.rows = min(f.rows, r.it.seq.y * a.d.group - r.it.i * f.rows);
+      cut.last = static_cast<int>((first + r.it.tiles - 1) / per);
+    }
+    end_segment(a, f, r, t1);
+  }
+  f.cuts[blockIdx.x] = cut;
+}
+
 // Floats of a partial output: the rows' outputs, then their (reference, sum).
 __host__ __device__ constexpr int part_floats(int rows) { return rows * (kDim + 2); }
 
@@ -342,9 +361,12 @@ __device__ __forceinline__ void load_query8(const ExtendArgs& a, long long at, f
 }
 
 // Vector (token x query head) of row r of an item's sequence and KV head.
-__device__ __forceinline__ long long row_vector(const ExtendArgs& a, const Item& it, int r) {
-  const int tok = r / a.d.group;
-  return (static_cast<long long>(it.seq.x) + tok) * a.d.n_q + it.kvh * a.d.group + r - tok * a.d.group;
+__device__ __forceinline__ int row_token(const ExtendArgs& a, int r) {
+  return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(r)) * a.group_mul) >> (31 + a.group_shift));
+}
+__device__ __forceinline__ long long row_vector(const ExtendArgs& a, int row0, int kvh, int r) {
+  const int tok = row_token(a, r);
+  return (static_cast<long long>(row0) + tok) * a.d.n_q + kvh * a.d.group + r - tok * a.d.group;
 }
 
 // Brings the query rows of the run's next item to L2 while a segment that ends
@@ -358,7 +380,7 @@ __device__ __forceinline__ void prefetch_queries(const ExtendArgs& a, const Exte
   const int lines = a.q_bf16 ? 2 : 4;             // of 128 bytes
   const int rows = min(f.rows, it.seq.y * a.d.group - it.i * f.rows);
   for (int k = t; k < rows * lines; k += threads) {
-    const long long vec = row_vector(a, it, it.i * f.rows + k / lines);
+    const long long vec = row_vector(a, it.seq.x, it.kvh, it.i * f.rows + k / lines);
     const char* const p = static_cast<const char*>(a.d.q) + (vec * lines + k % lines) * 128;
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
   }

@@ -86,7 +86,10 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
   Run run;
   run.pos = blockIdx.x * per;
   run.end = run.pos + per < total ? run.pos + per : total;
-  if (run.pos >= run.end) return;                 // (the whole CTA)
+  if (run.pos >= run.end) {                       // (the whole CTA)
+    if (threadIdx.x == 0) write_cut(a, a.narrow, run, per, false);
+    return;
+  }
 
   if (tid == 0) {
     abort_s = 0;
@@ -153,8 +156,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       const int n_rows = it.seq.y * d.group;
       const int r = it.i * kTile + row;
       const bool live = r < n_rows;
-      const int tok = (live ? r : n_rows - 1) / d.group;
-      const long long vec = (static_cast<long long>(it.seq.x) + tok) * d.n_q + it.kvh * d.group + r - tok * d.group;
+      const int tok = row_token(a, live ? r : n_rows - 1);
+      const long long vec = row_vector(a, it.seq.x, it.kvh, r);
       const int seen = max(0, it.seq.z - it.seq.y + tok + 1);     // positions this row sees
       float other;
 
@@ -384,6 +387,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
     const int mine = dim < 64 ? dim >> 5 : -1;
     const LevelBytes lev = level_bytes<true>(d.tables->v_levels, VB);
     int jt = 0;
+    if (tid == kSoftThreads + kKeyThreads) write_cut(a, a.narrow, run, per, true);
     while (ok && next_segment(a, a.narrow, run, t0, t1)) {
       Cursor c;
       RawValue<VB> next;

@@ -33,31 +33,52 @@ namespace {
 
 // ---- expansion -----------------------------------------------------------------
 
-constexpr int kExpandThreads = 256;
+// Two groups of 256 threads with a tile each, around one copy of R^T and S^T.
+constexpr int kGroupThreads = 256;
+constexpr int kExpandThreads = 2 * kGroupThreads;
 constexpr int kExpandKey0 = 2 * kExtendImageBytes;
-constexpr int kExpandSmem = kExpandKey0 + 4 * kBlockBytes + 1024;     // (1024: alignment)
+constexpr int kExpandSmem = kExpandKey0 + 2 * 4 * kBlockBytes + 1024; // (1024: alignment)
+
+// Barrier of one group that also ORs a flag over it.
+__device__ __forceinline__ bool group_sync(int group, bool flag) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(flag)), "r"(group + 1), "n"(kGroupThreads)
+      : "memory");
+  return r != 0;
+}
+
+// What a group's threads share about their tile.
+struct ExpandShared {
+  float factor[kTile], norm[kTile], square[2][kTile], reach[4];
+  uint32_t valid[4];
+  uint64_t done;
+};
 
 template <int KB, int VB>
 __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(ExtendArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t done;
+  __shared__ ExpandShared group_s[2];
   __shared__ uint32_t tmem_s;
   __shared__ int abort_s;
-  __shared__ float factor_s[kTile], norm_s[kTile], square_s[2][kTile], reach_s[4];
-  __shared__ uint32_t valid_s[4];
   uint8_t* const smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   const DecodeArgs& d = a.d;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = threadIdx.x / kGroupThreads, tid = threadIdx.x % kGroupThreads;
+  const int warp = tid >> 5, lane = tid & 31;     // of the group
+  ExpandShared& sh = group_s[group];
   volatile int* const abort = &abort_s;
   const long long total = a.ws_expand[d.batch];
-  if (blockIdx.x >= total) return;                // (the whole CTA)
-  if (tid == 0) {
+  if (2ll * blockIdx.x >= total) return;          // (the whole CTA)
+  if (threadIdx.x == 0) {
     abort_s = 0;
-    ptx::mbar_init(&done, 1);
+    ptx::mbar_init(&group_s[0].done, 1);
+    ptx::mbar_init(&group_s[1].done, 1);
     ptx::fence_mbar_init();
   }
-  if (warp == 0) {
-    ptx::tmem_alloc(&tmem_s, 128);
+  if (threadIdx.x < 32) {
+    ptx::tmem_alloc(&tmem_s, 256);
     ptx::tmem_relinquish();
   }
   const bool qjl = d.k_qjl != nullptr;
@@ -65,11 +86,12 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
     const uint4* const src = a.images + 3 * (kExtendImageBytes / 16);
     uint4* const dst = reinterpret_cast<uint4*>(smem);
 #pragma unroll 8
-    for (int i = tid; i < 2 * (kExtendImageBytes / 16); i += kExpandThreads) dst[i] = __ldg(src + i);
+    for (int i = threadIdx.x; i < 2 * (kExtendImageBytes / 16); i += kExpandThreads) dst[i] = __ldg(src + i);
   }
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = tmem_s;
+  const uint32_t tmem = tmem_s + 128 * group;
+  uint8_t* const keys_s = smem + kExpandKey0 + group * 4 * kBlockBytes;
   const int row = tid & (kTile - 1), half = tid / kTile;   // key row or value coordinate; half of the other side
   const LevelBytes key_levels = level_bytes<false>(d.tables->k_levels, KB);
   const LevelBytes value_levels = level_bytes<false>(d.tables->v_levels, VB);
@@ -97,16 +119,17 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
     load_key(d, it, kc, expanded_bit(lane), half, next_key);
     load_value(d, it, vc, row, mine, expanded_bit(lane), next_value);
   };
-  load_tile(blockIdx.x);
+  const long long g0 = 2ll * blockIdx.x + group, step = 2ll * gridDim.x;
+  if (g0 < total) load_tile(g0);
   uint32_t phase = 0;
-  for (long long g = blockIdx.x; g < total; g += gridDim.x, phase ^= 1) {
+  for (long long g = g0; g < total; g += step, phase ^= 1) {
     uint8_t* const out = a.ws_tiles + g * kTileImageBytes;
     TileMeta* const meta = a.ws_meta + g;
     const RawKey<KB> k = next_key;
     const RawValue<VB> v = next_value;
-    if (g + gridDim.x < total) load_tile(g + gridDim.x);
+    if (g + step < total) load_tile(g + step);
     {
-      const RowChunks at = row_chunks(ptx::smem_u32(smem + kExpandKey0) + half * kBlockBytes, row);
+      const RowChunks at = row_chunks(ptx::smem_u32(keys_s) + half * kBlockBytes, row);
       uint32_t w0[KB], w1[KB];
 #pragma unroll
       for (int p = 0; p < KB; ++p) w0[p] = k.planes[p].x, w1[p] = k.planes[p].y;
@@ -121,22 +144,22 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
     }
     if (half == 0) {
       const unsigned bit = __reduce_or_sync(0xffffffffu, k.valid ? 1u << expanded_bit(lane) : 0u);
-      factor_s[row] = k.valid ? k.norm * to_log2 : 0.f;
-      if (lane == 0) valid_s[warp] = bit;
+      sh.factor[row] = k.valid ? k.norm * to_log2 : 0.f;
+      if (lane == 0) sh.valid[warp] = bit;
     }
-    if (mine >= 0) norm_s[64 * half + row] = v.norm;
+    if (mine >= 0) sh.norm[64 * half + row] = v.norm;
     ptx::fence_async_shared();
-    __syncthreads();
+    group_sync(group, false);
     if (warp == 0 && ptx::elect_one()) {
       ptx::tc_fence_after();
-      const uint64_t keys = ptx::desc_k_sw128(ptx::smem_u32(smem + kExpandKey0));
+      const uint64_t keys = ptx::desc_k_sw128(ptx::smem_u32(keys_s));
       const uint64_t turn = ptx::desc_k_sw128(ptx::smem_u32(smem));
 #pragma unroll
       for (int ks = 0; ks < 16; ++ks) {
         const uint64_t off = (ks >> 2) * (kBlockBytes / 16) + (ks & 3) * 2;
         if (ks < 8 || qjl) ptx::mma_bf16(tmem, keys + off, turn + off, kIdescF16, ks > 0);
       }
-      ptx::mma_commit(&done);
+      ptx::mma_commit(&sh.done);
     }
     __syncwarp();
     // the values, under the product
@@ -157,15 +180,15 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&l[e]));
-          const float2 n = *reinterpret_cast<const float2*>(&norm_s[64 * half + 32 * w + 8 * i + 2 * e]);
+          const float2 n = *reinterpret_cast<const float2*>(&sh.norm[64 * half + 32 * w + 8 * i + 2 * e]);
           o[e] = pack_bf16(f.x * n.x, f.y * n.y);
         }
         *reinterpret_cast<uint4*>(out + kExtendImageBytes + half * kBlockBytes + row * 128 +
                                   (((4 * w + i) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
-    const bool ok = TQ_WAIT(done, phase);
-    if (__syncthreads_or(!ok)) break;
+    const bool ok = TQ_WAIT(sh.done, phase);
+    if (group_sync(group, !ok)) break;
     ptx::tc_fence_after();
     {
       const int r = (warp & 3) * 32 + lane, h = warp >> 2;   // tensor-memory lane, columns 64 h .. + 63
@@ -184,31 +207,31 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
         *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
       }
-      square_s[h][r] = square;
+      sh.square[h][r] = square;
     }
     ptx::tc_fence_before();
-    __syncthreads();
+    group_sync(group, false);
     if (tid < kTile) {
-      const float f = factor_s[tid];
+      const float f = sh.factor[tid];
       meta->key_factor[tid] = f;
-      const float reach = fabsf(f) * sqrtf(square_s[0][tid] + square_s[1][tid]);
+      const float reach = fabsf(f) * sqrtf(sh.square[0][tid] + sh.square[1][tid]);
       const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(reach) & 0x7fffffffu);   // (not negative)
       if (lane == 0) {
-        reach_s[warp] = __uint_as_float(bits);
-        meta->valid[warp] = valid_s[warp];
+        sh.reach[warp] = __uint_as_float(bits);
+        meta->valid[warp] = sh.valid[warp];
       }
     }
-    __syncthreads();
+    group_sync(group, false);
     if (tid == 0) {
       // (a NaN has the largest bits, and takes the path that looks at every score)
       unsigned bits = 0;
-      for (int w = 0; w < 4; ++w) bits = max(bits, __float_as_uint(reach_s[w]));
+      for (int w = 0; w < 4; ++w) bits = max(bits, __float_as_uint(sh.reach[w]));
       meta->reach = __uint_as_float(bits);
     }
-    __syncthreads();                              // (the next tile overwrites what was read)
+    group_sync(group, false);                     // (the next tile overwrites what was read)
   }
   __syncthreads();
-  if (warp == 0) ptx::tmem_dealloc(tmem, 128);
+  if (threadIdx.x < 32) ptx::tmem_dealloc(tmem_s, 256);
 }
 
 // ---- attention -------------------------------------------------------------------
@@ -253,7 +276,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
   Run run;
   run.pos = blockIdx.x * per;
   run.end = run.pos + per < total ? run.pos + per : total;
-  if (run.pos >= run.end) return;                 // (the whole CTA)
+  if (run.pos >= run.end) {                       // (the whole CTA)
+    if (threadIdx.x == 0) write_cut(a, a.wide, run, per, false);
+    return;
+  }
 
   if (tid == 0) {
     abort_s = 0;
@@ -325,7 +351,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
       const int n_rows = it.seq.y * d.group;
       const int r = it.i * kWideRows + kTile * x + row;
       const bool live = r < n_rows;
-      const int tok = (live ? r : n_rows - 1) / d.group;
+      const int tok = row_token(a, live ? r : n_rows - 1);
       const int seen = max(0, it.seq.z - it.seq.y + tok + 1);     // positions this row sees
       float other;
       // The queries, sixteen lanes to a row (whole lines, and a row's largest
@@ -338,7 +364,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         for (int k = 0; k < 4; ++k) {
           const int rr = it.i * kWideRows + kTile * x + copy_row + 2 * (k0 + k);
           if (rr < n_rows) {
-            load_query8(a, row_vector(a, it, rr) * kDim + copy_chunk * 8, v[k]);
+            load_query8(a, row_vector(a, it.seq.x, it.kvh, rr) * kDim + copy_chunk * 8, v[k]);
           } else {
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[k][q] = 0.f;
@@ -459,7 +485,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         for (int k = 0; k < 8; ++k) {
           const int qr = copy_row + 2 * k, rr = it.i * kWideRows + kTile * x + qr;
           if (rr < n_rows)
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row_vector(a, it, rr) * kDim + copy_chunk * 8) =
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row_vector(a, it.seq.x, it.kvh, rr) * kDim + copy_chunk * 8) =
                 *reinterpret_cast<const uint4*>(copy_base + qr * 128 + (((copy_chunk & 7) ^ (qr & 7)) << 4));
         }
       }
@@ -547,6 +573,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
     // ---------------- copies ----------------
     // the whole warp walks the segments and waits; lane 0 copies
     int kc = 0, jt = 0;
+    if (lane == 1) write_cut(a, a.wide, run, per, true);
     while (ok && next_segment(a, a.wide, run, t0, t1)) {
       const long long first = it.seq.w + static_cast<long long>(it.kvh) * max(1, (it.seq.z + kTile - 1) / kTile);
       for (int t = t0; t < t1; ++t, ++jt, ++kc) {

@@ -268,10 +268,14 @@ constexpr int kExtendImageBytes = kDim * kDim * 2;
 // item costs besides its key tiles (in key tiles), the units of work (cost and
 // key tiles of the items) before each sequence's first ([batch + 1]), and the
 // partial outputs of the row tiles that its CTAs' runs cut.
+struct CutItem {              // a row tile that the runs from `run` to `last` share
+  int row0, kvh, i, rows, last;   // first row of the sequence, KV head, row tile, rows (0: none)
+};
 struct ExtendForm {
   int rows, cost;
   long long* first;
   float* part;
+  CutItem* cuts;              // [ctas]: what run c begins and does not end
 };
 constexpr int kNarrowRows = 128, kWideRows = 256;
 constexpr int kNarrowCost = 3, kWideCost = 6;
@@ -293,6 +297,8 @@ struct ExtendArgs {
   void* out;                  // bf16 [n_tokens][n_q][128]
   bool q_bf16;
   const uint4* images;
+  uint32_t group_mul;         // row / group = row * group_mul >> 31 + group_shift (31-bit rows)
+  int group_shift;
   // workspace regions
   int4* ws_seq;               // [batch]: first row, new tokens, context (checked), first expanded tile or -1
   ExtendForm narrow, wide;
