@@ -50,6 +50,15 @@ __device__ __forceinline__ bool group_sync(int group, bool flag) {
   return r != 0;
 }
 
+// Bulk copy shared -> global, and the wait until its reads are done.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+               ::"l"(reinterpret_cast<uint64_t>(dst)), "r"(ptx::smem_u32(src)), "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
 // What a group's threads share about their tile.
 struct ExpandShared {
   float factor[kTile], norm[kTile], square[2][kTile], reach[4];
@@ -162,7 +171,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
       ptx::mma_commit(&sh.done);
     }
     __syncwarp();
-    // the values, under the product
+    const bool ok = TQ_WAIT(sh.done, phase);
+    if (group_sync(group, !ok)) break;
+    // the product has read its operand: the tile's image takes its place
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       uint32_t planes[VB];
@@ -183,12 +194,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
           const float2 n = *reinterpret_cast<const float2*>(&sh.norm[64 * half + 32 * w + 8 * i + 2 * e]);
           o[e] = pack_bf16(f.x * n.x, f.y * n.y);
         }
-        *reinterpret_cast<uint4*>(out + kExtendImageBytes + half * kBlockBytes + row * 128 +
+        *reinterpret_cast<uint4*>(keys_s + kExtendImageBytes + half * kBlockBytes + row * 128 +
                                   (((4 * w + i) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
-    const bool ok = TQ_WAIT(sh.done, phase);
-    if (group_sync(group, !ok)) break;
     ptx::tc_fence_after();
     {
       const int r = (warp & 3) * 32 + lane, h = warp >> 2;   // tensor-memory lane, columns 64 h .. + 63
@@ -203,14 +212,16 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
           square = fmaf(f0, f0, fmaf(f1, f1, square));
           w[e] = pack_f16(f0, f1);
         }
-        uint8_t* const dst = out + h * kBlockBytes + r * 128;
+        uint8_t* const dst = keys_s + h * kBlockBytes + r * 128;
         *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
       }
       sh.square[h][r] = square;
     }
     ptx::tc_fence_before();
+    ptx::fence_async_shared();
     group_sync(group, false);
+    if (tid == 0) bulk_store(out, keys_s, kTileImageBytes);     // (in whole lines)
     if (tid < kTile) {
       const float f = sh.factor[tid];
       meta->key_factor[tid] = f;
@@ -228,6 +239,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
       for (int w = 0; w < 4; ++w) bits = max(bits, __float_as_uint(sh.reach[w]));
       meta->reach = __uint_as_float(bits);
     }
+    if (tid == 0) bulk_store_wait();
     group_sync(group, false);                     // (the next tile overwrites what was read)
   }
   __syncthreads();

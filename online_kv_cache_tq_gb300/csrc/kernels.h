@@ -239,7 +239,7 @@ struct NormRopeArgs {
   const int32_t* positions;   // [n_tokens]; negative: the token is left alone
   const double* inv_freq;     // [rot_dim / 2], radians per position
   int rot_dim, interleaved;
-  int group_tokens;           // set by the launcher
+  int token_runs, run_heads;  // set by the launcher: runs of heads that a token is cut into
 };
 cudaError_t launch_norm_rope(const NormRopeArgs& args, bool bf16, int num_sms, cudaStream_t stream);
 

@@ -8,16 +8,16 @@
 // arithmetic is a few operations per element.  Sixteen lanes share a vector; a
 // lane takes two groups of four coordinates, placed so that the partners of a
 // rotation are in one lane (coordinates 4 l .. and rot / 2 + 4 l .. , or eight
-// neighbours), and the norm is four shuffles.  Each sixteen lanes keep to one
-// token, whose cosines and sines then stay in registers for all its heads, and
-// have four vectors in flight.
+// neighbours), and the norm is four shuffles.  Sixteen lanes take a run of one
+// token's heads: each lane forms the four cosines and sines of its pairs once
+// and keeps them in registers, and there is no barrier between runs.  A lane
+// has 64 bytes in flight.
 //
 // Angles: position * inv_freq loses its fraction of a turn in 32 bits at far
 // positions.  inv_freq / (2 pi) is kept as a 64-bit fixed-point fraction of a
 // turn, so the product with the position is exact modulo one turn (an integer
 // multiplication that wraps), and what is rounded is an angle within an eighth
-// of a turn of a quarter-turn multiple.  The fractions are formed once per
-// CTA, cosines and sines once per token and CTA: all heads share them.
+// of a turn of a quarter-turn multiple.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -26,9 +26,9 @@ namespace tq {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeVecs = kRopeThreads / 16;      // vectors side by side in a CTA
-constexpr int kRopeTokens = 4;                    // most tokens a CTA takes at a time
-constexpr int kRopeUnroll = 4;                    // vectors a lane has in flight
+constexpr int kRopeVecs = kRopeThreads / 16;      // runs side by side in a CTA
+template <typename T>
+constexpr int kRopeUnroll = sizeof(T) == 2 ? 4 : 2;   // vectors a lane has in flight
 
 // Four coordinates, as loaded (streamed: nothing is read twice) and as floats.
 template <typename T>
@@ -73,40 +73,31 @@ __device__ __forceinline__ float2 cos_sin(unsigned long long turns) {
   return quarter & 2 ? make_float2(-c, -s) : make_float2(c, s);
 }
 
-// What a lane keeps for its token: where its coordinates are, its pairs'
-// cosines and sines, whether they turn.
-struct LaneTurn {
-  int a, b;                  // coordinates a .. a + 3 and b .. b + 3
-  float2 cs[4];
-  bool turned, interleaved;
-};
-
-// The heads first, first + step, .. of one token's tensor (x, out: this token's
-// rows; live: whether the token is there).  The loop is the same for every lane.
-template <typename T>
-__device__ __forceinline__ void turn_heads(const T* x, T* out, int heads, int first, int step, bool live, const T* weight,
-                                           float eps, const LaneTurn& l) {
-  float wa[4], wb[4];
+// Heads h0 .. h1 - 1 of one tensor of a token (x, out: its rows), coordinates
+// ca .. ca + 3 and cb .. cb + 3 of each; cs: the lane's four pairs.
+template <typename T, bool INTERLEAVED>
+__device__ __forceinline__ void turn_heads(const T* x, T* out, int h0, int h1, const T* weight, float eps, int ca, int cb,
+                                           bool turned, const float2 (&cs)[4]) {
+  if (h0 >= h1) return;
+  float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
   if (weight != nullptr) {
     Four<T> w;
-    w.load(weight + l.a);
+    w.load(weight + ca);
     w.get(wa);
-    w.load(weight + l.b);
+    w.load(weight + cb);
     w.get(wb);
   }
-  for (int h0 = first - first % step; h0 < heads; h0 += step * kRopeUnroll) {
-    Four<T> xa[kRopeUnroll], xb[kRopeUnroll];
+  const unsigned lanes = 0xffffu << (threadIdx.x & 16);
+  for (int h = h0; h < h1; h += kRopeUnroll<T>) {
+    Four<T> xa[kRopeUnroll<T>], xb[kRopeUnroll<T>];
 #pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      const int h = h0 + first % step + u * step;
-      if (live && h < heads) {
-        xa[u].load(x + h * kDim + l.a);
-        xb[u].load(x + h * kDim + l.b);
-      }
+    for (int u = 0; u < kRopeUnroll<T>; ++u) {
+      const T* const p = x + min(h + u, h1 - 1) * kDim;   // (the last one again where there are no more)
+      xa[u].load(p + ca);
+      xb[u].load(p + cb);
     }
 #pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      const int h = h0 + first % step + u * step;
+    for (int u = 0; u < kRopeUnroll<T>; ++u) {
       float a[4], b[4];
       xa[u].get(a);
       xb[u].get(b);
@@ -115,7 +106,7 @@ __device__ __forceinline__ void turn_heads(const T* x, T* out, int heads, int fi
 #pragma unroll
         for (int i = 0; i < 4; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
 #pragma unroll
-        for (int d = 1; d < 16; d <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+        for (int d = 1; d < 16; d <<= 1) ss += __shfl_xor_sync(lanes, ss, d);
         const float r = 1.0f / sqrtf(ss * (1.0f / kDim) + eps);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -123,89 +114,96 @@ __device__ __forceinline__ void turn_heads(const T* x, T* out, int heads, int fi
           b[i] *= r * wb[i];
         }
       }
-      if (l.turned) {
-        if (l.interleaved) {
+      if (turned) {
+        if (INTERLEAVED) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float p = a[2 * i], q = a[2 * i + 1], s = b[2 * i], t = b[2 * i + 1];
-            a[2 * i] = p * l.cs[i].x - q * l.cs[i].y;
-            a[2 * i + 1] = q * l.cs[i].x + p * l.cs[i].y;
-            b[2 * i] = s * l.cs[i + 2].x - t * l.cs[i + 2].y;
-            b[2 * i + 1] = t * l.cs[i + 2].x + s * l.cs[i + 2].y;
+            a[2 * i] = p * cs[i].x - q * cs[i].y;
+            a[2 * i + 1] = q * cs[i].x + p * cs[i].y;
+            b[2 * i] = s * cs[i + 2].x - t * cs[i + 2].y;
+            b[2 * i + 1] = t * cs[i + 2].x + s * cs[i + 2].y;
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float p = a[i], q = b[i];
-            a[i] = p * l.cs[i].x - q * l.cs[i].y;
-            b[i] = q * l.cs[i].x + p * l.cs[i].y;
+            a[i] = p * cs[i].x - q * cs[i].y;
+            b[i] = q * cs[i].x + p * cs[i].y;
           }
         }
       }
-      if (live && h < heads) {
-        Four<T>::store(out + h * kDim + l.a, a);
-        Four<T>::store(out + h * kDim + l.b, b);
+      if (h + u < h1) {
+        T* const p = out + (h + u) * kDim;
+        Four<T>::store(p + ca, a);
+        Four<T>::store(p + cb, b);
       }
     }
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(NormRopeArgs a) {
+template <typename T, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(NormRopeArgs a) {
   __shared__ unsigned long long freq_s[kDim / 2];
-  __shared__ float2 turn_s[kRopeTokens][kDim / 2];
-  const int tid = threadIdx.x, l16 = tid & 15, vec = tid >> 4;
-  const int half = a.rot_dim / 2, tokens = a.group_tokens;
+  const int tid = threadIdx.x, l16 = tid & 15;
+  const int half = a.rot_dim / 2;
   if (tid < half) {
     double f = a.inv_freq[tid] * 0.15915494309189533577;        // turns per position
     f -= floor(f);
     freq_s[tid] = __double2ull_rn(f * 0x1p63) << 1;             // (f < 1: 63 bits hold it)
   }
-  LaneTurn l;
-  l.turned = 8 * l16 < a.rot_dim;
-  l.interleaved = a.interleaved;
-  l.a = l.turned && !a.interleaved ? 4 * l16 : 8 * l16;
-  l.b = l.turned && !a.interleaved ? half + 4 * l16 : 8 * l16 + 4;
-  const int t = vec % tokens, first = vec / tokens, step = kRopeVecs / tokens;   // its token, its heads
-  const T* const q = static_cast<const T*>(a.q);
-  const T* const k = static_cast<const T*>(a.k);
-  T* const q_out = static_cast<T*>(a.q_out);
-  T* const k_out = static_cast<T*>(a.k_out);
-  const int n_groups = a.n_tokens / tokens + (a.n_tokens % tokens != 0);
-  for (int group = blockIdx.x; group < n_groups; group += gridDim.x) {
-    const int t0 = group * tokens;
-    if (half > 0) {
-      __syncthreads();                            // freq_s written; the previous tokens' angles read
-      for (int i = tid; i < tokens * half; i += kRopeThreads) {
-        const int u = i / half, j = i - u * half;
-        if (t0 + u < a.n_tokens)
-          turn_s[u][j] = cos_sin(freq_s[j] * static_cast<unsigned long long>(static_cast<long long>(a.positions[t0 + u])));
-      }
-      __syncthreads();
-    }
-    const bool live = t0 + t < a.n_tokens && (a.positions == nullptr || a.positions[t0 + t] >= 0);
-    if (l.turned)
+  __syncthreads();
+  const bool turned = 8 * l16 < a.rot_dim;
+  const int ca = turned && !INTERLEAVED ? 4 * l16 : 8 * l16;
+  const int cb = turned && !INTERLEAVED ? half + 4 * l16 : 8 * l16 + 4;
+  const int heads = a.n_q + a.n_kv;
+  const long long n_runs = static_cast<long long>(a.n_tokens) * a.token_runs;
+  for (long long run = static_cast<long long>(blockIdx.x) * kRopeVecs + (tid >> 4); run < n_runs;
+       run += static_cast<long long>(gridDim.x) * kRopeVecs) {
+    const long long token = run / a.token_runs;
+    const int h0 = static_cast<int>(run - token * a.token_runs) * a.run_heads, h1 = min(h0 + a.run_heads, heads);
+    float2 cs[4] = {};
+    if (a.positions != nullptr) {
+      const long long pos = a.positions[token];
+      if (pos < 0) continue;                      // (all sixteen lanes)
+      if (turned)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) l.cs[i] = turn_s[t][4 * l16 + i];
-    const long long row = live ? t0 + t : 0;
-    turn_heads(q + row * a.q_stride, q_out + row * a.q_out_stride, a.n_q, first, step, live,
-               static_cast<const T*>(a.q_weight), a.eps, l);
-    turn_heads(k + row * a.k_stride, k_out + row * a.k_out_stride, a.n_kv, first, step, live,
-               static_cast<const T*>(a.k_weight), a.eps, l);
+        for (int i = 0; i < 4; ++i) cs[i] = cos_sin(freq_s[4 * l16 + i] * static_cast<unsigned long long>(pos));
+    }
+    turn_heads<T, INTERLEAVED>(static_cast<const T*>(a.q) + token * a.q_stride,
+                               static_cast<T*>(a.q_out) + token * a.q_out_stride, h0, min(h1, a.n_q),
+                               static_cast<const T*>(a.q_weight), a.eps, ca, cb, turned, cs);
+    turn_heads<T, INTERLEAVED>(static_cast<const T*>(a.k) + token * a.k_stride,
+                               static_cast<T*>(a.k_out) + token * a.k_out_stride, max(h0 - a.n_q, 0), h1 - a.n_q,
+                               static_cast<const T*>(a.k_weight), a.eps, ca, cb, turned, cs);
   }
+}
+
+template <typename T>
+void launch_type(const NormRopeArgs& a, int grid, cudaStream_t stream) {
+  if (a.interleaved) norm_rope_kernel<T, true><<<grid, kRopeThreads, 0, stream>>>(a);
+  else norm_rope_kernel<T, false><<<grid, kRopeThreads, 0, stream>>>(a);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRopeArgs& args, bool bf16, int num_sms, cudaStream_t stream) {
-  // few tokens: one per CTA, so that a decode step's heads spread over the SMs;
-  // otherwise four, whose angles are one per thread
+  // A run is a whole token where there are tokens for every sixteen lanes of
+  // the GPU; else a token's heads are cut into runs of at least as many as a
+  // lane has in flight, so that a decode step spreads over the SMs.
   NormRopeArgs a = args;
-  a.group_tokens = a.n_tokens <= 8 * num_sms ? 1 : kRopeTokens;
-  const int n_groups = a.n_tokens / a.group_tokens + (a.n_tokens % a.group_tokens != 0);
-  const int grid = n_groups < num_sms * 8 ? n_groups : num_sms * 8;   // 8 CTAs of 256 threads fill an SM
-  if (bf16) norm_rope_kernel<__nv_bfloat16><<<grid, kRopeThreads, 0, stream>>>(a);
-  else norm_rope_kernel<float><<<grid, kRopeThreads, 0, stream>>>(a);
+  const int heads = a.n_q + a.n_kv;
+  const long long slots = 4ll * num_sms * kRopeVecs;
+  const int least = bf16 ? kRopeUnroll<__nv_bfloat16> : kRopeUnroll<float>;
+  long long runs = a.n_tokens >= slots ? 1 : slots / a.n_tokens;
+  const long long most = (heads + least - 1) / least;
+  if (runs > most) runs = most;
+  a.run_heads = static_cast<int>((heads + runs - 1) / runs + least - 1) / least * least;
+  a.token_runs = (heads + a.run_heads - 1) / a.run_heads;
+  const long long ctas = (static_cast<long long>(a.n_tokens) * a.token_runs + kRopeVecs - 1) / kRopeVecs;
+  const int grid = static_cast<int>(ctas < 4ll * num_sms ? ctas : 4ll * num_sms);
+  if (bf16) launch_type<__nv_bfloat16>(a, grid, stream);
+  else launch_type<float>(a, grid, stream);
   return cudaGetLastError();
 }
 
