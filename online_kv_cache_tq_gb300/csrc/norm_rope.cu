@@ -58,19 +58,20 @@ struct Four<float> {
   }
 };
 
-// cos and sin of turns / 2^64 turns.
-__device__ __forceinline__ float2 cos_sin(unsigned long long turns) {
-  const unsigned long long shifted = turns + (1ull << 61);      // nearest quarter turn
-  const int quarter = static_cast<int>(shifted >> 62);
-  const long long rest = static_cast<long long>(shifted & ((1ull << 62) - 1)) - (1ll << 61);
-  float s, c;
-  sincospif(static_cast<float>(rest) * 0x1p-63f, &s, &c);       // half turns, |.| <= 1/4
-  if (quarter & 1) {
-    const float t = c;
-    c = -s;
-    s = t;
-  }
-  return quarter & 2 ? make_float2(-c, -s) : make_float2(c, s);
+// cos and sin of position * freq / 2^64 turns.  The top 32 bits of the product
+// (modulo a turn) are a quarter turn's number and an angle within an eighth
+// of a turn of it, for which the Taylor series to the 9th and 10th power
+// leave less than 2e-9.
+__device__ __forceinline__ float2 cos_sin(unsigned long long freq, unsigned pos) {
+  const unsigned turn = static_cast<unsigned>(freq >> 32) * pos + __umulhi(static_cast<unsigned>(freq), pos);
+  const unsigned shifted = turn + (1u << 29);                   // nearest quarter turn
+  const int rest = static_cast<int>(shifted & 0x3fffffffu) - (1 << 29);
+  const float x = static_cast<float>(rest) * 1.46291807926715968e-9f;   // 2 pi / 2^32
+  const float z = x * x;
+  const float s = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
+  const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+  const float cc = shifted & (1u << 30) ? -s : c, ss = shifted & (1u << 30) ? c : s;
+  return shifted & (1u << 31) ? make_float2(-cc, -ss) : make_float2(cc, ss);
 }
 
 // Heads h0 .. h1 - 1 of one tensor of a token (x, out: its rows), coordinates
@@ -157,18 +158,22 @@ __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(NormRopeArgs
   const int ca = turned && !INTERLEAVED ? 4 * l16 : 8 * l16;
   const int cb = turned && !INTERLEAVED ? half + 4 * l16 : 8 * l16 + 4;
   const int heads = a.n_q + a.n_kv;
-  const long long n_runs = static_cast<long long>(a.n_tokens) * a.token_runs;
-  for (long long run = static_cast<long long>(blockIdx.x) * kRopeVecs + (tid >> 4); run < n_runs;
-       run += static_cast<long long>(gridDim.x) * kRopeVecs) {
-    const long long token = run / a.token_runs;
-    const int h0 = static_cast<int>(run - token * a.token_runs) * a.run_heads, h1 = min(h0 + a.run_heads, heads);
+  // The halves of a warp take the same heads of neighbouring tokens, so that
+  // they stay together.
+  const int warps = kRopeThreads / 32;
+  const long long n_runs = (static_cast<long long>(a.n_tokens) + 1) / 2 * a.token_runs;
+  for (long long run = static_cast<long long>(blockIdx.x) * warps + (tid >> 5); run < n_runs;
+       run += static_cast<long long>(gridDim.x) * warps) {
+    const long long token_pair = run / a.token_runs, token = 2 * token_pair + ((tid >> 4) & 1);
+    const int h0 = static_cast<int>(run - token_pair * a.token_runs) * a.run_heads, h1 = min(h0 + a.run_heads, heads);
+    if (token >= a.n_tokens) continue;            // (all sixteen lanes, here and below)
     float2 cs[4] = {};
     if (a.positions != nullptr) {
-      const long long pos = a.positions[token];
-      if (pos < 0) continue;                      // (all sixteen lanes)
+      const int pos = a.positions[token];
+      if (pos < 0) continue;
       if (turned)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cs[i] = cos_sin(freq_s[4 * l16 + i] * static_cast<unsigned long long>(pos));
+        for (int i = 0; i < 4; ++i) cs[i] = cos_sin(freq_s[4 * l16 + i], static_cast<unsigned>(pos));
     }
     turn_heads<T, INTERLEAVED>(static_cast<const T*>(a.q) + token * a.q_stride,
                                static_cast<T*>(a.q_out) + token * a.q_out_stride, h0, min(h1, a.n_q),
@@ -188,19 +193,23 @@ void launch_type(const NormRopeArgs& a, int grid, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRopeArgs& args, bool bf16, int num_sms, cudaStream_t stream) {
-  // A run is a whole token where there are tokens for every sixteen lanes of
-  // the GPU; else a token's heads are cut into runs of at least as many as a
-  // lane has in flight, so that a decode step spreads over the SMs.
+  // A token's heads are cut into runs so that the last round of runs over the
+  // GPU's sixteen-lane slots weighs little: six rounds where runs of eight
+  // heads allow it (32768 tokens of 72 heads: runs of 36 take 212 us, of 72
+  // 220 us, of 8 227 us; 5001 tokens of 40 fp32 heads: runs of 8 take 44 us, of
+  // 40 47 us); fewer heads than eight only where that leaves slots empty, down
+  // to what a lane has in flight (a decode step).
   NormRopeArgs a = args;
   const int heads = a.n_q + a.n_kv;
   const long long slots = 4ll * num_sms * kRopeVecs;
   const int least = bf16 ? kRopeUnroll<__nv_bfloat16> : kRopeUnroll<float>;
-  long long runs = a.n_tokens >= slots ? 1 : slots / a.n_tokens;
-  const long long most = (heads + least - 1) / least;
-  if (runs > most) runs = most;
+  const long long eights = (heads + 7) / 8, most = (heads + least - 1) / least;
+  long long runs = (6 * slots + a.n_tokens - 1) / a.n_tokens;
+  if (runs > eights) runs = a.n_tokens * eights >= slots ? eights : most;
   a.run_heads = static_cast<int>((heads + runs - 1) / runs + least - 1) / least * least;
   a.token_runs = (heads + a.run_heads - 1) / a.run_heads;
-  const long long ctas = (static_cast<long long>(a.n_tokens) * a.token_runs + kRopeVecs - 1) / kRopeVecs;
+  const int warps = kRopeThreads / 32;
+  const long long ctas = ((static_cast<long long>(a.n_tokens) + 1) / 2 * a.token_runs + warps - 1) / warps;
   const int grid = static_cast<int>(ctas < 4ll * num_sms ? ctas : 4ll * num_sms);
   if (bf16) launch_type<__nv_bfloat16>(a, grid, stream);
   else launch_type<float>(a, grid, stream);
