@@ -151,12 +151,19 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+_RAW_STREAM = None
+
+
 def _book_stream(book, stream):
-    """As _stream, the default being the current stream of the handle's device."""
-    if stream is None and book.device >= 0:
+    """As _stream, the default being the current stream of the handle's device
+    (its raw handle: no stream object is made, a call costs its launch)."""
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    global _RAW_STREAM
+    if _RAW_STREAM is None:
         import torch
-        return torch.cuda.current_stream(book.device).cuda_stream if torch.cuda.is_available() else None
-    return _stream(stream)
+        _RAW_STREAM = torch._C._cuda_getCurrentRawStream if torch.cuda.is_available() else lambda device: None
+    return _RAW_STREAM(book.device) if book.device >= 0 else None
 
 
 class Codebook:

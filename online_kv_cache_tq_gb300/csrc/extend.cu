@@ -18,49 +18,75 @@ constexpr int kWideFrom = 512;
 constexpr long long kTileCap = 1 << 15;
 
 // One CTA checks the lengths, chooses the forms and forms the prefix sums of
-// units of work and expanded tiles, a warp per sequence.
+// units of work and expanded tiles: a thread per sequence for what is read and
+// written, a warp per sequence for the sums over its row tiles.
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanWarps = kPlanThreads / 32;
 
-// Inclusive sum over the CTA's threads.
-__device__ __forceinline__ long long plan_scan(long long v, long long* warp_s) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+struct Sums {
+  long long narrow, wide, expand;
+};
+__device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) {
+  return Sums{a.narrow + b.narrow, a.wide + b.wide, a.expand + b.expand};
+}
+__device__ __forceinline__ Sums shfl_up(const Sums& v, int d) {
+  return Sums{__shfl_up_sync(0xffffffffu, v.narrow, d), __shfl_up_sync(0xffffffffu, v.wide, d),
+              __shfl_up_sync(0xffffffffu, v.expand, d)};
+}
+
+// Inclusive sums over the CTA's threads; *total: over all of them.
+__device__ __forceinline__ Sums plan_scan(Sums v, Sums* warp_s, Sums* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x / 32;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += o;
+    const Sums o = shfl_up(v, d);
+    if (lane >= d) v = v + o;
   }
   if (lane == 31) warp_s[warp] = v;
   __syncthreads();
-  for (int w = 0; w < warp; ++w) v += warp_s[w];
+  Sums w = lane < warps ? warp_s[lane] : Sums{0, 0, 0};
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const Sums o = shfl_up(w, d);
+    if (lane >= d) w = w + o;
+  }
+  *total = Sums{__shfl_sync(0xffffffffu, w.narrow, 31), __shfl_sync(0xffffffffu, w.wide, 31),
+                __shfl_sync(0xffffffffu, w.expand, 31)};
+  const Sums before{__shfl_sync(0xffffffffu, w.narrow, warp - 1), __shfl_sync(0xffffffffu, w.wide, warp - 1),
+                    __shfl_sync(0xffffffffu, w.expand, warp - 1)};
   __syncthreads();
-  return v;
+  return warp > 0 ? v + before : v;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(ExtendArgs a) {
   __shared__ long long narrow_s[kPlanThreads], wide_s[kPlanThreads];
-  __shared__ int4 seq_s[kPlanThreads];
-  __shared__ long long warp_s[kPlanWarps];
-  __shared__ long long last_s[3];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ int2 seq_s[kPlanThreads];
+  __shared__ Sums warp_s[32];
+  launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
   const int group = a.d.group;
-  long long base_n = 0, base_w = 0, base_e = 0, asked = 0;
-  for (int b0 = 0; b0 < a.d.batch; b0 += kPlanThreads) {
-    const int nb = min(kPlanThreads, a.d.batch - b0);
-    for (int k = warp; k < nb; k += kPlanWarps) {
-      const int b = b0 + k;
-      int s0 = a.query_start[b], s1 = a.query_start[b + 1], ctx = a.d.context_lens[b];
+  Sums base{0, 0, 0};
+  long long asked = 0;                            // expanded tiles of the sequences that could be wide
+  for (int b0 = 0; b0 < a.d.batch; b0 += threads) {
+    const int nb = min(threads, a.d.batch - b0), b = b0 + tid;
+    const bool here = tid < nb;
+    int4 seq = make_int4(0, 0, 0, 0);
+    if (here) {
+      const int s0 = a.query_start[b], s1 = a.query_start[b + 1], ctx = a.d.context_lens[b];
       const bool rows_ok = s0 >= 0 && s0 <= s1 && s1 <= a.n_tokens;
       const bool ctx_ok = ctx >= 0 && ctx <= a.d.max_context &&
                           ctx <= static_cast<long long>(a.d.max_blocks) * a.d.block_size;
-      if (lane == 0 && (!rows_ok || !ctx_ok)) atomicCAS(a.d.error, 0, kErrContext);
-      if (!rows_ok) s0 = s1 = 0;
-      if (!ctx_ok) ctx = 0;
-      const int n = s1 - s0;
-      const bool eligible = a.tile_cap > 0 && static_cast<long long>(n) * group >= kWideFrom;
+      if (!rows_ok || !ctx_ok) atomicCAS(a.d.error, 0, kErrContext);
+      seq = make_int4(rows_ok ? s0 : 0, rows_ok ? s1 - s0 : 0, ctx_ok ? ctx : 0, 0);
+      seq_s[tid] = make_int2(seq.y, seq.z);
+    }
+    const bool eligible = a.tile_cap > 0 && static_cast<long long>(seq.y) * group >= kWideFrom;
+    __syncthreads();
+    for (int k = warp; k < nb; k += threads / 32) {
+      const int n = seq_s[k].x, ctx = seq_s[k].y;
       long long narrow = 0, wide = 0;
-      for (int i = lane; i < row_tiles(kNarrowRows, n, group); i += 32) narrow += kNarrowCost + key_tiles(i, kNarrowRows, n, ctx, group);
-      if (eligible)
+      for (int i = lane; i < row_tiles(kNarrowRows, n, group); i += 32)
+        narrow += kNarrowCost + key_tiles(i, kNarrowRows, n, ctx, group);
+      if (a.tile_cap > 0)
         for (int i = lane; i < row_tiles(kWideRows, n, group); i += 32)
           wide += kWideCost + key_tiles(i, kWideRows, n, ctx, group);
 #pragma unroll
@@ -71,45 +97,36 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(ExtendArgs a)
       if (lane == 0) {
         narrow_s[k] = narrow * a.d.n_kv;
         wide_s[k] = wide * a.d.n_kv;
-        // (at least one tile: rows that see nothing are given one)
-        seq_s[k] = make_int4(s0, n, ctx, eligible ? max(1, (ctx + kTile - 1) / kTile) : 0);
       }
     }
     __syncthreads();
-    const bool here = tid < nb;
-    int4 seq = here ? seq_s[tid] : make_int4(0, 0, 0, 0);
-    // expanded tiles asked for up to and with this sequence; it is wide if they fit
-    const long long want = static_cast<long long>(seq.w) * a.d.n_kv;
-    const long long upto = asked + plan_scan(want, warp_s);
-    const bool wide = want > 0 && upto <= a.tile_cap;
-    const long long n_tiles = here && !wide ? narrow_s[tid] : 0, w_tiles = wide ? wide_s[tid] : 0;
-    const long long e_tiles = wide ? want : 0;
-    const long long n_upto = base_n + plan_scan(n_tiles, warp_s), w_upto = base_w + plan_scan(w_tiles, warp_s);
-    const long long e_upto = base_e + plan_scan(e_tiles, warp_s);
+    bool wide = false;
+    long long want = 0;
+    if (a.tile_cap > 0) {
+      // a sequence that could be wide is, if its tiles fit behind those of the
+      // ones before (at least one tile: rows that see nothing are given one)
+      want = eligible ? static_cast<long long>(max(1, (seq.z + kTile - 1) / kTile)) * a.d.n_kv : 0;
+      Sums total;
+      const Sums upto = plan_scan(Sums{want, 0, 0}, warp_s, &total);
+      wide = want > 0 && asked + upto.narrow <= a.tile_cap;
+      asked += total.narrow;
+    }
+    const Sums own{here && !wide ? narrow_s[tid] : 0, wide ? wide_s[tid] : 0, wide ? want : 0};
+    Sums total;
+    const Sums upto = base + plan_scan(own, warp_s, &total);
     if (here) {
-      a.narrow.first[b0 + tid] = n_upto - n_tiles;
-      a.wide.first[b0 + tid] = w_upto - w_tiles;
-      a.ws_expand[b0 + tid] = e_upto - e_tiles;
-      seq.w = wide ? static_cast<int>(e_upto - e_tiles) : -1;
-      a.ws_seq[b0 + tid] = seq;
+      a.narrow.first[b] = upto.narrow - own.narrow;
+      a.wide.first[b] = upto.wide - own.wide;
+      a.ws_expand[b] = upto.expand - own.expand;
+      seq.w = wide ? static_cast<int>(upto.expand - own.expand) : -1;
+      a.ws_seq[b] = seq;
     }
-    if (tid == kPlanThreads - 1) {
-      last_s[0] = n_upto;
-      last_s[1] = w_upto;
-      last_s[2] = e_upto;
-      warp_s[0] = upto;
-    }
-    __syncthreads();
-    base_n = last_s[0];
-    base_w = last_s[1];
-    base_e = last_s[2];
-    asked = warp_s[0];
-    __syncthreads();
+    base = base + total;
   }
   if (tid == 0) {
-    a.narrow.first[a.d.batch] = base_n;
-    a.wide.first[a.d.batch] = base_w;
-    a.ws_expand[a.d.batch] = base_e;
+    a.narrow.first[a.d.batch] = base.narrow;
+    a.wide.first[a.d.batch] = base.wide;
+    a.ws_expand[a.d.batch] = base.expand;
   }
 }
 
@@ -121,6 +138,7 @@ constexpr int kJoinSplit = 8;
 __global__ void __launch_bounds__(32 * kJoinWarps) extend_join_kernel(ExtendArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const ExtendForm f = blockIdx.z == 0 ? a.narrow : a.wide;
+  wait_prerequisites();
   const CutItem cut = f.cuts[blockIdx.x];
   const int c0 = blockIdx.x;
   // (the run that holds key tile 0 wrote its second slot, the others their first)
@@ -208,13 +226,13 @@ cudaError_t launch_extend(const ExtendArgs& args, void* workspace, cudaStream_t 
   a.group_shift = 0;
   while ((1 << a.group_shift) < a.d.group) ++a.group_shift;
   a.group_mul = static_cast<uint32_t>(((1ull << (31 + a.group_shift)) + a.d.group - 1) / a.d.group);
-  extend_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+  const int plan_threads = a.d.batch >= kPlanThreads ? kPlanThreads : (a.d.batch + 255) / 256 * 256;
+  extend_plan_kernel<<<1, plan_threads, 0, stream>>>(a);
   cudaError_t err = cudaGetLastError();
   if (err == cudaSuccess && a.tile_cap > 0) err = launch_extend_wide(a, ctas, stream);
   if (err == cudaSuccess) err = launch_extend_narrow(a, ctas, stream);
   if (err != cudaSuccess || ctas < 2) return err;
-  extend_join_kernel<<<dim3(ctas, kJoinSplit, a.tile_cap > 0 ? 2 : 1), 32 * kJoinWarps, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(extend_join_kernel, dim3(ctas, kJoinSplit, a.tile_cap > 0 ? 2 : 1), 32 * kJoinWarps, 0, stream, a);
 }
 
 }  // namespace tq

@@ -20,6 +20,28 @@ constexpr float kRaise = 90.f;                    // log2 by which scores may pa
 constexpr uint32_t kIdescBf16 = ptx::idesc_bf16_f32(128, 128);
 constexpr uint32_t kIdescF16 = kIdescBf16 & ~((7u << 7) | (7u << 10));
 
+// The launches of a call follow one another as programmatic dependents: each
+// starts while the one before runs (or waits for room), sets itself up, and
+// waits here before it reads or writes memory.  Every CTA waits, so that a
+// launch is complete only after all before it are.
+__device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename Kernel>
+cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const ExtendArgs& a) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 // ---- work items ------------------------------------------------------------
 
 // Key tiles of row tile i (`rows` rows) of a sequence: those its last token

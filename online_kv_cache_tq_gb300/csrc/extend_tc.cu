@@ -81,6 +81,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
   const DecodeArgs& d = a.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* const abort = &abort_s;
+  launch_dependents();
+  wait_prerequisites();
   const long long total = a.narrow.first[d.batch];
   const long long per = run_length(total, gridDim.x);
   Run run;
@@ -507,8 +509,7 @@ cudaError_t launch_bits(const ExtendArgs& a, int ctas, cudaStream_t stream) {
   const cudaError_t err =
       cudaFuncSetAttribute(extend_kernel<KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (err != cudaSuccess) return err;
-  extend_kernel<KB, VB><<<ctas, kExtThreads, kSmemBytes, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(extend_kernel<KB, VB>, dim3(ctas), kExtThreads, kSmemBytes, stream, a);
 }
 
 template <int KB>

@@ -78,6 +78,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
   const int warp = tid >> 5, lane = tid & 31;     // of the group
   ExpandShared& sh = group_s[group];
   volatile int* const abort = &abort_s;
+  launch_dependents();
+  wait_prerequisites();
   const long long total = a.ws_expand[d.batch];
   if (2ll * blockIdx.x >= total) return;          // (the whole CTA)
   if (threadIdx.x == 0) {
@@ -283,6 +285,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
   const DecodeArgs& d = a.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* const abort = &abort_s;
+  launch_dependents();
+  wait_prerequisites();
   const long long total = a.wide.first[d.batch];
   const long long per = run_length(total, gridDim.x);
   Run run;
@@ -640,8 +644,7 @@ cudaError_t expand_bits(const ExtendArgs& a, int ctas, cudaStream_t stream) {
   const cudaError_t err =
       cudaFuncSetAttribute(extend_expand_kernel<KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmem);
   if (err != cudaSuccess) return err;
-  extend_expand_kernel<KB, VB><<<ctas, kExpandThreads, kExpandSmem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(extend_expand_kernel<KB, VB>, dim3(ctas), kExpandThreads, kExpandSmem, stream, a);
 }
 
 template <int KB>
@@ -670,8 +673,7 @@ cudaError_t launch_extend_wide(const ExtendArgs& a, int ctas, cudaStream_t strea
   if (err != cudaSuccess) return err;
   err = cudaFuncSetAttribute(extend_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem);
   if (err != cudaSuccess) return err;
-  extend_wide_kernel<<<ctas, kWideThreads, kWideSmem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(extend_wide_kernel, dim3(ctas), kWideThreads, kWideSmem, stream, a);
 }
 
 }  // namespace tq
