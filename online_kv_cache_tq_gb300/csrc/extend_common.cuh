@@ -42,6 +42,26 @@ cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+// ptx::wait_bar without its suspension hint: a waiting warp sleeps for the
+// hardware's own short time, which wakes it sooner than the hint does; the
+// clock and the abort flag are looked at once in 64 tries.
+__device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity, volatile int* abort, int* error) {
+  uint64_t t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    const uint64_t now = ptx::global_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > ptx::kWaitLimitNs) {
+      *abort = 1;
+      atomicCAS(error, 0, kErrTimeout);
+      return false;
+    }
+  }
+}
+
 // ---- work items ------------------------------------------------------------
 
 // Key tiles of row tile i (`rows` rows) of a sequence: those its last token

@@ -233,6 +233,12 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
         ok = TQ_WAIT(bar.s_full[sb], ph) && TQ_WAIT(bar.v_full[sb], ph);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        if (it.i * kTile + quarter * 32 >= n_rows) {
+          // none of the warp's rows is there (a decode step's few rows): its
+          // weights, and what they add to rows that nobody reads, are left
+          ptx::mbar_arrive(&bar.p_full[sb]);
+          continue;
+        }
         ptx::tc_fence_after();
         // this thread's 64 scores; their weights go to the first 32 of the columns
         const uint32_t s_addr = lane_addr + (sb ? kS1 : kS0) + 64 * half;
@@ -420,7 +426,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
   } else {
     // ---------------- products ----------------
     // the whole warp walks the tiles and waits; an elected lane issues
-#define TQ_WARP_WAIT(b, ph) __all_sync(0xffffffffu, TQ_WAIT(b, ph))
+#define TQ_WARP_WAIT(b, ph) __all_sync(0xffffffffu, wait_short(&(b), (ph), abort, d.error))
     const uint64_t key_desc = ptx::desc_k_sw128(ptx::smem_u32(smem + kKey0));
     const uint64_t value_desc = ptx::desc_k_sw128(ptx::smem_u32(smem + kValue0));
     int kc = 0, jt = 0;
