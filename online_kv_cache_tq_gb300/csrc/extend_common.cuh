@@ -42,6 +42,26 @@ cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+// ptx::wait_bar without its suspension hint: a waiting warp sleeps for the
+// hardware's own short time, which wakes it sooner than the hint does; the
+// clock and the abort flag are looked at once in 64 tries.
+__device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity, volatile int* abort, int* error) {
+  uint64_t t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    const uint64_t now = ptx::global_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > ptx::kWaitLimitNs) {
+      *abort = 1;
+      atomicCAS(error, 0, kErrTimeout);
+      return false;
+    }
+  }
+}
+
 // ---- work items ------------------------------------------------------------
 
 // Key tiles of row tile i (`rows` rows) of a sequence: those its last token
@@ -178,10 +198,6 @@ __device__ __forceinline__ void store16(uint32_t saddr, const uint4& v) {
                ::"r"(saddr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "n"(OFFSET)
                : "memory");
 }
-__device__ __forceinline__ void store2(uint32_t saddr, uint32_t v) {   // the low 16 bits
-  asm volatile("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tst.shared.b16 [%0], lo;\n\t}" ::"r"(saddr), "r"(v)
-               : "memory");
-}
 __device__ __forceinline__ float4 load16(uint32_t saddr) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(saddr));
@@ -255,6 +271,10 @@ __device__ __forceinline__ RowChunks second_word(const RowChunks& r) {   // chun
   return RowChunks{{r.at[0] ^ 64, r.at[1] ^ 64, r.at[2] ^ 64, r.at[3] ^ 64}};
 }
 
+__device__ __forceinline__ RowChunks next_block(const RowChunks& r) {
+  return RowChunks{{r.at[0] + kBlockBytes, r.at[1] + kBlockBytes, r.at[2] + kBlockBytes, r.at[3] + kBlockBytes}};
+}
+
 // One word per plane (32 coordinates or tokens) into four chunks of a row.
 template <int BITS, int OFFSET>
 __device__ __forceinline__ void expand32(const RowChunks& r, uint32_t (&w)[BITS], const LevelBytes& t) {
@@ -278,36 +298,6 @@ __device__ __forceinline__ void expand_signs(const RowChunks& r, uint32_t bits, 
   }
 }
 
-// The same expansions into 16 tensor-memory columns of the thread's lane.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-template <int BITS>
-__device__ __forceinline__ void store_levels(uint32_t taddr, uint32_t (&w)[BITS], const LevelBytes& t) {
-  if constexpr (BITS == 4) {
-#pragma unroll
-    for (int p = 0; p < 3; ++p) w[p] = w[p] ^ ~w[3];
-  }
-  uint32_t r[16];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 v = expand8<BITS>(w, i, t);
-    r[4 * i] = v.x, r[4 * i + 1] = v.y, r[4 * i + 2] = v.z, r[4 * i + 3] = v.w;
-  }
-  tmem_st16(taddr, r);
-}
-__device__ __forceinline__ void store_signs(uint32_t taddr, uint32_t bits, uint32_t minus_rho) {
-  uint32_t r[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = ((bits << (15 - i)) & 0x80008000u) ^ minus_rho;
-  tmem_st16(taddr, r);
-}
-
 // ---- products ----------------------------------------------------------------
 
 // D (+)= A B^T over STEPS K steps of 16, issued by one lane: A in tensor
@@ -319,17 +309,6 @@ __device__ __forceinline__ void product(uint32_t d, uint32_t a_tmem, uint64_t b_
   for (int ks = 0; ks < STEPS; ++ks)
     ptx::mma_bf16_tmem_a(d, a_tmem + 8 * ks, b_desc + (ks >> 2) * (kBlockBytes / 16) + (ks & 3) * 2, idesc,
                          accumulate || ks > 0);
-}
-
-// The same with both operands in shared memory, their K blocks a_block and
-// b_block (in the descriptors' units) apart.
-template <int STEPS>
-__device__ __forceinline__ void shared_product(uint32_t d, uint64_t a_desc, uint64_t a_block, uint64_t b_desc,
-                                               uint64_t b_block, uint32_t idesc, bool accumulate) {
-#pragma unroll
-  for (int ks = 0; ks < STEPS; ++ks)
-    ptx::mma_bf16(d, a_desc + (ks >> 2) * a_block + (ks & 3) * 2, b_desc + (ks >> 2) * b_block + (ks & 3) * 2, idesc,
-                  accumulate || ks > 0);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {

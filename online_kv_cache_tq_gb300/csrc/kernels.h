@@ -277,7 +277,7 @@ struct ExtendForm {
   float* part;
   CutItem* cuts;              // [ctas]: what run c begins and does not end
 };
-constexpr int kNarrowRows = 64, kWideRows = 256;
+constexpr int kNarrowRows = 128, kWideRows = 256;
 constexpr int kNarrowCost = 3, kWideCost = 6;
 
 // A key tile expanded for the wide form: the keys (R^T c + rho S^T signs,
