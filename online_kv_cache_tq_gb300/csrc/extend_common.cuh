@@ -198,11 +198,7 @@ __device__ __forceinline__ void store16(uint32_t saddr, const uint4& v) {
                ::"r"(saddr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "n"(OFFSET)
                : "memory");
 }
-__device__ __forceinline__ float4 load16(uint32_t saddr) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(saddr));
-  return v;
-}
+__device__ __forceinline__ float4 load16(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 // The 16-bit patterns of a codebook's levels as byte tables: low and high
 // bytes of levels 0..7 (for 16 levels, of the eight positive ones; the sign is
@@ -539,13 +535,13 @@ __device__ __forceinline__ void load_value(const DecodeArgs& d, const Item& it, 
 // ---- softmax of a score tile ---------------------------------------------------
 //
 // A thread has 64 scores of its row at tensor-memory columns s .. s + 63 and
-// leaves its weights (bf16 pairs) in the first 32 of them.  kf, vf: shared
-// addresses of the columns' key and value factors; VF: whether weights are
+// leaves its weights (bf16 pairs) in the first 32 of them.  kf, vf: the
+// columns' key and value factors in shared memory; VF: whether weights are
 // multiplied by a value factor (else the values are scaled already).
 
 // No score hidden, none that may pass the reference by 2^kRaise.
 template <bool VF>
-__device__ __forceinline__ void weigh_usual(uint32_t s, uint32_t kf, uint32_t vf, float ref, uint64_t& sum2) {
+__device__ __forceinline__ void weigh_usual(uint32_t s, const float* kf, const float* vf, float ref, uint64_t& sum2) {
   const uint64_t minus = pair(-ref, -ref);
   uint32_t x[2][16];
   tmem_ld16_start(s, x[0]);
@@ -557,7 +553,7 @@ __device__ __forceinline__ void weigh_usual(uint32_t s, uint32_t kf, uint32_t vf
     uint32_t w[8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float4 f = load16(kf + 64 * c + 16 * k);
+      const float4 f = load16(kf + 16 * c + 4 * k);
       const float2 z0 = unpair(fma2(pair(__uint_as_float(y[4 * k]), __uint_as_float(y[4 * k + 1])), pair(f.x, f.y), minus));
       const float2 z1 =
           unpair(fma2(pair(__uint_as_float(y[4 * k + 2]), __uint_as_float(y[4 * k + 3])), pair(f.z, f.w), minus));
@@ -565,7 +561,7 @@ __device__ __forceinline__ void weigh_usual(uint32_t s, uint32_t kf, uint32_t vf
       sum2 = add2(sum2, add2(p0, p1));
       float2 w0 = unpair(p0), w1 = unpair(p1);
       if (VF) {
-        const float4 g = load16(vf + 64 * c + 16 * k);
+        const float4 g = load16(vf + 16 * c + 4 * k);
         w0 = unpair(mul2(p0, pair(g.x, g.y)));
         w1 = unpair(mul2(p1, pair(g.z, g.w)));
       }
@@ -584,7 +580,7 @@ __device__ __forceinline__ uint32_t visible(const uint32_t* valid, int here, int
 }
 
 // The largest of the thread's scores.
-__device__ __forceinline__ float plain_top(uint32_t s, uint32_t kf) {
+__device__ __forceinline__ float plain_top(uint32_t s, const float* kf) {
   float top = -INFINITY;
   uint32_t x[2][16];
   tmem_ld16_start(s, x[0]);
@@ -595,7 +591,7 @@ __device__ __forceinline__ float plain_top(uint32_t s, uint32_t kf) {
     const uint32_t(&y)[16] = x[c & 1];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float4 f = load16(kf + 64 * c + 16 * k);
+      const float4 f = load16(kf + 16 * c + 4 * k);
       top = fmaxf(fmaxf(top, __uint_as_float(y[4 * k]) * f.x), __uint_as_float(y[4 * k + 1]) * f.y);
       top = fmaxf(fmaxf(top, __uint_as_float(y[4 * k + 2]) * f.z), __uint_as_float(y[4 * k + 3]) * f.w);
     }
@@ -604,7 +600,7 @@ __device__ __forceinline__ float plain_top(uint32_t s, uint32_t kf) {
 }
 
 // The same of the visible scores, or of a scaled query.
-__device__ __forceinline__ float masked_top(uint32_t s, uint32_t kf, float factor, const uint32_t* valid, int here,
+__device__ __forceinline__ float masked_top(uint32_t s, const float* kf, float factor, const uint32_t* valid, int here,
                                             int half) {
   float top = -INFINITY;
 #pragma unroll 1
@@ -616,7 +612,7 @@ __device__ __forceinline__ float masked_top(uint32_t s, uint32_t kf, float facto
       ptx::tmem_ld16(s + 32 * c + 16 * h, y);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float4 f = load16(kf + 128 * c + 64 * h + 16 * k);
+        const float4 f = load16(kf + 32 * c + 16 * h + 4 * k);
         const float fk[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -630,7 +626,7 @@ __device__ __forceinline__ float masked_top(uint32_t s, uint32_t kf, float facto
 }
 
 template <bool VF>
-__device__ __forceinline__ float weigh_masked(uint32_t s, uint32_t kf, uint32_t vf, float factor, float shift,
+__device__ __forceinline__ float weigh_masked(uint32_t s, const float* kf, const float* vf, float factor, float shift,
                                               const uint32_t* valid, int here, int half) {
   float sum = 0.f;
 #pragma unroll 1
@@ -642,8 +638,8 @@ __device__ __forceinline__ float weigh_masked(uint32_t s, uint32_t kf, uint32_t 
       ptx::tmem_ld16(s + 32 * c + 16 * h, y);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float4 f = load16(kf + 128 * c + 64 * h + 16 * k);
-        const float4 g = VF ? load16(vf + 128 * c + 64 * h + 16 * k) : make_float4(1.f, 1.f, 1.f, 1.f);
+        const float4 f = load16(kf + 32 * c + 16 * h + 4 * k);
+        const float4 g = VF ? load16(vf + 32 * c + 16 * h + 4 * k) : make_float4(1.f, 1.f, 1.f, 1.f);
         const float fk[4] = {f.x, f.y, f.z, f.w}, gk[4] = {g.x, g.y, g.z, g.w};
         float p[4];
 #pragma unroll

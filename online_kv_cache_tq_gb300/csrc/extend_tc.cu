@@ -35,7 +35,7 @@
 // Tiles with hidden positions take a second path that masks.
 //
 // Twenty-one warps: 0-7 softmax (two threads per row, 64 columns each), 8-15
-// keys (two threads per token), 16-19 values (a thread per coordinate), 20
+// keys (two threads per token), 16-19 values (a thread per coordinate), 23
 // issues the products.
 // Tensor memory: two score tiles of 128 columns (weights overwrite them),
 // the output, the query operand.
@@ -47,8 +47,8 @@ namespace {
 constexpr int kSoftThreads = 256;
 constexpr int kKeyThreads = 256;
 constexpr int kValueThreads = 128;
-constexpr int kMmaWarp = 20;
-constexpr int kExtThreads = kSoftThreads + kKeyThreads + kValueThreads + 32;
+constexpr int kMmaWarp = 23;                      // (20-22 have nothing to do: 23 is not on the scheduler of the first rows)
+constexpr int kExtThreads = (kMmaWarp + 1) * 32;
 constexpr int kKeyBytes = 4 * kBlockBytes;
 constexpr int kValueBytes = 2 * kBlockBytes;
 constexpr int kRing = 4;                          // key and value factors of the tiles in flight
@@ -123,8 +123,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
   __shared__ Item item_s;
   __shared__ int offset_s;
   __shared__ float swap_s[2][2][kTile];           // what the two threads of a row tell each other
-  __shared__ float2 reach_s[kRing][4];            // per 32 tokens of a tile: bounds of the longest scaled key halves
-  __shared__ uint32_t valid_s[kRing][4];          // tokens of a tile, by expanded column
+  __shared__ __align__(16) float2 reach_s[kRing][4];           // per 32 tokens of a tile: bounds of the longest scaled key halves
+  __shared__ __align__(16) uint32_t valid_s[kRing][4];         // tokens of a tile, by expanded column
 
   // 1024-byte aligned, as an offset from smem_raw so that accesses stay shared-space
   uint8_t* const smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -292,13 +292,15 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
         ptx::tc_fence_after();
         // this thread's 64 scores; their weights go to the first 32 of the columns
         const uint32_t s_addr = lane_addr + (sb ? kS1 : kS0) + 64 * half;
-        const uint32_t kf = ptx::smem_u32(key_factor + rg * kTile + 64 * half);
-        const uint32_t vf = ptx::smem_u32(value_factor + rg * kTile + 64 * half);
-        const uint32_t all = valid_s[rg][0] & valid_s[rg][1] & valid_s[rg][2] & valid_s[rg][3];
-        float top_bound = 0.f;                    // |score| <= |R q| |n c| + |S q| |n rho signs|
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          top_bound = fmaxf(top_bound, fmaf(len_r, reach_s[rg][g].x, len_s * reach_s[rg][g].y));
+        const float* const kf = key_factor + rg * kTile + 64 * half;
+        const float* const vf = value_factor + rg * kTile + 64 * half;
+        const uint4 there = *reinterpret_cast<const uint4*>(valid_s[rg]);
+        const uint32_t all = there.x & there.y & there.z & there.w;
+        const float4 reach0 = *reinterpret_cast<const float4*>(&reach_s[rg][0]);
+        const float4 reach1 = *reinterpret_cast<const float4*>(&reach_s[rg][2]);
+        // |score| <= |R q| |n c| + |S q| |n rho signs|
+        const float top_bound = fmaf(len_r, fmaxf(fmaxf(reach0.x, reach0.z), fmaxf(reach1.x, reach1.z)),
+                                     len_s * fmaxf(fmaxf(reach0.y, reach0.w), fmaxf(reach1.y, reach1.w)));
         // (both the same for the two threads of a row, and so for their warps)
         const bool mask = __any_sync(0xffffffffu, e != 0 || seen < (t + 1) * kTile || all != 0xffffffffu);
         const bool search = __any_sync(0xffffffffu, !(ref > -INFINITY && top_bound <= ref + kRaise));
@@ -437,7 +439,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       ok = ok && image(2, 1);
       end_segment(a, a.narrow, run, t1);
     }
-  } else if (warp < kMmaWarp) {
+  } else if (warp < 20) {
     // ---------------- values ----------------
     const int dim = tid - kSoftThreads - kKeyThreads;   // also the column whose token's factor this thread writes
     const LevelBytes lev = level_bytes<true>(d.tables->v_levels, VB);
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       }
       end_segment(a, a.narrow, run, t1);
     }
-  } else {
+  } else if (warp == kMmaWarp) {
     // ---------------- products ----------------
     // the whole warp walks the tiles and waits; an elected lane issues
 #define TQ_WARP_WAIT(b, ph) __all_sync(0xffffffffu, wait_short(&(b), (ph), abort, d.error))

@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         if (!ok) break;
         ptx::tc_fence_after();
         const TileMeta* const meta = reinterpret_cast<const TileMeta*>(smem + kMeta0) + (jt & (kRing - 1));
-        const uint32_t kf = ptx::smem_u32(meta->key_factor + 64 * half);
+        const float* const kf = meta->key_factor + 64 * half;
         const uint32_t all = meta->valid[0] & meta->valid[1] & meta->valid[2] & meta->valid[3];
         // (both the same for the two threads of a row, and so for their warps)
         const bool mask = __any_sync(0xffffffffu, e != 0 || seen < (t + 1) * kTile || all != 0xffffffffu);
@@ -454,8 +454,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
           }
         }
         const float shift = ref == -INFINITY ? 0.f : ref;
-        if (mask) sum2 = add2(sum2, pair(weigh_masked<false>(s_addr, kf, 0, factor, shift, meta->valid, here, half), 0.f));
-        else weigh_usual<false>(s_addr, kf, 0, shift, sum2);
+        if (mask) sum2 = add2(sum2, pair(weigh_masked<false>(s_addr, kf, nullptr, factor, shift, meta->valid, here, half), 0.f));
+        else weigh_usual<false>(s_addr, kf, nullptr, shift, sum2);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar.p_full[x]);
