@@ -386,21 +386,29 @@ __device__ __forceinline__ int exponent_of(float x) {   // clamped so that 2^-e 
   return e < -100 ? -100 : (e > 100 ? 100 : e);
 }
 
+__device__ __forceinline__ void unpack_bf16(const uint4& w, float (&v)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
 __device__ __forceinline__ void load_query8(const ExtendArgs& a, long long at, float (&v)[8]) {
   if (a.q_bf16) {
-    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.d.q) + at);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
+    unpack_bf16(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.d.q) + at), v);
   } else {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.d.q) + at);
     const float4 x = p[0], y = p[1];
     v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
   }
 }
+
+// A thread's own 16-byte copies global -> shared, and the wait for them.
+__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Vector (token x query head) of row r of an item's sequence and KV head.
 __device__ __forceinline__ int row_token(const ExtendArgs& a, int r) {
@@ -675,14 +683,12 @@ __device__ __forceinline__ void scale_output(uint32_t o, float scale) {
 // the row's output out of fp16's range.)
 __device__ __forceinline__ float largest_output(uint32_t o, float inv) {
   float top = 0.f;
-  uint32_t x[2][16];
-  tmem_ld16_start(o, x[0]);
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < 4; ++c) {
-    tmem_ld16_wait(x[c & 1]);
-    if (c < 3) tmem_ld16_start(o + 16 * (c + 1), x[(c + 1) & 1]);
+    uint32_t y[16];
+    ptx::tmem_ld16(o + 16 * c, y);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(__uint_as_float(x[c & 1][k]) * inv));
+    for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(__uint_as_float(y[k]) * inv));
   }
   return top;
 }
@@ -737,7 +743,7 @@ __device__ __forceinline__ void store_row(uint32_t o, float scale, __nv_bfloat16
 
 // The same as bf16 into eight swizzled 16-byte chunks of a row in shared memory.
 __device__ __forceinline__ void output_rows(uint32_t o, float scale, uint8_t* dst, int row) {
-#pragma unroll 2
+#pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t y[16], w[8];
     ptx::tmem_ld16(o + 16 * c, y);

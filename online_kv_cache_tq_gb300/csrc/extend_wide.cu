@@ -372,44 +372,48 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
       float other;
       // The queries, sixteen lanes to a row (whole lines, and a row's largest
       // coordinate and length in four shuffles): fp16, scaled by a power of
-      // two if outside the range, swizzled.
+      // two if outside the range, swizzled.  bf16 rows are copied to their
+      // place first, all in flight at once, and converted where they lie; the
+      // loops are short because this code is met cold, once per segment.
+      uint8_t* const copy_at = copy_base + copy_row * 128;
+      if (a.q_bf16) {
 #pragma unroll 1
-      for (int k0 = 0; k0 < 8; k0 += 4) {
-        float v[4][8];
+        for (int k = 0; k < 8; ++k) {
+          const int rr = it.i * kWideRows + kTile * x + copy_row + 2 * k;
+          const long long vec = row_vector(a, it.seq.x, it.kvh, min(rr, n_rows - 1));
+          copy16_async(copy_at + k * 256 + (((copy_chunk ^ (copy_row + 2 * k)) & 7) << 4),
+                       static_cast<const __nv_bfloat16*>(d.q) + vec * kDim + copy_chunk * 8);
+        }
+        copies_wait();
+      }
+#pragma unroll 1
+      for (int k = 0; k < 8; ++k) {
+        const int qr = copy_row + 2 * k, rr = it.i * kWideRows + kTile * x + qr;
+        uint4* const place = reinterpret_cast<uint4*>(copy_at + k * 256 + (((copy_chunk ^ qr) & 7) << 4));
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (rr < n_rows) {
+          if (a.q_bf16) unpack_bf16(*place, v);
+          else load_query8(a, row_vector(a, it.seq.x, it.kvh, rr) * kDim + copy_chunk * 8, v);
+        }
+        float biggest = 0.f, square = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int rr = it.i * kWideRows + kTile * x + copy_row + 2 * (k0 + k);
-          if (rr < n_rows) {
-            load_query8(a, row_vector(a, it.seq.x, it.kvh, rr) * kDim + copy_chunk * 8, v[k]);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[k][q] = 0.f;
-          }
+        for (int q = 0; q < 8; ++q) {
+          biggest = fmaxf(biggest, fabsf(v[q]));
+          square = fmaf(v[q], v[q], square);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int qr = copy_row + 2 * (k0 + k);
-          float biggest = 0.f, square = 0.f;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            biggest = fmaxf(biggest, fabsf(v[k][q]));
-            square = fmaf(v[k][q], v[k][q], square);
-          }
-#pragma unroll
-          for (int o = 1; o < 16; o <<= 1) {
-            biggest = fmaxf(biggest, __shfl_xor_sync(0xffffffffu, biggest, o));
-            square += __shfl_xor_sync(0xffffffffu, square, o);
-          }
-          int qe = exponent_of(biggest);
-          if (biggest == 0.f || (qe >= -8 && qe < 10)) qe = 0;
-          const float down = exp2_int(-qe);
-          if (copy_chunk == 0) query_s[kTile * x + qr] = make_float2(sqrtf(square), static_cast<float>(qe));
-          uint32_t w[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) w[q] = pack_f16(v[k][2 * q] * down, v[k][2 * q + 1] * down);
-          *reinterpret_cast<uint4*>(copy_base + qr * 128 + (((copy_chunk & 7) ^ (qr & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+        for (int o = 1; o < 16; o <<= 1) {
+          biggest = fmaxf(biggest, __shfl_xor_sync(0xffffffffu, biggest, o));
+          square += __shfl_xor_sync(0xffffffffu, square, o);
         }
+        int qe = exponent_of(biggest);
+        if (biggest == 0.f || (qe >= -8 && qe < 10)) qe = 0;
+        const float down = exp2_int(-qe);
+        if (copy_chunk == 0) query_s[kTile * x + qr] = make_float2(sqrtf(square), static_cast<float>(qe));
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = pack_f16(v[2 * q] * down, v[2 * q + 1] * down);
+        *place = make_uint4(w[0], w[1], w[2], w[3]);
       }
       ptx::fence_async_shared();
       ptx::mbar_arrive(&bar.q_full);
@@ -497,7 +501,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         output_rows(o_addr, exp2_int(eo), smem + kQuery0 + x * kImage + half * kBlockBytes + row * 128, row);
         ok = together();
         if (!ok) break;
-#pragma unroll 4
+#pragma unroll 2
         for (int k = 0; k < 8; ++k) {
           const int qr = copy_row + 2 * k, rr = it.i * kWideRows + kTile * x + qr;
           if (rr < n_rows)
