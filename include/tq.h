@@ -445,17 +445,21 @@ size_t tq_extend_workspace_bytes(const tq_codebook* book, int n_tokens, int batc
  * zero row; a sequence may have no new tokens.  Query head h reads KV head
  * h / (n_q_heads / n_kv_heads), any whole ratio.  out: device bf16
  * [n_tokens][n_q_heads][128]; rows behind query_start[batch] are left as they
- * were.  The scores' operands are rounded to fp16 (queries scaled by a power
- * of two, unit-norm keys), softmax weights and value levels to bf16;
- * everything is summed in float32 and rounded to bf16 once at the end.
- * cache, block_table, max_blocks, max_context and scale as in
- * tq_decode_attention (max_context bounds every context_lens[b]).  workspace:
- * device scratch of tq_extend_workspace_bytes bytes, 256-byte aligned, not
- * used by any concurrent call.  Device errors: 2 a block id out of range (its
- * tokens are skipped), 3 a context length or query_start out of range (rows
- * of that sequence are zero where query_start places them inside n_tokens,
- * else left as they were), 4 as elsewhere.  PolarQuant handles are not built
- * (TQ_ERR_UNSUPPORTED).  Asynchronous on `stream`. */
+ * were.  Queries (scaled by a power of two where that is needed) and keys are
+ * rounded to fp16, softmax weights and values to bf16; every sum is float32,
+ * and the output is rounded to bf16 once at the end.  The same call gives the
+ * same bits.  cache, block_table, max_blocks, max_context and scale as in
+ * tq_decode_attention (max_context bounds every context_lens[b] and is at most
+ * 2^30, else TQ_ERR_UNSUPPORTED).  workspace: device scratch of
+ * tq_extend_workspace_bytes bytes, 256-byte aligned, not used by any
+ * concurrent call: about 20 MB, and where sequences can have 512 rows (new
+ * tokens x n_q_heads / n_kv_heads) or more, 520 bytes per context token and KV
+ * head of as many sequences of max_context, 2.2 GB at most.  Device errors: 2
+ * a block id out of range (its tokens are skipped), 3 a context length or
+ * query_start out of range (the rows of a sequence with a bad length are zero,
+ * those with a bad query_start are left as they were), 4 as elsewhere.
+ * PolarQuant handles are not built (TQ_ERR_UNSUPPORTED).  Asynchronous on
+ * `stream`. */
 tq_status tq_extend_attention(const tq_codebook* book, const void* q, tq_dtype dtype, int n_tokens, int batch,
                               int n_q_heads, int n_kv_heads, const tq_cache_view* cache, const int32_t* block_table,
                               int max_blocks, const int32_t* query_start, const int32_t* context_lens, int max_context,

@@ -1095,6 +1095,7 @@ tq_status tq_extend_attention(const tq_codebook* book, const void* q, tq_dtype d
     return TQ_ERR_INVALID_ARG;
   }
   if (book->polar) return TQ_ERR_UNSUPPORTED;     // (PolarQuant records: decode one token at a time)
+  if (max_context > (1 << 30)) return TQ_ERR_UNSUPPORTED;   // (positions and tile bounds are ints)
   if (!any) return TQ_OK;
   const size_t need = tq_extend_workspace_bytes(book, n_tokens, batch, n_q_heads, n_kv_heads, max_context);
   if (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) {

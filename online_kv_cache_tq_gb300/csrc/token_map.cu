@@ -128,8 +128,8 @@ __global__ void __launch_bounds__(kMapThreads) token_map_kernel(TokenMapArgs a) 
 
   // tokens
   const int total = start_s[a.batch];
-  const int t_end = min(static_cast<long long>(a.n_tokens), (blockIdx.x + 1ll) * kMapTokens);
-  for (int t = blockIdx.x * kMapTokens + tid; t < t_end; t += kMapThreads) {
+  const long long t_end = min(static_cast<long long>(a.n_tokens), (blockIdx.x + 1ll) * kMapTokens);
+  for (long long t = static_cast<long long>(blockIdx.x) * kMapTokens + tid; t < t_end; t += kMapThreads) {
     int pos = -1;
     long long slot = -1;
     if (t < total) {
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kMapThreads) token_map_kernel(TokenMapArgs a) 
       }
       int past, fresh;
       sequence_lengths(a, lo, &past, &fresh);
-      pos = past + t - start_s[lo];
+      pos = past + static_cast<int>(t - start_s[lo]);
       const int before = blocks_of(past, a.block_size), col = pos / a.block_size;
       int id;
       if (col >= before) {

@@ -277,6 +277,59 @@ def test_bad_lengths_are_recorded():
 
 
 @pytest.mark.gpu
+def test_more_expanded_tiles_than_the_workspace_holds():
+    # five sequences of 512 rows over 64 KV heads: 8256 expanded tiles each, of
+    # which the workspace holds 32768, so the last one is read from its packed cache
+    c = Case([512] * 5, [16500, 16400, 16512, 16385, 16450], n_kv=64, group=1, seed=17, bs=128)
+    assert c.nbytes < 3 << 30
+    c.run()
+    torch.cuda.synchronize()
+    hc, got, qn = host_cache(c.cache), c.out.double().cpu().numpy(), c.q.double().cpu().numpy()
+    assert B.tq_get_last_device_error(c.book) == 0
+    for b in range(5):
+        last = slice(512 * b + 509, 512 * b + 512)
+        for h in (0, 41, 63):
+            expect, bound = reference(qn[last, h:h + 1], hc, c.table[b], int(c.ctx[b]), 3, h, c.ref,
+                                      1.0 / math.sqrt(128))
+            err = np.abs(got[last, h:h + 1] - expect)
+            assert (err <= bound).all()
+            assert math.sqrt((err ** 2).sum() / (expect ** 2).sum()) <= 2.0 * V
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [1, 4, 8])
+def test_both_forms_in_one_call(group):
+    # sequences on either side of 512 rows, some with rows that see nothing, row tiles cut at every place
+    n = 512 // group
+    c = Case([n - 1, n, n + 1, 2, 3 * n, n + 5], [n + 70, n, 4000, 5000, 3 * n + 1, n - 9], n_kv=2, group=group, seed=18)
+    c.run()
+    c.check(tokens=40)
+    c.run()
+    c.check(sequences=[0, 2, 4], tokens=n - 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [3, 300])
+def test_a_later_tile_passes_the_reference(new):
+    # keys that grow along the context raise the reference again and again; a huge value behind a row's limit
+    # leaves the rows before it as they are
+    c = Case([new], [900], n_kv=1, group=4, seed=19)
+    g = generator(4)
+    k = torch.randn((900, 1, 128), generator=g, device="cuda") * torch.linspace(1, 60, 900, device="cuda")[:, None, None]
+    v = torch.randn((900, 1, 128), generator=g, device="cuda")
+    v[899] *= 1e6
+    slots = torch.as_tensor(W.slots_for(c.table[0], np.arange(900), 64), device="cuda")
+    B.tq_quantize_append(c.book, k.contiguous(), v.contiguous(), B.TQ_FP32, 900, 1, slots, C.cache_view(c.book, c.cache))
+    c.run()
+    torch.cuda.synchronize()
+    hc, got, qn = host_cache(c.cache), c.out.double().cpu().numpy(), c.q.double().cpu().numpy()
+    expect, bound = reference(qn, hc, c.table[0], 900, new, 0, c.ref, 1.0 / math.sqrt(128))
+    assert np.isfinite(got).all() and (np.abs(got - expect) <= bound).all()
+    before = np.abs(got - expect)[:-1], expect[:-1]
+    assert math.sqrt((before[0] ** 2).sum() / (before[1] ** 2).sum()) <= 32.0 * V
+
+
+@pytest.mark.gpu
 def test_one_token_agrees_with_decode():
     c = Case([1, 1, 1], [77, 512, 1300], seed=14)
     c.run()
