@@ -14,7 +14,9 @@ namespace {
 
 constexpr int kTile = 128;                        // rows of a product, tokens of a key tile
 constexpr int kBlockBytes = kTile * 128;          // a 64-column K block of a 128-row operand
-constexpr float kRaise = 90.f;                    // log2 by which scores may pass the reference
+// log2 by which scores may pass the reference (zero at first): 2^80 leaves fp32
+// sums and bf16 weights room for 2^20 tokens with values of 2^27.
+constexpr float kRaise = 80.f;
 
 // kind::f16 with fp16 or bf16 operands, fp32 accumulators, 128 x 128.
 constexpr uint32_t kIdescBf16 = ptx::idesc_bf16_f32(128, 128);
@@ -546,6 +548,14 @@ __device__ __forceinline__ void load_value(const DecodeArgs& d, const Item& it, 
 // leaves its weights (bf16 pairs) in the first 32 of them.  kf, vf: the
 // columns' key and value factors in shared memory; VF: whether weights are
 // multiplied by a value factor (else the values are scaled already).
+
+// The row's reference after a search found `top` (-inf: nothing visible).  A
+// first maximum in bounds leaves zero, as it would be without the search, so
+// that what other rows see does not change a row's bits.
+__device__ __forceinline__ float raised(float ref, float top) {
+  if (ref == -INFINITY) return top > -INFINITY && fabsf(top) <= kRaise ? 0.f : top;
+  return top > ref + kRaise ? top : ref;
+}
 
 // No score hidden, none that may pass the reference by 2^kRaise.
 template <bool VF>

@@ -26,12 +26,12 @@
 // needed.  A query is scaled by a power of two into fp16's range when its
 // largest coordinate is outside 2^-8 .. 2^10.
 //
-// Softmax.  Scores are kept against a reference that is the maximum of the
-// row's first visible tile and moves only when a later score may pass it by
-// 2^90: fp32 and bf16 hold p exactly as well at 2^80 as at 1.  Whether it may
-// is known without looking at the scores, from the length of the query and
-// the largest key of the tile, so the usual tile is read once and pays a
-// multiply-add, an exponential, a sum, a product and a conversion per score.
+// Softmax.  No maximum is searched as long as the lengths of the query and of
+// the tile's keys bound the scores by 2^80 in either direction: fp32 and bf16
+// hold p exactly as well at 2^70 or 2^-70 as at 1, so the reference is zero and
+// a tile is read once, with a multiply-add, an exponential, a sum, a product
+// and a conversion per score.  A tile that may pass this bound (or an earlier
+// reference by 2^80) is searched for each row's maximum first.
 // Tiles with hidden positions take a second path that masks.
 //
 // Twenty-one warps: 0-7 softmax (two threads per row, 64 columns each), 8-15
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
         const float* const kf = key_factor + rg * kTile + 64 * half;
         const float* const vf = value_factor + rg * kTile + 64 * half;
         const uint4 there = *reinterpret_cast<const uint4*>(valid_s[rg]);
-        const uint32_t all = there.x & there.y & there.z & there.w;
+        const uint32_t all = there.x & there.y & there.z & there.w, any = there.x | there.y | there.z | there.w;
         const float4 reach0 = *reinterpret_cast<const float4*>(&reach_s[rg][0]);
         const float4 reach1 = *reinterpret_cast<const float4*>(&reach_s[rg][2]);
         // |score| <= |R q| |n c| + |S q| |n rho signs|
@@ -303,18 +303,16 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
                                      len_s * fmaxf(fmaxf(reach0.y, reach0.w), fmaxf(reach1.y, reach1.w)));
         // (both the same for the two threads of a row, and so for their warps)
         const bool mask = __any_sync(0xffffffffu, e != 0 || seen < (t + 1) * kTile || all != 0xffffffffu);
-        const bool search = __any_sync(0xffffffffu, !(ref > -INFINITY && top_bound <= ref + kRaise));
+        const bool search = __any_sync(0xffffffffu, !(top_bound <= (ref == -INFINITY ? 0.f : ref) + kRaise));
         const int here = min(kTile, max(0, seen - t * kTile));
         if (search) {
-          // no reference yet, or scores that may pass it: the tile's maximum first
-          float top = mask ? masked_top(s_addr, kf, factor, valid_s[rg], here, half) : plain_top(s_addr, kf);
+          // scores that may pass the reference: the tile's maximum first
+          const float top = mask ? masked_top(s_addr, kf, factor, valid_s[rg], here, half) : plain_top(s_addr, kf);
           ok = swap(top, &other);
           if (!ok) break;
-          top = fmaxf(top, other);
-          const bool raise = top > ref + kRaise || (ref == -INFINITY && top > ref);
-          if (__any_sync(0xffffffffu, raise)) {
-            const float scale = raise ? exp2_fast(ref - top) : 1.f;
-            if (raise) ref = top;
+          const float to = raised(ref, fmaxf(top, other));
+          if (__any_sync(0xffffffffu, to != ref)) {
+            const float scale = to != ref ? exp2_fast(ref - to) : 1.f;
             if (t > t0) {
               // the output so far, once the product before has added to it
               ok = __all_sync(0xffffffffu, TQ_WAIT(bar.v_empty[(jt - 1) & 1], ((jt - 1) >> 1) & 1));
@@ -323,7 +321,10 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
               sum2 = mul2(sum2, pair(scale, scale));
               scale_output(lane_addr + kO + 64 * half, scale);
             }
+            ref = to;
           }
+        } else if (ref == -INFINITY && any != 0) {
+          ref = 0.f;                              // scores in bounds, and the row's first tokens (if it sees any here)
         }
         const float shift = ref == -INFINITY ? 0.f : ref;
         if (mask) sum2 = add2(sum2, pair(weigh_masked<true>(s_addr, kf, vf, factor, shift, valid_s[rg], here, half), 0.f));

@@ -432,21 +432,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         ptx::tc_fence_after();
         const TileMeta* const meta = reinterpret_cast<const TileMeta*>(smem + kMeta0) + (jt & (kRing - 1));
         const float* const kf = meta->key_factor + 64 * half;
-        const uint32_t all = meta->valid[0] & meta->valid[1] & meta->valid[2] & meta->valid[3];
+        const uint4 there = *reinterpret_cast<const uint4*>(meta->valid);
+        const uint32_t all = there.x & there.y & there.z & there.w, any = there.x | there.y | there.z | there.w;
         // (both the same for the two threads of a row, and so for their warps)
         const bool mask = __any_sync(0xffffffffu, e != 0 || seen < (t + 1) * kTile || all != 0xffffffffu);
-        const bool search = __any_sync(0xffffffffu, !(ref > -INFINITY && len * meta->reach <= ref + kRaise));
+        const bool search = __any_sync(0xffffffffu, !(len * meta->reach <= (ref == -INFINITY ? 0.f : ref) + kRaise));
         const int here = min(kTile, max(0, seen - t * kTile));
         if (search) {
-          // no reference yet, or scores that may pass it: the tile's maximum first
-          float top = mask ? masked_top(s_addr, kf, factor, meta->valid, here, half) : plain_top(s_addr, kf);
+          // scores that may pass the reference: the tile's maximum first
+          const float top = mask ? masked_top(s_addr, kf, factor, meta->valid, here, half) : plain_top(s_addr, kf);
           ok = swap(top, &other);
           if (!ok) break;
-          top = fmaxf(top, other);
-          const bool raise = top > ref + kRaise || (ref == -INFINITY && top > ref);
-          if (__any_sync(0xffffffffu, raise)) {
-            const float scale = raise ? exp2_fast(ref - top) : 1.f;
-            if (raise) ref = top;
+          const float to = raised(ref, fmaxf(top, other));
+          if (__any_sync(0xffffffffu, to != ref)) {
+            const float scale = to != ref ? exp2_fast(ref - to) : 1.f;
             if (t > t0) {
               // the output so far, once the product before has added to it
               ok = TQ_WARP_WAIT(bar.added[x], (jt - 1) & 1);
@@ -455,7 +454,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
               sum2 = mul2(sum2, pair(scale, scale));
               scale_output(o_addr, scale);
             }
+            ref = to;
           }
+        } else if (ref == -INFINITY && any != 0) {
+          ref = 0.f;                              // scores in bounds, and the row's first tokens (if it sees any here)
         }
         const float shift = ref == -INFINITY ? 0.f : ref;
         if (mask) sum2 = add2(sum2, pair(weigh_masked<false>(s_addr, kf, nullptr, factor, shift, meta->valid, here, half), 0.f));
