@@ -278,7 +278,9 @@ struct ExtendForm {
   CutItem* cuts;              // [ctas]: what run c begins and does not end
 };
 constexpr int kNarrowRows = 128, kWideRows = 256;
-constexpr int kNarrowCost = 3, kWideCost = 6;
+// (ragged prompts take 324, 298, 301, 322 us at a wide cost of 3, 4, 6, 9; a ragged
+// step of few rows 407, 396, 385, 389 us at a narrow cost of 2, 3, 5, 7)
+constexpr int kNarrowCost = 5, kWideCost = 4;
 
 // A key tile expanded for the wide form: the keys (R^T c + rho S^T signs,
 // fp16) and the values (n c, bf16, rotated) as swizzled 128 x 128 operands.
