@@ -146,6 +146,34 @@ bool walsh_coefficients(const std::vector<double>& levels, int bits, float* out)
   return ok;
 }
 
+// bf16 numbers out[i] and a factor with levels[i] ~ factor * out[i]: of 2^16
+// common multiples of the levels, the one whose worst relative rounding is
+// least (2^-11.7 for 3-bit codebooks and 2^-10.6 for 4 bits, where a plain
+// rounding is off by 2^-8.5), then the factor that fits best.
+float bf16_levels(const std::vector<double>& levels, float* out) {
+  double best = 1.0, multiple = 1.0;
+  for (int k = 0; k < (1 << 16); ++k) {
+    const double m = 1.0 + k / 65536.0;
+    double worst = 0.0;
+    for (size_t i = levels.size() / 2; i < levels.size(); ++i) {   // (odd-symmetric: the positive half)
+      const double x = m * levels[i];
+      worst = std::max(worst, std::fabs(bf16_value(bf16_bits(static_cast<float>(x))) / x - 1.0));
+    }
+    if (worst < best) {
+      best = worst;
+      multiple = m;
+    }
+  }
+  double xy = 0.0, yy = 0.0;
+  for (size_t i = 0; i < levels.size(); ++i) {
+    const double y = bf16_value(bf16_bits(static_cast<float>(multiple * levels[i])));
+    out[i] = static_cast<float>(y);
+    xy += levels[i] * y;
+    yy += y * y;
+  }
+  return static_cast<float>(xy / yy);
+}
+
 uint16_t fp16_bits(double x) {
   const __half h = __float2half_rn(static_cast<float>(x));
   uint16_t out;
@@ -207,6 +235,8 @@ tq_status upload_tables(tq_codebook* b) {
     t.k_bounds[i] = i < static_cast<int>(h.k_bounds.size()) ? static_cast<float>(h.k_bounds[i]) : INFINITY;
     t.v_bounds[i] = i < static_cast<int>(h.v_bounds.size()) ? static_cast<float>(h.v_bounds[i]) : INFINITY;
   }
+  std::fill(t.v_bf16, t.v_bf16 + tq::kMaxLevels, 0.f);
+  t.v_bf16_scale = bf16_levels(h.v_levels, t.v_bf16);
   b->walsh_ok = walsh_coefficients(h.k_levels, b->k_mse_bits, t.k_walsh) &&
                 walsh_coefficients(h.v_levels, b->v_bits, t.v_walsh) && !b->polar;
   std::vector<tq::DeviceTables> tv(1, t);

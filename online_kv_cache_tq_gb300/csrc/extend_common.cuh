@@ -546,8 +546,7 @@ __device__ __forceinline__ void load_value(const DecodeArgs& d, const Item& it, 
 //
 // A thread has 64 scores of its row at tensor-memory columns s .. s + 63 and
 // leaves its weights (bf16 pairs) in the first 32 of them.  kf, vf: the
-// columns' key and value factors in shared memory; VF: whether weights are
-// multiplied by a value factor (else the values are scaled already).
+// columns' key and value factors in shared memory.
 
 // The row's reference after a search found `top` (-inf: nothing visible).  A
 // first maximum in bounds leaves zero, as it would be without the search, so
@@ -558,7 +557,6 @@ __device__ __forceinline__ float raised(float ref, float top) {
 }
 
 // No score hidden, none that may pass the reference by 2^kRaise.
-template <bool VF>
 __device__ __forceinline__ void weigh_usual(uint32_t s, const float* kf, const float* vf, float ref, uint64_t& sum2) {
   const uint64_t minus = pair(-ref, -ref);
   uint32_t x[2][16];
@@ -577,12 +575,8 @@ __device__ __forceinline__ void weigh_usual(uint32_t s, const float* kf, const f
           unpair(fma2(pair(__uint_as_float(y[4 * k + 2]), __uint_as_float(y[4 * k + 3])), pair(f.z, f.w), minus));
       const uint64_t p0 = pair(exp2_fast(z0.x), exp2_fast(z0.y)), p1 = pair(exp2_fast(z1.x), exp2_fast(z1.y));
       sum2 = add2(sum2, add2(p0, p1));
-      float2 w0 = unpair(p0), w1 = unpair(p1);
-      if (VF) {
-        const float4 g = load16(vf + 16 * c + 4 * k);
-        w0 = unpair(mul2(p0, pair(g.x, g.y)));
-        w1 = unpair(mul2(p1, pair(g.z, g.w)));
-      }
+      const float4 g = load16(vf + 16 * c + 4 * k);
+      const float2 w0 = unpair(mul2(p0, pair(g.x, g.y))), w1 = unpair(mul2(p1, pair(g.z, g.w)));
       w[2 * k] = pack_bf16(w0.x, w0.y);
       w[2 * k + 1] = pack_bf16(w1.x, w1.y);
     }
@@ -643,7 +637,6 @@ __device__ __forceinline__ float masked_top(uint32_t s, const float* kf, float f
   return top;
 }
 
-template <bool VF>
 __device__ __forceinline__ float weigh_masked(uint32_t s, const float* kf, const float* vf, float factor, float shift,
                                               const uint32_t* valid, int here, int half) {
   float sum = 0.f;
@@ -657,7 +650,7 @@ __device__ __forceinline__ float weigh_masked(uint32_t s, const float* kf, const
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float4 f = load16(kf + 32 * c + 16 * h + 4 * k);
-        const float4 g = VF ? load16(vf + 32 * c + 16 * h + 4 * k) : make_float4(1.f, 1.f, 1.f, 1.f);
+        const float4 g = load16(vf + 32 * c + 16 * h + 4 * k);
         const float fk[4] = {f.x, f.y, f.z, f.w}, gk[4] = {g.x, g.y, g.z, g.w};
         float p[4];
 #pragma unroll
@@ -665,7 +658,7 @@ __device__ __forceinline__ float weigh_masked(uint32_t s, const float* kf, const
           const bool on = mask & (1u << expanded_bit(16 * h + 4 * k + q));
           p[q] = on ? exp2_fast(__uint_as_float(y[4 * k + q]) * fk[q] * factor - shift) : 0.f;
           sum += p[q];
-          if (VF) p[q] = on ? p[q] * gk[q] : 0.f;
+          p[q] = on ? p[q] * gk[q] : 0.f;
         }
         w[2 * k] = pack_bf16(p[0], p[1]);
         w[2 * k + 1] = pack_bf16(p[2], p[3]);

@@ -18,7 +18,10 @@
 //           (c[code_t], rho_t (2 bits_t - 1)), rho_t = gamma_t sqrt(pi/2) / (m n_t);
 //           n_t scale multiplies the score in fp32;
 //   output  [128 rows x 128 tokens] [128 x 128], bf16: p_t n^v_t against the
-//           value levels c^v[code_t], whose bits lie by token already.
+//           value levels c^v[code_t], whose bits lie by token already.  (The
+//           levels are scaled by a common factor for which bf16 holds them to
+//           2^-10.6; what rounding is left is that of the weights, up to 2^-9,
+//           which differs from token to token, and the output's.)
 // Queries and weights are operands in tensor memory (lane = row), so shared
 // memory feeds one operand only.  R q, S q and the back-rotation R^T are
 // products on the same tensor cores: their constants pass through the key
@@ -327,8 +330,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
           ref = 0.f;                              // scores in bounds, and the row's first tokens (if it sees any here)
         }
         const float shift = ref == -INFINITY ? 0.f : ref;
-        if (mask) sum2 = add2(sum2, pair(weigh_masked<true>(s_addr, kf, vf, factor, shift, valid_s[rg], here, half), 0.f));
-        else weigh_usual<true>(s_addr, kf, vf, shift, sum2);
+        if (mask) sum2 = add2(sum2, pair(weigh_masked(s_addr, kf, vf, factor, shift, valid_s[rg], here, half), 0.f));
+        else weigh_usual(s_addr, kf, vf, shift, sum2);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar.p_full[sb]);
@@ -443,7 +446,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
   } else if (warp < 20) {
     // ---------------- values ----------------
     const int dim = tid - kSoftThreads - kKeyThreads;   // also the column whose token's factor this thread writes
-    const LevelBytes lev = level_bytes<true>(d.tables->v_levels, VB);
+    const LevelBytes lev = level_bytes<true>(d.tables->v_bf16, VB);
+    const float scale = d.tables->v_bf16_scale;
     int jt = 0;
     if (tid == kSoftThreads + kKeyThreads) write_cut(a, a.narrow, run, per, true);
     while (ok && next_segment(a, a.narrow, run, t0, t1)) {
@@ -474,7 +478,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
           expand32<VB, 0>(second_word(at), w1, lev);
           at = next_block(at);
         }
-        value_factor[rg * kTile + dim] = v.norm;
+        value_factor[rg * kTile + dim] = v.norm * scale;
         ptx::fence_async_shared();
         ptx::mbar_arrive(&bar.v_full[s]);
       }

@@ -4,9 +4,9 @@
 // a sequence into two operands, once: the keys back in the original space,
 //   k_t = R^T c[code_t] + rho_t S^T (2 bits_t - 1)       (unit norm, fp16),
 // a product on the tensor cores of the expanded bits with R^T and S^T, and the
-// values n^v_t c^v[code_t] (rotated space, bf16).  They are stored in the
+// value levels c^v[code_t] (rotated space, bf16).  They are stored in the
 // swizzled layout the products read, 64 KB a tile, so that a tile is two bulk
-// copies later.  Per token and KV head this costs 98 K operations and writes
+// copies later.  Per token and KV head this costs 66 K operations and writes
 // 520 bytes; it saves every row tile the expansion and half of the score
 // product (128 columns in place of 256 with the sketch).
 //
@@ -14,7 +14,7 @@
 // take turns, so that the softmax of one runs under the products of the other.
 //   scores  [128 x 128] = q k^T, fp16, queries in shared memory as they come
 //           (scaled by a power of two outside 2^-8 .. 2^10);
-//   output  [128 x 128] += p v, bf16, weights in tensor memory over the scores;
+//   output  [128 x 128] += p n^v c, bf16, weights in tensor memory over the scores;
 // the last step turns the output back by R^T.  The softmax is that of the
 // narrow form (extend_tc.cu: its reference, and when a tile may skip the
 // search for its maximum).  The bound of the loop is the tensor cores: 2048
@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
   uint8_t* const keys_s = smem + kExpandKey0 + group * 4 * kBlockBytes;
   const int row = tid & (kTile - 1), half = tid / kTile;   // key row or value coordinate; half of the other side
   const LevelBytes key_levels = level_bytes<false>(d.tables->k_levels, KB);
-  const LevelBytes value_levels = level_bytes<false>(d.tables->v_levels, VB);
+  const LevelBytes value_levels = level_bytes<true>(d.tables->v_bf16, VB);
+  const float value_scale = d.tables->v_bf16_scale;
   const float to_log2 = d.scale * 1.4426950408889634f;
   // (the first two warps of a half read its 64 value norms, by expanded column)
   const int mine = row < 64 ? row >> 5 : -1;
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
       sh.factor[row] = k.valid ? k.norm * to_log2 : 0.f;
       if (lane == 0) sh.valid[warp] = bit;
     }
-    if (mine >= 0) sh.norm[64 * half + row] = v.norm;
+    if (mine >= 0) sh.norm[64 * half + row] = v.norm * value_scale;
     ptx::fence_async_shared();
     group_sync(group, false);
     if (warp == 0 && ptx::elect_one()) {
@@ -176,29 +177,13 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
     const bool ok = TQ_WAIT(sh.done, phase);
     if (group_sync(group, !ok)) break;
     // the product has read its operand: the tile's image takes its place
+    {
+      const RowChunks at = row_chunks(ptx::smem_u32(keys_s + kExtendImageBytes) + half * kBlockBytes, row);
+      uint32_t w0[VB], w1[VB];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      uint32_t planes[VB];
-#pragma unroll
-      for (int p = 0; p < VB; ++p) planes[p] = v.words[p][w];
-      if constexpr (VB == 4) {
-#pragma unroll
-        for (int p = 0; p < 3; ++p) planes[p] = planes[p] ^ ~planes[3];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 levels = expand8<VB>(planes, i, value_levels);
-        const uint32_t l[4] = {levels.x, levels.y, levels.z, levels.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&l[e]));
-          const float2 n = *reinterpret_cast<const float2*>(&sh.norm[64 * half + 32 * w + 8 * i + 2 * e]);
-          o[e] = pack_bf16(f.x * n.x, f.y * n.y);
-        }
-        *reinterpret_cast<uint4*>(keys_s + kExtendImageBytes + half * kBlockBytes + row * 128 +
-                                  (((4 * w + i) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-      }
+      for (int p = 0; p < VB; ++p) w0[p] = v.words[p][0], w1[p] = v.words[p][1];
+      expand32<VB, 0>(at, w0, value_levels);
+      expand32<VB, 0>(second_word(at), w1, value_levels);
     }
     ptx::tc_fence_after();
     {
@@ -227,6 +212,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
     if (tid < kTile) {
       const float f = sh.factor[tid];
       meta->key_factor[tid] = f;
+      meta->value_factor[tid] = sh.norm[tid];
       const float reach = fabsf(f) * sqrtf(sh.square[0][tid] + sh.square[1][tid]);
       const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(reach) & 0x7fffffffu);   // (not negative)
       if (lane == 0) {
@@ -431,7 +417,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         if (!ok) break;
         ptx::tc_fence_after();
         const TileMeta* const meta = reinterpret_cast<const TileMeta*>(smem + kMeta0) + (jt & (kRing - 1));
-        const float* const kf = meta->key_factor + 64 * half;
+        const float *const kf = meta->key_factor + 64 * half, *const vf = meta->value_factor + 64 * half;
         const uint4 there = *reinterpret_cast<const uint4*>(meta->valid);
         const uint32_t all = there.x & there.y & there.z & there.w, any = there.x | there.y | there.z | there.w;
         // (both the same for the two threads of a row, and so for their warps)
@@ -460,8 +446,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
           ref = 0.f;                              // scores in bounds, and the row's first tokens (if it sees any here)
         }
         const float shift = ref == -INFINITY ? 0.f : ref;
-        if (mask) sum2 = add2(sum2, pair(weigh_masked<false>(s_addr, kf, nullptr, factor, shift, meta->valid, here, half), 0.f));
-        else weigh_usual<false>(s_addr, kf, nullptr, shift, sum2);
+        if (mask) sum2 = add2(sum2, pair(weigh_masked(s_addr, kf, vf, factor, shift, meta->valid, here, half), 0.f));
+        else weigh_usual(s_addr, kf, vf, shift, sum2);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar.p_full[x]);

@@ -283,10 +283,11 @@ constexpr int kNarrowRows = 128, kWideRows = 256;
 constexpr int kNarrowCost = 5, kWideCost = 4;
 
 // A key tile expanded for the wide form: the keys (R^T c + rho S^T signs,
-// fp16) and the values (n c, bf16, rotated) as swizzled 128 x 128 operands.
+// fp16) and the value levels (bf16, rotated) as swizzled 128 x 128 operands.
 constexpr int kTileImageBytes = 2 * kExtendImageBytes;
 struct __align__(16) TileMeta {
   float key_factor[kDim];     // n scale log2(e) by operand row; 0 where there is no token
+  float value_factor[kDim];   // what a weight is multiplied by: the value's norm and the levels' scale
   uint32_t valid[4];          // tokens there are, by group of 32
   float reach;                // largest |factor key|
   float pad[3];

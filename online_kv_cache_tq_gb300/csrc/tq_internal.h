@@ -29,6 +29,11 @@ struct DeviceTables {
   // {1,2,3}).  Exact for the symmetric Lloyd-Max codebooks.
   float k_walsh[8];
   float v_walsh[8];
+  // Value levels as bf16 operands: v_bf16[i] are bf16 numbers and v_level[i]
+  // is v_bf16_scale * v_bf16[i] far closer than to a half step of bf16 (the
+  // common factor is chosen so that all of them round well).
+  float v_bf16[kMaxLevels];
+  float v_bf16_scale;
 };
 
 // Odd sign-plane subsets, as bit masks over the code bits, in walsh[] order.
