@@ -14,6 +14,12 @@ namespace {
 
 // Rows (new tokens x query heads of the group) from which a sequence takes the
 // wide form, and most expanded tiles that a workspace holds (2 GiB).
+// Sixteen sequences on 8192 (0) cached tokens, 32/8 heads, us, wide | narrow:
+//                2-bit keys, sketch, 3-bit values     4-bit keys, 4-bit values
+//    256 rows    333 | 242   (41 | 39)                334 | 305   (41 | 39)
+//    384         437 | 346   (50 | 52)                436 | 439   (51 | 51)
+//    512         443 | 450   (51 | 62)                441 | 575   (53 | 61)
+//   1024         651 | 861   (83 | 112)               652 | 1120  (84 | 113)
 constexpr int kWideFrom = 512;
 constexpr long long kTileCap = 1 << 15;
 

@@ -21,6 +21,11 @@
 // cycles of products for 256 x 128 scores, plus twice the time from a
 // product's end to the issue of the one that overwrites its operand.
 //
+// Measured.  2048 tokens on 14001, 64/8 heads: 706 us, 1.42 PFLOP/s, 3.4 K
+// cycles for 256 x 128 scores, tensor pipe 60 % busy; expansion 29 us.  Short
+// items cost 15 K cycles outside the loop (ragged prompts up to 4096 tokens,
+// 32/8 heads: 268 us, 0.80 PFLOP/s; expansion 24 us).
+//
 // Eighteen warps: 0-7 and 8-15 the softmax of the two row tiles (two threads
 // per row), 16 issues the products, 17 copies tiles.
 #include "extend_common.cuh"

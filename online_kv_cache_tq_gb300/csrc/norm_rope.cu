@@ -11,7 +11,9 @@
 // neighbours), and the norm is four shuffles.  Sixteen lanes take a run of one
 // token's heads: each lane forms the four cosines and sines of its pairs once
 // and keeps them in registers, and there is no barrier between runs.  A lane
-// has 64 bytes in flight.
+// has 64 bytes in flight.  32768 tokens x 72 heads, bf16: 207 us, 5.8 TB/s, 0.86 of
+// a plain copy (a partner eight lanes away and barriers between tokens: 430 us;
+// partners in one lane: 315 us).
 //
 // Angles: position * inv_freq loses its fraction of a turn in 32 bits at far
 // positions.  inv_freq / (2 pi) is kept as a 64-bit fixed-point fraction of a
