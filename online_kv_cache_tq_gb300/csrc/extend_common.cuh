@@ -383,9 +383,9 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
 
 // 2^e for a normal exponent.
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
-__device__ __forceinline__ int exponent_of(float x) {   // clamped so that 2^-e is a normal number
+__device__ __forceinline__ int exponent_of(float x) {   // clamped so that 2^e and 2^-e are normal numbers
   const int e = static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127;
-  return e < -100 ? -100 : (e > 100 ? 100 : e);
+  return e < -126 ? -126 : (e > 126 ? 126 : e);
 }
 
 __device__ __forceinline__ void unpack_bf16(const uint4& w, float (&v)[8]) {

@@ -208,6 +208,33 @@ def test_query_magnitudes(q_scale):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("new", [3, 300])
+def test_queries_near_the_largest_numbers(new, dtype):
+    # every query points along one long key (30 times the others) and has coordinates up to 2^118: the scores are
+    # finite numbers in 32 bits (6e37), and the weights are those of that token alone
+    c = Case([new], [400], n_kv=1, group=4, seed=20, dtype=dtype)
+    g = generator(5)
+    k = torch.randn((400, 1, 128), generator=g, device="cuda")
+    k[5] *= 30.0
+    v = torch.randn((400, 1, 128), generator=g, device="cuda")
+    slots = torch.as_tensor(W.slots_for(c.table[0], np.arange(400), 64), device="cuda")
+    B.tq_quantize_append(c.book, k, v, B.TQ_FP32, 400, 1, slots, C.cache_view(c.book, c.cache))
+    c.q.copy_((k[5] * 4e33).expand_as(c.q))
+    assert float(c.q.abs().max()) > 2.0 ** 117
+    c.run()
+    torch.cuda.synchronize()
+    assert B.tq_get_last_device_error(c.book) == 0
+    expect, _ = reference(c.q.double().cpu().numpy(), host_cache(c.cache), c.table[0], 400, new, 0, c.ref,
+                          1.0 / math.sqrt(128))
+    got = c.out.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    # one weight, so only the weight's and the value levels' roundings, R^T's and the output's are left
+    size = np.linalg.norm(expect, axis=2, keepdims=True)
+    assert (np.abs(got - expect) <= size * (2.1 * V + 4 * U) + V * np.abs(expect)).all()
+
+
+@pytest.mark.gpu
 def test_tokens_over_decades_of_magnitude_and_zero_vectors():
     c = Case([30], [400], seed=9, n_kv=1, group=8)
     g = generator(3)
