@@ -55,7 +55,7 @@ __device__ __forceinline__ bool group_sync(int group, bool flag) {
   return r != 0;
 }
 
-// Bulk copy shared -> global, and the wait until its reads are done.
+// Bulk copy shared -> global, and the waits until its reads and its writes are done.
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
                ::"l"(reinterpret_cast<uint64_t>(dst)), "r"(ptx::smem_u32(src)), "r"(bytes)
@@ -63,6 +63,7 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 __device__ __forceinline__ void bulk_store_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // What a group's threads share about their tile.
 struct ExpandShared {
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
     if (tid == 0) bulk_store_wait();
     group_sync(group, false);                     // (the next tile overwrites what was read)
   }
+  if (tid == 0) bulk_store_done();                // nothing is in flight when the CTA ends
   __syncthreads();
   if (threadIdx.x < 32) ptx::tmem_dealloc(tmem_s, 256);
 }

@@ -264,13 +264,14 @@ __host__ __device__ constexpr int swizzled_f16(int row, int col) {
 constexpr int kExtendImages = 5;
 constexpr int kExtendImageBytes = kDim * kDim * 2;
 
+// A row tile that the run which begins it and those up to `last` share.
+struct CutItem {
+  int row0, kvh, i, rows, last;   // first row of the sequence, KV head, row tile, rows (0: none)
+};
 // One of the two forms of the attention: the rows of its row tiles, what an
 // item costs besides its key tiles (in key tiles), the units of work (cost and
 // key tiles of the items) before each sequence's first ([batch + 1]), and the
 // partial outputs of the row tiles that its CTAs' runs cut.
-struct CutItem {              // a row tile that the runs from `run` to `last` share
-  int row0, kvh, i, rows, last;   // first row of the sequence, KV head, row tile, rows (0: none)
-};
 struct ExtendForm {
   int rows, cost;
   long long* first;
