@@ -91,10 +91,10 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(ExtendArgs a)
       const int n = seq_s[k].x, ctx = seq_s[k].y;
       long long narrow = 0, wide = 0;
       for (int i = lane; i < row_tiles(kNarrowRows, n, group); i += 32)
-        narrow += kNarrowCost + key_tiles(i, kNarrowRows, n, ctx, group);
+        narrow += kNarrowCost + key_tiles(a, i, kNarrowRows, n, ctx);
       if (a.tile_cap > 0)
         for (int i = lane; i < row_tiles(kWideRows, n, group); i += 32)
-          wide += kWideCost + key_tiles(i, kWideRows, n, ctx, group);
+          wide += kWideCost + key_tiles(a, i, kWideRows, n, ctx);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) {
         narrow += __shfl_xor_sync(0xffffffffu, narrow, d);

@@ -66,10 +66,15 @@ __device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity, volat
 
 // ---- work items ------------------------------------------------------------
 
+// Token of row r of a sequence and KV head: r / group.
+__device__ __forceinline__ int row_token(const ExtendArgs& a, int r) {
+  return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(r)) * a.group_mul) >> (31 + a.group_shift));
+}
+
 // Key tiles of row tile i (`rows` rows) of a sequence: those its last token
 // sees, at least one (rows that see nothing still need their zero output).
-__device__ __forceinline__ int key_tiles(int i, int rows, int n_new, int ctx, int group) {
-  const int last = min(n_new - 1, (rows * (i + 1) - 1) / group);
+__device__ __forceinline__ int key_tiles(const ExtendArgs& a, int i, int rows, int n_new, int ctx) {
+  const int last = min(n_new - 1, row_token(a, rows * (i + 1) - 1));
   const int seen = ctx - n_new + last + 1;
   return seen <= kTile ? 1 : (seen + kTile - 1) / kTile;
 }
@@ -116,7 +121,7 @@ __device__ __forceinline__ Item find_item(const ExtendArgs& a, const ExtendForm&
   it.tiles = 0;
   *offset = 0;
   for (int i0 = 0; i0 < mt; i0 += 32) {
-    const int nt = i0 + lane < mt ? key_tiles(i0 + lane, f.rows, it.seq.y, it.seq.z, a.d.group) : 0;
+    const int nt = i0 + lane < mt ? key_tiles(a, i0 + lane, f.rows, it.seq.y, it.seq.z) : 0;
     const long long units = i0 + lane < mt ? nt + f.cost : 0;
     long long upto = units;
 #pragma unroll
@@ -148,7 +153,7 @@ __device__ __forceinline__ void next_item(const ExtendArgs& a, const ExtendForm&
       it.seq = a.ws_seq[it.b];
     }
   }
-  it.tiles = key_tiles(it.i, f.rows, it.seq.y, it.seq.z, a.d.group);
+  it.tiles = key_tiles(a, it.i, f.rows, it.seq.y, it.seq.z);
 }
 
 // The run's next segment: key tiles t0 .. t1 - 1 of r.it.  `end_segment` moves behind it.
@@ -413,9 +418,6 @@ __device__ __forceinline__ void copy16_async(void* dst, const void* src) {
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Vector (token x query head) of row r of an item's sequence and KV head.
-__device__ __forceinline__ int row_token(const ExtendArgs& a, int r) {
-  return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(r)) * a.group_mul) >> (31 + a.group_shift));
-}
 __device__ __forceinline__ long long row_vector(const ExtendArgs& a, int row0, int kvh, int r) {
   const int tok = row_token(a, r);
   return (static_cast<long long>(row0) + tok) * a.d.n_q + kvh * a.d.group + r - tok * a.d.group;

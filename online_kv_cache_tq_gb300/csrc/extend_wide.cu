@@ -260,7 +260,6 @@ constexpr uint32_t kS = 0, kO = 256;              // tensor-memory columns, 128 
 struct WideBarriers {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2], added[2], o_raw[2], turned[2];   // by row tile
-  uint64_t shared[2];        // the eight warps of a row tile, for what they leave in shared memory
   uint64_t q_full, drain;
   uint64_t rows[8];          // the two warps that share 32 rows
 };
@@ -273,7 +272,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
   __shared__ Item item_s;
   __shared__ int offset_s;
   __shared__ float swap_s[2][2][kWideRows];       // what the two threads of a row tell each other
-  __shared__ float2 query_s[kWideRows];           // length and exponent of a row's query
+  __shared__ float2 query_s[2][kWideRows];        // largest coordinate and squared length of half a row's query
   uint8_t* const smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   const DecodeArgs& d = a.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -302,7 +301,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
       ptx::mbar_init(&bar.added[s], 1);
       ptx::mbar_init(&bar.o_raw[s], kSoftThreads / 2);
       ptx::mbar_init(&bar.turned[s], 1);
-      ptx::mbar_init(&bar.shared[s], kSoftThreads / 2);
     }
     ptx::mbar_init(&bar.q_full, kSoftThreads);
     ptx::mbar_init(&bar.drain, 1);
@@ -338,23 +336,23 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
     const uint32_t s_addr = lane_addr + kS + 128 * x + 64 * half, o_addr = lane_addr + kO + 128 * x + 64 * half;
     uint64_t* const pair_bar = &bar.rows[4 * x + quarter];
     int swaps = 0;
+    auto meet = [&]() {                           // the row's two threads (their warps)
+      ptx::mbar_arrive(pair_bar);
+      return TQ_WARP_WAIT(*pair_bar, swaps++ & 1);
+    };
     auto swap = [&](float mine, float* theirs) {  // the other thread of the row: its value of `mine`
       float(*const buf)[kWideRows] = swap_s[swaps & 1];
       buf[half][kTile * x + row] = mine;
-      ptx::mbar_arrive(pair_bar);
-      const bool done = TQ_WARP_WAIT(*pair_bar, swaps & 1);
+      const bool done = meet();
       *theirs = buf[half ^ 1][kTile * x + row];
-      ++swaps;
       return done;
     };
-    int meetings = 0;
-    auto together = [&]() {                       // all eight warps of the row tile
-      ptx::mbar_arrive(&bar.shared[x]);
-      return TQ_WARP_WAIT(bar.shared[x], meetings++ & 1);
-    };
-    // rows copy_row, copy_row + 2, .. + 14 and 16 bytes of each, for copies between memory and shared memory
-    const int copy_row = 16 * (warp & 7) + (lane >> 4), copy_chunk = lane & 15;
-    uint8_t* const copy_base = smem + kQuery0 + x * kImage + (copy_chunk >> 3) * kBlockBytes;
+    // A warp copies queries and outputs between memory and shared memory for its
+    // own rows and columns only, eight lanes to the 128 bytes of half a row: rows
+    // copy_row, copy_row + 4, .. + 28, 16 bytes of each.
+    const int copy_row = 32 * quarter + (lane >> 3), copy_chunk = lane & 7;
+    uint8_t* const half_s = smem + kQuery0 + x * kImage + half * kBlockBytes;
+    auto swizzled = [&](int qr, int chunk) { return reinterpret_cast<uint4*>(half_s + qr * 128 + (((chunk ^ qr) & 7) << 4)); };
     int jt = 0;                                   // key tiles so far
     for (int seg = 0; next_segment(a, a.wide, run, t0, t1); ++seg) {
       const int n_rows = it.seq.y * d.group;
@@ -363,59 +361,60 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
       const int tok = row_token(a, live ? r : n_rows - 1);
       const int seen = max(0, it.seq.z - it.seq.y + tok + 1);     // positions this row sees
       float other;
-      // The queries, sixteen lanes to a row (whole lines, and a row's largest
-      // coordinate and length in four shuffles): fp16, scaled by a power of
-      // two if outside the range, swizzled.  bf16 rows are copied to their
-      // place first, all in flight at once, and converted where they lie; the
-      // loops are short because this code is met cold, once per segment.
-      uint8_t* const copy_at = copy_base + copy_row * 128;
+      // The queries: fp16, scaled by a power of two if outside the range,
+      // swizzled.  bf16 rows are copied to their place first, in whole lines and
+      // all in flight at once (a warp copies what it converts), then a thread
+      // converts its half of a row where it lies.
       if (a.q_bf16) {
 #pragma unroll 1
         for (int k = 0; k < 8; ++k) {
-          const int rr = it.i * kWideRows + kTile * x + copy_row + 2 * k;
+          const int qr = copy_row + 4 * k, rr = it.i * kWideRows + kTile * x + qr;
           const long long vec = row_vector(a, it.seq.x, it.kvh, min(rr, n_rows - 1));
-          copy16_async(copy_at + k * 256 + (((copy_chunk ^ (copy_row + 2 * k)) & 7) << 4),
-                       static_cast<const __nv_bfloat16*>(d.q) + vec * kDim + copy_chunk * 8);
+          copy16_async(swizzled(qr, copy_chunk),
+                       static_cast<const __nv_bfloat16*>(d.q) + vec * kDim + 64 * half + copy_chunk * 8);
         }
         copies_wait();
+        __syncwarp();
       }
-#pragma unroll 1
-      for (int k = 0; k < 8; ++k) {
-        const int qr = copy_row + 2 * k, rr = it.i * kWideRows + kTile * x + qr;
-        uint4* const place = reinterpret_cast<uint4*>(copy_at + k * 256 + (((copy_chunk ^ qr) & 7) << 4));
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (rr < n_rows) {
-          if (a.q_bf16) unpack_bf16(*place, v);
-          else load_query8(a, row_vector(a, it.seq.x, it.kvh, rr) * kDim + copy_chunk * 8, v);
-        }
-        float biggest = 0.f, square = 0.f;
+      const long long query = row_vector(a, it.seq.x, it.kvh, live ? r : n_rows - 1) * kDim + 64 * half;
+      auto query8 = [&](int c, float (&v)[8]) {     // (rows that are not there convert another row's query)
+        if (a.q_bf16) unpack_bf16(*swizzled(row, c), v);
+        else load_query8(a, query + 8 * c, v);
+      };
+      float biggest = 0.f;
+      uint64_t square2 = 0;                       // (two fp32 zeros)
+#pragma unroll 2
+      for (int c = 0; c < 8; ++c) {
+        float v[8];
+        query8(c, v);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          biggest = fmaxf(biggest, fabsf(v[q]));
-          square = fmaf(v[q], v[q], square);
+        for (int q = 0; q < 8; q += 2) {
+          biggest = fmaxf(biggest, fmaxf(fabsf(v[q]), fabsf(v[q + 1])));
+          square2 = fma2(pair(v[q], v[q + 1]), pair(v[q], v[q + 1]), square2);
         }
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) {
-          biggest = fmaxf(biggest, __shfl_xor_sync(0xffffffffu, biggest, o));
-          square += __shfl_xor_sync(0xffffffffu, square, o);
-        }
-        int qe = exponent_of(biggest);
-        if (biggest == 0.f || (qe >= -8 && qe < 10)) qe = 0;
-        const float down = exp2_int(-qe);
-        if (copy_chunk == 0) query_s[kTile * x + qr] = make_float2(sqrtf(square), static_cast<float>(qe));
+      }
+      float2 square = unpair(square2);
+      square.x += square.y;
+      query_s[half][kTile * x + row] = make_float2(biggest, square.x);
+      ok = meet();
+      if (!ok) break;
+      const float2 others = query_s[half ^ 1][kTile * x + row];
+      biggest = fmaxf(biggest, others.x);
+      const float len = sqrtf(square.x + others.y) * 1.01f;       // (1.01: the operands' roundings)
+      int e = exponent_of(biggest);
+      if (biggest == 0.f || (e >= -8 && e < 10)) e = 0;
+      const float down = exp2_int(-e), factor = exp2_int(e);
+#pragma unroll 2
+      for (int c = 0; c < 8; ++c) {
+        float v[8];
+        query8(c, v);
         uint32_t w[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) w[q] = pack_f16(v[2 * q] * down, v[2 * q + 1] * down);
-        *place = make_uint4(w[0], w[1], w[2], w[3]);
+        *swizzled(row, c) = make_uint4(w[0], w[1], w[2], w[3]);
       }
       ptx::fence_async_shared();
       ptx::mbar_arrive(&bar.q_full);
-      ok = together();
-      if (!ok) break;
-      const float2 query = query_s[kTile * x + row];
-      const float len = query.x * 1.01f;          // (1.01: the operands' roundings)
-      const int e = static_cast<int>(query.y);
-      const float factor = exp2_int(e);
 
       float ref = -INFINITY;
       uint64_t sum2 = 0;                          // (two fp32 zeros)
@@ -493,16 +492,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         store_partial(o_addr, exp2_int(eo), part + part_row * kDim + 64 * half, live);
       } else {
         // bf16 rows through the queries' place in shared memory, to leave in whole lines
-        output_rows(o_addr, exp2_int(eo), smem + kQuery0 + x * kImage + half * kBlockBytes + row * 128, row);
-        ok = together();
-        if (!ok) break;
+        output_rows(o_addr, exp2_int(eo), half_s + row * 128, row);
+        __syncwarp();
 #pragma unroll 2
         for (int k = 0; k < 8; ++k) {
-          const int qr = copy_row + 2 * k, rr = it.i * kWideRows + kTile * x + qr;
+          const int qr = copy_row + 4 * k, rr = it.i * kWideRows + kTile * x + qr;
           if (rr < n_rows)
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row_vector(a, it.seq.x, it.kvh, rr) * kDim + copy_chunk * 8) =
-                *reinterpret_cast<const uint4*>(copy_base + qr * 128 + (((copy_chunk & 7) ^ (qr & 7)) << 4));
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row_vector(a, it.seq.x, it.kvh, rr) * kDim +
+                                      64 * half + copy_chunk * 8) = *swizzled(qr, copy_chunk);
         }
+        __syncwarp();                             // (the next queries take their place)
       }
       ptx::tc_fence_before();
       end_segment(a, a.wide, run, t1);
