@@ -645,6 +645,11 @@ __device__ __forceinline__ float weigh_masked(uint32_t s, const float* kf, const
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
     const uint32_t mask = visible(valid, here, 2 * half + c);
+    if (!__any_sync(0xffffffffu, mask != 0)) {    // no row of the warp sees them
+#pragma unroll
+      for (int h = 0; h < 2; ++h) ptx::tmem_st8(s + 16 * c + 8 * h, 0, 0, 0, 0, 0, 0, 0, 0);
+      continue;
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t y[16], w[8];
