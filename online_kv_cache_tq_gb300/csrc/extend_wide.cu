@@ -360,6 +360,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
       const bool live = r < n_rows;
       const int tok = row_token(a, live ? r : n_rows - 1);
       const int seen = max(0, it.seq.z - it.seq.y + tok + 1);     // positions this row sees
+      // vector (token x query head) of row rr of the sequence and KV head (below 2^31)
+      const uint32_t first_vec = it.seq.x * d.n_q + it.kvh * d.group, other_heads = d.n_q - d.group;
+      auto vector_of = [&](int rr) { return static_cast<long long>(first_vec + row_token(a, rr) * other_heads + rr); };
       float other;
       // The queries: fp16, scaled by a power of two if outside the range,
       // swizzled.  bf16 rows are copied to their place first, in whole lines and
@@ -369,14 +372,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
 #pragma unroll 1
         for (int k = 0; k < 8; ++k) {
           const int qr = copy_row + 4 * k, rr = it.i * kWideRows + kTile * x + qr;
-          const long long vec = row_vector(a, it.seq.x, it.kvh, min(rr, n_rows - 1));
+          const long long vec = vector_of(min(rr, n_rows - 1));
           copy16_async(swizzled(qr, copy_chunk),
                        static_cast<const __nv_bfloat16*>(d.q) + vec * kDim + 64 * half + copy_chunk * 8);
         }
         copies_wait();
         __syncwarp();
       }
-      const long long query = row_vector(a, it.seq.x, it.kvh, live ? r : n_rows - 1) * kDim + 64 * half;
+      const long long query = vector_of(live ? r : n_rows - 1) * kDim + 64 * half;
       auto query8 = [&](int c, float (&v)[8]) {     // (rows that are not there convert another row's query)
         if (a.q_bf16) unpack_bf16(*swizzled(row, c), v);
         else load_query8(a, query + 8 * c, v);
@@ -498,8 +501,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         for (int k = 0; k < 8; ++k) {
           const int qr = copy_row + 4 * k, rr = it.i * kWideRows + kTile * x + qr;
           if (rr < n_rows)
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row_vector(a, it.seq.x, it.kvh, rr) * kDim +
-                                      64 * half + copy_chunk * 8) = *swizzled(qr, copy_chunk);
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + vector_of(rr) * kDim + 64 * half +
+                                      copy_chunk * 8) = *swizzled(qr, copy_chunk);
         }
         __syncwarp();                             // (the next queries take their place)
       }
