@@ -17,6 +17,10 @@ constexpr int kBlockBytes = kTile * 128;          // a 64-column K block of a 12
 // log2 by which scores may pass the reference (zero at first): 2^80 leaves fp32
 // sums and bf16 weights room for 2^20 tokens with values of 2^27.
 constexpr float kRaise = 80.f;
+// References up to which a score may keep its product's low bits while the
+// reference, a rounded product, does not: they differ by 2^-24 of it, 1/16 here.
+// Beyond, both are rounded alike (else 2^32 could leave an exponent of 256).
+constexpr float kFused = 1048576.f;
 
 // kind::f16 with fp16 or bf16 operands, fp32 accumulators, 128 x 128.
 constexpr uint32_t kIdescBf16 = ptx::idesc_bf16_f32(128, 128);

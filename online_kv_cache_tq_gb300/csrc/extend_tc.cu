@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
         const float top_bound = fmaf(len_r, fmaxf(fmaxf(reach0.x, reach0.z), fmaxf(reach1.x, reach1.z)),
                                      len_s * fmaxf(fmaxf(reach0.y, reach0.w), fmaxf(reach1.y, reach1.w)));
         // (both the same for the two threads of a row, and so for their warps)
-        const bool mask = __any_sync(0xffffffffu, e != 0 || seen < (t + 1) * kTile || all != 0xffffffffu);
+        bool mask = __any_sync(0xffffffffu, e != 0 || seen < (t + 1) * kTile || all != 0xffffffffu);
         const bool search = __any_sync(0xffffffffu, !(top_bound <= (ref == -INFINITY ? 0.f : ref) + kRaise));
         const int here = min(kTile, max(0, seen - t * kTile));
         if (search) {
@@ -335,6 +335,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
             }
             ref = to;
           }
+          // (a tile that is not searched stays 1 % below a large reference)
+          mask = mask || __any_sync(0xffffffffu, fabsf(ref) < INFINITY && fabsf(ref) > kFused);
         } else if (ref == -INFINITY && any != 0) {
           ref = 0.f;                              // scores in bounds, and the row's first tokens (if it sees any here)
         }

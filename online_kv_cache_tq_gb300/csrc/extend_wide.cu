@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         const uint4 there = *reinterpret_cast<const uint4*>(meta->valid);
         const uint32_t all = there.x & there.y & there.z & there.w, any = there.x | there.y | there.z | there.w;
         // (both the same for the two threads of a row, and so for their warps)
-        const bool mask = __any_sync(0xffffffffu, e != 0 || seen < (t + 1) * kTile || all != 0xffffffffu);
+        bool mask = __any_sync(0xffffffffu, e != 0 || seen < (t + 1) * kTile || all != 0xffffffffu);
         const bool search = __any_sync(0xffffffffu, !(len * meta->reach <= (ref == -INFINITY ? 0.f : ref) + kRaise));
         const int here = min(kTile, max(0, seen - t * kTile));
         if (search) {
@@ -451,6 +451,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
             }
             ref = to;
           }
+          // (a tile that is not searched stays 1 % below a large reference)
+          mask = mask || __any_sync(0xffffffffu, fabsf(ref) < INFINITY && fabsf(ref) > kFused);
         } else if (ref == -INFINITY && any != 0) {
           ref = 0.f;                              // scores in bounds, and the row's first tokens (if it sees any here)
         }

@@ -210,18 +210,20 @@ def test_query_magnitudes(q_scale):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("new", [3, 300])
-def test_queries_near_the_largest_numbers(new, dtype):
-    # every query points along one long key (30 times the others) and has coordinates up to 2^118: the scores are
-    # finite numbers in 32 bits (6e37), and the weights are those of that token alone
+@pytest.mark.parametrize("q_scale,k_scale", [(4e33, 1.0), (1 / 30, 1e9), (4e8, 1e4)])
+def test_scores_of_huge_magnitude(new, dtype, q_scale, k_scale):
+    # every query points along one long key (30 times the others), with coordinates up to 2^118 or keys of 1e11: the
+    # scores are finite numbers in 32 bits (6e37, 5e11, 6e16), and the weights are those of that token alone
     c = Case([new], [400], n_kv=1, group=4, seed=20, dtype=dtype)
     g = generator(5)
     k = torch.randn((400, 1, 128), generator=g, device="cuda")
     k[5] *= 30.0
+    direction = k[5] * q_scale
+    k *= k_scale
     v = torch.randn((400, 1, 128), generator=g, device="cuda")
     slots = torch.as_tensor(W.slots_for(c.table[0], np.arange(400), 64), device="cuda")
     B.tq_quantize_append(c.book, k, v, B.TQ_FP32, 400, 1, slots, C.cache_view(c.book, c.cache))
-    c.q.copy_((k[5] * 4e33).expand_as(c.q))
-    assert float(c.q.abs().max()) > 2.0 ** 117
+    c.q.copy_(direction.expand_as(c.q))
     c.run()
     torch.cuda.synchronize()
     assert B.tq_get_last_device_error(c.book) == 0
