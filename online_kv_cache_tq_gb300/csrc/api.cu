@@ -146,18 +146,29 @@ bool walsh_coefficients(const std::vector<double>& levels, int bits, float* out)
   return ok;
 }
 
-// bf16 numbers out[i] and a factor with levels[i] ~ factor * out[i]: of 2^16
-// common multiples of the levels, the one whose worst relative rounding is
-// least (2^-11.7 for 3-bit codebooks and 2^-10.6 for 4 bits, where a plain
-// rounding is off by 2^-8.5), then the factor that fits best.
-float bf16_levels(const std::vector<double>& levels, float* out) {
+uint16_t fp16_bits(double x) {
+  const __half h = __float2half_rn(static_cast<float>(x));
+  uint16_t out;
+  std::memcpy(&out, &h, sizeof(out));
+  return out;
+}
+
+double to_bf16(double x) { return bf16_value(bf16_bits(static_cast<float>(x))); }
+double to_fp16(double x) { return __half2float(__float2half_rn(static_cast<float>(x))); }
+
+// Numbers out[i] of a 16-bit type and a factor with levels[i] ~ factor * out[i]:
+// of 2^16 common multiples of the levels, the one whose worst relative
+// rounding is least, then the factor that fits best.  (Worst of a level in
+// bf16: 2^-11.7 for 3-bit codebooks and 2^-10.6 for 4 bits, where a plain
+// rounding is off by 2^-8.5; fp16 is three bits finer.)
+float rounded_levels(const std::vector<double>& levels, double (*rounded)(double), float* out) {
   double best = 1.0, multiple = 1.0;
   for (int k = 0; k < (1 << 16); ++k) {
     const double m = 1.0 + k / 65536.0;
     double worst = 0.0;
     for (size_t i = levels.size() / 2; i < levels.size(); ++i) {   // (odd-symmetric: the positive half)
       const double x = m * levels[i];
-      worst = std::max(worst, std::fabs(bf16_value(bf16_bits(static_cast<float>(x))) / x - 1.0));
+      worst = std::max(worst, std::fabs(rounded(x) / x - 1.0));
     }
     if (worst < best) {
       best = worst;
@@ -166,19 +177,12 @@ float bf16_levels(const std::vector<double>& levels, float* out) {
   }
   double xy = 0.0, yy = 0.0;
   for (size_t i = 0; i < levels.size(); ++i) {
-    const double y = bf16_value(bf16_bits(static_cast<float>(multiple * levels[i])));
+    const double y = rounded(multiple * levels[i]);
     out[i] = static_cast<float>(y);
     xy += levels[i] * y;
     yy += y * y;
   }
   return static_cast<float>(xy / yy);
-}
-
-uint16_t fp16_bits(double x) {
-  const __half h = __float2half_rn(static_cast<float>(x));
-  uint16_t out;
-  std::memcpy(&out, &h, sizeof(out));
-  return out;
 }
 
 // The multi-token attention's operand images (see kExtendImages in kernels.h),
@@ -236,7 +240,9 @@ tq_status upload_tables(tq_codebook* b) {
     t.v_bounds[i] = i < static_cast<int>(h.v_bounds.size()) ? static_cast<float>(h.v_bounds[i]) : INFINITY;
   }
   std::fill(t.v_bf16, t.v_bf16 + tq::kMaxLevels, 0.f);
-  t.v_bf16_scale = bf16_levels(h.v_levels, t.v_bf16);
+  std::fill(t.k_fp16, t.k_fp16 + tq::kMaxLevels, 0.f);
+  t.v_bf16_scale = rounded_levels(h.v_levels, to_bf16, t.v_bf16);
+  b->k_fp16_scale = rounded_levels(h.k_levels, to_fp16, t.k_fp16);
   b->walsh_ok = walsh_coefficients(h.k_levels, b->k_mse_bits, t.k_walsh) &&
                 walsh_coefficients(h.v_levels, b->v_bits, t.v_walsh) && !b->polar;
   std::vector<tq::DeviceTables> tv(1, t);
@@ -1143,7 +1149,9 @@ tq_status tq_extend_attention(const tq_codebook* book, const void* q, tq_dtype d
   d.max_blocks = max_blocks;
   d.context_lens = context_lens;
   d.max_context = max_context;
-  d.scale = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(book->cfg.d));
+  // (k_fp16_scale: the factor of the key levels, which the sketch does not have)
+  d.scale = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(book->cfg.d))) * book->k_fp16_scale;
+  d.qjl_coef /= book->k_fp16_scale;
   a.n_tokens = n_tokens;
   a.query_start = query_start;
   a.out = out;

@@ -328,6 +328,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
   return w;
 }
+// What is left of (lo, hi) beside the bf16 pair `w`, as another one.
+__device__ __forceinline__ uint32_t remainder_bf16(float lo, float hi, uint32_t w) {
+  return pack_bf16(lo - __uint_as_float(w << 16), hi - __uint_as_float(w & 0xffff0000u));
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t w;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
@@ -551,8 +555,13 @@ __device__ __forceinline__ void load_value(const DecodeArgs& d, const Item& it, 
 // ---- softmax of a score tile ---------------------------------------------------
 //
 // A thread has 64 scores of its row at tensor-memory columns s .. s + 63 and
-// leaves its weights (bf16 pairs) in the first 32 of them.  kf, vf: the
-// columns' key and value factors in shared memory.
+// leaves its weights (bf16 pairs) in the first 32 of them, and what the
+// rounding left of the last sixteen in the next 8 (another step of the output
+// product).  kf, vf: the columns' key and value factors in shared memory.
+//
+// The weights' rounding is as large as the output's own (1.7e-3 of it each in
+// the rms); every other rounding brings the sum to 1.5 times the latter.  A
+// quarter of the remainders makes it 1.4.
 
 // The row's reference after a search found `top` (-inf: nothing visible).  A
 // first maximum in bounds leaves zero, as it would be without the search, so
@@ -565,7 +574,7 @@ __device__ __forceinline__ float raised(float ref, float top) {
 // No score hidden, none that may pass the reference by 2^kRaise.
 __device__ __forceinline__ void weigh_usual(uint32_t s, const float* kf, const float* vf, float ref, uint64_t& sum2) {
   const uint64_t minus = pair(-ref, -ref);
-  uint32_t x[2][16];
+  uint32_t x[2][16], rest[8];
   tmem_ld16_start(s, x[0]);
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -585,9 +594,14 @@ __device__ __forceinline__ void weigh_usual(uint32_t s, const float* kf, const f
       const float2 w0 = unpair(mul2(p0, pair(g.x, g.y))), w1 = unpair(mul2(p1, pair(g.z, g.w)));
       w[2 * k] = pack_bf16(w0.x, w0.y);
       w[2 * k + 1] = pack_bf16(w1.x, w1.y);
+      if (c == 3) {
+        rest[2 * k] = remainder_bf16(w0.x, w0.y, w[2 * k]);
+        rest[2 * k + 1] = remainder_bf16(w1.x, w1.y, w[2 * k + 1]);
+      }
     }
     ptx::tmem_st8(s + 8 * c, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
   }
+  ptx::tmem_st8(s + 32, rest[0], rest[1], rest[2], rest[3], rest[4], rest[5], rest[6], rest[7]);
 }
 
 // Visible tokens of group g (32 bits by token) when `here` of the tile's are
@@ -646,12 +660,15 @@ __device__ __forceinline__ float masked_top(uint32_t s, const float* kf, float f
 __device__ __forceinline__ float weigh_masked(uint32_t s, const float* kf, const float* vf, float factor, float shift,
                                               const uint32_t* valid, int here, int half) {
   float sum = 0.f;
+  uint32_t rest[8];                               // (of the last sixteen)
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
     const uint32_t mask = visible(valid, here, 2 * half + c);
     if (!__any_sync(0xffffffffu, mask != 0)) {    // no row of the warp sees them
 #pragma unroll
       for (int h = 0; h < 2; ++h) ptx::tmem_st8(s + 16 * c + 8 * h, 0, 0, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) rest[k] = 0;
       continue;
     }
 #pragma unroll
@@ -673,10 +690,13 @@ __device__ __forceinline__ float weigh_masked(uint32_t s, const float* kf, const
         }
         w[2 * k] = pack_bf16(p[0], p[1]);
         w[2 * k + 1] = pack_bf16(p[2], p[3]);
+        rest[2 * k] = remainder_bf16(p[0], p[1], w[2 * k]);
+        rest[2 * k + 1] = remainder_bf16(p[2], p[3], w[2 * k + 1]);
       }
       ptx::tmem_st8(s + 16 * c + 8 * h, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
     }
   }
+  ptx::tmem_st8(s + 32, rest[0], rest[1], rest[2], rest[3], rest[4], rest[5], rest[6], rest[7]);
   return sum;
 }
 

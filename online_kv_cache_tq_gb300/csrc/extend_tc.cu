@@ -16,7 +16,9 @@
 // into shared memory:
 //   scores  [128 rows x 256] [256 x 128 tokens], fp16: q~ = (R q, S q) against
 //           (c[code_t], rho_t (2 bits_t - 1)), rho_t = gamma_t sqrt(pi/2) / (m n_t);
-//           n_t scale multiplies the score in fp32;
+//           n_t scale multiplies the score in fp32 (the levels are scaled by
+//           a common factor for which fp16 holds them to 2^-13.4, and rho_t
+//           with them);
 //   output  [128 rows x 128 tokens] [128 x 128], bf16: p_t n^v_t against the
 //           value levels c^v[code_t], whose bits lie by token already.  (The
 //           levels are scaled by a common factor for which bf16 holds them to
@@ -386,9 +388,9 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
     // ---------------- keys ----------------
     const int row = (tid - kSoftThreads) & (kTile - 1);   // row of the tile: token expanded_bit(lane) of the warp's group
     const int half = (tid - kSoftThreads) / kTile;        // coordinates 64 half .. + 63 of both operand halves
-    const LevelBytes lev = level_bytes<false>(d.tables->k_levels, KB);
+    const LevelBytes lev = level_bytes<false>(d.tables->k_fp16, KB);
     float biggest = 0.f;                          // the outermost level
-    for (int i = 0; i < (1 << KB); ++i) biggest = fmaxf(biggest, fabsf(d.tables->k_levels[i]));
+    for (int i = 0; i < (1 << KB); ++i) biggest = fmaxf(biggest, fabsf(d.tables->k_fp16[i]));
     const float to_log2 = d.scale * 1.4426950408889634f;
     int kc = 0, jt = 0;                           // ring entries, key tiles so far
     auto image = [&](int first, int count) {      // operand images as a ring entry
@@ -549,6 +551,9 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
           const uint64_t v = value_desc + s * (kValueBytes / 16);
           product<4>(tmem + kO, w, v, kIdescBf16, t > t0);
           product<4>(tmem + kO, w + 64, v + kBlockBytes / 16, kIdescBf16, true);
+          // (the last sixteen of each 64 once more, their remainders)
+          product<1>(tmem + kO, w + 32, v + 6, kIdescBf16, true);
+          product<1>(tmem + kO, w + 96, v + kBlockBytes / 16 + 6, kIdescBf16, true);
           ptx::mma_commit(&bar.v_empty[s]);
         }
         __syncwarp();

@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
   const uint32_t tmem = tmem_s + 128 * group;
   uint8_t* const keys_s = smem + kExpandKey0 + group * 4 * kBlockBytes;
   const int row = tid & (kTile - 1), half = tid / kTile;   // key row or value coordinate; half of the other side
-  const LevelBytes key_levels = level_bytes<false>(d.tables->k_levels, KB);
+  const LevelBytes key_levels = level_bytes<false>(d.tables->k_fp16, KB);
   const LevelBytes value_levels = level_bytes<true>(d.tables->v_bf16, VB);
   const float value_scale = d.tables->v_bf16_scale;
   const float to_log2 = d.scale * 1.4426950408889634f;
@@ -552,6 +552,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
             const uint64_t v = value_desc + (jt & 1) * (kImage / 16);
             product<4>(o, w, v, kIdescBf16, t > t0);
             product<4>(o, w + 64, v + kBlockBytes / 16, kIdescBf16, true);
+            // (the last sixteen of each 64 once more, their remainders)
+            product<1>(o, w + 32, v + 6, kIdescBf16, true);
+            product<1>(o, w + 96, v + kBlockBytes / 16 + 6, kIdescBf16, true);
             ptx::mma_commit(&bar.added[x]);
             if (x == 1) ptx::mma_commit(&bar.v_empty[jt & 1]);
           }

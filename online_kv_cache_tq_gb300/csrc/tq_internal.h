@@ -34,6 +34,7 @@ struct DeviceTables {
   // common factor is chosen so that all of them round well).
   float v_bf16[kMaxLevels];
   float v_bf16_scale;
+  float k_fp16[kMaxLevels];   // key levels likewise, as fp16 numbers (factor: tq_codebook::k_fp16_scale)
 };
 
 // Odd sign-plane subsets, as bit masks over the code bits, in walsh[] order.
@@ -74,6 +75,7 @@ struct tq_codebook {
   float* d_Spt;       // [d][m] S' transposed (column k of S' is row k)
   float* d_St;        // [d][m] S transposed: S q = S' R q for a query q
   uint16_t* d_rot_tc; // bf16 hi/lo operand images for the tensor-core quantizer
+  float k_fp16_scale;  // of DeviceTables::k_fp16
   uint16_t* d_rot_f16; // fp16 operand images for the multi-token attention (kernels.h)
   tq::DeviceTables* d_tables;
   int* d_error;       // first device-side error code, 0 when none
