@@ -446,8 +446,9 @@ size_t tq_extend_workspace_bytes(const tq_codebook* book, int n_tokens, int batc
  * h / (n_q_heads / n_kv_heads), any whole ratio.  out: device bf16
  * [n_tokens][n_q_heads][128]; rows behind query_start[batch] are left as they
  * were.  Queries (scaled by a power of two where that is needed) and keys are
- * rounded to fp16, softmax weights to bf16, value levels to bf16 by a common
- * factor that holds them to 2^-10; every sum is float32, and the output is
+ * rounded to fp16, softmax weights to bf16 (a quarter of them with a second
+ * bf16 number for the remainder), value levels to bf16 by a common factor that
+ * holds them to 2^-10; every sum is float32, and the output is
  * rounded to bf16 once at the end.  The same call gives the
  * same bits.  cache, block_table, max_blocks, max_context and scale as in
  * tq_decode_attention (max_context bounds every context_lens[b] and is at most

@@ -16,10 +16,10 @@ namespace {
 // wide form, and most expanded tiles that a workspace holds (2 GiB).
 // Sixteen sequences on 8192 (0) cached tokens, 32/8 heads, us, wide | narrow:
 //                2-bit keys, sketch, 3-bit values     4-bit keys, 4-bit values
-//    256 rows    333 | 242   (41 | 39)                334 | 305   (41 | 39)
-//    384         437 | 346   (50 | 52)                436 | 439   (51 | 51)
-//    512         443 | 450   (51 | 62)                441 | 575   (53 | 61)
-//   1024         651 | 861   (83 | 112)               652 | 1120  (84 | 113)
+//    256 rows    337 | 248   (40 | 39)                338 | 303   (39 | 39)
+//    384         447 | 355   (48 | 51)                448 | 437   (48 | 51)
+//    512         450 | 463   (50 | 63)                451 | 573   (49 | 61)
+//   1024         674 | 890   (76 | 112)               674 | 1118  (76 | 114)
 constexpr int kWideFrom = 512;
 constexpr long long kTileCap = 1 << 15;
 

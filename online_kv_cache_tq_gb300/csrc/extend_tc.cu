@@ -23,7 +23,9 @@
 //           value levels c^v[code_t], whose bits lie by token already.  (The
 //           levels are scaled by a common factor for which bf16 holds them to
 //           2^-10.6; what rounding is left is that of the weights, up to 2^-8,
-//           which differs from token to token, and the output's.)
+//           which differs from token to token, and the output's.  What the
+//           weights' rounding leaves of a quarter of the tokens is added by a
+//           product of its own.)
 // Queries and weights are operands in tensor memory (lane = row), so shared
 // memory feeds one operand only.  R q, S q and the back-rotation R^T are
 // products on the same tensor cores: their constants pass through the key
@@ -46,10 +48,12 @@
 // the output, the query operand.
 //
 // Measured.  16 sequences x 4 tokens at context 8192, 32/8 heads, 2-bit keys
-// with the sketch, 3-bit values: 109 us for 113 MB of cache (1.04 TB/s), 3.6 K
-// cycles a key tile, of which the products take 1.6 K.  What bounds a tile is
-// the expansion of its 49 K elements (7.0 K warp instructions, 1.9 a cycle,
-// the logic pipe 47 % busy) and how far the softmax overlaps with it.  Eight
+// with the sketch, 3-bit values: 113 us for 113 MB of cache (1.0 TB/s), 3.8 K
+// cycles a key tile, of which the products take 1.7 K.  What bounds a tile is
+// the expansion of its 49 K elements (7.1 K warp instructions, 1.9 a cycle,
+// the logic pipe 46 % busy) and how far the softmax overlaps with it.  (Few
+// rows repeated over all 128, every softmax warp with a part of the tokens:
+// 152 against 119 us, so the softmax of few rows is not what a tile waits for.)  Eight
 // warps for keys and four for values: four and four took 117 us there but 456
 // against 393 us for 24 sequences of 1 to 16 tokens with 64/8 heads; eight and
 // eight 127 and 418 us; eight and four 119 and 393 us.

@@ -17,14 +17,16 @@
 //   output  [128 x 128] += p n^v c, bf16, weights in tensor memory over the scores;
 // the last step turns the output back by R^T.  The softmax is that of the
 // narrow form (extend_tc.cu: its reference, and when a tile may skip the
-// search for its maximum).  The bound of the loop is the tensor cores: 2048
-// cycles of products for 256 x 128 scores, plus twice the time from a
+// search for its maximum).  The bound of the loop is the tensor cores: 2304
+// cycles of products for 256 x 128 scores (256 of them for the remainders), plus twice the time from a
 // product's end to the issue of the one that overwrites its operand.
 //
-// Measured.  2048 tokens on 14001, 64/8 heads: 706 us, 1.42 PFLOP/s, 3.4 K
-// cycles for 256 x 128 scores, tensor pipe 60 % busy; expansion 29 us.  Short
-// items cost 15 K cycles outside the loop (ragged prompts up to 4096 tokens,
-// 32/8 heads: 268 us, 0.80 PFLOP/s; expansion 24 us).
+// Measured.  2048 tokens on 14001, 64/8 heads: 753 us, 1.34 PFLOP/s, 3.6 K
+// cycles for 256 x 128 scores, tensor pipe 64 % busy; expansion 28 us.  Short
+// items cost 13 K cycles outside the loop (ragged prompts up to 4096 tokens,
+// 32/8 heads: 249 us, 0.86 PFLOP/s; expansion 25 us).  Queries held in
+// registers from one reading to the next spill into the loop (310 against 287
+// us for those prompts, 852 against 753 us for the 2048 tokens).
 //
 // Eighteen warps: 0-7 and 8-15 the softmax of the two row tiles (two threads
 // per row), 16 issues the products, 17 copies tiles.
