@@ -727,14 +727,17 @@ __device__ __forceinline__ float largest_output(uint32_t o, float inv) {
   return top;
 }
 
-// 64 columns of the output as an fp16 operand at `dst` (32 columns).
-__device__ __forceinline__ void output_operand(uint32_t o, uint32_t dst, float scale) {
+// 64 columns of the output, divided by the row's sum and by a power of two, as
+// an fp16 operand at `dst` (32 columns).  (One after the other: the two factors'
+// product can pass fp32's range, and zero times infinity is no zero.)
+__device__ __forceinline__ void output_operand(uint32_t o, uint32_t dst, float inv, float down) {
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t y[16], w[8];
     ptx::tmem_ld16(o + 16 * c, y);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w[k] = pack_f16(__uint_as_float(y[2 * k]) * scale, __uint_as_float(y[2 * k + 1]) * scale);
+    for (int k = 0; k < 8; ++k)
+      w[k] = pack_f16(__uint_as_float(y[2 * k]) * inv * down, __uint_as_float(y[2 * k + 1]) * inv * down);
     ptx::tmem_st8(dst + 8 * c, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
   }
 }

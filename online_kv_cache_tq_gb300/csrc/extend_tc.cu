@@ -369,8 +369,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       ok = swap(top, &other);
       if (!ok) break;
       const int eo = exponent_of(fmaxf(top, other));
-      const float out_down = inv * exp2_int(-eo), out_up = exp2_int(eo);
-      output_operand(lane_addr + kO + 64 * half, lane_addr + kS0 + 32 * half, out_down);
+      const float out_up = exp2_int(eo);
+      output_operand(lane_addr + kO + 64 * half, lane_addr + kS0 + 32 * half, inv, exp2_int(-eo));
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       ptx::mbar_arrive(&bar.o_raw);

@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
       ok = swap(top, &other);
       if (!ok) break;
       const int eo = exponent_of(fmaxf(top, other));
-      output_operand(o_addr, lane_addr + kS + 128 * x + 32 * half, inv * exp2_int(-eo));
+      output_operand(o_addr, lane_addr + kS + 128 * x + 32 * half, inv, exp2_int(-eo));
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       ptx::mbar_arrive(&bar.o_raw[x]);

@@ -457,3 +457,22 @@ def test_refusals():
     args[2] = 0
     B.tq_extend_attention(c.book, *args)           # no tokens: nothing to do
     assert B.tq_get_last_device_error(c.book) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [3, 300])
+def test_zero_values_under_small_weights(new):
+    # every score is near -15 (as a power of two), so the weights sum to 2^-6 or less; the values a row sees first are
+    # zero vectors: zero rows, not 0 * infinity
+    c = Case([new], [new], n_kv=1, group=4, seed=25)
+    g = generator(8)
+    base = torch.randn((1, 1, 128), generator=g, device="cuda")
+    k = base + 0.05 * torch.randn((new, 1, 128), generator=g, device="cuda")
+    v = torch.randn((new, 1, 128), generator=g, device="cuda")
+    v[:max(2, new // 2)] = 0.0
+    slots = torch.as_tensor(W.slots_for(c.table[0], np.arange(new), 64), device="cuda")
+    B.tq_quantize_append(c.book, k, v, B.TQ_FP32, new, 1, slots, C.cache_view(c.book, c.cache))
+    c.q.copy_((base[0, 0] * (-10.0 * math.sqrt(128.0) / float(base.norm()) ** 2)).expand_as(c.q))
+    c.run()
+    c.check()
+    assert bool((c.out[:max(2, new // 2)] == 0).all())
