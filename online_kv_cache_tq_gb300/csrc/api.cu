@@ -205,6 +205,21 @@ std::vector<uint16_t> extend_images(const tq::HostTables& h) {
   return img;
 }
 
+// The largest e for which coordinates below 2^e keep every coordinate of R q
+// and S q (a row's sum of magnitudes times 2^e at most) under 2^15.9: fp16
+// ends at 2^16, and the operands' roundings add less than 2^-8 of it.
+int query_top(const tq::HostTables& h) {
+  double most = 0.0;
+  for (const std::vector<double>* m : {&h.R, &h.S}) {
+    for (size_t r = 0; r < m->size(); r += tq::kDim) {
+      double sum = 0.0;
+      for (int c = 0; c < tq::kDim; ++c) sum += std::fabs((*m)[r + c]);
+      most = std::max(most, sum);
+    }
+  }
+  return static_cast<int>(std::floor(15.9 - std::log2(most)));
+}
+
 tq_status upload_tables(tq_codebook* b) {
   const int d = b->cfg.d;
   const int m = b->cfg.qjl_m;
@@ -243,6 +258,7 @@ tq_status upload_tables(tq_codebook* b) {
   std::fill(t.k_fp16, t.k_fp16 + tq::kMaxLevels, 0.f);
   t.v_bf16_scale = rounded_levels(h.v_levels, to_bf16, t.v_bf16);
   b->k_fp16_scale = rounded_levels(h.k_levels, to_fp16, t.k_fp16);
+  b->query_top = query_top(h);
   b->walsh_ok = walsh_coefficients(h.k_levels, b->k_mse_bits, t.k_walsh) &&
                 walsh_coefficients(h.v_levels, b->v_bits, t.v_walsh) && !b->polar;
   std::vector<tq::DeviceTables> tv(1, t);
@@ -1157,6 +1173,7 @@ tq_status tq_extend_attention(const tq_codebook* book, const void* q, tq_dtype d
   a.out = out;
   a.q_bf16 = dtype == TQ_BF16;
   a.images = reinterpret_cast<const uint4*>(book->d_rot_f16);
+  a.query_top = book->query_top;
   DeviceGuard guard(book->device);
   return launched(tq::launch_extend(a, workspace, static_cast<cudaStream_t>(stream)));
 }

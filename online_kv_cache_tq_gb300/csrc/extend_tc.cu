@@ -30,8 +30,8 @@
 // memory feeds one operand only.  R q, S q and the back-rotation R^T are
 // products on the same tensor cores: their constants pass through the key
 // ring as tiles of their own, so no other buffer and no other launch is
-// needed.  A query is scaled by a power of two into fp16's range when its
-// largest coordinate is outside 2^-8 .. 2^10.
+// needed.  A query is scaled by a power of two when its largest coordinate is
+// outside 2^-8 .. 2^query_top, up to which R q and S q fit fp16.
 //
 // Softmax.  No maximum is searched as long as the lengths of the query and of
 // the tile's keys bound the scores by 2^80 in either direction: fp32 and bf16
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
       if (!ok) break;
       biggest = fmaxf(biggest, other);
       int e = exponent_of(biggest);
-      if (biggest == 0.f || (e >= -8 && e < 10)) e = 0;
+      if (biggest == 0.f || (e >= -8 && e < a.query_top)) e = 0;
       const float down = exp2_int(-e), factor = exp2_int(e);
 #pragma unroll 1
       for (int h = 0; h < 4; ++h) {

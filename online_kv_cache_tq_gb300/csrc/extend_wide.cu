@@ -13,7 +13,7 @@
 // extend_wide_kernel then works on row tiles of 256: two products of 128 rows
 // take turns, so that the softmax of one runs under the products of the other.
 //   scores  [128 x 128] = q k^T, fp16, queries in shared memory as they come
-//           (scaled by a power of two outside 2^-8 .. 2^10);
+//           (scaled by a power of two outside 2^-8 .. 2^query_top);
 //   output  [128 x 128] += p n^v c, bf16, weights in tensor memory over the scores;
 // the last step turns the output back by R^T.  The softmax is that of the
 // narrow form (extend_tc.cu: its reference, and when a tile may skip the
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
       biggest = fmaxf(biggest, others.x);
       const float len = sqrtf(square.x + others.y) * 1.01f;       // (1.01: the operands' roundings)
       int e = exponent_of(biggest);
-      if (biggest == 0.f || (e >= -8 && e < 10)) e = 0;
+      if (biggest == 0.f || (e >= -8 && e < a.query_top)) e = 0;
       const float down = exp2_int(-e), factor = exp2_int(e);
 #pragma unroll 2
       for (int c = 0; c < 8; ++c) {

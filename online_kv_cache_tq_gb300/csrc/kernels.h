@@ -301,6 +301,7 @@ struct ExtendArgs {
   void* out;                  // bf16 [n_tokens][n_q][128]
   bool q_bf16;
   const uint4* images;
+  int query_top;              // coordinates below 2^query_top keep R q and S q in fp16's range
   uint32_t group_mul;         // row / group = row * group_mul >> 31 + group_shift (31-bit rows)
   int group_shift;
   // workspace regions

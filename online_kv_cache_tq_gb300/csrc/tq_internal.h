@@ -76,6 +76,7 @@ struct tq_codebook {
   float* d_St;        // [d][m] S transposed: S q = S' R q for a query q
   uint16_t* d_rot_tc; // bf16 hi/lo operand images for the tensor-core quantizer
   float k_fp16_scale;  // of DeviceTables::k_fp16
+  int query_top;       // largest exponent of a query's coordinates that the multi-token attention takes unscaled
   uint16_t* d_rot_f16; // fp16 operand images for the multi-token attention (kernels.h)
   tq::DeviceTables* d_tables;
   int* d_error;       // first device-side error code, 0 when none

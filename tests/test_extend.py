@@ -476,3 +476,15 @@ def test_zero_values_under_small_weights(new):
     c.run()
     c.check()
     assert bool((c.out[:max(2, new // 2)] == 0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [3, 300])
+@pytest.mark.parametrize("size", [300.0, 500.0, 800.0, 1000.0])
+def test_queries_along_rows_of_the_sketch(new, size):
+    # the signs of a row of S make S q as large as it can be: `size` times the row's sum of magnitudes, 118000 for 1000
+    c = Case([new], [400], n_kv=1, group=4, scale=1e-4, seed=21)
+    rows = np.sign(c.ref["proj"][np.arange(c.total * 4) % 128]).reshape(c.total, 4, 128)
+    c.q.copy_(torch.as_tensor(size * rows))
+    c.run()
+    c.check()
