@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
   __shared__ Item item_s;
   __shared__ int offset_s;
   __shared__ float swap_s[2][2][kTile];           // what the two threads of a row tell each other
-  __shared__ __align__(16) float2 reach_s[kRing][4];           // per 32 tokens of a tile: bounds of the longest scaled key halves
+  __shared__ __align__(16) uint2 reach_s[kRing][4];            // per 32 tokens of a tile: bounds (bits) of the longest scaled key halves
   __shared__ __align__(16) uint32_t valid_s[kRing][4];         // tokens of a tile, by expanded column
 
   // 1024-byte aligned, as an offset from smem_raw so that accesses stay shared-space
@@ -314,11 +314,12 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
         const float* const vf = value_factor + rg * kTile + 64 * half;
         const uint4 there = *reinterpret_cast<const uint4*>(valid_s[rg]);
         const uint32_t all = there.x & there.y & there.z & there.w, any = there.x | there.y | there.z | there.w;
-        const float4 reach0 = *reinterpret_cast<const float4*>(&reach_s[rg][0]);
-        const float4 reach1 = *reinterpret_cast<const float4*>(&reach_s[rg][2]);
-        // |score| <= |R q| |n c| + |S q| |n rho signs|
-        const float top_bound = fmaf(len_r, fmaxf(fmaxf(reach0.x, reach0.z), fmaxf(reach1.x, reach1.z)),
-                                     len_s * fmaxf(fmaxf(reach0.y, reach0.w), fmaxf(reach1.y, reach1.w)));
+        const uint4 reach0 = *reinterpret_cast<const uint4*>(&reach_s[rg][0]);
+        const uint4 reach1 = *reinterpret_cast<const uint4*>(&reach_s[rg][2]);
+        // |score| <= |R q| |n c| + |S q| |n rho signs|  (largest as bits, so that a NaN stays: it makes the tile be searched)
+        const float top_bound =
+            fmaf(len_r, __uint_as_float(max(max(reach0.x, reach0.z), max(reach1.x, reach1.z))),
+                 len_s * __uint_as_float(max(max(reach0.y, reach0.w), max(reach1.y, reach1.w))));
         // (both the same for the two threads of a row, and so for their warps)
         bool mask = __any_sync(0xffffffffu, e != 0 || seen < (t + 1) * kTile || all != 0xffffffffu);
         const bool search = __any_sync(0xffffffffu, !(top_bound <= (ref == -INFINITY ? 0.f : ref) + kRaise));
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
           const unsigned bit = __reduce_or_sync(0xffffffffu, k.valid ? 1u << expanded_bit(lane) : 0u);
           if (lane == 0) {
             valid_s[rg][row >> 5] = bit;
-            reach_s[rg][row >> 5] = make_float2(__uint_as_float(bits_c), __uint_as_float(bits_q));
+            reach_s[rg][row >> 5] = make_uint2(bits_c, bits_q);
           }
         }
         ptx::fence_async_shared();

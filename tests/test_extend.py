@@ -488,3 +488,37 @@ def test_queries_along_rows_of_the_sketch(new, size):
     c.q.copy_(torch.as_tensor(size * rows))
     c.run()
     c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [6, 140])
+def test_nan_of_a_hidden_key_next_to_large_scores(new):
+    # the last token's key is NaN and lies in the same group of 32 tokens as a key whose score is 2^140 above the
+    # others'; only the last token sees it
+    ctx = max(30, new)
+    c = Case([new], [ctx], n_kv=1, group=4, seed=22)
+    g = generator(6)
+    k = torch.randn((ctx, 1, 128), generator=g, device="cuda")
+    long = ctx - new                               # (every row sees it)
+    k[long] *= 30.0
+    v = torch.randn((ctx, 1, 128), generator=g, device="cuda")
+    slots = torch.as_tensor(W.slots_for(c.table[0], np.arange(ctx), 64), device="cuda")
+    B.tq_quantize_append(c.book, k, v, B.TQ_FP32, ctx, 1, slots, C.cache_view(c.book, c.cache))
+    direction = k[long, 0].cpu().numpy() * (100.0 * math.sqrt(128.0) / float(k[long].norm()) ** 2)
+    c.q.copy_(torch.as_tensor(direction).expand_as(c.q))
+    c.run()
+    c.check(sequences=[])
+    first = c.out.clone()
+    assert bool(torch.isfinite(first.float()).all())
+    for hidden in (ctx - 1, (long // 32) * 32 + 31):
+        if hidden <= long or hidden >= ctx:
+            continue
+        last = (int(c.table[0, hidden // 64]), slice(None), hidden % 64)
+        kept = c.cache["k_norm"][last].clone()
+        c.cache["k_norm"][last] = float("nan")
+        c.run()
+        torch.cuda.synchronize()
+        rows = new - (ctx - hidden)                # rows before the hidden token
+        assert torch.equal(first[:rows], c.out[:rows])
+        assert bool(torch.isnan(c.out[rows:].float()).any())
+        c.cache["k_norm"][last] = kept
