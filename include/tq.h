@@ -449,8 +449,9 @@ size_t tq_extend_workspace_bytes(const tq_codebook* book, int n_tokens, int batc
  * rounded to fp16, softmax weights to bf16 (a quarter of them with a second
  * bf16 number for the remainder), value levels to bf16 by a common factor that
  * holds them to 2^-10; every sum is float32, and the output is
- * rounded to bf16 once at the end.  The same call gives the
- * same bits.  cache, block_table, max_blocks, max_context and scale as in
+ * rounded to bf16 once at the end.  Value vectors may have lengths from 2^-40
+ * to 2^27, and zero (weights are held as multiples of up to 2^80 or 2^-80).
+ * The same call gives the same bits.  cache, block_table, max_blocks, max_context and scale as in
  * tq_decode_attention (max_context bounds every context_lens[b] and is at most
  * 2^30, else TQ_ERR_UNSUPPORTED).  workspace: device scratch of
  * tq_extend_workspace_bytes bytes, 256-byte aligned, not used by any

@@ -522,3 +522,22 @@ def test_nan_of_a_hidden_key_next_to_large_scores(new):
         assert torch.equal(first[:rows], c.out[:rows])
         assert bool(torch.isnan(c.out[rows:].float()).any())
         c.cache["k_norm"][last] = kept
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [3, 300])
+@pytest.mark.parametrize("score,value_scale", [(52.0, 2.0 ** 23), (-52.0, 2.0 ** -43)])
+def test_values_at_the_ends_of_their_range_with_scores_far_from_zero(new, score, value_scale):
+    # every score is near +-75 (as a power of two), just inside the bound below which no maximum is searched, and the
+    # values have the largest and smallest lengths that the interface allows
+    c = Case([new], [400], n_kv=1, group=4, seed=23)
+    g = generator(7)
+    base = torch.randn((1, 1, 128), generator=g, device="cuda")
+    k = base + 0.05 * torch.randn((400, 1, 128), generator=g, device="cuda")
+    v = torch.randn((400, 1, 128), generator=g, device="cuda") * value_scale
+    slots = torch.as_tensor(W.slots_for(c.table[0], np.arange(400), 64), device="cuda")
+    B.tq_quantize_append(c.book, k, v, B.TQ_FP32, 400, 1, slots, C.cache_view(c.book, c.cache))
+    q = base[0, 0] * (score * math.sqrt(128.0) / float(base.norm()) ** 2)
+    c.q.copy_(q.expand_as(c.q))
+    c.run()
+    c.check()
