@@ -165,11 +165,12 @@ __global__ void __launch_bounds__(kMapThreads) token_map_kernel(TokenMapArgs a) 
 }  // namespace
 
 cudaError_t launch_token_map(const TokenMapArgs& a, cudaStream_t stream) {
-  static_assert(2 * (kMapMaxBatch + 1) * sizeof(int) <= 100 * 1024, "the starts of a batch fit in shared memory");
+  constexpr size_t kMost = (2 * kMapMaxBatch + 1) * sizeof(int);
+  static_assert(kMost <= 100 * 1024, "the starts of a batch fit in shared memory");
   const size_t smem = (2 * static_cast<size_t>(a.batch) + 1) * sizeof(int);
   if (smem > 40 * 1024) {
-    const cudaError_t err =
-        cudaFuncSetAttribute(token_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // (the limit is the process's: calls of other threads must not lower it, so it is the largest batch's)
+    const cudaError_t err = cudaFuncSetAttribute(token_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (err != cudaSuccess) return err;
   }
   // enough CTAs for the tokens, and for eight sequences of the table per warp

@@ -200,3 +200,40 @@ def test_captured_and_replayed_with_other_lengths():
     graph.replay()
     call.check(table, free, past, fewer, 64)
     assert B.tq_get_last_device_error(book) == 0
+
+
+@pytest.mark.gpu
+def test_large_and_middling_batches_from_several_threads():
+    # the starts of a batch take shared memory beyond the default limit, which is raised for the whole process
+    import threading
+    book = B.Codebook(block_size=32)
+    calls, failed = [], []
+    for batch in (8192, 5200, 8192, 5300):
+        past, new, table, free, num_blocks = make(batch, 32, batch, 100, 2)
+        call = Call(past, new, table, free, num_blocks, int(new.sum()) + 3)
+        calls.append((call, (table, free, past, new, 32)))
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    entry, ptr = B.load().tq_map_tokens, lambda t: ctypes.c_void_p(t.data_ptr())
+
+    def work(c, stream):
+        # (arguments made once, so that the threads spend their time in the library)
+        args = [book.handle, c.batch, ptr(c.past), ptr(c.new), ptr(c.table), c.table.shape[1], c.num_blocks,
+                ptr(c.free), c.free.numel(), c.n_tokens, ptr(c.ctx), ptr(c.start), ptr(c.positions), ptr(c.slots),
+                ptr(c.taken), ctypes.c_void_p(stream.cuda_stream)]
+        for _ in range(20000):
+            status = entry(*args)
+            if status:
+                failed.append(status)
+                return
+
+    threads = [threading.Thread(target=work, args=(c, s)) for (c, _), s in zip(calls, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for call, args in calls:
+        call.check(*args)
+    assert B.tq_get_last_device_error(book) == 0
