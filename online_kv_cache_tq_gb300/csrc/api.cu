@@ -19,6 +19,7 @@
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // cuTensorMapEncodeTiled from the driver, looked up once through the runtime.
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -1039,6 +1040,12 @@ tq_status tq_map_tokens(const tq_codebook* book, int batch, const int32_t* past_
   // (every CTA reads the lengths while the first one writes the contexts)
   if (batch > 0 && (context_lens == past_lens || context_lens == new_lens)) return TQ_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0) return TQ_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(past_lens), static_cast<const void*>(new_lens),
+                        static_cast<const void*>(block_table), static_cast<const void*>(free_blocks),
+                        static_cast<const void*>(context_lens), static_cast<const void*>(query_start),
+                        static_cast<const void*>(positions), static_cast<const void*>(blocks_taken)}) {
+    if (!aligned4(p)) return TQ_ERR_INVALID_ARG;
+  }
   if (static_cast<long long>(max_blocks) * book->cfg.block_size > (1ll << 31) - 1) return TQ_ERR_INVALID_ARG;
   if (batch > tq::kMapMaxBatch) return TQ_ERR_UNSUPPORTED;
   tq::TokenMapArgs a{};
@@ -1092,7 +1099,7 @@ tq_status tq_norm_rope(const tq_codebook* book, const void* q, const void* k, tq
     }
     if (t.x == t.out && t.stride != t.out_stride) return TQ_ERR_INVALID_ARG;
   }
-  if (n_tokens > 0 && rot_dim > 0 && positions == nullptr) return TQ_ERR_INVALID_ARG;
+  if ((n_tokens > 0 && rot_dim > 0 && positions == nullptr) || !aligned4(positions)) return TQ_ERR_INVALID_ARG;
   if (rot_dim % 16 != 0) return TQ_ERR_UNSUPPORTED;
   if (n_tokens == 0) return TQ_OK;
   tq::NormRopeArgs a{};
@@ -1146,6 +1153,7 @@ tq_status tq_extend_attention(const tq_codebook* book, const void* q, tq_dtype d
   if (any && (!q || !aligned16(q) || !out || !aligned16(out) || !query_start || !context_lens)) {
     return TQ_ERR_INVALID_ARG;
   }
+  if (!aligned4(query_start) || !aligned4(context_lens) || !aligned4(block_table)) return TQ_ERR_INVALID_ARG;
   if (book->polar) return TQ_ERR_UNSUPPORTED;     // (PolarQuant records: decode one token at a time)
   if (max_context > (1 << 30)) return TQ_ERR_UNSUPPORTED;   // (positions and tile bounds are ints)
   if (!any) return TQ_OK;

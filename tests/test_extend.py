@@ -541,3 +541,18 @@ def test_values_at_the_ends_of_their_range_with_scores_far_from_zero(new, score,
     c.q.copy_(q.expand_as(c.q))
     c.run()
     c.check()
+
+
+@pytest.mark.gpu
+def test_misaligned_lengths_and_tables_are_refused():
+    c = Case([3], [100])
+    base = [c.q, B.TQ_BF16, 3, 1, c.n_q, c.n_kv, C.cache_view(c.book, c.cache), c.table_t, c.table.shape[1], c.start,
+            c.ctx_t, 100, 0.0, c.out, c.ws, c.nbytes]
+    for i in (7, 9, 10):
+        args = list(base)
+        args[i] = base[i].data_ptr() + 2
+        with pytest.raises(B.TQError) as err:
+            B.tq_extend_attention(c.book, *args)
+        assert err.value.status == 1, i
+    torch.cuda.synchronize()
+    assert bool((c.out == 5.0).all())

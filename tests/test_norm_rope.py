@@ -191,3 +191,17 @@ def test_other_stream_and_graph():
     call(outs[0])
     torch.cuda.synchronize()
     assert torch.equal(outs[0], outs[2]) and not torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.gpu
+def test_misaligned_positions_are_refused():
+    x = torch.zeros((4, 3, 128), dtype=torch.bfloat16, device="cuda")
+    y = torch.full_like(x, 5.0)
+    pos = torch.zeros(5, dtype=torch.int32, device="cuda")
+    inv = torch.zeros(64, dtype=torch.float64, device="cuda")
+    with pytest.raises(B.TQError) as err:
+        B.tq_norm_rope(B.Codebook(), x, None, B.TQ_BF16, 4, 3, 0, 384, 0, None, None, 1e-6, pos.data_ptr() + 2, inv, 128,
+                       False, y, None, 384, 0)
+    assert err.value.status == 1
+    torch.cuda.synchronize()
+    assert bool((y == 5.0).all())

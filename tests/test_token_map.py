@@ -237,3 +237,20 @@ def test_large_and_middling_batches_from_several_threads():
     for call, args in calls:
         call.check(*args)
     assert B.tq_get_last_device_error(book) == 0
+
+
+@pytest.mark.gpu
+def test_misaligned_lengths_and_outputs_are_refused():
+    book = B.Codebook()
+    past, new, table, free, num_blocks = make(4, 64, 0, 100, 10)
+    ok = Call(past, new, table, free, num_blocks, int(new.sum()))
+    base = [4, ok.past, ok.new, ok.table, table.shape[1], num_blocks, ok.free, ok.free.numel(), ok.n_tokens, ok.ctx,
+            ok.start, ok.positions, ok.slots, ok.taken]
+    for i in (1, 2, 3, 6, 9, 10, 11, 13):
+        args = list(base)
+        args[i] = base[i].data_ptr() + 2
+        with pytest.raises(B.TQError) as err:
+            B.tq_map_tokens(book, *args)
+        assert err.value.status == 1, i
+    torch.cuda.synchronize()
+    assert bool((ok.slots == -9).all()) and bool((ok.start == -9).all())
