@@ -402,7 +402,8 @@ tq_status tq_map_tokens(const tq_codebook* book, int batch, const int32_t* past_
  * vector x of 128: y = x / sqrt(mean(x^2) + eps) * weight, then the first
  * rot_dim coordinates are rotated by angle position * inv_freq[j], j <
  * rot_dim / 2, in pairs (y_j, y_{j + rot_dim/2}), or (y_2j, y_{2j+1}) with
- * interleaved 1; float32 arithmetic, angles reduced to a turn in 64 bits (at
+ * interleaved 1; float32 arithmetic (also where the squares leave float32's
+ * range: such a vector is scaled first), angles reduced to a turn in 64 bits (at
  * any position as close as the product in doubles), one rounding to the type
  * at the end.
  * q, k: device rows of n_q_heads / n_kv_heads contiguous vectors in `dtype`,

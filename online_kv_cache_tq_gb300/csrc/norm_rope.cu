@@ -76,6 +76,66 @@ __device__ __forceinline__ float2 cos_sin(unsigned long long freq, unsigned pos)
   return shifted & (1u << 31) ? make_float2(-cc, -ss) : make_float2(cc, ss);
 }
 
+// The rotation of a lane's four pairs.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turn(float (&a)[4], float (&b)[4], const float2 (&cs)[4]) {
+  if (INTERLEAVED) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float p = a[2 * i], q = a[2 * i + 1], s = b[2 * i], t = b[2 * i + 1];
+      a[2 * i] = p * cs[i].x - q * cs[i].y;
+      a[2 * i + 1] = q * cs[i].x + p * cs[i].y;
+      b[2 * i] = s * cs[i + 2].x - t * cs[i + 2].y;
+      b[2 * i + 1] = t * cs[i + 2].x + s * cs[i + 2].y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float p = a[i], q = b[i];
+      a[i] = p * cs[i].x - q * cs[i].y;
+      b[i] = q * cs[i].x + p * cs[i].y;
+    }
+  }
+}
+
+// A vector whose squares leave fp32's range (rare): read again and scaled by
+// the power of two that brings its largest coordinate near 1 (2^100 at most, so
+// that the scaled eps stays a number).
+template <typename T, bool INTERLEAVED>
+__device__ __forceinline__ void far_vector(const T* x, T* out, const float (&wa)[4], const float (&wb)[4], float eps,
+                                           int ca, int cb, bool turned, const float2 (&cs)[4]) {
+  const unsigned lanes = 0xffffu << (threadIdx.x & 16);
+  Four<T> w;
+  float a[4], b[4], top = 0.f, ss = 0.f;
+  w.load(x + ca);
+  w.get(a);
+  w.load(x + cb);
+  w.get(b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(a[i]), fabsf(b[i])));
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, d));
+  const int e = max(-100, min(126, static_cast<int>(__float_as_uint(top) >> 23) - 127));
+  const float down = __uint_as_float(static_cast<unsigned>(127 - e) << 23);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] *= down;
+    b[i] *= down;
+    ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
+  }
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) ss += __shfl_xor_sync(lanes, ss, d);
+  const float r = 1.0f / sqrtf(ss * (1.0f / kDim) + eps * down * down);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] *= r * wa[i];
+    b[i] *= r * wb[i];
+  }
+  if (turned) turn<INTERLEAVED>(a, b, cs);
+  Four<T>::store(out + ca, a);
+  Four<T>::store(out + cb, b);
+}
+
 // Heads h0 .. h1 - 1 of one tensor of a token (x, out: its rows), coordinates
 // ca .. ca + 3 and cb .. cb + 3 of each; cs: the lane's four pairs.
 template <typename T, bool INTERLEAVED>
@@ -99,6 +159,7 @@ __device__ __forceinline__ void turn_heads(const T* x, T* out, int h0, int h1, c
       xa[u].load(p + ca);
       xb[u].load(p + cb);
     }
+    unsigned far = 0;                             // vectors that `far_vector` does
 #pragma unroll
     for (int u = 0; u < kRopeUnroll<T>; ++u) {
       float a[4], b[4];
@@ -110,6 +171,8 @@ __device__ __forceinline__ void turn_heads(const T* x, T* out, int h0, int h1, c
         for (int i = 0; i < 4; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) ss += __shfl_xor_sync(lanes, ss, d);
+        // (all sixteen lanes; beside an eps of 2^-118 and more, squares that vanish do not count)
+        if (!(ss < 0x1p120f) || (ss < 0x1p-100f && eps < 0x1p-118f)) far |= 1u << u;
         const float r = 1.0f / sqrtf(ss * (1.0f / kDim) + eps);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -117,30 +180,17 @@ __device__ __forceinline__ void turn_heads(const T* x, T* out, int h0, int h1, c
           b[i] *= r * wb[i];
         }
       }
-      if (turned) {
-        if (INTERLEAVED) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float p = a[2 * i], q = a[2 * i + 1], s = b[2 * i], t = b[2 * i + 1];
-            a[2 * i] = p * cs[i].x - q * cs[i].y;
-            a[2 * i + 1] = q * cs[i].x + p * cs[i].y;
-            b[2 * i] = s * cs[i + 2].x - t * cs[i + 2].y;
-            b[2 * i + 1] = t * cs[i + 2].x + s * cs[i + 2].y;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float p = a[i], q = b[i];
-            a[i] = p * cs[i].x - q * cs[i].y;
-            b[i] = q * cs[i].x + p * cs[i].y;
-          }
-        }
-      }
-      if (h + u < h1) {
+      if (turned) turn<INTERLEAVED>(a, b, cs);
+      if (h + u < h1 && !(far >> u & 1u)) {
         T* const p = out + (h + u) * kDim;
         Four<T>::store(p + ca, a);
         Four<T>::store(p + cb, b);
       }
+    }
+#pragma unroll 1
+    for (int u = 0; far != 0; ++u, far >>= 1) {
+      if ((far & 1u) && h + u < h1)
+        far_vector<T, INTERLEAVED>(x + (h + u) * kDim, out + (h + u) * kDim, wa, wb, eps, ca, cb, turned, cs);
     }
   }
 }

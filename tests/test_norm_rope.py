@@ -205,3 +205,29 @@ def test_misaligned_positions_are_refused():
     assert err.value.status == 1
     torch.cuda.synchronize()
     assert bool((y == 5.0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_vectors_whose_squares_leave_the_range(dtype, eps):
+    # sums of squares above 2^128 or below 2^-149: the norm itself is an ordinary number
+    book = B.Codebook()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    sizes = [2.0 ** 120, 2.0 ** 64, 2.0 ** 60, 1.0, 2.0 ** -40, 2.0 ** -60, 2.0 ** -80, 2.0 ** -120]
+    x = torch.randn((len(sizes), 3, 128), generator=g, device="cuda")
+    x = (x.clamp(-4, 4) * torch.tensor(sizes, device="cuda")[:, None, None]).to(dtype)
+    w = (1 + 0.3 * torch.randn(128, generator=g, device="cuda")).to(dtype)
+    out = torch.zeros_like(x)
+    inv = 10000.0 ** (-torch.arange(64, dtype=torch.float64, device="cuda") / 64)
+    pos = torch.arange(len(sizes), dtype=torch.int32, device="cuda") + 11
+    B.tq_norm_rope(book, x, None, B.TQ_BF16 if dtype == torch.bfloat16 else B.TQ_FP32, len(sizes), 3, 0, 384, 0, w,
+                   None, eps, pos, inv, 128, False, out, None, 384, 0)
+    torch.cuda.synchronize()
+    # (the kernel takes eps in 32 bits)
+    expect, bound = reference(x.double().cpu().numpy(), w.double().cpu().numpy(), float(np.float32(eps)),
+                              pos.cpu().numpy(), inv.cpu().numpy(), 128, False)
+    rounding = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+    err = np.abs(out.double().cpu().numpy() - expect)
+    assert (err <= bound * (1 + rounding) + rounding * np.abs(expect) + 1e-37).all()
