@@ -482,9 +482,10 @@ tq_status tq_get_last_device_error(const tq_codebook* book, void* stream, int* c
 
 /* A test aid for the bounded waits, off by default: while enabled on a
  * handle, the first CTA of the tensor-core decode kernel withholds the commit
- * of its first score MMAs, so its builders' wait for them runs out after the
- * kernels' one-second limit.  The call then ends normally with that CTA
- * stopped early (its in-flight copies and MMAs drained, its tensor memory
+ * of its first score MMAs (of tq_extend_attention's launches, the CTA with the
+ * first key tile that of its first product), so the wait for them runs out
+ * after the kernels' one-second limit.  The call then ends normally with that
+ * CTA stopped early (its in-flight copies and MMAs drained, its tensor memory
  * freed): tq_get_last_device_error reports code 4 and the outputs are
  * incomplete; later calls with it disabled are unaffected.  Not for use in
  * production. */

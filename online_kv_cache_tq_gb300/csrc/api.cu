@@ -680,6 +680,7 @@ void fill_cache_args(const tq_codebook* book, const tq_cache_view* cache, tq::De
   a->tables = book->d_tables;
   a->error = book->d_error;
   a->num_sms = book->num_sms;
+  a->debug_withhold = book->debug_withhold;
 }
 
 tq_status launched(cudaError_t err) { return err == cudaSuccess ? TQ_OK : TQ_ERR_CUDA; }

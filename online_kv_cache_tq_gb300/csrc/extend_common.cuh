@@ -183,6 +183,12 @@ __device__ __forceinline__ void end_segment(const ExtendArgs& a, const ExtendFor
   if (r.pos < r.end) next_item(a, f, r.it);
 }
 
+// A test of the bounded waits: the run with the form's first key tile withholds
+// its first product's completion.
+__device__ __forceinline__ bool withheld(const ExtendArgs& a, const ExtendForm& f, long long per, int seg) {
+  return a.d.debug_withhold && seg == 0 && blockIdx.x == f.cost / per;
+}
+
 // What run blockIdx.x leaves for the join: the item it begins and does not
 // end, if any (one thread, before the run is walked; `any`: the run has work).
 __device__ __forceinline__ void write_cut(const ExtendArgs& a, const ExtendForm& f, Run r, long long per, bool any) {

@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
         ptx::tc_fence_after();
         product<8>(tmem + kS0, tmem + kS1, key_stage(kc), kIdescF16, false);
         if (qjl) product<8>(tmem + kO, tmem + kS1, key_stage(kc) + 2 * (kBlockBytes / 16), kIdescF16, false);
-        ptx::mma_commit(&bar.rotated);
+        if (!withheld(a, a.narrow, per, seg)) ptx::mma_commit(&bar.rotated);
         ptx::mma_commit(&bar.k_empty[kc & 1]);
       }
       __syncwarp();

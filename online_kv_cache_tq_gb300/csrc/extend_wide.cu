@@ -71,7 +71,7 @@ __device__ __forceinline__ void bulk_store_done() { asm volatile("cp.async.bulk.
 struct ExpandShared {
   float factor[kTile], norm[kTile], square[2][kTile], reach[4];
   uint32_t valid[4];
-  uint64_t done;
+  uint64_t done, drain;
 };
 
 template <int KB, int VB>
@@ -92,8 +92,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
   if (2ll * blockIdx.x >= total) return;          // (the whole CTA)
   if (threadIdx.x == 0) {
     abort_s = 0;
-    ptx::mbar_init(&group_s[0].done, 1);
-    ptx::mbar_init(&group_s[1].done, 1);
+    for (ExpandShared& s : group_s) {
+      ptx::mbar_init(&s.done, 1);
+      ptx::mbar_init(&s.drain, 1);
+    }
     ptx::fence_mbar_init();
   }
   if (threadIdx.x < 32) {
@@ -179,7 +181,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
         const uint64_t off = (ks >> 2) * (kBlockBytes / 16) + (ks & 3) * 2;
         if (ks < 8 || qjl) ptx::mma_bf16(tmem, keys + off, turn + off, kIdescF16, ks > 0);
       }
-      ptx::mma_commit(&sh.done);
+      // (a test of the bounded waits: the first tile)
+      if (!(d.debug_withhold && blockIdx.x == 0 && g == g0)) ptx::mma_commit(&sh.done);
     }
     __syncwarp();
     const bool ok = TQ_WAIT(sh.done, phase);
@@ -238,7 +241,13 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
     if (tid == 0) bulk_store_wait();
     group_sync(group, false);                     // (the next tile overwrites what was read)
   }
-  if (tid == 0) bulk_store_done();                // nothing is in flight when the CTA ends
+  if (tid == 0) bulk_store_done();                // nothing is in flight when the CTA ends, also after a wait ran out
+  __syncwarp();
+  if (warp == 0 && ptx::elect_one()) {
+    ptx::mma_commit(&sh.drain);
+    ptx::drain_bar(&sh.drain, 0);
+  }
+  __syncwarp();
   __syncthreads();
   if (threadIdx.x < 32) ptx::tmem_dealloc(tmem_s, 256);
 }
@@ -520,7 +529,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
     const uint64_t key_desc = ptx::desc_k_sw128(ptx::smem_u32(smem + kKey0));
     const uint64_t value_desc = ptx::desc_k_sw128(ptx::smem_u32(smem + kValue0));
     int kc = 0, jt = 0;                           // key ring entries, key tiles so far
-    auto scores = [&](int x, bool last) {         // of row tile x against the key ring's next entry
+    auto scores = [&](int x, bool last, bool silent = false) {   // of row tile x against the key ring's next entry
       if (ptx::elect_one()) {
         ptx::tc_fence_after();
         const uint64_t q = query_desc + x * (kImage / 16), k = key_desc + (kc & 1) * (kImage / 16);
@@ -529,7 +538,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
           const uint64_t off = (ks >> 2) * (kBlockBytes / 16) + (ks & 3) * 2;
           ptx::mma_bf16(tmem + kS + 128 * x, q + off, k + off, kIdescF16, ks > 0);
         }
-        ptx::mma_commit(&bar.s_full[x]);
+        if (!silent) ptx::mma_commit(&bar.s_full[x]);
         if (last) ptx::mma_commit(&bar.k_empty[kc & 1]);
         ptx::mbar_arrive(&bar.s_full[x]);
       }
@@ -538,7 +547,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
     for (int seg = 0; ok && next_segment(a, a.wide, run, t0, t1); ++seg) {
       ok = TQ_WARP_WAIT(bar.q_full, seg & 1) && TQ_WARP_WAIT(bar.k_full[kc & 1], (kc >> 1) & 1);
       if (!ok) break;
-      scores(0, false);
+      scores(0, false, withheld(a, a.wide, per, seg));
       scores(1, true);
       ++kc;
       for (int t = t0; ok && t < t1; ++t, ++jt) {

@@ -118,7 +118,7 @@ struct DecodeArgs {
   int max_chunks;
   int merge_in_partials;    // the tensor-core kernel merges and writes `out` itself
   long long part_cap;       // partial entries the workspace holds (merges check records against it)
-  int debug_withhold;       // tests of the bounded waits: CTA 0 withholds its first score commit
+  int debug_withhold;       // tests of the bounded waits: a first product's commit is withheld
   const float* R;           // [128][128] row-major
   const float* Rt;
   const float* Spt;

@@ -556,3 +556,18 @@ def test_misaligned_lengths_and_tables_are_refused():
         assert err.value.status == 1, i
     torch.cuda.synchronize()
     assert bool((c.out == 5.0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,n_kv", [([2, 5], 1), ([300, 200], 2), ([3, 400], 2)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_correct(new, n_kv):
+    # the test aid withholds one product's completion in the first CTA of each launch: its waits run out after a second,
+    # what it has in flight is drained, the call ends with device error 4 and the handle works on
+    c = Case(new, [n + 700 for n in new], n_kv=n_kv, group=4, seed=24)
+    B.tq_debug_withhold_commit(c.book, True)
+    c.run()
+    torch.cuda.synchronize()
+    assert B.tq_get_last_device_error(c.book) == 4
+    B.tq_debug_withhold_commit(c.book, False)
+    c.run()
+    c.check(tokens=40)
