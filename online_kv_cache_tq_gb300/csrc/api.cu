@@ -159,9 +159,10 @@ double to_fp16(double x) { return __half2float(__float2half_rn(static_cast<float
 
 // Numbers out[i] of a 16-bit type and a factor with levels[i] ~ factor * out[i]:
 // of 2^16 common multiples of the levels, the one whose worst relative
-// rounding is least, then the factor that fits best.  (Worst of a level in
-// bf16: 2^-11.7 for 3-bit codebooks and 2^-10.6 for 4 bits, where a plain
-// rounding is off by 2^-8.5; fp16 is three bits finer.)
+// rounding is least, then the factor that fits best (least squares, so that a
+// product of many levels is least off; a single one is by a little more).
+// Worst of a level in bf16: 2^-11.5 for 3-bit codebooks and 2^-10.4 for 4 bits,
+// where a plain rounding is off by 2^-8.5; in fp16 2^-14.9 and 2^-12.9.
 float rounded_levels(const std::vector<double>& levels, double (*rounded)(double), float* out) {
   double best = 1.0, multiple = 1.0;
   for (int k = 0; k < (1 << 16); ++k) {

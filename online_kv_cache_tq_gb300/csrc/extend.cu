@@ -16,10 +16,11 @@ namespace {
 // wide form, and most expanded tiles that a workspace holds (2 GiB).
 // Sixteen sequences on 8192 (0) cached tokens, 32/8 heads, us, wide | narrow:
 //                2-bit keys, sketch, 3-bit values     4-bit keys, 4-bit values
-//    256 rows    337 | 248   (40 | 39)                338 | 303   (39 | 39)
-//    384         447 | 355   (48 | 51)                448 | 437   (48 | 51)
-//    512         450 | 463   (50 | 63)                451 | 573   (49 | 61)
-//   1024         674 | 890   (76 | 112)               674 | 1118  (76 | 114)
+//    256 rows    338 | 249   (39 | 38)                318 | 321   (41 | 38)
+//    384         447 | 358   (49 | 51)                427 | 462   (48 | 51)
+//    512         449 | 468   (49 | 63)                429 | 607   (50 | 62)
+//   1024         667 | 895   (78 | 113)               646 | 1185  (77 | 116)
+// (Four-bit codes would cross lower, at 256 rows; one limit serves all widths.)
 constexpr int kWideFrom = 512;
 constexpr long long kTileCap = 1 << 15;
 

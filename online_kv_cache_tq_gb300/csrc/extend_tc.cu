@@ -17,12 +17,12 @@
 //   scores  [128 rows x 256] [256 x 128 tokens], fp16: q~ = (R q, S q) against
 //           (c[code_t], rho_t (2 bits_t - 1)), rho_t = gamma_t sqrt(pi/2) / (m n_t);
 //           n_t scale multiplies the score in fp32 (the levels are scaled by
-//           a common factor for which fp16 holds them to 2^-13.4, and rho_t
+//           a common factor for which fp16 holds them to 2^-12.9, and rho_t
 //           with them);
 //   output  [128 rows x 128 tokens] [128 x 128], bf16: p_t n^v_t against the
 //           value levels c^v[code_t], whose bits lie by token already.  (The
 //           levels are scaled by a common factor for which bf16 holds them to
-//           2^-10.6; what rounding is left is that of the weights, up to 2^-8,
+//           2^-10.4; what rounding is left is that of the weights, up to 2^-8,
 //           which differs from token to token, and the output's.  What the
 //           weights' rounding leaves of a quarter of the tokens is added by a
 //           product of its own.)
@@ -41,14 +41,17 @@
 // reference by 2^80) is searched for each row's maximum first.
 // Tiles with hidden positions take a second path that masks.
 //
-// Twenty-one warps: 0-7 softmax (two threads per row, 64 columns each), 8-15
+// Twenty-four warps: 0-7 softmax (two threads per row, 64 columns each), 8-15
 // keys (two threads per token), 16-19 values (a thread per coordinate), 23
-// issues the products.
+// issues the products; 20-22 have nothing to do.  (Twenty-one warps, with the
+// values on 16-18 and 20 and the products on 19: 140 us in place of 128 for the
+// 16 x 4 tokens below.)
 // Tensor memory: two score tiles of 128 columns (weights overwrite them),
 // the output, the query operand.
 //
 // Measured.  16 sequences x 4 tokens at context 8192, 32/8 heads, 2-bit keys
-// with the sketch, 3-bit values: 113 us for 113 MB of cache (1.0 TB/s), 3.8 K
+// with the sketch, 3-bit values: 123 us a call for 113 MB of cache, of which
+// this launch takes 113 alone under a profiler (1.0 TB/s), 3.8 K
 // cycles a key tile, of which the products take 1.7 K.  What bounds a tile is
 // the expansion of its 49 K elements (7.1 K warp instructions, 1.9 a cycle,
 // the logic pipe 46 % busy) and how far the softmax overlaps with it.  (Few

@@ -279,8 +279,8 @@ struct ExtendForm {
   CutItem* cuts;              // [ctas]: what run c begins and does not end
 };
 constexpr int kNarrowRows = 128, kWideRows = 256;
-// (ragged prompts take 324, 298, 301, 322 us at a wide cost of 3, 4, 6, 9; a ragged
-// step of few rows 407, 396, 385, 389 us at a narrow cost of 2, 3, 5, 7)
+// (ragged prompts take 305, 300, 318, 339 us at a wide cost of 3, 4, 6, 9; a ragged
+// step of few rows 412, 405, 391, 394 us at a narrow cost of 2, 3, 5, 7)
 constexpr int kNarrowCost = 5, kWideCost = 4;
 
 // A key tile expanded for the wide form: the keys (R^T c + rho S^T signs,
