@@ -382,13 +382,15 @@ tq_status tq_decode_plan(const tq_codebook* book, int batch, int n_q_heads, int 
  * needs.  n_tokens may exceed the sum of new_lens (a padded batch): the rows
  * behind the last sequence get position -1 and slot -1, which tq_norm_rope
  * and tq_quantize_append skip.  Nothing is allocated and no workspace is
- * needed; a call with the same inputs writes the same outputs.
+ * needed; a call with the same inputs writes the same outputs.  n_free may be
+ * the list's capacity, the entries behind its end -1: then a captured step can
+ * move the list on by blocks_taken on the device and be replayed.
  * context_lens must not be past_lens or new_lens, and no output may overlap
  * an input.  batch is at most 8192 (else TQ_ERR_UNSUPPORTED).
  * Recorded as device errors: 3 lengths that are negative or beyond max_blocks
  * * block_size (the sequence counts as empty: context 0, no tokens), 6 the
  * free list is too short (entries without a block are -1, their tokens' slots
- * -1), 2 a block id outside the cache (slot -1), 7 the sum of new_lens
+ * -1), 2 a block id outside the cache or a free-list entry of -1 (slot -1), 7 the sum of new_lens
  * exceeds n_tokens (the first n_tokens rows are written).  Asynchronous on
  * `stream`. */
 tq_status tq_map_tokens(const tq_codebook* book, int batch, const int32_t* past_lens, const int32_t* new_lens,
@@ -446,19 +448,28 @@ size_t tq_extend_workspace_bytes(const tq_codebook* book, int n_tokens, int batc
  * zero row; a sequence may have no new tokens.  Query head h reads KV head
  * h / (n_q_heads / n_kv_heads), any whole ratio.  out: device bf16
  * [n_tokens][n_q_heads][128]; rows behind query_start[batch] are left as they
- * were.  Queries (scaled by a power of two where that is needed) and keys are
- * rounded to fp16, softmax weights to bf16 (a quarter of them with a second
- * bf16 number for the remainder), value levels to bf16 by a common factor that
- * holds them to 2^-10; every sum is float32, and the output is
- * rounded to bf16 once at the end.  Value vectors may have lengths from 2^-40
- * to 2^27, and zero (weights are held as multiples of up to 2^80 or 2^-80).
- * The same call gives the same bits.  cache, block_table, max_blocks, max_context and scale as in
+ * were.  Value vectors may have lengths from 2^-40 to 2^27, and zero (weights
+ * are held as multiples of up to 2^80 or 2^-80).  The same call gives the same
+ * bits.
+ * Accuracy: queries (float32 ones too; scaled by a power of two where that is
+ * needed) and keys are rounded to fp16, softmax weights to bf16 (a quarter of
+ * them with a second bf16 number for the remainder), value levels to bf16 by a
+ * common factor that holds them to 2^-10; every sum is float32, and the output
+ * is rounded to bf16 once at the end.  With ordinary scores the result is off
+ * by 0.0023 in the root mean square, of which the output's own rounding is
+ * 0.0017.  A score's error grows with |q| |k| scale: about 2^-14 of it in the
+ * root mean square, 2^-9 at most.  Where keys with outlier channels bring that
+ * product to many hundreds, rows whose weight hangs on a few close scores are
+ * off by per cents (0.0045 in the root mean square and 8 % in the worst row
+ * where it is 1400); tq_decode_attention rounds queries to 2^-17.
+ * cache, block_table, max_blocks, max_context and scale as in
  * tq_decode_attention (max_context bounds every context_lens[b] and is at most
  * 2^30, else TQ_ERR_UNSUPPORTED).  workspace: device scratch of
  * tq_extend_workspace_bytes bytes, 256-byte aligned, not used by any
  * concurrent call: about 20 MB, and where sequences can have 512 rows (new
- * tokens x n_q_heads / n_kv_heads) or more, 520 bytes per context token and KV
- * head of as many sequences of max_context, 2.2 GB at most.  Device errors: 2
+ * tokens x n_q_heads / n_kv_heads) or more, 40 MB besides and 520 bytes per
+ * context token and KV head, for as many sequences of max_context tokens as can
+ * have them, 2.2 GB at most.  Device errors: 2
  * a block id out of range (its tokens are skipped), 3 a context length or
  * query_start out of range (the rows of a sequence with a bad length are zero,
  * those with a bad query_start are left as they were), 4 as elsewhere.

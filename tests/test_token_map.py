@@ -254,3 +254,51 @@ def test_misaligned_lengths_and_outputs_are_refused():
         assert err.value.status == 1, i
     torch.cuda.synchronize()
     assert bool((ok.slots == -9).all()) and bool((ok.start == -9).all())
+
+
+@pytest.mark.gpu
+def test_a_captured_step_moves_on_in_its_free_list():
+    # the list in a buffer of fixed capacity, -1 behind its end: lengths and list move on on the device, so that a replay is
+    # the next step; the last steps find the list used up
+    bs, batch, num_blocks, cap = 32, 5, 40, 64
+    book = B.Codebook(block_size=bs)
+    rng = np.random.default_rng(11)
+    free = np.full(cap, -1, np.int32)
+    free[:num_blocks] = rng.permutation(num_blocks)
+    past, new = np.zeros(batch, np.int32), np.array([33, 0, 70, 1, 64], np.int32)
+    table = np.full((batch, 30), -1, np.int32)
+    call = Call(past, new, table, free, num_blocks, 220)
+    index = torch.arange(cap, device="cuda")
+    padded = torch.full((2 * cap,), -1, dtype=torch.int32, device="cuda")
+
+    def step():
+        call.run(book)
+        call.past.copy_(call.ctx)
+        padded[:cap].copy_(call.free)
+        call.free.copy_(padded[index + call.taken])
+
+    side = torch.cuda.Stream()                     # (a step outside the graph first, as PyTorch asks, then the start again)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    call.past.copy_(torch.as_tensor(past))
+    call.table.copy_(torch.as_tensor(table))
+    call.free.copy_(torch.as_tensor(free))
+    assert B.tq_get_last_device_error(book) == 0
+    codes = []
+    for _ in range(9):
+        graph.replay()
+        ctx, start, positions, slots, used = reference(past, new, table, free, 220, bs, num_blocks)
+        torch.cuda.synchronize()
+        assert np.array_equal(call.ctx.cpu().numpy(), ctx) and int(call.taken) == used
+        assert np.array_equal(call.positions.cpu().numpy()[:220], positions)
+        assert np.array_equal(call.slots.cpu().numpy()[:220], slots)
+        assert np.array_equal(call.table.cpu().numpy(), table)
+        past, free = ctx, np.concatenate([free[used:], np.full(min(used, cap), -1, np.int32)])[:cap]
+        assert np.array_equal(call.free.cpu().numpy(), free)
+        codes.append(B.tq_get_last_device_error(book))
+    assert codes[0] == 0 and codes[-1] == 2
