@@ -303,6 +303,23 @@ __device__ __forceinline__ void expand32(const RowChunks& r, uint32_t (&w)[BITS]
   for (int i = 0; i < 4; ++i) store16<OFFSET>(r.at[i], expand8<BITS>(w, i, t));
 }
 
+// The sketch's factor as fp16 numbers for four groups of sixteen coordinates
+// of a half (`half`), as the two packed words that expand_signs takes.  One
+// rounding for all 128 coordinates would be off by up to 2^-11 of the whole
+// sketch; instead as many of the eight groups take the number above rho as make
+// the mean right to 2^-14.5, and what is left differs in sign from coordinate
+// to coordinate.
+__device__ __forceinline__ uint2 minus_factors(float rho, int half) {
+  const uint32_t below = __half_as_ushort(__float2half_rd(rho));
+  const float lo = __half2float(__ushort_as_half(below)), hi = __half2float(__ushort_as_half(below + 1));
+  const float above = __fdividef(rho - lo, hi - lo) * 8.f;      // groups, of eight (0, 4, 2, 6 | 1, 5, 3, 7 in order)
+  const float first = above - 0.5f - half;
+  const uint32_t x = (first > 0.f ? 1u : 0u) + (first > 4.f ? 0x10000u : 0u);
+  const uint32_t y = (first > 2.f ? 1u : 0u) + (first > 6.f ? 0x10000u : 0u);
+  const uint32_t both = below * 0x00010001u;
+  return make_uint2((both + x) ^ 0x80008000u, (both + y) ^ 0x80008000u);
+}
+
 // A word of sketch signs: a set bit clears the sign of -rho.
 template <int OFFSET>
 __device__ __forceinline__ void expand_signs(const RowChunks& r, uint32_t bits, uint32_t minus_rho) {

@@ -18,7 +18,7 @@
 //           (c[code_t], rho_t (2 bits_t - 1)), rho_t = gamma_t sqrt(pi/2) / (m n_t);
 //           n_t scale multiplies the score in fp32 (the levels are scaled by
 //           a common factor for which fp16 holds them to 2^-12.9, and rho_t
-//           with them);
+//           with them, as two neighbouring numbers: see minus_factors);
 //   output  [128 rows x 128 tokens] [128 x 128], bf16: p_t n^v_t against the
 //           value levels c^v[code_t], whose bits lie by token already.  (The
 //           levels are scaled by a common factor for which bf16 holds them to
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
         if (!ok) break;
         const RowChunks at = row_chunks(ptx::smem_u32(smem + kKey0 + s * kKeyBytes) + half * kBlockBytes, row);
         const float rho = qjl && k.norm > 0.f ? __fdividef(k.rnorm * d.qjl_coef, k.norm) : 0.f;
-        const uint32_t minus_rho = __half_as_ushort(__float2half_rn(rho)) * 0x00010001u ^ 0x80008000u;
+        const uint2 minus_rho = minus_factors(rho, half);
         {
           uint32_t lo[KB], hi[KB];
 #pragma unroll
@@ -441,8 +441,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
           expand32<KB, 0>(second_word(at), hi, lev);
         }
         if (qjl) {
-          expand_signs<2 * kBlockBytes>(at, k.qjl.x, minus_rho);
-          expand_signs<2 * kBlockBytes>(second_word(at), k.qjl.y, minus_rho);
+          expand_signs<2 * kBlockBytes>(at, k.qjl.x, minus_rho.x);
+          expand_signs<2 * kBlockBytes>(second_word(at), k.qjl.y, minus_rho.y);
         }
         if (half == 0) {
           const float f = k.valid ? k.norm * to_log2 : 0.f;

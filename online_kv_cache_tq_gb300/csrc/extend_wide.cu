@@ -3,7 +3,8 @@
 // extend_expand_kernel turns every key tile (128 tokens of a KV head) of such
 // a sequence into two operands, once: the keys back in the original space,
 //   k_t = R^T c[code_t] + rho_t S^T (2 bits_t - 1)       (unit norm, fp16),
-// a product on the tensor cores of the expanded bits with R^T and S^T, and the
+// products on the tensor cores of the expanded bits with R^T and S^T, joined by
+// rho_t in fp32, and the
 // value levels c^v[code_t] (rotated space, bf16).  They are stored in the
 // swizzled layout the products read, 64 KB a tile, so that a tile is two bulk
 // copies later.  Per token and KV head this costs 66 K operations and writes
@@ -69,7 +70,7 @@ __device__ __forceinline__ void bulk_store_done() { asm volatile("cp.async.bulk.
 
 // What a group's threads share about their tile.
 struct ExpandShared {
-  float factor[kTile], norm[kTile], square[2][kTile], reach[4];
+  float factor[kTile], rho[kTile], norm[kTile], square[2][kTile], reach[4];
   uint32_t valid[4];
   uint64_t done, drain;
 };
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
     ptx::fence_mbar_init();
   }
   if (threadIdx.x < 32) {
-    ptx::tmem_alloc(&tmem_s, 256);
+    ptx::tmem_alloc(&tmem_s, 512);
     ptx::tmem_relinquish();
   }
   const bool qjl = d.k_qjl != nullptr;
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
   }
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = tmem_s + 128 * group;
+  const uint32_t tmem = tmem_s + 256 * group;           // R^T c, then S^T signs
   uint8_t* const keys_s = smem + kExpandKey0 + group * 4 * kBlockBytes;
   const int row = tid & (kTile - 1), half = tid / kTile;   // key row or value coordinate; half of the other side
   const LevelBytes key_levels = level_bytes<false>(d.tables->k_fp16, KB);
@@ -158,10 +159,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
       expand32<KB, 0>(at, w0, key_levels);
       expand32<KB, 0>(second_word(at), w1, key_levels);
       if (qjl) {
-        const float rho = k.norm > 0.f ? __fdividef(k.rnorm * d.qjl_coef, k.norm) : 0.f;
-        const uint32_t minus_rho = __half_as_ushort(__float2half_rn(rho)) * 0x00010001u ^ 0x80008000u;
-        expand_signs<2 * kBlockBytes>(at, k.qjl.x, minus_rho);
-        expand_signs<2 * kBlockBytes>(second_word(at), k.qjl.y, minus_rho);
+        constexpr uint32_t kMinusOne = 0xbc00bc00u;
+        if (half == 0) sh.rho[row] = k.norm > 0.f ? __fdividef(k.rnorm * d.qjl_coef, k.norm) : 0.f;
+        expand_signs<2 * kBlockBytes>(at, k.qjl.x, kMinusOne);
+        expand_signs<2 * kBlockBytes>(second_word(at), k.qjl.y, kMinusOne);
       }
     }
     if (half == 0) {
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
 #pragma unroll
       for (int ks = 0; ks < 16; ++ks) {
         const uint64_t off = (ks >> 2) * (kBlockBytes / 16) + (ks & 3) * 2;
-        if (ks < 8 || qjl) ptx::mma_bf16(tmem, keys + off, turn + off, kIdescF16, ks > 0);
+        if (ks < 8 || qjl) ptx::mma_bf16(tmem + (ks < 8 ? 0 : 128), keys + off, turn + off, kIdescF16, (ks & 7) > 0);
       }
       // (a test of the bounded waits: the first tile)
       if (!(d.debug_withhold && blockIdx.x == 0 && g == g0)) ptx::mma_commit(&sh.done);
@@ -199,14 +200,18 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
     ptx::tc_fence_after();
     {
       const int r = (warp & 3) * 32 + lane, h = warp >> 2;   // tensor-memory lane, columns 64 h .. + 63
+      const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 64 * h;
+      const float rho = qjl ? sh.rho[r] : 0.f;
       float square = 0.f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t y[16], w[8];
-        ptx::tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 64 * h + 16 * c, y);
+        uint32_t y[16], z[16] = {}, w[8];
+        ptx::tmem_ld16(at + 16 * c, y);
+        if (qjl) ptx::tmem_ld16(at + 128 + 16 * c, z);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float f0 = __uint_as_float(y[2 * e]), f1 = __uint_as_float(y[2 * e + 1]);
+          const float f0 = fmaf(rho, __uint_as_float(z[2 * e]), __uint_as_float(y[2 * e]));
+          const float f1 = fmaf(rho, __uint_as_float(z[2 * e + 1]), __uint_as_float(y[2 * e + 1]));
           square = fmaf(f0, f0, fmaf(f1, f1, square));
           w[e] = pack_f16(f0, f1);
         }
@@ -249,7 +254,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) extend_expand_kernel(Extend
   }
   __syncwarp();
   __syncthreads();
-  if (threadIdx.x < 32) ptx::tmem_dealloc(tmem_s, 256);
+  if (threadIdx.x < 32) ptx::tmem_dealloc(tmem_s, 512);
 }
 
 // ---- attention -------------------------------------------------------------------

@@ -180,3 +180,57 @@ def test_common_factor_of_the_levels(bits, bf16, fp16):
         # (rounded as they are, all but the one-bit levels would be an order of magnitude further off at bf16)
         assert np.abs(rounded(levels) / levels - 1.0).max() > 2.0 ** bound or bits == 1
     book.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [8, 160])
+def test_the_sketchs_factor_is_not_rounded_as_one(new):
+    # A query whose score on two keys is the sketch's part alone, 60 each: a common rounding of a key's factor would move its
+    # score by f 60, 0.012 in the rms, and their difference by 0.018.  The two share the row, whose mixture of their values
+    # gives the difference.  What is expected of its error are the independent roundings, and in the narrow form numbers
+    # next to the factor that alternate between coordinates, off by half a step (2^-11) in the rms, with a mean within
+    # 2^-14.5.
+    ctx, errors, share = 128, [], []
+    c = Case([new], [max(ctx, new)], n_kv=1, group=4, seed=34, profile=dict(log_uniform=None, outliers=0))
+    ctx, wide, scale = int(c.ctx[0]), new > 100, 1.0 / math.sqrt(128.0)
+    slots = torch.as_tensor(W.slots_for(c.table[0], np.arange(ctx), 64), device="cuda")
+    proj = c.ref["proj"]
+    for seed in range(40):
+        g = generator(900 + seed)
+        k = torch.randn((ctx, 1, 128), generator=g, device="cuda")
+        k[[3, 70]] *= 8.0 + 8.0 * torch.rand((2, 1, 1), generator=g, device="cuda")   # (the others' scores stay far below)
+        v = torch.randn((ctx, 1, 128), generator=g, device="cuda")
+        B.tq_quantize_append(c.book, k, v, B.TQ_FP32, ctx, 1, slots, C.cache_view(c.book, c.cache))
+        hc = host_cache(c.cache)
+        rows = attention.read_sequence(hc, c.table[0], ctx, 0, 64)
+        signs = 2.0 * packing.unpack_signs(rows["k_qjl"], 128) - 1.0
+        c_lv = c.ref["k_levels"][packing.unpack_planes(rows["k_codes"], c.ref["k_bits"], 128)]
+        kn, coef = rows["k_norm"].reshape(-1).astype(float), rows["k_rnorm"].reshape(-1).astype(float) * math.sqrt(
+            math.pi / 2) / 128
+        main, sketch = (c_lv * kn[:, None]) @ c.ref["rot"], coef[:, None] * (signs @ proj)
+        khat = main + sketch
+        q = np.linalg.lstsq(np.concatenate([main[[3, 70]], sketch[[3, 70]]]), np.array([0, 0, 60.0, 60.0]) / scale,
+                            rcond=None)[0]
+        c.q.copy_(torch.as_tensor(q).to(torch.bfloat16).expand_as(c.q))
+        qb = c.q[0, 0].double().cpu().numpy()
+        s = khat[[3, 70]] @ qb * scale
+        c.run()
+        torch.cuda.synchronize()
+        out = c.out[-1, 0].double().cpu().numpy()
+        vhat = quantize.reconstruct_mse(rows["v_norm"].reshape(-1), rows["v_code_values"], c.ref["rot"], c.ref["v_levels"])
+        w = np.linalg.lstsq(vhat[[3, 70]].T, out, rcond=None)[0]
+        if w.min() < 0.02:
+            continue
+        rq, sq = c.ref["rot"] @ qb, proj @ qb
+        d2 = 0.0
+        for t in (3, 70):
+            d2 += ((c.ref["rot"] ** 2) @ qb ** 2 * (c_lv[t] * kn[t]) ** 2).sum() + ((proj ** 2) @ qb ** 2).sum() * coef[t] ** 2
+            d2 += (rq ** 2 * (c_lv[t] * kn[t]) ** 2).sum() + (sq ** 2).sum() * coef[t] ** 2 * (1 + (2.0 ** -11 / FP16) ** 2) \
+                if not wide else (qb ** 2 * khat[t] ** 2).sum()
+            d2 += (2.0 ** -14.5 / FP16 * coef[t] * (sq @ signs[t])) ** 2 * (not wide)
+        errors.append(math.log(w[0] / w[1]) - (s[0] - s[1]))
+        share.append(d2 * (FP16 * scale) ** 2 + 2 * (1.5 * BF16) ** 2)   # (the weights' roundings, and the output's)
+    assert len(errors) >= 20
+    rms, model = math.sqrt(np.mean(np.square(errors))), math.sqrt(np.mean(share))
+    print("difference of two scores: rms error %.3g, expected %.3g" % (rms, model))
+    assert rms <= 1.4 * model                      # (20 to 40 samples: a factor of 1.4 is three deviations)
