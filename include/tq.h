@@ -460,7 +460,7 @@ size_t tq_extend_workspace_bytes(const tq_codebook* book, int n_tokens, int batc
  * 0.0017.  A score's error grows with |q| |k| scale: about 2^-14 of it in the
  * root mean square, 2^-8 at most.  Where keys with outlier channels bring that
  * product to many hundreds, rows whose weight hangs on a few close scores are
- * off by per cents (0.0045 in the root mean square and 8 % in the worst row
+ * off by per cents (0.0035 in the root mean square and 6 % in the worst row
  * where it is 1400); tq_decode_attention rounds queries to 2^-17.
  * cache, block_table, max_blocks, max_context and scale as in
  * tq_decode_attention (max_context bounds every context_lens[b] and is at most

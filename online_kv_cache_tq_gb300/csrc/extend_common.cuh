@@ -308,7 +308,8 @@ __device__ __forceinline__ void expand32(const RowChunks& r, uint32_t (&w)[BITS]
 // rounding for all 128 coordinates would be off by up to 2^-11 of the whole
 // sketch; instead as many of the eight groups take the number above rho as make
 // the mean right to 2^-14.5, and what is left differs in sign from coordinate
-// to coordinate.
+// to coordinate.  (24 sequences of 1 to 16 tokens: 389 us in place of 384; two
+// sketch scores of 60 differ by 0.007 in the rms where one rounding left 0.023.)
 __device__ __forceinline__ uint2 minus_factors(float rho, int half) {
   const uint32_t below = __half_as_ushort(__float2half_rd(rho));
   const float lo = __half2float(__ushort_as_half(below)), hi = __half2float(__ushort_as_half(below + 1));

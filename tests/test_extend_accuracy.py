@@ -8,8 +8,9 @@ and output o = sum p_t v_t:
   output     b |o|, b for bf16 (and fp16 for the back-rotation's two operands, value levels within 2^-10.4)
   weights    b p_t |v_t| for each token whose weight has no remainder (three in four, by place in the cache)
   scores     d_t p_t |v_t - o|, d_t the rms error of score t (times scale):
-             narrow form: R q and S q rounded (f for fp16) and their constants rounded, the sketch's factor rounded,
-             wide form: the key in the original space rounded, its constants rounded, the sketch's factor rounded;
+             narrow form: R q and S q rounded (f for fp16) and their constants rounded; the sketch's factor as the two
+             fp16 numbers around it, a step 2^-10 apart, sqrt(1/6) of it in the rms, with a mean within 2^-14.5,
+             wide form: the key in the original space rounded and its constants rounded;
              fp32 queries: the query rounded.  Key levels are within 2^-12.9 (one rounding in 2^-13 each, rms).
 """
 import math
@@ -29,6 +30,7 @@ from parity_helpers import generator, host_cache
 
 MANTISSA = math.sqrt(1.0 / 3.0) * math.sqrt(3.0 / (8.0 * math.log(2.0)))
 BF16, FP16 = 2.0 ** -8 * MANTISSA, 2.0 ** -11 * MANTISSA
+AROUND = 2.0 ** -10 * math.sqrt(1.0 / 6.0) * math.sqrt(3.0 / (8.0 * math.log(2.0)))
 
 
 def has_remainder(tokens):
@@ -58,9 +60,10 @@ def expected(q, hc, row, length, n_new, kvh, ref, scale, wide, round_q):
         sketch = (sq @ signs.T) * coef
         khat = khat + coef[:, None] * (signs @ ref["proj"])
         s = s + sketch
-        d2 += (q2 @ (ref["proj"] ** 2).T).sum(1)[:, None] * coef ** 2 + sketch ** 2
+        d2 += (q2 @ (ref["proj"] ** 2).T).sum(1)[:, None] * coef ** 2
         if not wide:
-            d2 += (sq ** 2).sum(1)[:, None] * coef ** 2
+            d2 += (sq ** 2).sum(1)[:, None] * coef ** 2 * (1.0 + (AROUND / FP16) ** 2)
+            d2 += (sketch * 2.0 ** -14.5 / FP16) ** 2
     d2 += (int(wide) + int(round_q)) * (q2 @ (khat ** 2).T)
     s, d2 = [x.reshape(n_new, g, length) for x in (s * scale, d2 * (FP16 * scale) ** 2)]
     seen = np.arange(length)[None, :] <= (length - n_new + np.arange(n_new))[:, None]
