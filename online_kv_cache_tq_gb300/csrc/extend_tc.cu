@@ -50,10 +50,10 @@
 // the output, the query operand.
 //
 // Measured.  16 sequences x 4 tokens at context 8192, 32/8 heads, 2-bit keys
-// with the sketch, 3-bit values: 123 us a call for 113 MB of cache, of which
-// this launch takes 113 alone under a profiler (1.0 TB/s), 3.8 K
+// with the sketch, 3-bit values: 124.5 us a call for 113 MB of cache, of which
+// this launch takes 117 alone under a profiler (1.0 TB/s), 3.8 K
 // cycles a key tile, of which the products take 1.7 K.  What bounds a tile is
-// the expansion of its 49 K elements (7.1 K warp instructions, 1.9 a cycle,
+// the expansion of its 49 K elements (7.3 K warp instructions, 1.9 a cycle,
 // the logic pipe 46 % busy) and how far the softmax overlaps with it.  (Few
 // rows repeated over all 128, every softmax warp with a part of the tokens:
 // 152 against 119 us, so the softmax of few rows is not what a tile waits for.)  Eight

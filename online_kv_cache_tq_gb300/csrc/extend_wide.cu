@@ -22,12 +22,12 @@
 // cycles of products for 256 x 128 scores (256 of them for the remainders), plus twice the time from a
 // product's end to the issue of the one that overwrites its operand.
 //
-// Measured.  2048 tokens on 14001, 64/8 heads: 757 us, 1.33 PFLOP/s, 3.6 K
+// Measured.  2048 tokens on 14001, 64/8 heads: 750 us, 1.34 PFLOP/s, 3.6 K
 // cycles for 256 x 128 scores, tensor pipe 64 % busy; expansion 31 us.  Short
 // items cost 13 K cycles outside the loop (ragged prompts up to 4096 tokens,
 // 32/8 heads: 249 us, 0.86 PFLOP/s; expansion 25 us).  Queries held in
 // registers from one reading to the next spill into the loop (310 against 287
-// us for those prompts, 852 against 757 us for the 2048 tokens).
+// us for those prompts, 852 against 753 us for the 2048 tokens).
 //
 // Eighteen warps: 0-7 and 8-15 the softmax of the two row tiles (two threads
 // per row), 16 issues the products, 17 copies tiles.
