@@ -1,0 +1,434 @@
+"""Timed cases of the 8-bit cache: quantising keys and values as they are
+written (``tq_fp8_append``), attention over it (``tq_fp8_attention``) and
+reading it back (``tq_fp8_read``).
+
+The cache holds e4m3 codes with one power-of-two scale per (block, KV head) of
+keys and of values:
+  k_codes  [blocks][KV heads][block / 8][8 chunks][8 tokens][16 coordinates]
+  v_codes  [blocks][KV heads][block / 16][128 coordinates][16 tokens]
+  k_scale, v_scale  float32 [blocks][KV heads]
+A scale is the smallest power of two 2^e, -56 <= e <= 56, with which 448 * 2^e
+is no less than any magnitude of the block; a block whose first token is
+written starts anew, any other keeps its scale or grows it, and then the codes
+of its earlier tokens are rounded once more.
+
+``run`` makes the library's calls where ``own`` is true; otherwise it computes
+the same operators with elementary torch operations in 32 bits, without the
+library.  ``exact`` gives the operators' values in 64 bits; a code's is what
+stands before its rounding.
+"""
+import functools
+import math
+import random
+
+import numpy as np
+import torch
+
+own = False
+
+D = 128
+DEVICE = "cuda"
+DTYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
+E4M3 = torch.float8_e4m3fn
+TOP = 448.0
+LEAST, MOST = -56, 56
+
+
+@functools.lru_cache(maxsize=None)
+def _book(block):
+    from online_kv_cache_tq_gb300 import binding
+    return binding.Codebook(k_bits=3, v_bits=3, qjl_m=D, seed=0, block_size=block, device=0)
+
+
+# ---- cases --------------------------------------------------------------------
+
+def listed():
+    return [
+        # one decode step of 64 sequences: one token each into blocks that are partly full or new; latency
+        dict(name="append_decode_b64", op="append", batch=64, n_kv=8, new_lo=1, new_hi=1, past_lo=0, past_hi=511,
+             block=64, dtype="bf16", pad=0, lens=1),
+        # a prompt of 32768 tokens
+        dict(name="append_prefill_32768", op="append", batch=1, n_kv=8, new_lo=32768, new_hi=32768, past_lo=0,
+             past_hi=0, block=64, dtype="bf16", pad=0, lens=2),
+        # a mixed step: prompt chunks beside single tokens, blocks of 96 tokens, float32, padded rows behind
+        dict(name="append_mixed_fp32", op="append", batch=24, n_kv=4, new_lo=1, new_hi=1500, past_lo=0, past_hi=1000,
+             block=96, dtype="fp32", pad=19, lens=3),
+        # one query on a short context: the smallest call
+        dict(name="attend_small", op="attend", batch=1, n_q=8, n_kv=1, new_lo=1, new_hi=1, past_lo=512, past_hi=512,
+             block=64, dtype="bf16", lens=4),
+        # the 8B-shaped decode batch
+        dict(name="attend_decode_8b", op="attend", batch=16, n_q=32, n_kv=8, new_lo=1, new_hi=1, past_lo=8191,
+             past_hi=8191, block=64, dtype="bf16", lens=5),
+        # the 70B-shaped decode batch, contexts of 1 K to 32 K
+        dict(name="attend_decode_70b", op="attend", batch=64, n_q=64, n_kv=8, new_lo=1, new_hi=1, past_lo=1023,
+             past_hi=32767, block=64, dtype="bf16", lens=6),
+        # one long context, blocks of 128 tokens
+        dict(name="attend_decode_long", op="attend", batch=1, n_q=64, n_kv=8, new_lo=1, new_hi=1, past_lo=131071,
+             past_hi=131071, block=128, dtype="bf16", lens=7),
+        # verification of 1 to 8 drafted tokens, ragged contexts, small blocks, float32 queries
+        dict(name="attend_verify_fp32", op="attend", batch=24, n_q=32, n_kv=8, new_lo=1, new_hi=8, past_lo=501,
+             past_hi=16000, block=32, dtype="fp32", lens=8),
+        # a prompt chunk of 2048 tokens on a cached prefix
+        dict(name="attend_chunk_2048", op="attend", batch=1, n_q=64, n_kv=8, new_lo=2048, new_hi=2048, past_lo=14001,
+             past_hi=14001, block=64, dtype="bf16", lens=9),
+        # the last 100 tokens of one sequence: the smallest read
+        dict(name="read_tail_100", op="read", batch=1, n_kv=8, new_lo=100, new_hi=100, past_lo=413, past_hi=413,
+             block=64, dtype="bf16", lens=10),
+        # a long context as a whole, as another engine or a cache of fewer bits takes it
+        dict(name="read_context_131072", op="read", batch=1, n_kv=8, new_lo=131072, new_hi=131072, past_lo=0,
+             past_hi=0, block=128, dtype="bf16", lens=11),
+        # ragged ranges of twelve sequences in float32, blocks of 96 tokens
+        dict(name="read_ragged_fp32", op="read", batch=12, n_kv=8, new_lo=1, new_hi=5000, past_lo=0, past_hi=3001,
+             block=96, dtype="fp32", lens=12),
+    ]
+
+
+def _spread(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["append", "attend", "attend", "read"])
+    lens = rng.randrange(1 << 30)
+    n_kv = rng.choice([1, 2, 4, 8])
+    case = dict(op=op, n_kv=n_kv, block=rng.choice([32, 64, 96, 128, 256]), dtype=rng.choice(["bf16", "bf16", "fp32"]),
+                lens=lens)
+    new = rng.choice([1, _spread(rng, 1, 2048)])
+    past = rng.choice([0, _spread(rng, 1, 32768)])
+    if op == "attend":
+        # rows x context, and cached vectors, of the largest listed cases bound the batch
+        n_q = n_kv * rng.choice([1, 2, 3, 4, 8])
+        past = max(0, min(past, int(2.0e9 // (n_q * new)) - new))
+        batch = _spread(rng, 1, max(1, min(64, int(2.0e9 // (n_q * new * (past + new))), (1 << 23) // (past + new))))
+        return dict(case, batch=batch, n_q=n_q, new_lo=max(1, new // 3), new_hi=new, past_lo=past // 2, past_hi=past)
+    if op == "read":
+        past //= 8
+    batch = _spread(rng, 1, max(1, min(128, 32768 // new)))
+    return dict(case, batch=batch, new_lo=max(1, new // 3), new_hi=new, past_lo=past // 2,
+                past_hi=min(past, 131072 // batch), **(dict(pad=rng.choice([0, 1, 50])) if op == "append" else {}))
+
+
+def _lengths(case):
+    """(past, new) per sequence: functions of the case alone."""
+    rng = random.Random(case["lens"])
+    past = [rng.randint(min(case["past_lo"], case["past_hi"]), case["past_hi"]) for _ in range(case["batch"])]
+    new = [rng.randint(case["new_lo"], case["new_hi"]) for _ in range(case["batch"])]
+    if case["op"] == "append" and case["new_hi"] > 64 and case["batch"] > 8:
+        # a mixed step: every other sequence decodes one token
+        new = [1 if p and rng.random() < 0.5 else n for p, n in zip(past, new)]
+    return past, new
+
+
+def _ceil(a, b):
+    return (a + b - 1) // b
+
+
+def work(case):
+    past, new = _lengths(case)
+    bs, n_kv, elem = case["block"], case["n_kv"], 2 if case["dtype"] == "bf16" else 4
+    blocks = sum(_ceil(p + n, bs) - p // bs for p, n in zip(past, new))
+    vecs = sum(new) * n_kv
+    if case["op"] == "append":     # a key and a value vector in, their codes and the blocks' scales out
+        return {"bytes": 2 * vecs * D * (elem + 1) + 8 * blocks * n_kv, "flops": 4 * vecs * D}
+    if case["op"] == "read":
+        return {"bytes": 2 * vecs * D * (elem + 1) + 8 * blocks * n_kv, "flops": 2 * vecs * D}
+    ctx = [p + n for p, n in zip(past, new)]
+    pairs = sum(n * p + n * (n + 1) // 2 for p, n in zip(past, new)) * case["n_q"]
+    cached = sum(ctx) * n_kv * 2 * D + 8 * n_kv * sum(_ceil(c, bs) for c in ctx)
+    return {"bytes": cached + sum(new) * case["n_q"] * D * (elem + 2), "flops": 4 * D * pairs}
+
+
+# ---- inputs -------------------------------------------------------------------
+
+def _generator(seed):
+    g = torch.Generator(device=DEVICE)
+    g.manual_seed(seed)
+    return g
+
+
+def _ints(values, dtype=torch.int32):
+    return torch.tensor(values, dtype=dtype, device=DEVICE)
+
+
+def _channels(n_kv, g):
+    """Scale profile of keys' and values' channels, and a few outlier channels of the keys."""
+    s = torch.exp(torch.randn((2, n_kv, D), generator=g, device=DEVICE) * 0.6)
+    s[0] *= torch.where(torch.rand((n_kv, D), generator=g, device=DEVICE) < 0.02, 8.0, 1.0)
+    return s
+
+
+def _scale_of(amax):
+    """The smallest power of two that holds magnitudes up to amax in 448 steps of it."""
+    m, e = torch.frexp(amax)                        # amax = m 2^e, 0.5 <= m < 1; 448 = 0.875 * 2^9
+    e = torch.where(m > 0.875, e + 1, e) - 9
+    return torch.ldexp(torch.ones_like(amax), torch.where(amax > 0, e, LEAST).clamp(LEAST, MOST))
+
+
+def _fill_cache(case, num_blocks, g):
+    """Codes and scales of ``num_blocks`` full blocks of Gaussian keys and values with per-channel scales."""
+    bs, n_kv = case["block"], case["n_kv"]
+    channels = _channels(n_kv, g)
+    cache = dict(k=torch.empty((num_blocks, n_kv, bs // 8, 8, 8, 16), dtype=torch.uint8, device=DEVICE),
+                 v=torch.empty((num_blocks, n_kv, bs // 16, D, 16), dtype=torch.uint8, device=DEVICE))
+    for name in ("k_scale", "v_scale"):
+        cache[name] = torch.empty((num_blocks, n_kv), dtype=torch.float32, device=DEVICE)
+    step = max(1, (1 << 20) // (bs * n_kv))
+    for b0 in range(0, num_blocks, step):
+        nb = min(step, num_blocks - b0)
+        for i, name in enumerate(("k", "v")):
+            x = torch.randn((nb, n_kv, bs, D), generator=g, device=DEVICE) * channels[i][:, None]
+            scale = _scale_of(x.abs().amax((2, 3)))
+            x = (x / scale[..., None, None]).to(E4M3).view(torch.uint8)
+            shaped = x.view(nb, n_kv, bs // 8, 8, 8, 16).transpose(3, 4) if name == "k" else \
+                x.view(nb, n_kv, bs // 16, 16, D).transpose(3, 4)
+            cache[name][b0:b0 + nb] = shaped
+            cache[name + "_scale"][b0:b0 + nb] = scale
+    return cache
+
+
+def prepare(case, seed):
+    past, new = _lengths(case)
+    g = _generator(seed)
+    bs, n_kv, batch = case["block"], case["n_kv"], case["batch"]
+    ctx = [p + n for p, n in zip(past, new)]
+    need = [_ceil(c, bs) for c in ctx]
+    num_blocks, max_blocks, total = sum(need), max(need), sum(new)
+    ids = np.random.default_rng(seed).permutation(num_blocks).astype(np.int32)
+    table = np.full((batch, max_blocks), -1, dtype=np.int32)
+    table[np.arange(max_blocks)[None, :] < np.array(need)[:, None]] = ids
+    start = [0]
+    for n in new:
+        start.append(start[-1] + n)
+    dt = DTYPES[case["dtype"]]
+    s = dict(case=case, op=case["op"], block=bs, n_kv=n_kv, batch=batch, max_blocks=max_blocks, num_blocks=num_blocks,
+             cache=_fill_cache(case, num_blocks, g), table=torch.as_tensor(table).cuda(), start=_ints(start),
+             ctx=_ints(ctx), max_ctx=max(ctx), max_new=max(new), total=total, dtype=dt)
+    if case["op"] == "attend":
+        s["q"] = torch.randn((total, case["n_q"], D), generator=g, device=DEVICE).to(dt)
+        s["out"] = torch.empty((total, case["n_q"], D), dtype=torch.bfloat16, device=DEVICE)
+    elif case["op"] == "append":
+        # keys and values lie side by side in the rows of one projection's output
+        x = torch.randn((total + case["pad"], 2, n_kv, D), generator=g, device=DEVICE) * _channels(n_kv, g)
+        s["kv"] = x.to(dt)
+    else:
+        s["k_out"], s["v_out"] = torch.empty((2, total, n_kv, D), dtype=dt, device=DEVICE)
+    if own:
+        from online_kv_cache_tq_gb300 import binding as B
+        s["book"] = _book(bs)
+        c = s["cache"]
+        s["view"] = B.make_fp8_view(c["k"], c["v"], c["k_scale"], c["v_scale"], num_blocks, n_kv, bs)
+        s["code"] = B.TQ_BF16 if dt == torch.bfloat16 else B.TQ_FP32
+        if case["op"] == "attend":
+            nbytes = B.tq_fp8_workspace_bytes(s["book"], total, batch, case["n_q"], n_kv, s["max_ctx"])
+            s["ws"], s["ws_bytes"] = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=DEVICE), nbytes
+    return s
+
+
+# ---- one pass -----------------------------------------------------------------
+
+def _outputs(s):
+    c = s["cache"]
+    return dict(k=c["k"].view(E4M3), v=c["v"].view(E4M3), k_scale=c["k_scale"], v_scale=c["v_scale"])
+
+
+def _own_append(s):
+    from online_kv_cache_tq_gb300 import binding as B
+    row = 2 * s["n_kv"] * D
+    B.tq_fp8_append(s["book"], s["kv"][:, 0], s["kv"][:, 1], s["code"], s["kv"].shape[0], s["batch"], s["n_kv"], row,
+                    row, s["view"], s["table"], s["max_blocks"], s["start"], s["ctx"])
+    return _outputs(s)
+
+
+def _tokens(s):
+    """(sequence, index in it, position) of the step's tokens."""
+    t = torch.arange(s["total"], device=DEVICE)
+    seq = torch.searchsorted(s["start"], t, right=True) - 1
+    at = t - s["start"][seq]
+    return seq, at, s["ctx"][seq] - (s["start"][seq + 1] - s["start"][seq]) + at
+
+
+def _plain_append(s):
+    bs, n_kv, c = s["block"], s["n_kv"], s["cache"]
+    seq, at, pos = _tokens(s)
+    blk, off = s["table"][seq, pos // bs].long(), pos % bs
+    # a run: the step's tokens of one block
+    first = (at == 0) | (off == 0)
+    run = torch.cumsum(first, 0) - 1
+    blocks, offset = blk[first], off[first]
+    x = s["kv"][:s["total"]].float()
+    held = torch.arange(bs, device=DEVICE)[None, :] < offset[:, None]       # earlier tokens of a run's block
+    for i, name in enumerate(("k", "v")):
+        amax = torch.zeros((blocks.numel(), n_kv), device=DEVICE)
+        amax.scatter_reduce_(0, run[:, None].expand(-1, n_kv), x[:, i].abs().amax(-1), "amax")
+        before = c[name + "_scale"][blocks]
+        scale = torch.where(offset[:, None] > 0, torch.maximum(before, _scale_of(amax)), _scale_of(amax))
+        # codes of the runs' blocks, token by token
+        codes = c[name][blocks].transpose(3, 4)
+        shape = codes.shape
+        codes = codes.reshape(-1, n_kv, bs, D)
+        old = (codes.view(E4M3).float() * (before / scale)[..., None, None]).to(E4M3).view(torch.uint8)
+        codes = torch.where(held[:, None, :, None], old, codes)
+        codes[run, :, off] = (x[:, i] / scale[run][..., None]).clamp(-TOP, TOP).to(E4M3).view(torch.uint8)
+        c[name][blocks] = codes.reshape(shape).transpose(3, 4)
+        c[name + "_scale"][blocks] = scale
+    return _outputs(s)
+
+
+def _own_attend(s):
+    from online_kv_cache_tq_gb300 import binding as B
+    c = s["case"]
+    B.tq_fp8_attention(s["book"], s["q"], s["code"], s["total"], s["batch"], c["n_q"], c["n_kv"], s["view"],
+                       s["table"], s["max_blocks"], s["start"], s["ctx"], s["max_ctx"], 0.0, s["out"], s["ws"],
+                       s["ws_bytes"])
+    return s["out"]
+
+
+def _vectors(s, name, blk, off):
+    """Keys or values [...][KV heads][128] in float32 at blocks and offsets [...]."""
+    c, bs, n_kv = s["cache"], s["block"], s["n_kv"]
+    if name == "k":
+        rows = c["k"].permute(0, 2, 4, 1, 3, 5).reshape(-1, n_kv, D)
+    else:
+        rows = c["v"].permute(0, 2, 4, 1, 3).reshape(-1, n_kv, D)
+    return rows[blk * bs + off].view(E4M3).float() * c[name + "_scale"][blk][..., None]
+
+
+def _plain_attend(s):
+    n_kv, batch, n_q = s["n_kv"], s["batch"], s["case"]["n_q"]
+    group, length, most = n_q // n_kv, s["max_ctx"], s["max_new"]
+    pos = torch.arange(length, device=DEVICE).expand(batch, -1).clamp(max=(s["ctx"] - 1)[:, None])
+    blk = s["table"].gather(1, pos // s["block"]).long()
+    new = s["start"][1:] - s["start"][:-1]
+    # queries [batch][KV head][token, head of the group], rows that are not there repeated
+    rows = torch.arange(most, device=DEVICE)[None, :].clamp(max=(new - 1)[:, None])
+    q = s["q"][s["start"][:-1, None] + rows].float()
+    q = q.reshape(batch, most, n_kv, group, D).transpose(1, 2).reshape(batch, n_kv, most * group, D)
+    scores = q @ _vectors(s, "k", blk, pos % s["block"]).permute(0, 2, 3, 1)
+    scores *= 1.0 / math.sqrt(D)
+    seen = (s["ctx"] - new)[:, None] + rows                                  # last position a token sees
+    hidden = torch.arange(length, device=DEVICE) > seen[..., None]           # [batch][token][position]
+    scores.masked_fill_(hidden.repeat_interleave(group, 1)[:, None], float("-inf"))
+    scores -= scores.amax(-1, keepdim=True)
+    scores.exp_()
+    sums = scores.sum(-1, keepdim=True)
+    o = (scores @ _vectors(s, "v", blk, pos % s["block"]).transpose(1, 2)) / sums
+    o = o.reshape(batch, n_kv, most, group, D).transpose(1, 2).reshape(batch, most, n_q, D)
+    seq, at, _ = _tokens(s)
+    return o[seq, at].to(torch.bfloat16)
+
+
+def _own_read(s):
+    from online_kv_cache_tq_gb300 import binding as B
+    row = s["n_kv"] * D
+    B.tq_fp8_read(s["book"], s["view"], s["table"], s["max_blocks"], s["total"], s["batch"], s["n_kv"], s["start"],
+                  s["ctx"], s["code"], s["k_out"], s["v_out"], row, row)
+    return s["k_out"], s["v_out"]
+
+
+def _plain_read(s):
+    seq, _, pos = _tokens(s)
+    blk, off = s["table"][seq, pos // s["block"]].long(), pos % s["block"]
+    return _vectors(s, "k", blk, off).to(s["dtype"]), _vectors(s, "v", blk, off).to(s["dtype"])
+
+
+def run(state):
+    op = state["op"]
+    if own:
+        return {"append": _own_append, "attend": _own_attend, "read": _own_read}[op](state)
+    return {"append": _plain_append, "attend": _plain_attend, "read": _plain_read}[op](state)
+
+
+# ---- 64-bit values ------------------------------------------------------------
+
+_E4M3_VALUES = [(-1.0 if b & 128 else 1.0) * (math.nan if b & 127 == 127 else
+                ((b & 7) / 8.0 * 2.0 ** -6 if b & 120 == 0 else (1 + (b & 7) / 8.0) * 2.0 ** ((b >> 3 & 15) - 7)))
+                for b in range(256)]
+
+
+def _exact_append(case, seed):
+    s = prepare(case, seed)
+    past, new = _lengths(case)
+    bs, n_kv, table = case["block"], case["n_kv"], s["table"].tolist()
+    value = torch.tensor(_E4M3_VALUES, dtype=torch.float64, device=DEVICE)
+    out = dict(k=value[s["cache"]["k"].long()], v=value[s["cache"]["v"].long()],
+               k_scale=s["cache"]["k_scale"].double(), v_scale=s["cache"]["v_scale"].double())
+    kv, row = s["kv"].double(), 0
+    token = torch.arange(bs, device=DEVICE)
+    for b in range(case["batch"]):
+        pos = past[b]
+        while pos < past[b] + new[b]:
+            block, off = table[b][pos // bs], pos % bs
+            n = min(bs - off, past[b] + new[b] - pos)
+            for i, name in enumerate("kv"):
+                x = kv[row:row + n, i]                                       # [n][n_kv][128]
+                top = x.abs().flatten(2).amax((0, 2)).clamp(min=1e-300)
+                e = torch.ceil(torch.log2(top / 448.0) - 1e-13).clamp(LEAST, MOST)
+                scale = torch.exp2(e)
+                if off:
+                    scale = torch.maximum(scale, out[name + "_scale"][block])
+                    held = out[name + "_scale"][block] / scale
+                    if name == "k":
+                        grid = (token < off).reshape(-1, 1, 8, 1).expand(-1, 8, -1, 16)
+                        factor = held[:, None, None, None, None]
+                    else:
+                        grid = (token < off).reshape(-1, 1, 16).expand(-1, D, -1)
+                        factor = held[:, None, None, None]
+                    out[name][block] = torch.where(grid, out[name][block] * factor, out[name][block])
+                code = (x / scale[None, :, None]).clamp(-448.0, 448.0)
+                at = off + torch.arange(n, device=DEVICE)
+                if name == "k":
+                    out[name][block][:, at // 8, :, at % 8] = code.reshape(n, n_kv, 8, 16)
+                else:
+                    out[name][block][:, at // 16, :, at % 16] = code
+                out[name + "_scale"][block] = scale
+            pos, row = pos + n, row + n
+    return out
+
+
+def _exact_rows(s, name, blocks, head, length):
+    """Keys or values [length][128] of one head of a sequence, from its blocks."""
+    value = torch.tensor(_E4M3_VALUES, dtype=torch.float64, device=DEVICE)
+    codes = s["cache"][name][blocks, head]
+    x = value[codes.long()]
+    x = x.transpose(2, 3).flatten(3) if name == "k" else x.transpose(2, 3)
+    x = x.reshape(blocks.numel(), -1, D) * s["cache"][name + "_scale"][blocks, head].double()[:, None, None]
+    return x.reshape(-1, D)[:length]
+
+
+def _exact_attend(case, seed):
+    s = prepare(case, seed)
+    past, new = _lengths(case)
+    group, bs = case["n_q"] // case["n_kv"], case["block"]
+    out = torch.zeros(s["q"].shape, dtype=torch.float64, device=DEVICE)
+    t0 = 0
+    for b in range(case["batch"]):
+        n, length = new[b], past[b] + new[b]
+        blocks = s["table"][b, :_ceil(length, bs)].long()
+        hidden = torch.arange(length, device=DEVICE)[None, :] > past[b] + torch.arange(n, device=DEVICE)[:, None]
+        for h in range(case["n_kv"]):
+            heads = slice(h * group, (h + 1) * group)
+            q = s["q"][t0:t0 + n, heads].double().transpose(0, 1)            # [group][n][128]
+            score = q @ _exact_rows(s, "k", blocks, h, length).T / math.sqrt(D)
+            weight = torch.softmax(score.masked_fill(hidden, -math.inf), dim=-1)
+            out[t0:t0 + n, heads] = (weight @ _exact_rows(s, "v", blocks, h, length)).transpose(0, 1)
+        t0 += n
+    return out
+
+
+def _exact_read(case, seed):
+    s = prepare(case, seed)
+    past, new = _lengths(case)
+    outs, bs = [], case["block"]
+    for name in "kv":
+        out, t0 = torch.zeros((s["total"], case["n_kv"], D), dtype=torch.float64, device=DEVICE), 0
+        for b in range(case["batch"]):
+            blocks = s["table"][b, :_ceil(past[b] + new[b], bs)].long()
+            for h in range(case["n_kv"]):
+                out[t0:t0 + new[b], h] = _exact_rows(s, name, blocks, h, past[b] + new[b])[past[b]:]
+            t0 += new[b]
+        outs.append(out)
+    return tuple(outs)
+
+
+def exact(case, seed):
+    return {"append": _exact_append, "attend": _exact_attend, "read": _exact_read}[case["op"]](case, seed)
