@@ -7,7 +7,7 @@ keys and of values:
   k_codes  [blocks][KV heads][block / 8][8 chunks][8 tokens][16 coordinates]
   v_codes  [blocks][KV heads][block / 16][128 coordinates][16 tokens]
   k_scale, v_scale  float32 [blocks][KV heads]
-A scale is the smallest power of two 2^e, -56 <= e <= 56, with which 448 * 2^e
+A scale is the smallest power of two 2^e, -40 <= e <= 14, with which 448 * 2^e
 is no less than any magnitude of the block; a block whose first token is
 written starts anew, any other keeps its scale or grows it, and then the codes
 of its earlier tokens are rounded once more.
@@ -31,7 +31,7 @@ DEVICE = "cuda"
 DTYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
 E4M3 = torch.float8_e4m3fn
 TOP = 448.0
-LEAST, MOST = -56, 56
+LEAST, MOST = -40, 14
 
 
 @functools.lru_cache(maxsize=None)
