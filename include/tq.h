@@ -480,6 +480,92 @@ tq_status tq_extend_attention(const tq_codebook* book, const void* q, tq_dtype d
                               int max_blocks, const int32_t* query_start, const int32_t* context_lens, int max_context,
                               float scale, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/* The 8-bit cache: keys and values as e4m3 codes with one scale for each block
+ * and head, beside the packed cache (for layers, drafts or recent tokens that
+ * need more than its bits).  x = code * scale.  Caller-owned device arrays,
+ * 16-byte aligned.  A block's codes of one KV head are one run of block_size *
+ * 128 bytes:
+ *   k_codes  [num_blocks][n_kv_heads][block_size / 8][8 chunks][8 tokens][16]
+ *            (coordinate 16 chunk + i of token 8 group + j),
+ *   v_codes  [num_blocks][n_kv_heads][block_size / 16][128 coordinates][16 tokens],
+ * the order in which the tensor cores read them.  k_scale, v_scale: float32
+ * [num_blocks][n_kv_heads], powers of two from 2^-40 to 2^14 (tq_fp8_append
+ * writes them).  block_size is the handle's; any device handle serves, its
+ * codebooks and bit widths play no part.
+ *
+ * The three entry points name tokens alike: query_start (device int32
+ * [batch + 1], non-decreasing, from 0, at most n_tokens) gives the rows of each
+ * sequence, context_lens (device int32 [batch]) its length with them: the n
+ * rows of a sequence are its last n positions, context - n .. context - 1.
+ * block_table and max_blocks as in tq_decode_attention. */
+typedef struct {
+  void* k_codes;
+  void* v_codes;
+  float* k_scale;
+  float* v_scale;
+  int num_blocks;
+  int n_kv_heads;
+  int block_size;
+} tq_fp8_view;
+
+/* Quantise keys and values as they are written.  For each block and head that
+ * gets tokens, the scale is the least power of two 2^e, -40 <= e <= 14, with
+ * which no magnitude of the new tokens is beyond 448 * 2^e; where the block
+ * already holds earlier tokens of the sequence (its first offset is not among
+ * the call's rows), it is the block's old scale if that is larger, and where it
+ * grows, the earlier tokens' codes are rounded once more (they lose something
+ * only below 2^-6 of the scale).  Codes are x / scale rounded to nearest even,
+ * magnitudes beyond 448 * 2^14 saturate; a vector with a NaN is stored with all
+ * its codes NaN and does not count for the scale.  Codes behind a sequence's
+ * last token are left as they were.
+ * k, v: device rows of n_kv_heads contiguous vectors in `dtype`, k_stride /
+ * v_stride elements from token to token (slices of a projection's output are
+ * taken as they are); either may be NULL to skip that tensor.  Pointers 16-byte
+ * aligned, strides multiples of 16 bytes and at least n_kv_heads * 128.  Rows
+ * behind query_start[batch] are not read.  No two sequences of a call may write
+ * to one block.  The same call on the same cache gives the same bits.  Device
+ * errors: 2 a block id out of range (its tokens are skipped), 3 a query_start
+ * or context out of range, or more rows than context (the sequence is
+ * skipped).  Asynchronous on `stream`. */
+tq_status tq_fp8_append(const tq_codebook* book, const void* k, const void* v, tq_dtype dtype, int n_tokens, int batch,
+                        int n_kv_heads, int64_t k_stride, int64_t v_stride, const tq_fp8_view* cache,
+                        const int32_t* block_table, int max_blocks, const int32_t* query_start,
+                        const int32_t* context_lens, void* stream);
+
+/* Read back the last query_start[b + 1] - query_start[b] tokens of each
+ * sequence's context (any range: context_lens need not be the sequence's whole
+ * length): code * scale, exact in `dtype`, to k_out and v_out, device rows laid
+ * out as the append's k and v (either may be NULL).  Rows behind
+ * query_start[batch] and rows with a device error (as the append's) are left as
+ * they were.  No output may overlap the cache.  Asynchronous on `stream`. */
+tq_status tq_fp8_read(const tq_codebook* book, const tq_fp8_view* cache, const int32_t* block_table, int max_blocks,
+                      int n_tokens, int batch, int n_kv_heads, const int32_t* query_start, const int32_t* context_lens,
+                      tq_dtype dtype, void* k_out, void* v_out, int64_t k_stride, int64_t v_stride, void* stream);
+
+/* Device workspace bytes tq_fp8_attention needs for this shape (0 for invalid
+ * arguments). */
+size_t tq_fp8_workspace_bytes(const tq_codebook* book, int n_tokens, int batch, int n_q_heads, int n_kv_heads,
+                              int max_context);
+
+/* Attention over the 8-bit cache, of one new token per sequence or of several:
+ * softmax(scale <q, k>) v with k and v as tq_fp8_read gives them; the new
+ * tokens' own keys and values are appended first, and token i of a sequence's n
+ * sees positions 0 .. context - n + i.  A token that sees nothing (more new
+ * tokens than context) gets a zero row; what stands behind a sequence's
+ * context, or at positions that a token does not see, has no influence.
+ * q: device [n_tokens][n_q_heads][128] in `dtype`.  Query head h reads KV head
+ * h / (n_q_heads / n_kv_heads), any whole ratio.  out: device bf16
+ * [n_tokens][n_q_heads][128]; rows behind query_start[batch] are left as they
+ * were.  max_context bounds every context_lens[b] and is at most 2^30 (else
+ * TQ_ERR_UNSUPPORTED).  scale: 0 selects 1/sqrt(d).  workspace: device scratch
+ * of tq_fp8_workspace_bytes bytes, 256-byte aligned, not used by any concurrent
+ * call.  The same call gives the same bits.  Device errors as
+ * tq_extend_attention's.  Asynchronous on `stream`. */
+tq_status tq_fp8_attention(const tq_codebook* book, const void* q, tq_dtype dtype, int n_tokens, int batch,
+                           int n_q_heads, int n_kv_heads, const tq_fp8_view* cache, const int32_t* block_table,
+                           int max_blocks, const int32_t* query_start, const int32_t* context_lens, int max_context,
+                           float scale, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronise `stream`, then return (and clear) the first device-side error
  * code recorded since the last call: 0 none, 1 slot out of range in
  * quantize-append, 2 block id out of range in decode, 3 context length out of

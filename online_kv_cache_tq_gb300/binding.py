@@ -29,6 +29,7 @@ EXPORTED = ("tq_codebook_build", "tq_codebook_destroy", "tq_codebook_levels", "t
             "tq_decode_attention_static", "tq_decode_kernel_kind", "tq_decode_plan", "tq_debug_withhold_commit",
             "tq_decode_parts_workspace_bytes", "tq_decode_attention_parts",
             "tq_map_tokens", "tq_norm_rope", "tq_extend_workspace_bytes", "tq_extend_attention",
+            "tq_fp8_append", "tq_fp8_read", "tq_fp8_workspace_bytes", "tq_fp8_attention",
             "tq_get_last_device_error",
             "tq_status_string")
 
@@ -49,6 +50,12 @@ class tq_cache_view(ctypes.Structure):
     _fields_ = [("k_codes", ctypes.c_void_p), ("k_qjl", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
                 ("k_rnorm", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("v_norm", ctypes.c_void_p),
                 ("num_blocks", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("block_size", ctypes.c_int)]
+
+
+class tq_fp8_view(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("block_size", ctypes.c_int)]
 
 
 class tq_decode_plan_info(ctypes.Structure):
@@ -118,6 +125,13 @@ def load():
     lib.tq_extend_workspace_bytes.restype = sz
     lib.tq_extend_attention.argtypes = [vp, vp, i32, i32, i32, i32, i32, ctypes.POINTER(tq_cache_view), vp, i32, vp,
                                         vp, i32, ctypes.c_float, vp, vp, sz, vp]
+    view, i64 = ctypes.POINTER(tq_fp8_view), ctypes.c_int64
+    lib.tq_fp8_append.argtypes = [vp, vp, vp, i32, i32, i32, i32, i64, i64, view, vp, i32, vp, vp, vp]
+    lib.tq_fp8_read.argtypes = [vp, view, vp, i32, i32, i32, i32, vp, vp, i32, vp, vp, i64, i64, vp]
+    lib.tq_fp8_workspace_bytes.argtypes = [vp, i32, i32, i32, i32, i32]
+    lib.tq_fp8_workspace_bytes.restype = sz
+    lib.tq_fp8_attention.argtypes = [vp, vp, i32, i32, i32, i32, i32, view, vp, i32, vp, vp, i32, ctypes.c_float, vp,
+                                     vp, sz, vp]
     lib.tq_get_last_device_error.argtypes = [vp, vp, ctypes.POINTER(i32)]
     lib.tq_status_string.argtypes = [i32]
     lib.tq_status_string.restype = ctypes.c_char_p
@@ -426,3 +440,38 @@ def tq_extend_attention(book, q, dtype, n_tokens, batch, n_q_heads, n_kv_heads, 
                                       ctypes.byref(view), _ptr(block_table), max_blocks, _ptr(query_start),
                                       _ptr(context_lens), max_context, scale, _ptr(out), _ptr(workspace),
                                       workspace_bytes, _book_stream(book, stream)), "tq_extend_attention")
+
+
+def make_fp8_view(k_codes, v_codes, k_scale, v_scale, num_blocks, n_kv_heads, block_size):
+    """tq_fp8_view of an 8-bit cache's device tensors."""
+    return tq_fp8_view(_ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale), num_blocks, n_kv_heads, block_size)
+
+
+def tq_fp8_append(book, k, v, dtype, n_tokens, batch, n_kv_heads, k_stride, v_stride, view, block_table, max_blocks,
+                  query_start, context_lens, stream=None):
+    """Quantise each sequence's last tokens into the 8-bit cache; strides in
+    elements from token to token."""
+    _check(load().tq_fp8_append(book.handle, _ptr(k), _ptr(v), dtype, n_tokens, batch, n_kv_heads, k_stride, v_stride,
+                                ctypes.byref(view), _ptr(block_table), max_blocks, _ptr(query_start),
+                                _ptr(context_lens), _book_stream(book, stream)), "tq_fp8_append")
+
+
+def tq_fp8_read(book, view, block_table, max_blocks, n_tokens, batch, n_kv_heads, query_start, context_lens, dtype,
+                k_out, v_out, k_stride, v_stride, stream=None):
+    """Each sequence's last tokens of the 8-bit cache, as vectors."""
+    _check(load().tq_fp8_read(book.handle, ctypes.byref(view), _ptr(block_table), max_blocks, n_tokens, batch,
+                              n_kv_heads, _ptr(query_start), _ptr(context_lens), dtype, _ptr(k_out), _ptr(v_out),
+                              k_stride, v_stride, _book_stream(book, stream)), "tq_fp8_read")
+
+
+def tq_fp8_workspace_bytes(book, n_tokens, batch, n_q_heads, n_kv_heads, max_context):
+    return load().tq_fp8_workspace_bytes(book.handle, n_tokens, batch, n_q_heads, n_kv_heads, max_context)
+
+
+def tq_fp8_attention(book, q, dtype, n_tokens, batch, n_q_heads, n_kv_heads, view, block_table, max_blocks,
+                     query_start, context_lens, max_context, scale, out, workspace, workspace_bytes, stream=None):
+    """Attention of each sequence's last tokens over its 8-bit context."""
+    _check(load().tq_fp8_attention(book.handle, _ptr(q), dtype, n_tokens, batch, n_q_heads, n_kv_heads,
+                                   ctypes.byref(view), _ptr(block_table), max_blocks, _ptr(query_start),
+                                   _ptr(context_lens), max_context, scale, _ptr(out), _ptr(workspace),
+                                   workspace_bytes, _book_stream(book, stream)), "tq_fp8_attention")

@@ -46,5 +46,25 @@ def allocate_extend_workspace(book, n_tokens, batch, n_q_heads, n_kv_heads, max_
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), nbytes
 
 
+def allocate_fp8_cache(book, num_blocks, n_kv_heads, device="cuda"):
+    """Dict of zero-filled device tensors of an 8-bit cache (blocks of the handle's size)."""
+    bs = book.block_size
+    return dict(k_codes=torch.zeros((num_blocks, n_kv_heads, bs // 8, 8, 8, 16), dtype=torch.uint8, device=device),
+                v_codes=torch.zeros((num_blocks, n_kv_heads, bs // 16, 128, 16), dtype=torch.uint8, device=device),
+                k_scale=torch.ones((num_blocks, n_kv_heads), dtype=torch.float32, device=device),
+                v_scale=torch.ones((num_blocks, n_kv_heads), dtype=torch.float32, device=device))
+
+
+def fp8_view(book, cache):
+    num_blocks, n_kv = cache["k_scale"].shape
+    return binding.make_fp8_view(cache["k_codes"], cache["v_codes"], cache["k_scale"], cache["v_scale"], num_blocks,
+                                 n_kv, book.block_size)
+
+
+def allocate_fp8_workspace(book, n_tokens, batch, n_q_heads, n_kv_heads, max_context, device="cuda"):
+    nbytes = binding.tq_fp8_workspace_bytes(book, n_tokens, batch, n_q_heads, n_kv_heads, max_context)
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), nbytes
+
+
 def cache_bytes_per_token_head(book):
     return sum(binding.tq_cache_field_bytes(book).values())

@@ -1188,6 +1188,119 @@ tq_status tq_extend_attention(const tq_codebook* book, const void* q, tq_dtype d
   return launched(tq::launch_extend(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
+// The checks that the entry points of the 8-bit cache share, and their cache
+// arguments.
+static tq_status fp8_cache_args(const tq_codebook* book, const tq_fp8_view* cache, const int32_t* block_table,
+                                int max_blocks, int n_tokens, int batch, int n_kv_heads, const int32_t* query_start,
+                                const int32_t* context_lens, tq::Fp8Cache* c) {
+  if (!valid_device_handle(book) || cache == nullptr || n_tokens < 0 || batch < 0 || n_kv_heads <= 0 || max_blocks <= 0) {
+    return TQ_ERR_INVALID_ARG;
+  }
+  if (cache->num_blocks <= 0 || cache->n_kv_heads != n_kv_heads || cache->block_size != book->cfg.block_size) {
+    return TQ_ERR_INVALID_ARG;
+  }
+  for (const void* p : {static_cast<const void*>(cache->k_codes), static_cast<const void*>(cache->v_codes),
+                        static_cast<const void*>(cache->k_scale), static_cast<const void*>(cache->v_scale)}) {
+    if (p == nullptr || !aligned16(p)) return TQ_ERR_INVALID_ARG;
+  }
+  if (block_table == nullptr && static_cast<long long>(batch) * max_blocks > cache->num_blocks) {
+    return TQ_ERR_INVALID_ARG;
+  }
+  if (n_tokens > 0 && batch > 0 && (!query_start || !context_lens)) return TQ_ERR_INVALID_ARG;
+  if (!aligned4(query_start) || !aligned4(context_lens) || !aligned4(block_table)) return TQ_ERR_INVALID_ARG;
+  if (n_kv_heads > 65535) return TQ_ERR_UNSUPPORTED;   // (a grid dimension)
+  *c = tq::Fp8Cache{static_cast<uint8_t*>(cache->k_codes), static_cast<uint8_t*>(cache->v_codes), cache->k_scale,
+                    cache->v_scale, cache->num_blocks, n_kv_heads, cache->block_size, block_table, max_blocks, batch,
+                    n_tokens, query_start, context_lens, book->d_error};
+  return TQ_OK;
+}
+
+// Rows of keys and values that the append reads and the read writes.
+static tq_status fp8_rows_args(const void* k, const void* v, tq_dtype dtype, int n_tokens, int n_kv_heads,
+                               int64_t k_stride, int64_t v_stride, tq::Fp8RowsArgs* a) {
+  if (dtype != TQ_BF16 && dtype != TQ_FP32) return TQ_ERR_INVALID_ARG;
+  if (n_tokens > 0 && k == nullptr && v == nullptr) return TQ_ERR_INVALID_ARG;
+  const int64_t vec = dtype == TQ_BF16 ? 8 : 4;   // elements of a 16-byte access
+  for (int i = 0; i < 2; ++i) {
+    const void* const rows = i == 0 ? k : v;
+    const int64_t stride = i == 0 ? k_stride : v_stride;
+    a->rows[i] = const_cast<void*>(rows);
+    a->stride[i] = stride;
+    if (rows == nullptr) continue;
+    if (!aligned16(rows) || stride < static_cast<int64_t>(n_kv_heads) * tq::kDim || stride % vec != 0) {
+      return TQ_ERR_INVALID_ARG;
+    }
+  }
+  return TQ_OK;
+}
+
+tq_status tq_fp8_append(const tq_codebook* book, const void* k, const void* v, tq_dtype dtype, int n_tokens, int batch,
+                        int n_kv_heads, int64_t k_stride, int64_t v_stride, const tq_fp8_view* cache,
+                        const int32_t* block_table, int max_blocks, const int32_t* query_start,
+                        const int32_t* context_lens, void* stream) {
+  tq::Fp8RowsArgs a{};
+  tq_status st = fp8_cache_args(book, cache, block_table, max_blocks, n_tokens, batch, n_kv_heads, query_start,
+                                context_lens, &a.c);
+  if (st == TQ_OK) st = fp8_rows_args(k, v, dtype, n_tokens, n_kv_heads, k_stride, v_stride, &a);
+  if (st != TQ_OK || n_tokens == 0 || batch == 0) return st;
+  DeviceGuard guard(book->device);
+  return launched(tq::launch_fp8_append(a, dtype == TQ_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+tq_status tq_fp8_read(const tq_codebook* book, const tq_fp8_view* cache, const int32_t* block_table, int max_blocks,
+                      int n_tokens, int batch, int n_kv_heads, const int32_t* query_start, const int32_t* context_lens,
+                      tq_dtype dtype, void* k_out, void* v_out, int64_t k_stride, int64_t v_stride, void* stream) {
+  tq::Fp8RowsArgs a{};
+  tq_status st = fp8_cache_args(book, cache, block_table, max_blocks, n_tokens, batch, n_kv_heads, query_start,
+                                context_lens, &a.c);
+  if (st == TQ_OK) st = fp8_rows_args(k_out, v_out, dtype, n_tokens, n_kv_heads, k_stride, v_stride, &a);
+  if (st != TQ_OK || n_tokens == 0 || batch == 0) return st;
+  DeviceGuard guard(book->device);
+  return launched(tq::launch_fp8_read(a, dtype == TQ_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+size_t tq_fp8_workspace_bytes(const tq_codebook* book, int n_tokens, int batch, int n_q_heads, int n_kv_heads,
+                              int max_context) {
+  if (!valid_device_handle(book) || n_tokens <= 0 || batch <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 ||
+      n_q_heads % n_kv_heads != 0 || max_context < 0) {
+    return 0;
+  }
+  return tq::fp8_workspace_bytes(n_tokens, batch, n_q_heads, n_kv_heads, max_context, book->num_sms);
+}
+
+tq_status tq_fp8_attention(const tq_codebook* book, const void* q, tq_dtype dtype, int n_tokens, int batch,
+                           int n_q_heads, int n_kv_heads, const tq_fp8_view* cache, const int32_t* block_table,
+                           int max_blocks, const int32_t* query_start, const int32_t* context_lens, int max_context,
+                           float scale, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  tq::Fp8AttendArgs a{};
+  const tq_status st = fp8_cache_args(book, cache, block_table, max_blocks, n_tokens, batch, n_kv_heads, query_start,
+                                      context_lens, &a.c);
+  if (st != TQ_OK) return st;
+  if (dtype != TQ_BF16 && dtype != TQ_FP32) return TQ_ERR_INVALID_ARG;
+  if (n_q_heads <= 0 || n_q_heads % n_kv_heads != 0 || max_context < 0) return TQ_ERR_INVALID_ARG;
+  if (!(scale >= 0.f) || !std::isfinite(scale)) return TQ_ERR_INVALID_ARG;
+  if (static_cast<long long>(n_tokens) * n_q_heads > (1ll << 31) - 1) return TQ_ERR_INVALID_ARG;
+  const bool any = n_tokens > 0 && batch > 0;
+  if (any && (!q || !aligned16(q) || !out || !aligned16(out))) return TQ_ERR_INVALID_ARG;
+  if (max_context > (1 << 30)) return TQ_ERR_UNSUPPORTED;   // (positions and tile bounds are ints)
+  if (!any) return TQ_OK;
+  const size_t need = tq_fp8_workspace_bytes(book, n_tokens, batch, n_q_heads, n_kv_heads, max_context);
+  if (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) {
+    return TQ_ERR_WORKSPACE;
+  }
+  a.q = q;
+  a.q_bf16 = dtype == TQ_BF16;
+  a.n_q = n_q_heads;
+  a.group = n_q_heads / n_kv_heads;
+  a.max_context = max_context;
+  a.scale = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(book->cfg.d));
+  a.out = out;
+  a.num_sms = book->num_sms;
+  a.debug_withhold = book->debug_withhold;
+  DeviceGuard guard(book->device);
+  return launched(tq::launch_fp8_attention(a, workspace, static_cast<cudaStream_t>(stream)));
+}
+
 tq_status tq_debug_withhold_commit(tq_codebook* book, int enable) {
   if (!valid_device_handle(book)) return TQ_ERR_INVALID_ARG;
   book->debug_withhold = enable ? 1 : 0;

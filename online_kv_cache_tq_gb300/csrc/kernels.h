@@ -317,4 +317,47 @@ cudaError_t launch_extend(const ExtendArgs& args, void* workspace, cudaStream_t 
 cudaError_t launch_extend_narrow(const ExtendArgs& args, int ctas, cudaStream_t stream);   // (extend_tc.cu)
 cudaError_t launch_extend_wide(const ExtendArgs& args, int ctas, cudaStream_t stream);     // (extend_wide.cu)
 
+// The 8-bit cache (fp8_cache.cu, fp8_attention.cu): e4m3 codes with one power
+// of two as scale per (block, KV head) of keys and of values.  A block's codes
+// of a KV head are one run in the order in which tcgen05.mma reads a K-major
+// operand without swizzle (core matrices of 8 rows x 16 bytes), so that a bulk
+// copy of it is an operand:
+//   keys    [block_size / 8][8 chunks][8 tokens][16 coordinates]
+//   values  [block_size / 16][128 coordinates][16 tokens]
+constexpr int kFp8MinExp = -40, kFp8MaxExp = 14;   // of the scales
+struct Fp8Cache {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;             // [num_blocks][n_kv]
+  float* v_scale;
+  int num_blocks, n_kv, block_size;
+  const int32_t* block_table; // [batch][max_blocks]; null: identity
+  int max_blocks, batch, n_tokens;
+  const int32_t* query_start; // [batch + 1]
+  const int32_t* context_lens;
+  int* error;
+};
+struct Fp8RowsArgs {
+  Fp8Cache c;
+  void* rows[2];              // keys and values (null: not this call's): read by the append, written by the read
+  long long stride[2];        // elements from token to token
+  int window;                 // tokens per CTA (set by the launcher)
+};
+cudaError_t launch_fp8_append(const Fp8RowsArgs& args, bool bf16, cudaStream_t stream);
+cudaError_t launch_fp8_read(const Fp8RowsArgs& args, bool bf16, cudaStream_t stream);
+
+struct Fp8AttendArgs {
+  Fp8Cache c;
+  const void* q;              // [n_tokens][n_q][128]
+  bool q_bf16;
+  int n_q, group;
+  int max_context;
+  float scale;
+  void* out;                  // bf16 [n_tokens][n_q][128]
+  int num_sms;
+  int debug_withhold;
+};
+size_t fp8_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms);
+cudaError_t launch_fp8_attention(const Fp8AttendArgs& args, void* workspace, cudaStream_t stream);
+
 }  // namespace tq
