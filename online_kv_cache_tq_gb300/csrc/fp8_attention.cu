@@ -1,92 +1,797 @@
-// Attention over the 8-bit cache: a warp per (token, query head), a lane per
-// cached token for the scores and per four coordinates for the values.
+// Attention over the 8-bit cache, few rows (new tokens x query heads of a
+// group) per sequence: a decode step, the verification of drafted tokens.
+//
+//   s_tr = scale <q_r, c_t> 2^{e_k(t)},  o_r = sum_t p_tr c^v_t 2^{e_v(t)},  p = softmax(s)
+//
+// Both products run on the tensor cores on the codes as they lie in memory: a
+// block's run of a KV head is a K-major operand without swizzle, so that a key
+// or value tile (128 tokens) is four bulk copies of 32 tokens and no
+// instruction touches its bytes.  Cached tokens are the lanes of the score
+// product, coordinates those of the output product; rows are its columns:
+//   scores [128 tokens x 4 RT]  = keys x (four e4m3 pieces of each query)^T,
+//   output [128 coordinates x 3 RT] = values^T x (three pieces of each weight)^T,
+// pieces as in e4m3_pieces.cuh (queries to 2^-16 of a coordinate, weights to
+// 2^-12).  A thread owns a token for the softmax and a coordinate for the
+// output, of eight rows; it keeps the output in registers and adds a tile's
+// product to it, so nothing is rescaled in tensor memory.
+//
+// The bound is HBM: 256 bytes per token and KV head.  A tile of 32 KB takes an
+// SM 1490 cycles at the copy rate, and eight rows of it 1600 warp instructions,
+// a quarter of what the four schedulers issue in that time.
+//
+// Work is split as in extend.cu: an item is a row tile of a sequence and KV
+// head, worth kItemCost units and one per key tile; every CTA takes an equal
+// run of units, and row tiles that runs cut are joined by a second launch.
+// Every CTA forms the sums over the batch itself, which costs less than a
+// launch before it.
+#include <cstddef>
+
+#include "e4m3_pieces.cuh"
 #include "fp8_common.cuh"
+#include "tc_ptx.cuh"
 
 namespace tq {
 namespace {
 
-__global__ void __launch_bounds__(32) fp8_attend_kernel(Fp8AttendArgs a) {
-  __shared__ float q_s[kDim], p_s[32];
-  __shared__ int token_s[32];
+#define TQ_WAIT(b, ph) ptx::wait_bar(&(b), (ph), abort, c.error, kErrTimeout)
+#define TQ_WARP_WAIT(b, ph) __all_sync(0xffffffffu, TQ_WAIT(b, ph))
+
+constexpr int kTile = 128;             // tokens of a key tile
+constexpr int kSlotBytes = kTile * kDim;
+constexpr int kGroupBytes = 32 * kDim; // keys or values of 32 tokens: one copy
+constexpr int kRowsPerThread = 8;
+constexpr int kMetaRing = 16;          // more tiles than can be on their way
+constexpr int kItemCost = 2;
+constexpr float kWeightScale = 256.f;  // weights are at most 1: times this in e4m3
+
+// RT rows a tile: 8 (two CTAs an SM), 16 (two), 32 (one).
+template <int RT>
+struct Shape {
+  static constexpr int kSplit = RT / kRowsPerThread;        // threads per token
+  static constexpr int kSoftWarps = 4 * kSplit;
+  static constexpr int kThreads = 32 * (kSoftWarps + 3);
+  static constexpr int kCtas = RT == 32 ? 1 : 2;            // per SM
+  static constexpr int kSlots = RT == 32 ? 10 : 5;          // ring of key and value tiles in turn
+  static constexpr int kQueryCols = 4 * RT;
+  static constexpr int kWeightCols = (3 * RT + 15) / 16 * 16;
+  static constexpr int kQueryBytes = kQueryCols * kDim, kWeightBytes = kWeightCols * kTile;
+  static constexpr int kTmem = RT == 8 ? 128 : RT == 16 ? 256 : 512;
+  static constexpr int kSmem = kSlots * kSlotBytes + 2 * kQueryBytes + 2 * kWeightBytes + 128;   // (128: alignment)
+  static_assert(2 * kQueryCols + 2 * kWeightCols <= kTmem, "two buffers of scores and of outputs");
+};
+
+struct TileInfo {
+  float k_scale[4], v_scale[4];   // by group of 32 tokens
+  uint32_t groups;                // those that there are
+};
+
+// A sequence as the launch sees it.
+struct Sequence {
+  int row0, n, ctx;
+  long long units;
+  bool ok;
+};
+__device__ __forceinline__ int row_tiles(int rows, int rt) { return (rows + rt - 1) / rt; }
+__device__ __forceinline__ int key_tiles(int ctx) { return max(1, (ctx + kTile - 1) / kTile); }
+template <int RT>
+__device__ __forceinline__ Sequence load_sequence(const Fp8AttendArgs& a, int b) {
   const Fp8Cache& c = a.c;
-  const int t = blockIdx.x, h = blockIdx.y, kvh = h / a.group, lane = threadIdx.x;
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int b = lane; b < c.batch; b += 32) {
-      const int r0 = c.query_start[b], r1 = c.query_start[b + 1];
-      if (r0 < 0 || r0 > r1 || r1 > c.n_tokens) atomicCAS(c.error, 0, kErrContext);
-    }
-  int lo = 0, hi = c.batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (c.query_start[mid] <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  const int s0 = c.query_start[lo], s1 = c.query_start[lo + 1];
-  if (s0 > t || t >= s1) return;
-  int ctx = c.context_lens[lo];
-  const bool rows_ok = s0 >= 0 && s1 <= c.n_tokens;
+  const int s0 = c.query_start[b], s1 = c.query_start[b + 1], ctx = c.context_lens[b];
+  const bool rows_ok = s0 >= 0 && s0 <= s1 && s1 <= c.n_tokens;
   const bool ctx_ok = ctx >= 0 && ctx <= a.max_context && ctx <= static_cast<long long>(c.max_blocks) * c.block_size;
-  if (!rows_ok || !ctx_ok) atomicCAS(c.error, 0, kErrContext);
-  if (!rows_ok) return;
-  const int seen = ctx_ok ? max(0, ctx - (s1 - s0) + t - s0 + 1) : 0;
-  const long long vec = static_cast<long long>(t) * a.n_q + h;
-  for (int i = lane; i < kDim; i += 32)
-    q_s[i] = a.q_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[vec * kDim + i])
-                      : static_cast<const float*>(a.q)[vec * kDim + i];
-  __syncwarp();
-  float top = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int p0 = 0; p0 < seen; p0 += 32) {
-    const int col = p0 / c.block_size, off = p0 - col * c.block_size;
-    const long long id = c.block_table ? c.block_table[static_cast<long long>(lo) * c.max_blocks + col]
-                                       : static_cast<long long>(lo) * c.max_blocks + col;
-    if (id < 0 || id >= c.num_blocks) {
-      atomicCAS(c.error, 0, kErrBlock);
-      continue;
-    }
-    const long long row = id * c.n_kv + kvh;
-    const int token = off + lane;
-    float s = -INFINITY;
-    if (p0 + lane < seen) {
-      const uint8_t* const k = c.k + row * c.block_size * kDim + (token >> 3) * 1024 + (token & 7) * 16;
-      float dot = 0.f;
-      for (int i = 0; i < kDim; i += 2) {
-        const float2 f = fp8_floats(*reinterpret_cast<const uint16_t*>(k + (i >> 4) * 128 + (i & 15)));
-        dot = fmaf(q_s[i], f.x, fmaf(q_s[i + 1], f.y, dot));
-      }
-      s = dot * c.k_scale[row] * a.scale;
-    }
-    float m = s;
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float next = fmaxf(top, m), keep = top == -INFINITY ? 0.f : expf(top - next);
-    const float p = p0 + lane < seen ? expf(s - next) : 0.f;
-    top = next;
-    p_s[lane] = p;
-    token_s[lane] = token;
-    float part = p;
-    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-    sum = sum * keep + part;
-    __syncwarp();
-    const float vs = c.v_scale[row];
-    for (int j = 0; j < 4; ++j) acc[j] *= keep;
-    for (int i = 0; i < 32 && p0 + i < seen; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int tok = token_s[i];
-        const uint8_t b = c.v[row * c.block_size * kDim + (tok >> 4) * 2048 + (4 * lane + j) * 16 + (tok & 15)];
-        acc[j] = fmaf(p_s[i], fp8_floats(b).x * vs, acc[j]);
-      }
-    __syncwarp();
+  Sequence s;
+  s.row0 = rows_ok ? s0 : 0;
+  s.n = rows_ok ? s1 - s0 : 0;
+  s.ctx = ctx_ok ? ctx : 0;
+  s.ok = rows_ok && ctx_ok;
+  s.units = s.n == 0 ? 0 : static_cast<long long>(c.n_kv) * row_tiles(s.n * a.group, RT) * (kItemCost + key_tiles(s.ctx));
+  return s;
+}
+
+// A walk over the key tiles of a run of units.
+template <int RT>
+struct Walk {
+  int b, kvh, rt;        // sequence, KV head, row tile
+  int tile, tiles;       // key tile, and how many the item has
+  int tile0;             // the run's first one of the item
+  Sequence s;
+  long long pos, end;    // unit of the tile, end of the run
+
+  // At unit `rem` of sequence b; false when the run ends before a key tile.
+  __device__ __forceinline__ bool start(const Fp8AttendArgs& a, int seq, long long rem) {
+    b = seq;
+    s = load_sequence<RT>(a, b);
+    tiles = key_tiles(s.ctx);
+    const long long item = rem / (kItemCost + tiles);
+    const int offset = static_cast<int>(rem - item * (kItemCost + tiles)), rts = row_tiles(s.n * a.group, RT);
+    kvh = static_cast<int>(item / rts);
+    rt = static_cast<int>(item - static_cast<long long>(kvh) * rts);
+    tile = tile0 = max(0, offset - kItemCost);
+    pos += max(0, kItemCost - offset);
+    return pos < end;
   }
-  for (int j = 0; j < 4; ++j)
-    static_cast<__nv_bfloat16*>(a.out)[vec * kDim + 4 * lane + j] = __float2bfloat16_rn(sum == 0.f ? 0.f : acc[j] / sum);
+  // Whether the tile is the run's last one of the item.
+  __device__ __forceinline__ bool last_of_item() const { return tile + 1 == tiles || pos + 1 == end; }
+  // To the next tile; false at the run's end.
+  __device__ __forceinline__ bool next(const Fp8AttendArgs& a) {
+    ++pos;
+    if (tile + 1 < tiles) {
+      ++tile;
+      return pos < end;
+    }
+    if (pos + kItemCost >= end) {
+      pos = end;
+      return false;
+    }
+    if (++rt >= row_tiles(s.n * a.group, RT)) {
+      rt = 0;
+      if (++kvh >= a.c.n_kv) {
+        kvh = 0;
+        do {
+          s = load_sequence<RT>(a, ++b);          // (units are left, so there is one with work)
+        } while (s.units == 0);
+        tiles = key_tiles(s.ctx);
+      }
+    }
+    pos += kItemCost;
+    tile = tile0 = 0;
+    return true;
+  }
+};
+
+struct RunStart {
+  long long total, rem;
+  int b;
+};
+
+// The run's first sequence and the unit in it, by the whole CTA.
+template <int RT>
+__device__ __forceinline__ void find_run(const Fp8AttendArgs& a, RunStart* out, long long* warp_s) {
+  constexpr int kWarps = Shape<RT>::kThreads / 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int batch = a.c.batch;
+  // all units: in one round while the batch has no more sequences than the CTA threads
+  long long mine = 0;
+  Sequence s{};
+  for (int b = tid; b < batch; b += blockDim.x) {
+    s = load_sequence<RT>(a, b);
+    if (!s.ok && blockIdx.x == 0) atomicCAS(a.c.error, 0, kErrContext);
+    mine += s.units;
+  }
+  auto scan = [&](long long v, long long* total) {      // inclusive
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += o;
+    }
+    if (lane == 31) warp_s[warp] = v;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += warp_s[w];
+      all += warp_s[w];
+    }
+    __syncthreads();
+    *total = all;
+    return v + before;
+  };
+  long long total;
+  const long long upto = scan(mine, &total);
+  const long long pos = blockIdx.x * ((total + gridDim.x - 1) / gridDim.x);
+  if (tid == 0) out->total = total;
+  auto look = [&](int b, long long end, long long units) {
+    if (units > 0 && end - units <= pos && pos < end) {
+      out->b = b;
+      out->rem = pos - (end - units);
+    }
+  };
+  if (batch <= static_cast<int>(blockDim.x)) {
+    look(tid, upto, mine);
+  } else {
+    long long base = 0;
+    for (int b0 = 0; b0 < batch; b0 += blockDim.x) {
+      const int b = b0 + tid;
+      const long long units = b < batch ? load_sequence<RT>(a, b).units : 0;
+      long long all;
+      const long long end = base + scan(units, &all);
+      look(b, end, units);
+      base += all;
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Floats in the order of their values, as integers (a positive NaN above all).
+__device__ __forceinline__ int ordered(float x) {
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+
+template <int RT>
+struct Barriers {
+  uint64_t full[Shape<RT>::kSlots], empty[Shape<RT>::kSlots];
+  uint64_t s_full[2], p_full[2], o_full[2];   // scores, weights and output product of a tile
+  uint64_t q_full[2], q_empty[2];             // queries of a segment
+  uint64_t maxima[Shape<RT>::kSplit], sums;   // the softmax warps of a row split, and all of them
+  uint64_t drain;
+};
+
+template <int RT>
+struct Shared {
+  Barriers<RT> bar;
+  TileInfo info[kMetaRing];
+  float factor[2][RT];           // scale log2(e) over the query's piece scale
+  int seen[2][RT];               // positions a row sees
+  __align__(16) float top[2][Shape<RT>::kSplit][4][kRowsPerThread];   // (16-byte stores)
+  float sum[2][Shape<RT>::kSoftWarps][kRowsPerThread];
+  uint32_t poison[3][RT];        // rows that see a value that is NaN
+  long long warp_s[Shape<RT>::kThreads / 32];
+  RunStart start;
+  uint32_t tmem;
+  int abort;
+};
+
+// Floats of a partial output: the rows' outputs, then their (reference, sum).
+__host__ __device__ constexpr int part_floats(int rows) { return rows * (kDim + 2); }
+
+// Vector (token x query head) of row r of a sequence and KV head.
+__device__ __forceinline__ long long row_vector(const Fp8AttendArgs& a, int row0, int kvh, int r) {
+  const int tok = r / a.group;
+  return (static_cast<long long>(row0) + tok) * a.n_q + kvh * a.group + r - tok * a.group;
+}
+
+template <int RT>
+__global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_attend_kernel(Fp8AttendArgs a) {
+  using P = Shape<RT>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared<RT> sh;
+  static_assert(offsetof(Shared<RT>, top) % 16 == 0 && alignof(Shared<RT>) >= 16, "16-byte stores");
+  uint8_t* const smem = smem_raw + ((128u - (ptx::smem_u32(smem_raw) & 127u)) & 127u);
+  uint8_t* const query_s = smem + P::kSlots * kSlotBytes;
+  uint8_t* const weight_s = query_s + 2 * P::kQueryBytes;
+  const Fp8Cache& c = a.c;
+  Barriers<RT>& bar = sh.bar;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* const abort = &sh.abort;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  find_run<RT>(a, &sh.start, sh.warp_s);
+  const long long total = sh.start.total, per = (total + gridDim.x - 1) / gridDim.x;
+  Walk<RT> walk;
+  walk.pos = blockIdx.x * per;
+  walk.end = min(walk.pos + per, total);
+  bool more = walk.pos < walk.end && walk.start(a, sh.start.b, sh.start.rem);
+  if (!more) {                                    // (the whole CTA)
+    if (tid == 0) a.cuts[blockIdx.x] = CutItem{0, 0, 0, 0, 0};
+    return;
+  }
+  if (tid == 0) {
+    sh.abort = 0;
+    for (int s = 0; s < P::kSlots; ++s) {
+      ptx::mbar_init(&bar.full[s], 1);
+      ptx::mbar_init(&bar.empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(&bar.s_full[s], 1);
+      ptx::mbar_init(&bar.p_full[s], 32 * P::kSoftWarps);
+      ptx::mbar_init(&bar.o_full[s], 1);
+      ptx::mbar_init(&bar.q_full[s], 1);
+      ptx::mbar_init(&bar.q_empty[s], 1 + P::kSoftWarps);   // the scores' products, and who reads the factors
+    }
+    for (int s = 0; s < P::kSplit; ++s) ptx::mbar_init(&bar.maxima[s], 4);
+    ptx::mbar_init(&bar.sums, P::kSoftWarps);
+    ptx::mbar_init(&bar.drain, 1);
+    ptx::fence_mbar_init();
+  }
+  for (int i = tid; i < 3 * RT; i += P::kThreads) (&sh.poison[0][0])[i] = 0;
+  if (warp == P::kSoftWarps) {
+    ptx::tmem_alloc(&sh.tmem, P::kTmem);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t scores_t = tmem, outputs_t = tmem + 2 * P::kQueryCols;
+  bool ok = true;
+
+  if (warp < P::kSoftWarps) {
+    // ---------------- softmax and output ----------------
+    const int quarter = warp & 3, split = warp >> 2, token = 32 * quarter + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    const uint32_t my_scores = scores_t + lanes + 4 * kRowsPerThread * split;
+    const uint32_t my_outputs = outputs_t + lanes + 3 * kRowsPerThread * split;
+    uint8_t* const my_weights = weight_s + (token >> 4) * (P::kWeightCols * 16) + 3 * kRowsPerThread * split * 16 + (token & 15);
+    int jt = 0;                                   // key tiles so far
+    for (int seg = 0; more; ++seg) {
+      const int n = walk.s.n, ctx = walk.s.ctx, row0 = walk.s.row0, kvh = walk.kvh, rt = walk.rt;
+      const int first = rt * RT + split * kRowsPerThread;     // my first row of the sequence
+      ok = TQ_WARP_WAIT(bar.q_full[seg & 1], (seg >> 1) & 1);
+      if (!ok) break;
+      const float* const factor = sh.factor[seg & 1] + split * kRowsPerThread;
+      const int* const seen = sh.seen[seg & 1] + split * kRowsPerThread;
+      const int all_see = sh.seen[seg & 1][0];    // positions that every row sees
+      float acc[kRowsPerThread], sum[kRowsPerThread], ref[kRowsPerThread];
+#pragma unroll
+      for (int r = 0; r < kRowsPerThread; ++r) acc[r] = sum[r] = 0.f, ref[r] = -INFINITY;
+      auto add_output = [&](int j, const float (&keep)[kRowsPerThread]) {   // tile j's product, then times keep
+        if (!TQ_WARP_WAIT(bar.o_full[j & 1], (j >> 1) & 1)) return false;
+        ptx::tc_fence_after();
+        uint32_t d[3][8];
+        const uint32_t at = my_outputs + (j & 1) * P::kWeightCols;
+        tmem_ld8(at, d[0]);
+        tmem_ld8(at + 8, d[1]);
+        tmem_ld8(at + 16, d[2]);
+        const bool there = sh.info[j & (kMetaRing - 1)].groups != 0;   // (else nothing was multiplied)
+#pragma unroll
+        for (int r = 0; r < kRowsPerThread; ++r) {
+          const float d0 = __uint_as_float(d[(3 * r) >> 3][(3 * r) & 7]);
+          const float d1 = __uint_as_float(d[(3 * r + 1) >> 3][(3 * r + 1) & 7]);
+          const float d2 = __uint_as_float(d[(3 * r + 2) >> 3][(3 * r + 2) & 7]);
+          const float o = fmaf(fmaf(d2, 0.0625f, d1), 0.0625f, d0);
+          acc[r] = (there ? acc[r] + o : acc[r]) * keep[r];
+        }
+        return true;
+      };
+      const int tile0 = walk.tile0, tiles = walk.tiles;
+      int reached = 0;                            // key tiles of the item that are done
+      bool last = false;
+      for (; !last; ++jt) {
+        const int t = walk.tile;
+        last = walk.last_of_item();
+        reached = t + 1;
+        ok = TQ_WARP_WAIT(bar.s_full[jt & 1], (jt >> 1) & 1);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        uint32_t s[32];
+        ptx::tmem_ld32(my_scores + (jt & 1) * P::kQueryCols, s);
+        const int slot_turn = 2 * jt + 1, slot = slot_turn % P::kSlots;
+        ok = TQ_WARP_WAIT(bar.full[slot], (slot_turn / P::kSlots) & 1);
+        if (!ok) break;
+        const TileInfo& info = sh.info[jt & (kMetaRing - 1)];
+        const uint32_t groups = info.groups;
+        const float ks = info.k_scale[quarter], vs = info.v_scale[quarter];
+        const float up = static_cast<float>(fp8_exponent(vs)), down = fp8_power(-fp8_exponent(vs));
+        const bool here = groups >> quarter & 1u;
+        const int pos = t * kTile + token;
+        float x[kRowsPerThread];
+#pragma unroll
+        for (int r = 0; r < kRowsPerThread; ++r) {
+          const float d = fmaf(fmaf(fmaf(__uint_as_float(s[4 * r + 3]), 0.0625f, __uint_as_float(s[4 * r + 2])), 0.0625f,
+                                    __uint_as_float(s[4 * r + 1])), 0.0625f, __uint_as_float(s[4 * r]));
+          // (with the value's scale: what the weight is of the block's codes)
+          x[r] = fmaf(d * ks, factor[r], up);
+        }
+        if (groups != 15u || (t + 1) * kTile > all_see) {
+#pragma unroll
+          for (int r = 0; r < kRowsPerThread; ++r) x[r] = here && pos < seen[r] ? x[r] : -INFINITY;
+        }
+        // the tile's largest, over the four warps
+        float keep[kRowsPerThread];
+        {
+          int top[kRowsPerThread];
+#pragma unroll
+          for (int r = 0; r < kRowsPerThread; ++r) top[r] = __reduce_max_sync(0xffffffffu, ordered(x[r]));
+          float(*const buf)[kRowsPerThread] = sh.top[jt & 1][split];
+          if (lane == 0) {
+            float4* const dst = reinterpret_cast<float4*>(buf[quarter]);
+            dst[0] = make_float4(unordered(top[0]), unordered(top[1]), unordered(top[2]), unordered(top[3]));
+            dst[1] = make_float4(unordered(top[4]), unordered(top[5]), unordered(top[6]), unordered(top[7]));
+            ptx::mbar_arrive(&bar.maxima[split]);
+          }
+          __syncwarp();
+          ok = TQ_WARP_WAIT(bar.maxima[split], jt & 1);
+          if (!ok) break;
+#pragma unroll
+          for (int r = 0; r < kRowsPerThread; ++r) {
+            int m = ordered(ref[r]);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) m = max(m, ordered(buf[w][r]));
+            const float to = unordered(m);
+            keep[r] = to == ref[r] ? 1.f : exp2_fast(ref[r] - to);
+            ref[r] = to;
+          }
+        }
+        // weights: at most 1, of the block's codes
+        uint8_t* const dst = my_weights + (jt & 1) * P::kWeightBytes;
+#pragma unroll
+        for (int r = 0; r < kRowsPerThread; r += 2) {
+          float2 w;
+          w.x = exp2_fast(x[r] - (ref[r] == -INFINITY ? 0.f : ref[r]));
+          w.y = exp2_fast(x[r + 1] - (ref[r + 1] == -INFINITY ? 0.f : ref[r + 1]));
+          sum[r] = fmaf(sum[r], keep[r], w.x * down);
+          sum[r + 1] = fmaf(sum[r + 1], keep[r + 1], w.y * down);
+          float2 y = __fmul2_rn(w, make_float2(kWeightScale, kWeightScale));
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const uint32_t p = fp8_pair(y.x, y.y);
+            dst[(3 * r + i) * 16] = static_cast<uint8_t>(p & 0xffu);
+            dst[(3 * r + 3 + i) * 16] = static_cast<uint8_t>(p >> 8);
+            if (i < 2) y = __fmul2_rn(__ffma2_rn(fp8_floats(p), make_float2(-1.f, -1.f), y), make_float2(16.f, 16.f));
+          }
+        }
+        if (split == 0 && here) {
+          // values that no weight may meet: slots behind the context, whatever
+          // they hold, and vectors that are NaN (whose rows are marked)
+          uint8_t* const value = smem + slot * kSlotBytes + (token >> 4) * 2048 + (token & 15);
+          const bool nan = (value[0] & 0x7fu) == 0x7fu;
+          if (pos >= ctx || nan) {
+            if (pos < ctx)
+              for (int r = 0; r < RT; ++r)
+                if (pos < sh.seen[seg & 1][r]) sh.poison[seg % 3][r] = 1;
+#pragma unroll 4
+            for (int d = 0; d < kDim; ++d) value[d * 16] = 0;
+          }
+        }
+        ptx::fence_async_shared();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&bar.p_full[jt & 1]);
+        if (t > tile0) {
+          ok = add_output(jt - 1, keep);
+          if (!ok) break;
+          ptx::tc_fence_before();
+        }
+        more = walk.next(a);
+      }
+      if (!ok) break;
+      const float one[kRowsPerThread] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+      ok = add_output(jt - 1, one);
+      if (!ok) break;
+      ptx::tc_fence_before();
+      // the rows' sums over the four warps
+#pragma unroll
+      for (int r = 0; r < kRowsPerThread; ++r) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], o);
+        if (lane == 0) sh.sum[seg & 1][warp][r] = sum[r];
+      }
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(&bar.sums);
+        ptx::mbar_arrive(&bar.q_empty[seg & 1]);  // (factors and limits are read)
+      }
+      ok = TQ_WARP_WAIT(bar.sums, seg & 1);
+      if (!ok) break;
+      if (tid < RT) sh.poison[(seg + 2) % 3][tid] = 0;        // (read by all before they came here)
+      // (a run's first item may have begun in the run before, its last may go on)
+      const bool whole = tile0 == 0 && reached == tiles;
+      float* const part = a.part + (2ll * blockIdx.x + (tile0 == 0 ? 1 : 0)) * part_floats(RT);
+#pragma unroll
+      for (int r = 0; r < kRowsPerThread; ++r) {
+        const int row = split * kRowsPerThread + r;
+        if (first + r >= n * a.group) break;
+        float all = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) all += sh.sum[seg & 1][4 * split + w][r];
+        if (sh.poison[seg % 3][row] != 0) all = __int_as_float(0x7fc00000);
+        if (whole) {
+          static_cast<__nv_bfloat16*>(a.out)[row_vector(a, row0, kvh, first + r) * kDim + token] =
+              __float2bfloat16_rn(all == 0.f ? 0.f : acc[r] / (kWeightScale * all));
+        } else {
+          part[row * kDim + token] = acc[r];
+          if (token == 0) {
+            part[RT * kDim + 2 * row] = ref[r];
+            part[RT * kDim + 2 * row + 1] = all;
+          }
+        }
+      }
+    }
+  } else if (warp == P::kSoftWarps) {
+    // ---------------- products ----------------
+    // the whole warp walks the tiles and waits; an elected lane issues
+    const uint32_t ring = ptx::smem_u32(smem);
+    const uint64_t key_desc = ptx::desc_k_plain(ring, 128, 1024), value_desc = ptx::desc_k_plain(ring, 2048, 128);
+    const uint64_t query_desc = ptx::desc_k_plain(ptx::smem_u32(query_s), P::kQueryCols * 16, 128);
+    const uint64_t weight_desc = ptx::desc_k_plain(ptx::smem_u32(weight_s), P::kWeightCols * 16, 128);
+    constexpr uint32_t kScores = ptx::idesc_e4m3_f32(kTile, P::kQueryCols), kOutput = ptx::idesc_e4m3_f32(kDim, P::kWeightCols);
+    int seg = 0;
+    auto scores = [&](int j) {                    // of tile j, at which the walk stands
+      const int turn = 2 * j, slot = turn % P::kSlots;
+      if (walk.tile == walk.tile0 && !TQ_WARP_WAIT(bar.q_full[seg & 1], (seg >> 1) & 1)) return false;
+      if (!TQ_WARP_WAIT(bar.full[slot], (turn / P::kSlots) & 1)) return false;
+      const bool last = walk.last_of_item();
+      if (ptx::elect_one()) {
+        ptx::tc_fence_after();
+        const uint64_t k = key_desc + slot * (kSlotBytes / 16), q = query_desc + (seg & 1) * (P::kQueryBytes / 16);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          ptx::mma_e4m3(scores_t + (j & 1) * P::kQueryCols, k + ks * 16, q + ks * 2 * P::kQueryCols, kScores, ks > 0);
+        // (a test of the bounded waits: the first tile)
+        if (!(a.debug_withhold && blockIdx.x == 0 && j == 0)) ptx::mma_commit(&bar.s_full[j & 1]);
+        ptx::mma_commit(&bar.empty[slot]);
+        if (last) ptx::mma_commit(&bar.q_empty[seg & 1]);
+      }
+      __syncwarp();
+      if (last) ++seg;
+      return true;
+    };
+    ok = scores(0);
+    more = walk.next(a);
+    for (int j = 0; ok; ++j) {
+      const bool next = more;
+      if (next) {
+        ok = scores(j + 1);
+        if (!ok) break;
+        more = walk.next(a);
+      }
+      const int turn = 2 * j + 1, slot = turn % P::kSlots;
+      ok = TQ_WARP_WAIT(bar.full[slot], (turn / P::kSlots) & 1) && TQ_WARP_WAIT(bar.p_full[j & 1], (j >> 1) & 1);
+      if (!ok) break;
+      const uint32_t groups = sh.info[j & (kMetaRing - 1)].groups;
+      if (ptx::elect_one()) {
+        ptx::tc_fence_after();
+        const uint64_t v = value_desc + slot * (kSlotBytes / 16), w = weight_desc + (j & 1) * (P::kWeightBytes / 16);
+        bool added = false;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (!(groups >> g & 1u)) continue;
+          ptx::mma_e4m3(outputs_t + (j & 1) * P::kWeightCols, v + g * (kGroupBytes / 16), w + g * 2 * P::kWeightCols,
+                        kOutput, added);
+          added = true;
+        }
+        ptx::mma_commit(&bar.o_full[j & 1]);
+        ptx::mma_commit(&bar.empty[slot]);
+      }
+      __syncwarp();
+      if (!next) break;
+    }
+    if (ptx::elect_one()) {
+      ptx::mma_commit(&bar.drain);                // nothing is in flight when the CTA ends
+      ptx::drain_bar(&bar.drain, 0);
+    }
+  } else if (warp == P::kSoftWarps + 1) {
+    // ---------------- copies ----------------
+    // lane g < 4 has the tile's group g; block ids are read two tiles ahead and
+    // scales one, so that no tile waits for either
+    struct Group {
+      long long row;             // (block, KV head), -1: none
+      int off, id, kvh;
+      float ks, vs;
+      bool here;
+    };
+    auto read_id = [&]() {       // of the tile at which the walk stands
+      Group g{-1, 0, -1, walk.kvh, 1.f, 1.f, false};
+      const int pos = walk.tile * kTile + 32 * lane;
+      if (lane < 4 && pos < walk.s.ctx) {
+        const int col = pos / c.block_size;
+        g.off = pos - col * c.block_size;
+        const long long at = static_cast<long long>(walk.b) * c.max_blocks + col;
+        g.id = c.block_table ? __ldg(c.block_table + at) : static_cast<int>(at);
+        g.here = true;
+      }
+      return g;
+    };
+    auto read_scales = [&](Group& g) {
+      if (!g.here) return;
+      if (g.id < 0 || g.id >= c.num_blocks) {
+        atomicCAS(c.error, 0, kErrBlock);
+        return;
+      }
+      g.row = static_cast<long long>(g.id) * c.n_kv + g.kvh;
+      g.ks = __ldg(c.k_scale + g.row);
+      g.vs = __ldg(c.v_scale + g.row);
+    };
+    int turn = 0;
+    auto copy = [&](const Group& g, const uint8_t* field, uint32_t bytes) {
+      const int slot = turn % P::kSlots;
+      if (!TQ_WARP_WAIT(bar.empty[slot], ((turn / P::kSlots) & 1) ^ 1)) return false;
+      if (lane == 0) ptx::mbar_arrive_expect_tx(&bar.full[slot], bytes);
+      __syncwarp();
+      if (g.row >= 0)
+        ptx::bulk_load(smem + slot * kSlotBytes + lane * kGroupBytes, field + (g.row * c.block_size + g.off) * kDim,
+                       kGroupBytes, &bar.full[slot]);
+      ++turn;
+      return true;
+    };
+    Group now = read_id();
+    bool more1 = walk.next(a);
+    Group ahead = now;
+    if (more1) ahead = read_id();
+    read_scales(now);
+    for (int j = 0;; ++j) {
+      Group third = ahead;
+      bool more2 = false;
+      if (more1) {
+        read_scales(ahead);
+        more2 = walk.next(a);
+        if (more2) third = read_id();
+      }
+      const uint32_t groups = __ballot_sync(0xffffffffu, now.row >= 0);
+      const uint32_t bytes = __popc(groups) * kGroupBytes;
+      TileInfo& info = sh.info[j & (kMetaRing - 1)];
+      // (the tile sixteen before is done: its slots have been filled again since)
+      if (lane < 4) info.k_scale[lane] = now.ks, info.v_scale[lane] = now.vs;
+      if (lane == 0) info.groups = groups;
+      __syncwarp();
+      ok = copy(now, c.k, bytes) && copy(now, c.v, bytes);
+      if (!ok || !more1) break;
+      now = ahead;
+      ahead = third;
+      more1 = more2;
+    }
+    if (*abort && lane == 0)                      // copies in flight land before the CTA ends
+      for (int t = max(0, turn - P::kSlots); t < turn; ++t) ptx::drain_bar(&bar.full[t % P::kSlots], (t / P::kSlots) & 1);
+  } else {
+    // ---------------- queries ----------------
+    // one segment ahead of the others: e4m3 pieces of its rows, four coordinates a lane
+    CutItem cut{0, 0, 0, 0, 0};
+    for (int seg = 0; more; ++seg) {
+      ok = TQ_WARP_WAIT(bar.q_empty[seg & 1], ((seg >> 1) & 1) ^ 1);
+      if (!ok) break;
+      uint8_t* const dst = query_s + (seg & 1) * P::kQueryBytes + (lane >> 2) * (P::kQueryCols * 16) + (lane & 3) * 4;
+      const int rows = walk.s.n * a.group, first = walk.rt * RT;
+#pragma unroll 1
+      for (int r0 = 0; r0 < RT; r0 += 8) {
+        float v[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = first + r0 + i;
+          v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+          if (row >= rows) continue;
+          const long long at = row_vector(a, walk.s.row0, walk.kvh, row) * kDim + 4 * lane;
+          if (a.q_bf16) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + at));
+            v[i][0] = __uint_as_float(u.x << 16), v[i][1] = __uint_as_float(u.x & 0xffff0000u);
+            v[i][2] = __uint_as_float(u.y << 16), v[i][3] = __uint_as_float(u.y & 0xffff0000u);
+          } else {
+            const float4 u = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at));
+            v[i][0] = u.x, v[i][1] = u.y, v[i][2] = u.z, v[i][3] = u.w;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float most = fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
+          const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+          // 2^e <= most < 2^(e+1) goes to [64, 128); tiny queries stay tiny
+          const int e = max(-100, static_cast<int>(bits >> 23) - 127);
+          const float up = e > 126 ? __int_as_float(0x7fc00000) : fp8_power(6 - e);   // (infinite: the row is NaN)
+          float4 y = make_float4(v[i][0] * up, v[i][1] * up, v[i][2] * up, v[i][3] * up);
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const uint32_t w = fp8_four(y.x, y.y, y.z, y.w);
+            *reinterpret_cast<uint32_t*>(dst + (4 * (r0 + i) + p) * 16) = w;
+            const float2 lo = fp8_floats(w), hi = fp8_floats(w >> 16);
+            y = make_float4((y.x - lo.x) * 16.f, (y.y - lo.y) * 16.f, (y.z - hi.x) * 16.f, (y.w - hi.y) * 16.f);
+          }
+          if (lane == 0) {
+            const int row = first + r0 + i;
+            sh.factor[seg & 1][r0 + i] = row < rows ? a.scale * 1.4426950408889634f * fp8_power(e - 6) : 0.f;
+            sh.seen[seg & 1][r0 + i] = row < rows ? walk.s.ctx - walk.s.n + row / a.group + 1 : walk.s.ctx;
+          }
+        }
+      }
+      ptx::fence_async_shared();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bar.q_full[seg & 1]);
+      // to the end of the item or run
+      const long long left = min(static_cast<long long>(walk.tiles - walk.tile), walk.end - walk.pos) - 1;
+      if (walk.tile == 0 && left + 1 < walk.tiles) {
+        cut = CutItem{walk.s.row0, walk.kvh, walk.rt, min(RT, rows - first),
+                      static_cast<int>((walk.pos + walk.tiles - 1) / per)};
+      }
+      walk.pos += left;
+      walk.tile += static_cast<int>(left);
+      more = walk.next(a);
+    }
+    if (lane == 0) a.cuts[blockIdx.x] = cut;
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == P::kSoftWarps) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, P::kTmem);
+  }
+}
+
+// Joins the partial outputs of a row tile: sum_s 2^{m_s - M} o_s over
+// sum_s 2^{m_s - M} l_s.  Block (x, y) joins row y of the item that run x begins
+// and does not end; its warps take every fourth part, four coordinates a lane.
+constexpr int kJoinWarps = 4;
+__global__ void __launch_bounds__(32 * kJoinWarps) fp8_join_kernel(Fp8AttendArgs a, int rt_rows) {
+  __shared__ float4 acc_s[kJoinWarps][32];
+  __shared__ float sum_s[kJoinWarps], top_s[kJoinWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y, c0 = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const CutItem cut = a.cuts[c0];
+  if (row >= cut.rows) return;                    // (the whole CTA)
+  // (the run that holds key tile 0 wrote its second slot, the others their first)
+  auto part = [&](int s) { return a.part + (2ll * s + (s == c0 ? 1 : 0)) * part_floats(rt_rows); };
+  const int stats = rt_rows * kDim + 2 * row;
+  float top = -INFINITY;
+  for (int s = c0 + static_cast<int>(threadIdx.x); s <= cut.last; s += 32 * kJoinWarps) top = fmaxf(top, part(s)[stats]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) top_s[warp] = top;
+  __syncthreads();
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, top_s[w]);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll 4
+  for (int s = c0 + warp; s <= cut.last; s += kJoinWarps) {
+    const float* const p = part(s);
+    const float2 ml = *reinterpret_cast<const float2*>(p + stats);
+    const float4 o = reinterpret_cast<const float4*>(p + row * kDim)[lane];
+    if (ml.y == 0.f) continue;                    // (a part that saw nothing)
+    const float w = exp2_fast(ml.x - top);
+    acc.x = fmaf(w, o.x, acc.x), acc.y = fmaf(w, o.y, acc.y), acc.z = fmaf(w, o.z, acc.z), acc.w = fmaf(w, o.w, acc.w);
+    sum = fmaf(w, ml.y, sum);
+  }
+  acc_s[warp][lane] = acc;
+  if (lane == 0) sum_s[warp] = sum;
+  __syncthreads();
+  if (warp != 0) return;
+  for (int w = 1; w < kJoinWarps; ++w) {
+    const float4 o = acc_s[w][lane];
+    acc.x += o.x, acc.y += o.y, acc.z += o.z, acc.w += o.w;
+    sum += sum_s[w];
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / (kWeightScale * sum);
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  const long long vec = row_vector(a, cut.row0, cut.kvh, cut.i * rt_rows + row);
+  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + vec * kDim)[lane] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+constexpr size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Rows of a row tile: as many as the average sequence of the call has, 8 to 32.
+int tile_rows(int n_tokens, int batch, int group) {
+  const long long rows = (static_cast<long long>(n_tokens) + batch - 1) / batch * group;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
+
+template <int RT>
+cudaError_t attend(const Fp8AttendArgs& a, cudaStream_t stream) {
+  using P = Shape<RT>;
+  cudaError_t err = cudaFuncSetAttribute(fp8_attend_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  if (err != cudaSuccess) return err;
+  const int ctas = P::kCtas * a.num_sms;
+  fp8_attend_kernel<RT><<<ctas, P::kThreads, P::kSmem, stream>>>(a);
+  err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas, RT);
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fp8_join_kernel, a, RT);
 }
 
 }  // namespace
 
-size_t fp8_workspace_bytes(int, int, int, int, int, int) { return 256; }
+size_t fp8_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms) {
+  const int rt = tile_rows(n_tokens, batch, n_q / n_kv), ctas = num_sms * (rt == 32 ? 1 : 2);
+  return align256(ctas * sizeof(CutItem)) + align256(2ull * ctas * part_floats(rt) * sizeof(float));
+}
 
-cudaError_t launch_fp8_attention(const Fp8AttendArgs& a, void*, cudaStream_t stream) {
-  fp8_attend_kernel<<<dim3(a.c.n_tokens, a.n_q), 32, 0, stream>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_fp8_attention(const Fp8AttendArgs& args, void* workspace, cudaStream_t stream) {
+  Fp8AttendArgs a = args;
+  const int rt = tile_rows(a.c.n_tokens, a.c.batch, a.group), ctas = a.num_sms * (rt == 32 ? 1 : 2);
+  a.cuts = static_cast<CutItem*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(ctas * sizeof(CutItem)));
+  return rt == 8 ? attend<8>(a, stream) : rt == 16 ? attend<16>(a, stream) : attend<32>(a, stream);
 }
 
 }  // namespace tq

@@ -356,6 +356,9 @@ struct Fp8AttendArgs {
   void* out;                  // bf16 [n_tokens][n_q][128]
   int num_sms;
   int debug_withhold;
+  // workspace regions
+  float* part;                // partial outputs of the row tiles that runs cut
+  CutItem* cuts;              // [ctas]: what run c begins and does not end
 };
 size_t fp8_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms);
 cudaError_t launch_fp8_attention(const Fp8AttendArgs& args, void* workspace, cudaStream_t stream);

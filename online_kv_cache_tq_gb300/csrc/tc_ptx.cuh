@@ -289,6 +289,30 @@ __device__ __forceinline__ void mma_e4m3_tmem_a(uint32_t d_tmem, uint32_t a_tmem
       : "memory");
 }
 
+// Shared-memory matrix descriptor of a K-major operand without swizzle: core
+// matrices of 8 rows x 16 bytes (128 consecutive bytes each), `k_stride` bytes
+// from one to the next along K, `row_stride` along the rows (descriptor
+// version 1, swizzle mode 0).  A K step of 32 bytes is two core matrices.
+__device__ __forceinline__ uint64_t desc_k_plain(uint32_t saddr, uint32_t k_stride, uint32_t row_stride) {
+  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(k_stride >> 4) << 16;
+  d |= static_cast<uint64_t>(row_stride >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  return d;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T for e4m3 operands (K = 32 per instruction),
+// issued by one thread.
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Arrive once on `bar` when every tcgen05 operation this thread issued so far
 // has completed.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
