@@ -19,7 +19,7 @@ OBJ_DIR = os.path.join(LIB_DIR, "obj")
 LIB_PATH = os.path.join(LIB_DIR, "libtq.so")
 
 SOURCES = ["api.cu", "quantize_tc.cu", "vector_kernels.cu", "decode.cu", "decode_tc.cu", "decode_static.cu", "monitor.cu", "polar.cu",
-           "token_map.cu", "norm_rope.cu", "extend.cu", "extend_tc.cu", "extend_wide.cu", "fp8_cache.cu", "fp8_attention.cu",
+           "token_map.cu", "norm_rope.cu", "extend.cu", "extend_tc.cu", "extend_wide.cu", "fp8_cache.cu", "fp8_attention.cu", "fp8_wide.cu",
            "host_builder.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(ExtendArgs a)
       seq = make_int4(rows_ok ? s0 : 0, rows_ok ? s1 - s0 : 0, ctx_ok ? ctx : 0, 0);
       seq_s[tid] = make_int2(seq.y, seq.z);
     }
-    const bool eligible = a.tile_cap > 0 && static_cast<long long>(seq.y) * group >= kWideFrom;
+    const bool eligible = a.tile_cap > 0 && static_cast<long long>(seq.y) * group >= a.wide_from;
     __syncthreads();
     for (int k = warp; k < nb; k += threads / 32) {
       const int n = seq_s[k].x, ctx = seq_s[k].y;
@@ -186,10 +186,11 @@ struct Layout {
 };
 
 // The wide form's regions are there only if some sequence can have the rows
-// for it; then as many expanded tiles as that many sequences can need.
-Layout layout(int n_tokens, int batch, int group, int n_kv, int max_context, int num_sms) {
+// for it (`wide_from`); then as many expanded tiles as that many sequences can
+// need.  The narrow form's partials are there if its rows are not zero.
+Layout layout(int n_tokens, int batch, int group, int n_kv, int max_context, int num_sms, int wide_from, int narrow_rows) {
   Layout l;
-  const long long wide = static_cast<long long>(n_tokens) * group / kWideFrom;
+  const long long wide = static_cast<long long>(n_tokens) * group / wide_from;
   const long long sequences = wide < batch ? wide : batch;
   const long long context_tiles = max_context > kTile ? (static_cast<long long>(max_context) + kTile - 1) / kTile : 1;
   long long cap = context_tiles > kTileCap / n_kv ? (sequences > 0 ? kTileCap : 0) : sequences * context_tiles * n_kv;
@@ -202,7 +203,7 @@ Layout layout(int n_tokens, int batch, int group, int n_kv, int max_context, int
   l.seq = 3 * sums;
   l.cuts = l.seq + align256(static_cast<size_t>(batch) * sizeof(int4));
   l.part = l.cuts + align256(2 * static_cast<size_t>(num_sms) * sizeof(CutItem));
-  l.wide_part = l.part + align256(2 * static_cast<size_t>(num_sms) * part_floats(kNarrowRows) * sizeof(float));
+  l.wide_part = l.part + align256(2 * static_cast<size_t>(num_sms) * part_floats(narrow_rows) * sizeof(float));
   l.meta = l.wide_part +
            (cap > 0 ? align256(2 * static_cast<size_t>(num_sms) * part_floats(kWideRows) * sizeof(float)) : 0);
   l.tiles = l.meta + align256(static_cast<size_t>(cap) * sizeof(TileMeta));
@@ -210,17 +211,8 @@ Layout layout(int n_tokens, int batch, int group, int n_kv, int max_context, int
   return l;
 }
 
-}  // namespace
-
-size_t extend_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms) {
-  return layout(n_tokens, batch, n_q / n_kv, n_kv, max_context, num_sms).total;
-}
-
-cudaError_t launch_extend(const ExtendArgs& args, void* workspace, cudaStream_t stream) {
-  ExtendArgs a = args;
-  char* const ws = static_cast<char*>(workspace);
-  const int ctas = a.d.num_sms;
-  const Layout l = layout(a.n_tokens, a.d.batch, a.d.group, a.d.n_kv, a.d.max_context, ctas);
+// Workspace regions and row arithmetic, then the launch of the plan.
+cudaError_t launch_plan(ExtendArgs& a, const Layout& l, char* ws, int ctas, cudaStream_t stream) {
   a.narrow = ExtendForm{kNarrowRows, kNarrowCost, reinterpret_cast<long long*>(ws + l.first),
                         reinterpret_cast<float*>(ws + l.part), reinterpret_cast<CutItem*>(ws + l.cuts)};
   a.wide = ExtendForm{kWideRows, kWideCost, reinterpret_cast<long long*>(ws + l.wide_first),
@@ -235,11 +227,44 @@ cudaError_t launch_extend(const ExtendArgs& args, void* workspace, cudaStream_t 
   a.group_mul = static_cast<uint32_t>(((1ull << (31 + a.group_shift)) + a.d.group - 1) / a.d.group);
   const int plan_threads = a.d.batch >= kPlanThreads ? kPlanThreads : (a.d.batch + 255) / 256 * 256;
   extend_plan_kernel<<<1, plan_threads, 0, stream>>>(a);
-  cudaError_t err = cudaGetLastError();
-  if (err == cudaSuccess && a.tile_cap > 0) err = launch_extend_wide(a, ctas, stream);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t extend_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms) {
+  return layout(n_tokens, batch, n_q / n_kv, n_kv, max_context, num_sms, kWideFrom, kNarrowRows).total;
+}
+
+cudaError_t launch_extend(const ExtendArgs& args, void* workspace, cudaStream_t stream) {
+  ExtendArgs a = args;
+  const int ctas = a.d.num_sms;
+  a.wide_from = kWideFrom;
+  const Layout l = layout(a.n_tokens, a.d.batch, a.d.group, a.d.n_kv, a.d.max_context, ctas, kWideFrom, kNarrowRows);
+  cudaError_t err = launch_plan(a, l, static_cast<char*>(workspace), ctas, stream);
+  if (err == cudaSuccess && a.tile_cap > 0) err = launch_extend_expand(a, ctas, stream);
+  if (err == cudaSuccess && a.tile_cap > 0) err = launch_extend_wide(a, true, ctas, stream);
   if (err == cudaSuccess) err = launch_extend_narrow(a, ctas, stream);
   if (err != cudaSuccess || ctas < 2) return err;
   return launch_dependent(extend_join_kernel, dim3(ctas, kJoinSplit, a.tile_cap > 0 ? 2 : 1), 32 * kJoinWarps, 0, stream, a);
+}
+
+// The wide form for another cache: the plan and the join, without a narrow form.
+size_t extend_wide_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms, int wide_from) {
+  const Layout l = layout(n_tokens, batch, n_q / n_kv, n_kv, max_context, num_sms, wide_from, 0);
+  return l.tile_cap > 0 ? l.total : 0;
+}
+
+cudaError_t launch_extend_wide_plan(ExtendArgs& a, void* workspace, cudaStream_t stream) {
+  const int ctas = a.d.num_sms;
+  const Layout l = layout(a.n_tokens, a.d.batch, a.d.group, a.d.n_kv, a.d.max_context, ctas, a.wide_from, 0);
+  return launch_plan(a, l, static_cast<char*>(workspace), ctas, stream);
+}
+
+cudaError_t launch_extend_wide_join(const ExtendArgs& args, cudaStream_t stream) {
+  ExtendArgs a = args;
+  a.narrow = a.wide;                              // (the join of one form)
+  return launch_dependent(extend_join_kernel, dim3(a.d.num_sms, kJoinSplit, 1), 32 * kJoinWarps, 0, stream, a);
 }
 
 }  // namespace tq

@@ -280,6 +280,8 @@ struct WideBarriers {
   uint64_t rows[8];          // the two warps that share 32 rows
 };
 
+// TURN: values are in the rotated space, and an output is turned back by R^T.
+template <bool TURN>
 __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ WideBarriers bar;
@@ -490,17 +492,21 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
       ok = TQ_WARP_WAIT(bar.added[x], (jt - 1) & 1);
       if (!ok) break;
       ptx::tc_fence_after();
-      const float top = largest_output(o_addr, inv);
-      ok = swap(top, &other);
-      if (!ok) break;
-      const int eo = exponent_of(fmaxf(top, other));
-      output_operand(o_addr, lane_addr + kS + 128 * x + 32 * half, inv, exp2_int(-eo));
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(&bar.o_raw[x]);
-      ok = TQ_WARP_WAIT(bar.turned[x], seg & 1);
-      if (!ok) break;
-      ptx::tc_fence_after();
+      float factor_o = inv;                       // of what the output's columns hold
+      if constexpr (TURN) {
+        const float top = largest_output(o_addr, inv);
+        ok = swap(top, &other);
+        if (!ok) break;
+        const int eo = exponent_of(fmaxf(top, other));
+        output_operand(o_addr, lane_addr + kS + 128 * x + 32 * half, inv, exp2_int(-eo));
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&bar.o_raw[x]);
+        ok = TQ_WARP_WAIT(bar.turned[x], seg & 1);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        factor_o = exp2_int(eo);
+      }
       const bool whole = t0 == 0 && t1 == it.tiles;
       // a run's first item may have begun in the run before, its last may go on
       float* const part = a.wide.part + (2ll * blockIdx.x + (t0 == 0 ? 1 : 0)) * part_floats(kWideRows);
@@ -510,10 +516,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         part[kWideRows * kDim + 2 * part_row + 1] = sum;
       }
       if (!whole) {
-        store_partial(o_addr, exp2_int(eo), part + part_row * kDim + 64 * half, live);
+        store_partial(o_addr, factor_o, part + part_row * kDim + 64 * half, live);
       } else {
         // bf16 rows through the queries' place in shared memory, to leave in whole lines
-        output_rows(o_addr, exp2_int(eo), half_s + row * 128, row);
+        output_rows(o_addr, factor_o, half_s + row * 128, row);
         __syncwarp();
 #pragma unroll 2
         for (int k = 0; k < 8; ++k) {
@@ -585,22 +591,23 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
           }
         }
       }
-      // R^T out
-      ok = ok && TQ_WARP_WAIT(bar.k_full[kc & 1], (kc >> 1) & 1);
+      if constexpr (TURN) {                       // R^T out
+        ok = ok && TQ_WARP_WAIT(bar.k_full[kc & 1], (kc >> 1) & 1);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        ok = ok && TQ_WARP_WAIT(bar.o_raw[x], seg & 1);
-        if (!ok) break;
-        if (ptx::elect_one()) {
-          ptx::tc_fence_after();
-          product<8>(tmem + kO + 128 * x, tmem + kS + 128 * x, key_desc + (kc & 1) * (kImage / 16), kIdescF16, false);
-          ptx::mma_commit(&bar.turned[x]);
-          if (x == 1) ptx::mma_commit(&bar.k_empty[kc & 1]);
+        for (int x = 0; x < 2; ++x) {
+          ok = ok && TQ_WARP_WAIT(bar.o_raw[x], seg & 1);
+          if (!ok) break;
+          if (ptx::elect_one()) {
+            ptx::tc_fence_after();
+            product<8>(tmem + kO + 128 * x, tmem + kS + 128 * x, key_desc + (kc & 1) * (kImage / 16), kIdescF16, false);
+            ptx::mma_commit(&bar.turned[x]);
+            if (x == 1) ptx::mma_commit(&bar.k_empty[kc & 1]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        ++kc;
       }
       if (!ok) break;
-      ++kc;
       end_segment(a, a.wide, run, t1);
     }
     if (ptx::elect_one()) {
@@ -637,14 +644,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         if (t == t0) prefetch_queries(a, a.wide, run, t1, lane, 32);
       }
       if (!ok) break;
-      const int s = kc & 1;
-      ok = TQ_WARP_WAIT(bar.k_empty[s], ((kc >> 1) & 1) ^ 1);
-      if (!ok) break;
-      if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(&bar.k_full[s], kImage);
-        ptx::bulk_load(smem + kKey0 + s * kImage, a.images + 2 * (kImage / 16), kImage, &bar.k_full[s]);
+      if constexpr (TURN) {
+        const int s = kc & 1;
+        ok = TQ_WARP_WAIT(bar.k_empty[s], ((kc >> 1) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(&bar.k_full[s], kImage);
+          ptx::bulk_load(smem + kKey0 + s * kImage, a.images + 2 * (kImage / 16), kImage, &bar.k_full[s]);
+        }
+        ++kc;
       }
-      ++kc;
       end_segment(a, a.wide, run, t1);
     }
     if (*abort && lane == 0) {                    // copies in flight land before the CTA ends
@@ -688,14 +697,20 @@ cudaError_t expand(const ExtendArgs& a, int ctas, cudaStream_t stream) {
   }
 }
 
+template <bool TURN>
+cudaError_t wide(const ExtendArgs& a, int ctas, cudaStream_t stream) {
+  const cudaError_t err =
+      cudaFuncSetAttribute(extend_wide_kernel<TURN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem);
+  if (err != cudaSuccess) return err;
+  return launch_dependent(extend_wide_kernel<TURN>, dim3(ctas), kWideThreads, kWideSmem, stream, a);
+}
+
 }  // namespace
 
-cudaError_t launch_extend_wide(const ExtendArgs& a, int ctas, cudaStream_t stream) {
-  cudaError_t err = expand(a, ctas, stream);
-  if (err != cudaSuccess) return err;
-  err = cudaFuncSetAttribute(extend_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem);
-  if (err != cudaSuccess) return err;
-  return launch_dependent(extend_wide_kernel, dim3(ctas), kWideThreads, kWideSmem, stream, a);
+cudaError_t launch_extend_expand(const ExtendArgs& a, int ctas, cudaStream_t stream) { return expand(a, ctas, stream); }
+
+cudaError_t launch_extend_wide(const ExtendArgs& a, bool turn, int ctas, cudaStream_t stream) {
+  return turn ? wide<true>(a, ctas, stream) : wide<false>(a, ctas, stream);
 }
 
 }  // namespace tq

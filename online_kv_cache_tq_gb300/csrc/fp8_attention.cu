@@ -76,10 +76,19 @@ __device__ __forceinline__ int key_tiles(int ctx) { return max(1, (ctx + kTile -
 template <int RT>
 __device__ __forceinline__ Sequence load_sequence(const Fp8AttendArgs& a, int b) {
   const Fp8Cache& c = a.c;
+  Sequence s;
+  if (a.seq != nullptr) {                         // (checked by the plan; the wide form's have no work here)
+    const int4 q = a.seq[b];
+    s.row0 = q.x;
+    s.n = q.w >= 0 ? 0 : q.y;
+    s.ctx = q.z;
+    s.ok = true;
+    s.units = s.n == 0 ? 0 : static_cast<long long>(c.n_kv) * row_tiles(s.n * a.group, RT) * (kItemCost + key_tiles(s.ctx));
+    return s;
+  }
   const int s0 = c.query_start[b], s1 = c.query_start[b + 1], ctx = c.context_lens[b];
   const bool rows_ok = s0 >= 0 && s0 <= s1 && s1 <= c.n_tokens;
   const bool ctx_ok = ctx >= 0 && ctx <= a.max_context && ctx <= static_cast<long long>(c.max_blocks) * c.block_size;
-  Sequence s;
   s.row0 = rows_ok ? s0 : 0;
   s.n = rows_ok ? s1 - s0 : 0;
   s.ctx = ctx_ok ? ctx : 0;
@@ -272,6 +281,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* const abort = &sh.abort;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");        // (for the plan, where there is one)
   find_run<RT>(a, &sh.start, sh.warp_s);
   const long long total = sh.start.total, per = (total + gridDim.x - 1) / gridDim.x;
   Walk<RT> walk;
@@ -757,41 +767,99 @@ int tile_rows(int n_tokens, int batch, int group) {
   const long long rows = (static_cast<long long>(n_tokens) + batch - 1) / batch * group;
   return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
 }
+// Rows from which a sequence takes the wide form (extend_wide.cu over tiles
+// that fp8_wide.cu expands).
+constexpr int kWideFrom = 256;
 
-template <int RT>
-cudaError_t attend(const Fp8AttendArgs& a, cudaStream_t stream) {
-  using P = Shape<RT>;
-  cudaError_t err = cudaFuncSetAttribute(fp8_attend_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
-  if (err != cudaSuccess) return err;
-  const int ctas = P::kCtas * a.num_sms;
-  fp8_attend_kernel<RT><<<ctas, P::kThreads, P::kSmem, stream>>>(a);
-  err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
+template <typename Kernel, typename... Args>
+cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, RT);
-  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fp8_join_kernel, a, RT);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// `planned`: launches of the same call come before.
+template <int RT>
+cudaError_t attend(const Fp8AttendArgs& a, bool planned, cudaStream_t stream) {
+  using P = Shape<RT>;
+  cudaError_t err = cudaFuncSetAttribute(fp8_attend_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  if (err != cudaSuccess) return err;
+  const int ctas = P::kCtas * a.num_sms;
+  if (planned) {
+    err = launch_dependent(fp8_attend_kernel<RT>, dim3(ctas), P::kThreads, P::kSmem, stream, a);
+  } else {
+    fp8_attend_kernel<RT><<<ctas, P::kThreads, P::kSmem, stream>>>(a);
+    err = cudaGetLastError();
+  }
+  if (err != cudaSuccess) return err;
+  return launch_dependent(fp8_join_kernel, dim3(ctas, RT), 32 * kJoinWarps, 0, stream, a, RT);
+}
+
+struct Layout {
+  size_t part, wide, total;
+};
+Layout layout(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms) {
+  const int rt = tile_rows(n_tokens, batch, n_q / n_kv), ctas = num_sms * (rt == 32 ? 1 : 2);
+  Layout l;
+  l.part = align256(ctas * sizeof(CutItem));
+  l.wide = l.part + align256(2ull * ctas * part_floats(rt) * sizeof(float));
+  l.total = l.wide + extend_wide_workspace_bytes(n_tokens, batch, n_q, n_kv, max_context, num_sms, kWideFrom);
+  return l;
 }
 
 }  // namespace
 
 size_t fp8_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms) {
-  const int rt = tile_rows(n_tokens, batch, n_q / n_kv), ctas = num_sms * (rt == 32 ? 1 : 2);
-  return align256(ctas * sizeof(CutItem)) + align256(2ull * ctas * part_floats(rt) * sizeof(float));
+  return layout(n_tokens, batch, n_q, n_kv, max_context, num_sms).total;
 }
 
 cudaError_t launch_fp8_attention(const Fp8AttendArgs& args, void* workspace, cudaStream_t stream) {
   Fp8AttendArgs a = args;
-  const int rt = tile_rows(a.c.n_tokens, a.c.batch, a.group), ctas = a.num_sms * (rt == 32 ? 1 : 2);
-  a.cuts = static_cast<CutItem*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(ctas * sizeof(CutItem)));
-  return rt == 8 ? attend<8>(a, stream) : rt == 16 ? attend<16>(a, stream) : attend<32>(a, stream);
+  const Fp8Cache& c = a.c;
+  char* const ws = static_cast<char*>(workspace);
+  const Layout l = layout(c.n_tokens, c.batch, a.n_q, c.n_kv, a.max_context, a.num_sms);
+  a.cuts = reinterpret_cast<CutItem*>(ws);
+  a.part = reinterpret_cast<float*>(ws + l.part);
+  cudaError_t err = cudaSuccess;
+  if (l.total > l.wide) {
+    // some sequence may have the rows for the wide form: the plan says which
+    ExtendArgs e{};
+    e.d.q = a.q;
+    e.d.batch = c.batch;
+    e.d.n_q = a.n_q;
+    e.d.n_kv = c.n_kv;
+    e.d.group = a.group;
+    e.d.block_size = c.block_size;
+    e.d.max_blocks = c.max_blocks;
+    e.d.context_lens = c.context_lens;
+    e.d.max_context = a.max_context;
+    e.d.error = c.error;
+    e.d.num_sms = a.num_sms;
+    e.d.debug_withhold = a.debug_withhold;
+    e.n_tokens = c.n_tokens;
+    e.query_start = c.query_start;
+    e.out = a.out;
+    e.q_bf16 = a.q_bf16;
+    e.query_top = 15;                             // coordinates below 2^15 are fp16 numbers as they are
+    e.wide_from = kWideFrom;
+    err = launch_extend_wide_plan(e, ws + l.wide, stream);
+    if (err == cudaSuccess) err = launch_fp8_expand(c, e, a.scale, stream);
+    if (err == cudaSuccess) err = launch_extend_wide(e, false, a.num_sms, stream);
+    if (err == cudaSuccess) err = launch_extend_wide_join(e, stream);
+    if (err != cudaSuccess) return err;
+    a.seq = e.ws_seq;
+  }
+  const bool planned = a.seq != nullptr;
+  const int rt = tile_rows(c.n_tokens, c.batch, a.group);
+  return rt == 8 ? attend<8>(a, planned, stream) : rt == 16 ? attend<16>(a, planned, stream) : attend<32>(a, planned, stream);
 }
 
 }  // namespace tq

@@ -311,11 +311,19 @@ struct ExtendArgs {
   uint8_t* ws_tiles;          // [tile_cap][kTileImageBytes]
   TileMeta* ws_meta;          // [tile_cap]
   int tile_cap;               // 0: no sequence takes the wide form
+  int wide_from;              // rows from which a sequence may take it
 };
 size_t extend_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms);
 cudaError_t launch_extend(const ExtendArgs& args, void* workspace, cudaStream_t stream);
 cudaError_t launch_extend_narrow(const ExtendArgs& args, int ctas, cudaStream_t stream);   // (extend_tc.cu)
-cudaError_t launch_extend_wide(const ExtendArgs& args, int ctas, cudaStream_t stream);     // (extend_wide.cu)
+cudaError_t launch_extend_expand(const ExtendArgs& args, int ctas, cudaStream_t stream);   // (extend_wide.cu)
+// turn: the outputs are turned back by R^T (values in the rotated space).
+cudaError_t launch_extend_wide(const ExtendArgs& args, bool turn, int ctas, cudaStream_t stream);
+// The wide form over tiles that another cache's kernel expands: the plan (sets
+// the workspace regions of `args`) and the join around it (extend.cu).
+size_t extend_wide_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms, int wide_from);
+cudaError_t launch_extend_wide_plan(ExtendArgs& args, void* workspace, cudaStream_t stream);
+cudaError_t launch_extend_wide_join(const ExtendArgs& args, cudaStream_t stream);
 
 // The 8-bit cache (fp8_cache.cu, fp8_attention.cu): e4m3 codes with one power
 // of two as scale per (block, KV head) of keys and of values.  A block's codes
@@ -359,7 +367,9 @@ struct Fp8AttendArgs {
   // workspace regions
   float* part;                // partial outputs of the row tiles that runs cut
   CutItem* cuts;              // [ctas]: what run c begins and does not end
+  const int4* seq;            // the plan's sequences (ExtendArgs::ws_seq), where some take the wide form; or null
 };
+cudaError_t launch_fp8_expand(const Fp8Cache& cache, const ExtendArgs& args, float scale, cudaStream_t stream);   // (fp8_wide.cu)
 size_t fp8_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms);
 cudaError_t launch_fp8_attention(const Fp8AttendArgs& args, void* workspace, cudaStream_t stream);
 
