@@ -42,6 +42,7 @@ constexpr int kGroupBytes = 32 * kDim; // keys or values of 32 tokens: one copy
 constexpr int kRowsPerThread = 8;
 constexpr int kMetaRing = 16;          // more tiles than can be on their way
 constexpr int kItemCost = 2;
+constexpr float kNothing = -3e38f;     // a row's reference before it sees a token
 constexpr float kWeightScale = 256.f;  // weights are at most 1: times this in e4m3
 
 // RT rows a tile: 8 (two CTAs an SM), 16 (two), 32 (one).
@@ -97,41 +98,40 @@ __device__ __forceinline__ Sequence load_sequence(const Fp8AttendArgs& a, int b)
   return s;
 }
 
-// A walk over the key tiles of a run of units.
+// Where a run of units begins: a sequence and the unit in it.
+struct RunStart {
+  long long total, rem;
+  int b;
+  Sequence s;
+};
+
+// A walk over a run's items.
 template <int RT>
 struct Walk {
   int b, kvh, rt;        // sequence, KV head, row tile
-  int tile, tiles;       // key tile, and how many the item has
-  int tile0;             // the run's first one of the item
+  int tile, tiles;       // the run's first key tile of the item, and how many the item has
   Sequence s;
-  long long pos, end;    // unit of the tile, end of the run
+  long long pos, end;    // unit of that tile, end of the run
 
-  // At unit `rem` of sequence b; false when the run ends before a key tile.
-  __device__ __forceinline__ bool start(const Fp8AttendArgs& a, int seq, long long rem) {
-    b = seq;
-    s = load_sequence<RT>(a, b);
+  // At the run's first item; false when the run ends before a key tile.
+  __device__ __forceinline__ bool start(const Fp8AttendArgs& a, const RunStart& at) {
+    b = at.b;
+    s = at.s;
     tiles = key_tiles(s.ctx);
-    const long long item = rem / (kItemCost + tiles);
-    const int offset = static_cast<int>(rem - item * (kItemCost + tiles)), rts = row_tiles(s.n * a.group, RT);
+    const long long item = at.rem / (kItemCost + tiles);
+    const int offset = static_cast<int>(at.rem - item * (kItemCost + tiles)), rts = row_tiles(s.n * a.group, RT);
     kvh = static_cast<int>(item / rts);
     rt = static_cast<int>(item - static_cast<long long>(kvh) * rts);
-    tile = tile0 = max(0, offset - kItemCost);
+    tile = max(0, offset - kItemCost);
     pos += max(0, kItemCost - offset);
     return pos < end;
   }
-  // Whether the tile is the run's last one of the item.
-  __device__ __forceinline__ bool last_of_item() const { return tile + 1 == tiles || pos + 1 == end; }
-  // To the next tile; false at the run's end.
+  // The run's key tiles of the item.
+  __device__ __forceinline__ int span() const { return static_cast<int>(min(static_cast<long long>(tiles - tile), end - pos)); }
+  // To the next item; false at the run's end.
   __device__ __forceinline__ bool next(const Fp8AttendArgs& a) {
-    ++pos;
-    if (tile + 1 < tiles) {
-      ++tile;
-      return pos < end;
-    }
-    if (pos + kItemCost >= end) {
-      pos = end;
-      return false;
-    }
+    pos += (tiles - tile) + kItemCost;
+    if (pos >= end) return false;
     if (++rt >= row_tiles(s.n * a.group, RT)) {
       rt = 0;
       if (++kvh >= a.c.n_kv) {
@@ -142,18 +142,12 @@ struct Walk {
         tiles = key_tiles(s.ctx);
       }
     }
-    pos += kItemCost;
-    tile = tile0 = 0;
+    tile = 0;
     return true;
   }
 };
 
-struct RunStart {
-  long long total, rem;
-  int b;
-};
-
-// The run's first sequence and the unit in it, by the whole CTA.
+// The run's start, by the whole CTA.
 template <int RT>
 __device__ __forceinline__ void find_run(const Fp8AttendArgs& a, RunStart* out, long long* warp_s) {
   constexpr int kWarps = Shape<RT>::kThreads / 32;
@@ -176,7 +170,7 @@ __device__ __forceinline__ void find_run(const Fp8AttendArgs& a, RunStart* out, 
     if (lane == 31) warp_s[warp] = v;
     __syncthreads();
     long long before = 0, all = 0;
-#pragma unroll 1
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) before += warp_s[w];
       all += warp_s[w];
@@ -189,22 +183,24 @@ __device__ __forceinline__ void find_run(const Fp8AttendArgs& a, RunStart* out, 
   const long long upto = scan(mine, &total);
   const long long pos = blockIdx.x * ((total + gridDim.x - 1) / gridDim.x);
   if (tid == 0) out->total = total;
-  auto look = [&](int b, long long end, long long units) {
-    if (units > 0 && end - units <= pos && pos < end) {
+  auto look = [&](int b, long long end, const Sequence& seq) {
+    if (seq.units > 0 && end - seq.units <= pos && pos < end) {
       out->b = b;
-      out->rem = pos - (end - units);
+      out->rem = pos - (end - seq.units);
+      out->s = seq;
     }
   };
   if (batch <= static_cast<int>(blockDim.x)) {
-    look(tid, upto, mine);
+    look(tid, upto, s);
   } else {
     long long base = 0;
     for (int b0 = 0; b0 < batch; b0 += blockDim.x) {
       const int b = b0 + tid;
-      const long long units = b < batch ? load_sequence<RT>(a, b).units : 0;
+      Sequence one{};
+      if (b < batch) one = load_sequence<RT>(a, b);
       long long all;
-      const long long end = base + scan(units, &all);
-      look(b, end, units);
+      const long long end = base + scan(one.units, &all);
+      look(b, end, one);
       base += all;
     }
   }
@@ -216,12 +212,19 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Floats in the order of their values, as integers (a positive NaN above all).
-__device__ __forceinline__ int ordered(float x) {
-  const int i = __float_as_int(x);
-  return i ^ ((i >> 31) & 0x7fffffff);
+// The warp's largest (NaN does not count).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
 }
-__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+__device__ __forceinline__ void copy4_async(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+}
+// An arrival when the thread's copies so far have landed.
+__device__ __forceinline__ void arrive_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
+}
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -249,7 +252,7 @@ struct Shared {
   TileInfo info[kMetaRing];
   float factor[2][RT];           // scale log2(e) over the query's piece scale
   int seen[2][RT];               // positions a row sees
-  __align__(16) float top[2][Shape<RT>::kSplit][4][kRowsPerThread];   // (16-byte stores)
+  float4 top[2][Shape<RT>::kSplit][4][2];   // largest scores of a tile, by warp: eight rows
   float sum[2][Shape<RT>::kSoftWarps][kRowsPerThread];
   uint32_t poison[3][RT];        // rows that see a value that is NaN
   long long warp_s[Shape<RT>::kThreads / 32];
@@ -281,26 +284,19 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* const abort = &sh.abort;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");        // (for the plan, where there is one)
-  find_run<RT>(a, &sh.start, sh.warp_s);
-  const long long total = sh.start.total, per = (total + gridDim.x - 1) / gridDim.x;
-  Walk<RT> walk;
-  walk.pos = blockIdx.x * per;
-  walk.end = min(walk.pos + per, total);
-  bool more = walk.pos < walk.end && walk.start(a, sh.start.b, sh.start.rem);
-  if (!more) {                                    // (the whole CTA)
-    if (tid == 0) a.cuts[blockIdx.x] = CutItem{0, 0, 0, 0, 0};
-    return;
+  if (warp == P::kSoftWarps) {
+    ptx::tmem_alloc(&sh.tmem, P::kTmem);
+    ptx::tmem_relinquish();
   }
   if (tid == 0) {
     sh.abort = 0;
     for (int s = 0; s < P::kSlots; ++s) {
-      ptx::mbar_init(&bar.full[s], 1);
+      ptx::mbar_init(&bar.full[s], 5);            // the bytes, and four lanes
       ptx::mbar_init(&bar.empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(&bar.s_full[s], 1);
-      ptx::mbar_init(&bar.p_full[s], 32 * P::kSoftWarps);
+      ptx::mbar_init(&bar.p_full[s], P::kSoftWarps);
       ptx::mbar_init(&bar.o_full[s], 1);
       ptx::mbar_init(&bar.q_full[s], 1);
       ptx::mbar_init(&bar.q_empty[s], 1 + P::kSoftWarps);   // the scores' products, and who reads the factors
@@ -311,13 +307,15 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
     ptx::fence_mbar_init();
   }
   for (int i = tid; i < 3 * RT; i += P::kThreads) (&sh.poison[0][0])[i] = 0;
-  if (warp == P::kSoftWarps) {
-    ptx::tmem_alloc(&sh.tmem, P::kTmem);
-    ptx::tmem_relinquish();
-  }
   ptx::tc_fence_before();
-  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");        // (for the plan, where there is one)
+  find_run<RT>(a, &sh.start, sh.warp_s);
   ptx::tc_fence_after();
+  const long long total = sh.start.total, per = (total + gridDim.x - 1) / gridDim.x;
+  Walk<RT> walk;
+  walk.pos = blockIdx.x * per;
+  walk.end = min(walk.pos + per, total);
+  bool more = walk.pos < walk.end && walk.start(a, sh.start);
   const uint32_t tmem = sh.tmem;
   const uint32_t scores_t = tmem, outputs_t = tmem + 2 * P::kQueryCols;
   bool ok = true;
@@ -330,18 +328,37 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
     const uint32_t my_outputs = outputs_t + lanes + 3 * kRowsPerThread * split;
     uint8_t* const my_weights = weight_s + (token >> 4) * (P::kWeightCols * 16) + 3 * kRowsPerThread * split * 16 + (token & 15);
     int jt = 0;                                   // key tiles so far
-    for (int seg = 0; more; ++seg) {
+    int slot = 1, slot_phase = 0;                 // of the value tile
+    for (int seg = 0; more; ++seg, more = walk.next(a)) {
       const int n = walk.s.n, ctx = walk.s.ctx, row0 = walk.s.row0, kvh = walk.kvh, rt = walk.rt;
       const int first = rt * RT + split * kRowsPerThread;     // my first row of the sequence
+      const int tile0 = walk.tile, tiles = walk.tiles, reached = tile0 + walk.span();
+      if (first >= n * a.group) {
+        // no such rows: only keep in step
+        for (int t = tile0; ok && t < reached; ++t, ++jt) {
+          ok = TQ_WARP_WAIT(bar.s_full[jt & 1], (jt >> 1) & 1);
+          if (ok && lane == 0) ptx::mbar_arrive(&bar.p_full[jt & 1]);
+          slot += 2;
+          if (slot >= P::kSlots) slot -= P::kSlots, slot_phase ^= 1;
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          ptx::mbar_arrive(&bar.sums);
+          ptx::mbar_arrive(&bar.q_empty[seg & 1]);
+        }
+        ok = TQ_WARP_WAIT(bar.sums, seg & 1);
+        if (!ok) break;
+        continue;
+      }
       ok = TQ_WARP_WAIT(bar.q_full[seg & 1], (seg >> 1) & 1);
       if (!ok) break;
       const float* const factor = sh.factor[seg & 1] + split * kRowsPerThread;
       const int* const seen = sh.seen[seg & 1] + split * kRowsPerThread;
-      const int all_see = sh.seen[seg & 1][0];    // positions that every row sees
+      const int plain_tiles = sh.seen[seg & 1][0] / kTile;    // those before are seen by every row
       float acc[kRowsPerThread], sum[kRowsPerThread], ref[kRowsPerThread];
 #pragma unroll
-      for (int r = 0; r < kRowsPerThread; ++r) acc[r] = sum[r] = 0.f, ref[r] = -INFINITY;
-      auto add_output = [&](int j, const float (&keep)[kRowsPerThread]) {   // tile j's product, then times keep
+      for (int r = 0; r < kRowsPerThread; ++r) acc[r] = sum[r] = 0.f, ref[r] = kNothing;
+      auto add_output = [&](int j) {              // tile j's product
         if (!TQ_WARP_WAIT(bar.o_full[j & 1], (j >> 1) & 1)) return false;
         ptx::tc_fence_after();
         uint32_t d[3][8];
@@ -349,39 +366,32 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
         tmem_ld8(at, d[0]);
         tmem_ld8(at + 8, d[1]);
         tmem_ld8(at + 16, d[2]);
-        const bool there = sh.info[j & (kMetaRing - 1)].groups != 0;   // (else nothing was multiplied)
+        if (sh.info[j & (kMetaRing - 1)].groups == 0) return true;   // (nothing was multiplied)
 #pragma unroll
         for (int r = 0; r < kRowsPerThread; ++r) {
           const float d0 = __uint_as_float(d[(3 * r) >> 3][(3 * r) & 7]);
           const float d1 = __uint_as_float(d[(3 * r + 1) >> 3][(3 * r + 1) & 7]);
           const float d2 = __uint_as_float(d[(3 * r + 2) >> 3][(3 * r + 2) & 7]);
-          const float o = fmaf(fmaf(d2, 0.0625f, d1), 0.0625f, d0);
-          acc[r] = (there ? acc[r] + o : acc[r]) * keep[r];
+          acc[r] = fmaf(fmaf(d2, 0.0625f, d1), 0.0625f, acc[r] + d0);
         }
         return true;
       };
-      const int tile0 = walk.tile0, tiles = walk.tiles;
-      int reached = 0;                            // key tiles of the item that are done
-      bool last = false;
-      for (; !last; ++jt) {
-        const int t = walk.tile;
-        last = walk.last_of_item();
-        reached = t + 1;
+      for (int t = tile0; t < reached; ++t, ++jt) {
         ok = TQ_WARP_WAIT(bar.s_full[jt & 1], (jt >> 1) & 1);
         if (!ok) break;
         ptx::tc_fence_after();
         uint32_t s[32];
         ptx::tmem_ld32(my_scores + (jt & 1) * P::kQueryCols, s);
-        const int slot_turn = 2 * jt + 1, slot = slot_turn % P::kSlots;
-        ok = TQ_WARP_WAIT(bar.full[slot], (slot_turn / P::kSlots) & 1);
+        ok = TQ_WARP_WAIT(bar.full[slot], slot_phase);
         if (!ok) break;
         const TileInfo& info = sh.info[jt & (kMetaRing - 1)];
         const uint32_t groups = info.groups;
-        const float ks = info.k_scale[quarter], vs = info.v_scale[quarter];
-        const float up = static_cast<float>(fp8_exponent(vs)), down = fp8_power(-fp8_exponent(vs));
+        const float ks = info.k_scale[quarter];
+        const int e = fp8_exponent(info.v_scale[quarter]);
+        const float up = static_cast<float>(e), down = fp8_power(-e);
         const bool here = groups >> quarter & 1u;
         const int pos = t * kTile + token;
-        float x[kRowsPerThread];
+        float x[kRowsPerThread], top[kRowsPerThread];
 #pragma unroll
         for (int r = 0; r < kRowsPerThread; ++r) {
           const float d = fmaf(fmaf(fmaf(__uint_as_float(s[4 * r + 3]), 0.0625f, __uint_as_float(s[4 * r + 2])), 0.0625f,
@@ -389,33 +399,39 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
           // (with the value's scale: what the weight is of the block's codes)
           x[r] = fmaf(d * ks, factor[r], up);
         }
-        if (groups != 15u || (t + 1) * kTile > all_see) {
+        if (groups != 15u || t >= plain_tiles) {
 #pragma unroll
           for (int r = 0; r < kRowsPerThread; ++r) x[r] = here && pos < seen[r] ? x[r] : -INFINITY;
         }
         // the tile's largest, over the four warps
-        float keep[kRowsPerThread];
-        {
-          int top[kRowsPerThread];
 #pragma unroll
-          for (int r = 0; r < kRowsPerThread; ++r) top[r] = __reduce_max_sync(0xffffffffu, ordered(x[r]));
-          float(*const buf)[kRowsPerThread] = sh.top[jt & 1][split];
-          if (lane == 0) {
-            float4* const dst = reinterpret_cast<float4*>(buf[quarter]);
-            dst[0] = make_float4(unordered(top[0]), unordered(top[1]), unordered(top[2]), unordered(top[3]));
-            dst[1] = make_float4(unordered(top[4]), unordered(top[5]), unordered(top[6]), unordered(top[7]));
-            ptx::mbar_arrive(&bar.maxima[split]);
-          }
-          __syncwarp();
-          ok = TQ_WARP_WAIT(bar.maxima[split], jt & 1);
-          if (!ok) break;
+        for (int r = 0; r < kRowsPerThread; ++r) top[r] = warp_max(x[r]);
+        float4(*const buf)[2] = sh.top[jt & 1][split];
+        if (lane == 0) {
+          buf[quarter][0] = make_float4(top[0], top[1], top[2], top[3]);
+          buf[quarter][1] = make_float4(top[4], top[5], top[6], top[7]);
+          ptx::mbar_arrive(&bar.maxima[split]);
+        }
+        ok = TQ_WARP_WAIT(bar.maxima[split], jt & 1);
+        if (!ok) break;
+        bool raise = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 m0 = buf[0][h], m1 = buf[1][h], m2 = buf[2][h], m3 = buf[3][h];
+          top[4 * h] = fmaxf(fmaxf(m0.x, m1.x), fmaxf(m2.x, m3.x));
+          top[4 * h + 1] = fmaxf(fmaxf(m0.y, m1.y), fmaxf(m2.y, m3.y));
+          top[4 * h + 2] = fmaxf(fmaxf(m0.z, m1.z), fmaxf(m2.z, m3.z));
+          top[4 * h + 3] = fmaxf(fmaxf(m0.w, m1.w), fmaxf(m2.w, m3.w));
+        }
+#pragma unroll
+        for (int r = 0; r < kRowsPerThread; ++r) raise = raise || top[r] > ref[r];
+        float keep[kRowsPerThread];
+        if (raise) {                              // (the same for all four warps)
 #pragma unroll
           for (int r = 0; r < kRowsPerThread; ++r) {
-            int m = ordered(ref[r]);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) m = max(m, ordered(buf[w][r]));
-            const float to = unordered(m);
-            keep[r] = to == ref[r] ? 1.f : exp2_fast(ref[r] - to);
+            const float to = fmaxf(ref[r], top[r]);
+            keep[r] = exp2_fast(ref[r] - to);
+            sum[r] *= keep[r];
             ref[r] = to;
           }
         }
@@ -423,16 +439,14 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
         uint8_t* const dst = my_weights + (jt & 1) * P::kWeightBytes;
 #pragma unroll
         for (int r = 0; r < kRowsPerThread; r += 2) {
-          float2 w;
-          w.x = exp2_fast(x[r] - (ref[r] == -INFINITY ? 0.f : ref[r]));
-          w.y = exp2_fast(x[r + 1] - (ref[r + 1] == -INFINITY ? 0.f : ref[r + 1]));
-          sum[r] = fmaf(sum[r], keep[r], w.x * down);
-          sum[r + 1] = fmaf(sum[r + 1], keep[r + 1], w.y * down);
+          const float2 w = make_float2(exp2_fast(x[r] - ref[r]), exp2_fast(x[r + 1] - ref[r + 1]));
+          sum[r] = fmaf(w.x, down, sum[r]);
+          sum[r + 1] = fmaf(w.y, down, sum[r + 1]);
           float2 y = __fmul2_rn(w, make_float2(kWeightScale, kWeightScale));
 #pragma unroll
           for (int i = 0; i < 3; ++i) {
             const uint32_t p = fp8_pair(y.x, y.y);
-            dst[(3 * r + i) * 16] = static_cast<uint8_t>(p & 0xffu);
+            dst[(3 * r + i) * 16] = static_cast<uint8_t>(p);
             dst[(3 * r + 3 + i) * 16] = static_cast<uint8_t>(p >> 8);
             if (i < 2) y = __fmul2_rn(__ffma2_rn(fp8_floats(p), make_float2(-1.f, -1.f), y), make_float2(16.f, 16.f));
           }
@@ -452,17 +466,22 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
         }
         ptx::fence_async_shared();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(&bar.p_full[jt & 1]);
-        if (t > tile0) {
-          ok = add_output(jt - 1, keep);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bar.p_full[jt & 1]);
+        slot += 2;
+        if (slot >= P::kSlots) slot -= P::kSlots, slot_phase ^= 1;
+        if (t > tile0) {                          // the product before runs meanwhile
+          ok = add_output(jt - 1);
           if (!ok) break;
           ptx::tc_fence_before();
         }
-        more = walk.next(a);
+        if (raise) {
+#pragma unroll
+          for (int r = 0; r < kRowsPerThread; ++r) acc[r] *= keep[r];
+        }
       }
       if (!ok) break;
-      const float one[kRowsPerThread] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-      ok = add_output(jt - 1, one);
+      ok = add_output(jt - 1);
       if (!ok) break;
       ptx::tc_fence_before();
       // the rows' sums over the four warps
@@ -511,43 +530,45 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
     const uint64_t query_desc = ptx::desc_k_plain(ptx::smem_u32(query_s), P::kQueryCols * 16, 128);
     const uint64_t weight_desc = ptx::desc_k_plain(ptx::smem_u32(weight_s), P::kWeightCols * 16, 128);
     constexpr uint32_t kScores = ptx::idesc_e4m3_f32(kTile, P::kQueryCols), kOutput = ptx::idesc_e4m3_f32(kDim, P::kWeightCols);
-    int seg = 0;
-    auto scores = [&](int j) {                    // of tile j, at which the walk stands
-      const int turn = 2 * j, slot = turn % P::kSlots;
-      if (walk.tile == walk.tile0 && !TQ_WARP_WAIT(bar.q_full[seg & 1], (seg >> 1) & 1)) return false;
-      if (!TQ_WARP_WAIT(bar.full[slot], (turn / P::kSlots) & 1)) return false;
-      const bool last = walk.last_of_item();
+    int seg = 0, left = more ? walk.span() : 0;   // of the next scores: segment, its tiles to come
+    int k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0;
+    bool fresh = true;                            // the segment's first scores
+    auto scores = [&](int j) {
+      if (fresh && !TQ_WARP_WAIT(bar.q_full[seg & 1], (seg >> 1) & 1)) return false;
+      if (!TQ_WARP_WAIT(bar.full[k_slot], k_phase)) return false;
+      fresh = --left == 0;
       if (ptx::elect_one()) {
         ptx::tc_fence_after();
-        const uint64_t k = key_desc + slot * (kSlotBytes / 16), q = query_desc + (seg & 1) * (P::kQueryBytes / 16);
+        const uint64_t k = key_desc + k_slot * (kSlotBytes / 16), q = query_desc + (seg & 1) * (P::kQueryBytes / 16);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           ptx::mma_e4m3(scores_t + (j & 1) * P::kQueryCols, k + ks * 16, q + ks * 2 * P::kQueryCols, kScores, ks > 0);
         // (a test of the bounded waits: the first tile)
         if (!(a.debug_withhold && blockIdx.x == 0 && j == 0)) ptx::mma_commit(&bar.s_full[j & 1]);
-        ptx::mma_commit(&bar.empty[slot]);
-        if (last) ptx::mma_commit(&bar.q_empty[seg & 1]);
+        ptx::mma_commit(&bar.empty[k_slot]);
+        if (fresh) ptx::mma_commit(&bar.q_empty[seg & 1]);
       }
       __syncwarp();
-      if (last) ++seg;
+      k_slot += 2;
+      if (k_slot >= P::kSlots) k_slot -= P::kSlots, k_phase ^= 1;
+      if (fresh) {
+        ++seg;
+        more = walk.next(a);
+        if (more) left = walk.span();
+      }
       return true;
     };
-    ok = scores(0);
-    more = walk.next(a);
-    for (int j = 0; ok; ++j) {
-      const bool next = more;
-      if (next) {
-        ok = scores(j + 1);
-        if (!ok) break;
-        more = walk.next(a);
-      }
-      const int turn = 2 * j + 1, slot = turn % P::kSlots;
-      ok = TQ_WARP_WAIT(bar.full[slot], (turn / P::kSlots) & 1) && TQ_WARP_WAIT(bar.p_full[j & 1], (j >> 1) & 1);
+    ok = !more || scores(0);
+    bool work = left > 0 || seg > 0;              // (a run without work has no tile)
+    for (int j = 0; work && ok; ++j) {
+      work = more;
+      if (work) ok = scores(j + 1);
+      ok = ok && TQ_WARP_WAIT(bar.full[v_slot], v_phase) && TQ_WARP_WAIT(bar.p_full[j & 1], (j >> 1) & 1);
       if (!ok) break;
       const uint32_t groups = sh.info[j & (kMetaRing - 1)].groups;
       if (ptx::elect_one()) {
         ptx::tc_fence_after();
-        const uint64_t v = value_desc + slot * (kSlotBytes / 16), w = weight_desc + (j & 1) * (P::kWeightBytes / 16);
+        const uint64_t v = value_desc + v_slot * (kSlotBytes / 16), w = weight_desc + (j & 1) * (P::kWeightBytes / 16);
         bool added = false;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -557,10 +578,11 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
           added = true;
         }
         ptx::mma_commit(&bar.o_full[j & 1]);
-        ptx::mma_commit(&bar.empty[slot]);
+        ptx::mma_commit(&bar.empty[v_slot]);
       }
       __syncwarp();
-      if (!next) break;
+      v_slot += 2;
+      if (v_slot >= P::kSlots) v_slot -= P::kSlots, v_phase ^= 1;
     }
     if (ptx::elect_one()) {
       ptx::mma_commit(&bar.drain);                // nothing is in flight when the CTA ends
@@ -568,17 +590,16 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
     }
   } else if (warp == P::kSoftWarps + 1) {
     // ---------------- copies ----------------
-    // lane g < 4 has the tile's group g; block ids are read two tiles ahead and
-    // scales one, so that no tile waits for either
+    // lane g < 4 has the tile's group g; its block id is read a tile ahead
+    int slot = 0, phase = 1, issued = 0;
+    int t = more ? walk.tile : 0, reached = more ? t + walk.span() : 0;
     struct Group {
-      long long row;             // (block, KV head), -1: none
       int off, id, kvh;
-      float ks, vs;
       bool here;
     };
-    auto read_id = [&]() {       // of the tile at which the walk stands
-      Group g{-1, 0, -1, walk.kvh, 1.f, 1.f, false};
-      const int pos = walk.tile * kTile + 32 * lane;
+    auto read_id = [&]() {                        // of tile t of the walk's item
+      Group g{0, -1, walk.kvh, false};
+      const int pos = t * kTile + 32 * lane;
       if (lane < 4 && pos < walk.s.ctx) {
         const int col = pos / c.block_size;
         g.off = pos - col * c.block_size;
@@ -588,61 +609,60 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
       }
       return g;
     };
-    auto read_scales = [&](Group& g) {
-      if (!g.here) return;
-      if (g.id < 0 || g.id >= c.num_blocks) {
-        atomicCAS(c.error, 0, kErrBlock);
-        return;
-      }
-      g.row = static_cast<long long>(g.id) * c.n_kv + g.kvh;
-      g.ks = __ldg(c.k_scale + g.row);
-      g.vs = __ldg(c.v_scale + g.row);
-    };
-    int turn = 0;
-    auto copy = [&](const Group& g, const uint8_t* field, uint32_t bytes) {
-      const int slot = turn % P::kSlots;
-      if (!TQ_WARP_WAIT(bar.empty[slot], ((turn / P::kSlots) & 1) ^ 1)) return false;
+    auto fill = [&](const uint8_t* src, uint32_t bytes) {   // the next slot; false when its wait ran out
+      if (!TQ_WARP_WAIT(bar.empty[slot], phase)) return false;
       if (lane == 0) ptx::mbar_arrive_expect_tx(&bar.full[slot], bytes);
       __syncwarp();
-      if (g.row >= 0)
-        ptx::bulk_load(smem + slot * kSlotBytes + lane * kGroupBytes, field + (g.row * c.block_size + g.off) * kDim,
-                       kGroupBytes, &bar.full[slot]);
-      ++turn;
+      if (src != nullptr) ptx::bulk_load(smem + slot * kSlotBytes + lane * kGroupBytes, src, kGroupBytes, &bar.full[slot]);
       return true;
     };
-    Group now = read_id();
-    bool more1 = walk.next(a);
-    Group ahead = now;
-    if (more1) ahead = read_id();
-    read_scales(now);
-    for (int j = 0;; ++j) {
-      Group third = ahead;
-      bool more2 = false;
-      if (more1) {
-        read_scales(ahead);
-        more2 = walk.next(a);
-        if (more2) third = read_id();
+    auto step = [&]() {
+      ++issued;
+      if (++slot == P::kSlots) slot = 0, phase ^= 1;
+    };
+    Group now{};
+    if (more) now = read_id();
+    for (int j = 0; more; ++j) {
+      if (++t == reached) {
+        more = walk.next(a);
+        if (more) t = walk.tile, reached = t + walk.span();
       }
-      const uint32_t groups = __ballot_sync(0xffffffffu, now.row >= 0);
-      const uint32_t bytes = __popc(groups) * kGroupBytes;
-      TileInfo& info = sh.info[j & (kMetaRing - 1)];
+      Group ahead{};
+      if (more) ahead = read_id();
+      bool there = now.here;
+      if (there && (now.id < 0 || now.id >= c.num_blocks)) {
+        atomicCAS(c.error, 0, kErrBlock);
+        there = false;
+      }
+      const long long vec = static_cast<long long>(now.id) * c.n_kv + now.kvh;
+      const long long byte = (vec * c.block_size + now.off) * kDim;
+      const uint32_t groups = __ballot_sync(0xffffffffu, there), bytes = __popc(groups) * kGroupBytes;
       // (the tile sixteen before is done: its slots have been filled again since)
-      if (lane < 4) info.k_scale[lane] = now.ks, info.v_scale[lane] = now.vs;
+      TileInfo& info = sh.info[j & (kMetaRing - 1)];
+      ok = fill(there ? c.k + byte : nullptr, bytes);
+      if (!ok) break;
+      if (lane < 4) ptx::mbar_arrive(&bar.full[slot]);
+      step();
       if (lane == 0) info.groups = groups;
+      if (there) {
+        copy4_async(&info.k_scale[lane], c.k_scale + vec);
+        copy4_async(&info.v_scale[lane], c.v_scale + vec);
+      }
       __syncwarp();
-      ok = copy(now, c.k, bytes) && copy(now, c.v, bytes);
-      if (!ok || !more1) break;
+      ok = fill(there ? c.v + byte : nullptr, bytes);
+      if (!ok) break;
+      if (lane < 4) arrive_copies(&bar.full[slot]);
+      step();
       now = ahead;
-      ahead = third;
-      more1 = more2;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (*abort && lane == 0)                      // copies in flight land before the CTA ends
-      for (int t = max(0, turn - P::kSlots); t < turn; ++t) ptx::drain_bar(&bar.full[t % P::kSlots], (t / P::kSlots) & 1);
+      for (int i = max(0, issued - P::kSlots); i < issued; ++i) ptx::drain_bar(&bar.full[i % P::kSlots], (i / P::kSlots) & 1);
   } else {
     // ---------------- queries ----------------
     // one segment ahead of the others: e4m3 pieces of its rows, four coordinates a lane
     CutItem cut{0, 0, 0, 0, 0};
-    for (int seg = 0; more; ++seg) {
+    for (int seg = 0; more; ++seg, more = walk.next(a)) {
       ok = TQ_WARP_WAIT(bar.q_empty[seg & 1], ((seg >> 1) & 1) ^ 1);
       if (!ok) break;
       uint8_t* const dst = query_s + (seg & 1) * P::kQueryBytes + (lane >> 2) * (P::kQueryCols * 16) + (lane & 3) * 4;
@@ -690,15 +710,9 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
       ptx::fence_async_shared();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&bar.q_full[seg & 1]);
-      // to the end of the item or run
-      const long long left = min(static_cast<long long>(walk.tiles - walk.tile), walk.end - walk.pos) - 1;
-      if (walk.tile == 0 && left + 1 < walk.tiles) {
+      if (walk.tile == 0 && walk.span() < walk.tiles)
         cut = CutItem{walk.s.row0, walk.kvh, walk.rt, min(RT, rows - first),
                       static_cast<int>((walk.pos + walk.tiles - 1) / per)};
-      }
-      walk.pos += left;
-      walk.tile += static_cast<int>(left);
-      more = walk.next(a);
     }
     if (lane == 0) a.cuts[blockIdx.x] = cut;
   }
@@ -712,46 +726,50 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
 }
 
 // Joins the partial outputs of a row tile: sum_s 2^{m_s - M} o_s over
-// sum_s 2^{m_s - M} l_s.  Block (x, y) joins row y of the item that run x begins
-// and does not end; its warps take every fourth part, four coordinates a lane.
-constexpr int kJoinWarps = 4;
-__global__ void __launch_bounds__(32 * kJoinWarps) fp8_join_kernel(Fp8AttendArgs a, int rt_rows) {
-  __shared__ float4 acc_s[kJoinWarps][32];
-  __shared__ float sum_s[kJoinWarps], top_s[kJoinWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y, c0 = blockIdx.x;
+// sum_s 2^{m_s - M} l_s.  Block (x, y) joins kJoinRows rows of the item that
+// run x begins and does not end; four warps a row take every fourth part, four
+// coordinates a lane.
+constexpr int kJoinWarps = 4, kJoinRows = 4;
+__global__ void __launch_bounds__(32 * kJoinWarps * kJoinRows) fp8_join_kernel(Fp8AttendArgs a, int rt_rows) {
+  __shared__ float4 acc_s[kJoinRows][kJoinWarps][32];
+  __shared__ float sum_s[kJoinRows][kJoinWarps], top_s[kJoinRows][kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % kJoinWarps, mine = (threadIdx.x >> 5) / kJoinWarps;
+  const int row = blockIdx.y * kJoinRows + mine, c0 = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const CutItem cut = a.cuts[c0];
-  if (row >= cut.rows) return;                    // (the whole CTA)
+  if (static_cast<int>(blockIdx.y) * kJoinRows >= cut.rows) return;      // (the whole CTA)
+  const bool live = row < cut.rows;
   // (the run that holds key tile 0 wrote its second slot, the others their first)
   auto part = [&](int s) { return a.part + (2ll * s + (s == c0 ? 1 : 0)) * part_floats(rt_rows); };
   const int stats = rt_rows * kDim + 2 * row;
   float top = -INFINITY;
-  for (int s = c0 + static_cast<int>(threadIdx.x); s <= cut.last; s += 32 * kJoinWarps) top = fmaxf(top, part(s)[stats]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) top_s[warp] = top;
+  if (live)
+    for (int s = c0 + 32 * warp + lane; s <= cut.last; s += 32 * kJoinWarps) top = fmaxf(top, part(s)[stats]);
+  top = warp_max(top);
+  if (lane == 0) top_s[mine][warp] = top;
   __syncthreads();
-  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, top_s[w]);
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, top_s[mine][w]);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-#pragma unroll 4
-  for (int s = c0 + warp; s <= cut.last; s += kJoinWarps) {
-    const float* const p = part(s);
-    const float2 ml = *reinterpret_cast<const float2*>(p + stats);
-    const float4 o = reinterpret_cast<const float4*>(p + row * kDim)[lane];
-    if (ml.y == 0.f) continue;                    // (a part that saw nothing)
-    const float w = exp2_fast(ml.x - top);
-    acc.x = fmaf(w, o.x, acc.x), acc.y = fmaf(w, o.y, acc.y), acc.z = fmaf(w, o.z, acc.z), acc.w = fmaf(w, o.w, acc.w);
-    sum = fmaf(w, ml.y, sum);
+  if (live) {
+#pragma unroll 8
+    for (int s = c0 + warp; s <= cut.last; s += kJoinWarps) {
+      const float* const p = part(s);
+      const float2 ml = *reinterpret_cast<const float2*>(p + stats);
+      const float4 o = reinterpret_cast<const float4*>(p + row * kDim)[lane];
+      const float w = ml.y == 0.f ? 0.f : exp2_fast(ml.x - top);   // (0: a part that saw nothing)
+      acc.x = fmaf(w, o.x, acc.x), acc.y = fmaf(w, o.y, acc.y), acc.z = fmaf(w, o.z, acc.z), acc.w = fmaf(w, o.w, acc.w);
+      sum = fmaf(w, ml.y, sum);
+    }
   }
-  acc_s[warp][lane] = acc;
-  if (lane == 0) sum_s[warp] = sum;
+  acc_s[mine][warp][lane] = acc;
+  if (lane == 0) sum_s[mine][warp] = sum;
   __syncthreads();
-  if (warp != 0) return;
+  if (warp != 0 || !live) return;
   for (int w = 1; w < kJoinWarps; ++w) {
-    const float4 o = acc_s[w][lane];
+    const float4 o = acc_s[mine][w][lane];
     acc.x += o.x, acc.y += o.y, acc.z += o.z, acc.w += o.w;
-    sum += sum_s[w];
+    sum += sum_s[mine][w];
   }
   const float inv = sum == 0.f ? 0.f : 1.f / (kWeightScale * sum);
   const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
@@ -800,7 +818,7 @@ cudaError_t attend(const Fp8AttendArgs& a, bool planned, cudaStream_t stream) {
     err = cudaGetLastError();
   }
   if (err != cudaSuccess) return err;
-  return launch_dependent(fp8_join_kernel, dim3(ctas, RT), 32 * kJoinWarps, 0, stream, a, RT);
+  return launch_dependent(fp8_join_kernel, dim3(ctas, RT / kJoinRows), 32 * kJoinWarps * kJoinRows, 0, stream, a, RT);
 }
 
 struct Layout {
