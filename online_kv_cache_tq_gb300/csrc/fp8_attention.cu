@@ -212,6 +212,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ void mbar_arrive_many(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(ptx::smem_u32(bar)), "r"(count) : "memory");
+}
 // The warp's largest (NaN does not count).
 __device__ __forceinline__ float warp_max(float x) {
   float y;
@@ -270,6 +273,60 @@ __device__ __forceinline__ long long row_vector(const Fp8AttendArgs& a, int row0
   return (static_cast<long long>(row0) + tok) * a.n_q + kvh * a.group + r - tok * a.group;
 }
 
+// Rows r0, r0 + step, .. (N of them) of the walk's item as operand rows of the
+// score product, by a warp: four coordinates a lane, as e4m3 pieces of the
+// query times a power of two.
+template <int N, int RT>
+__device__ __forceinline__ void prepare_rows(const Fp8AttendArgs& a, const Walk<RT>& walk, int r0, int step, uint8_t* operand,
+                                             float* factor, int* seen) {
+  const int lane = threadIdx.x & 31, rows = walk.s.n * a.group, first = walk.rt * RT;
+  uint8_t* const dst = operand + (lane >> 2) * (Shape<RT>::kQueryCols * 16) + (lane & 3) * 4;
+  float v[N][4];
+  int token[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int row = first + r0 + i * step;
+    v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+    token[i] = row / a.group;
+    if (row < rows) {
+      const long long vec = (static_cast<long long>(walk.s.row0) + token[i]) * a.n_q + walk.kvh * a.group + row - token[i] * a.group;
+      const long long at = vec * kDim + 4 * lane;
+      if (a.q_bf16) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + at));
+        v[i][0] = __uint_as_float(u.x << 16), v[i][1] = __uint_as_float(u.x & 0xffff0000u);
+        v[i][2] = __uint_as_float(u.y << 16), v[i][3] = __uint_as_float(u.y & 0xffff0000u);
+      } else {
+        const float4 u = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at));
+        v[i][0] = u.x, v[i][1] = u.y, v[i][2] = u.z, v[i][3] = u.w;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int r = r0 + i * step;
+    const float most = fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+    // 2^e <= most < 2^(e+1) goes to [64, 128); tiny queries stay tiny
+    const int e = max(-100, static_cast<int>(bits >> 23) - 127);
+    const float up = e > 126 ? __int_as_float(0x7fc00000) : fp8_power(6 - e);   // (infinite: the row is NaN)
+    float4 y = make_float4(v[i][0] * up, v[i][1] * up, v[i][2] * up, v[i][3] * up);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const uint32_t w = fp8_four(y.x, y.y, y.z, y.w);
+      *reinterpret_cast<uint32_t*>(dst + (4 * r + p) * 16) = w;
+      const float2 lo = fp8_floats(w), hi = fp8_floats(w >> 16);
+      y = make_float4((y.x - lo.x) * 16.f, (y.y - lo.y) * 16.f, (y.z - hi.x) * 16.f, (y.w - hi.y) * 16.f);
+    }
+    if (lane == 0) {
+      const bool live = first + r < rows;
+      factor[r] = live ? a.scale * 1.4426950408889634f * fp8_power(e - 6) : 0.f;
+      seen[r] = live ? walk.s.ctx - walk.s.n + token[i] + 1 : walk.s.ctx;
+    }
+  }
+  ptx::fence_async_shared();
+  __syncwarp();
+}
+
 template <int RT>
 __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_attend_kernel(Fp8AttendArgs a) {
   using P = Shape<RT>;
@@ -298,7 +355,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
       ptx::mbar_init(&bar.s_full[s], 1);
       ptx::mbar_init(&bar.p_full[s], P::kSoftWarps);
       ptx::mbar_init(&bar.o_full[s], 1);
-      ptx::mbar_init(&bar.q_full[s], 1);
+      ptx::mbar_init(&bar.q_full[s], P::kSoftWarps);
       ptx::mbar_init(&bar.q_empty[s], 1 + P::kSoftWarps);   // the scores' products, and who reads the factors
     }
     for (int s = 0; s < P::kSplit; ++s) ptx::mbar_init(&bar.maxima[s], 4);
@@ -327,6 +384,10 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
     const uint32_t my_scores = scores_t + lanes + 4 * kRowsPerThread * split;
     const uint32_t my_outputs = outputs_t + lanes + 3 * kRowsPerThread * split;
     uint8_t* const my_weights = weight_s + (token >> 4) * (P::kWeightCols * 16) + 3 * kRowsPerThread * split * 16 + (token & 15);
+    if (more) {                                   // the first queries, which everything waits for
+      prepare_rows<RT / P::kSoftWarps, RT>(a, walk, warp, P::kSoftWarps, query_s, sh.factor[0], sh.seen[0]);
+      if (lane == 0) ptx::mbar_arrive(&bar.q_full[0]);
+    }
     int jt = 0;                                   // key tiles so far
     int slot = 1, slot_phase = 0;                 // of the value tile
     for (int seg = 0; more; ++seg, more = walk.next(a)) {
@@ -660,56 +721,18 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
       for (int i = max(0, issued - P::kSlots); i < issued; ++i) ptx::drain_bar(&bar.full[i % P::kSlots], (i / P::kSlots) & 1);
   } else {
     // ---------------- queries ----------------
-    // one segment ahead of the others: e4m3 pieces of its rows, four coordinates a lane
+    // one segment ahead of the others
     CutItem cut{0, 0, 0, 0, 0};
     for (int seg = 0; more; ++seg, more = walk.next(a)) {
       ok = TQ_WARP_WAIT(bar.q_empty[seg & 1], ((seg >> 1) & 1) ^ 1);
       if (!ok) break;
-      uint8_t* const dst = query_s + (seg & 1) * P::kQueryBytes + (lane >> 2) * (P::kQueryCols * 16) + (lane & 3) * 4;
       const int rows = walk.s.n * a.group, first = walk.rt * RT;
+      if (seg > 0) {                              // (the softmax warps prepare the run's first)
 #pragma unroll 1
-      for (int r0 = 0; r0 < RT; r0 += 8) {
-        float v[8][4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = first + r0 + i;
-          v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
-          if (row >= rows) continue;
-          const long long at = row_vector(a, walk.s.row0, walk.kvh, row) * kDim + 4 * lane;
-          if (a.q_bf16) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + at));
-            v[i][0] = __uint_as_float(u.x << 16), v[i][1] = __uint_as_float(u.x & 0xffff0000u);
-            v[i][2] = __uint_as_float(u.y << 16), v[i][3] = __uint_as_float(u.y & 0xffff0000u);
-          } else {
-            const float4 u = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at));
-            v[i][0] = u.x, v[i][1] = u.y, v[i][2] = u.z, v[i][3] = u.w;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float most = fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
-          const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
-          // 2^e <= most < 2^(e+1) goes to [64, 128); tiny queries stay tiny
-          const int e = max(-100, static_cast<int>(bits >> 23) - 127);
-          const float up = e > 126 ? __int_as_float(0x7fc00000) : fp8_power(6 - e);   // (infinite: the row is NaN)
-          float4 y = make_float4(v[i][0] * up, v[i][1] * up, v[i][2] * up, v[i][3] * up);
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const uint32_t w = fp8_four(y.x, y.y, y.z, y.w);
-            *reinterpret_cast<uint32_t*>(dst + (4 * (r0 + i) + p) * 16) = w;
-            const float2 lo = fp8_floats(w), hi = fp8_floats(w >> 16);
-            y = make_float4((y.x - lo.x) * 16.f, (y.y - lo.y) * 16.f, (y.z - hi.x) * 16.f, (y.w - hi.y) * 16.f);
-          }
-          if (lane == 0) {
-            const int row = first + r0 + i;
-            sh.factor[seg & 1][r0 + i] = row < rows ? a.scale * 1.4426950408889634f * fp8_power(e - 6) : 0.f;
-            sh.seen[seg & 1][r0 + i] = row < rows ? walk.s.ctx - walk.s.n + row / a.group + 1 : walk.s.ctx;
-          }
-        }
+        for (int r0 = 0; r0 < RT; r0 += 4)
+          prepare_rows<4, RT>(a, walk, r0, 1, query_s + (seg & 1) * P::kQueryBytes, sh.factor[seg & 1], sh.seen[seg & 1]);
+        if (lane == 0) mbar_arrive_many(&bar.q_full[seg & 1], P::kSoftWarps);
       }
-      ptx::fence_async_shared();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&bar.q_full[seg & 1]);
       if (walk.tile == 0 && walk.span() < walk.tiles)
         cut = CutItem{walk.s.row0, walk.kvh, walk.rt, min(RT, rows - first),
                       static_cast<int>((walk.pos + walk.tiles - 1) / per)};
@@ -729,8 +752,8 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
 // sum_s 2^{m_s - M} l_s.  Block (x, y) joins kJoinRows rows of the item that
 // run x begins and does not end; four warps a row take every fourth part, four
 // coordinates a lane.
-constexpr int kJoinWarps = 4, kJoinRows = 4;
-__global__ void __launch_bounds__(32 * kJoinWarps * kJoinRows) fp8_join_kernel(Fp8AttendArgs a, int rt_rows) {
+constexpr int kJoinWarps = 4, kJoinRows = 1;
+__global__ void __launch_bounds__(32 * kJoinWarps * kJoinRows, 8) fp8_join_kernel(Fp8AttendArgs a, int rt_rows) {
   __shared__ float4 acc_s[kJoinRows][kJoinWarps][32];
   __shared__ float sum_s[kJoinRows][kJoinWarps], top_s[kJoinRows][kJoinWarps];
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % kJoinWarps, mine = (threadIdx.x >> 5) / kJoinWarps;
@@ -742,34 +765,51 @@ __global__ void __launch_bounds__(32 * kJoinWarps * kJoinRows) fp8_join_kernel(F
   // (the run that holds key tile 0 wrote its second slot, the others their first)
   auto part = [&](int s) { return a.part + (2ll * s + (s == c0 ? 1 : 0)) * part_floats(rt_rows); };
   const int stats = rt_rows * kDim + 2 * row;
-  float top = -INFINITY;
-  if (live)
-    for (int s = c0 + 32 * warp + lane; s <= cut.last; s += 32 * kJoinWarps) top = fmaxf(top, part(s)[stats]);
-  top = warp_max(top);
-  if (lane == 0) top_s[mine][warp] = top;
-  __syncthreads();
-  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, top_s[mine][w]);
+  // one pass: eight parts' reads at once, the reference raised as they come
+  float top = kNothing, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-  if (live) {
-#pragma unroll 8
-    for (int s = c0 + warp; s <= cut.last; s += kJoinWarps) {
-      const float* const p = part(s);
-      const float2 ml = *reinterpret_cast<const float2*>(p + stats);
-      const float4 o = reinterpret_cast<const float4*>(p + row * kDim)[lane];
-      const float w = ml.y == 0.f ? 0.f : exp2_fast(ml.x - top);   // (0: a part that saw nothing)
-      acc.x = fmaf(w, o.x, acc.x), acc.y = fmaf(w, o.y, acc.y), acc.z = fmaf(w, o.z, acc.z), acc.w = fmaf(w, o.w, acc.w);
-      sum = fmaf(w, ml.y, sum);
+  for (int s0 = c0 + warp; live && s0 <= cut.last; s0 += 8 * kJoinWarps) {
+    float2 ml[8];
+    float4 o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int s = s0 + k * kJoinWarps;
+      ml[k] = make_float2(kNothing, 0.f);
+      o[k] = acc;
+      if (s <= cut.last) {
+        ml[k] = *reinterpret_cast<const float2*>(part(s) + stats);
+        o[k] = reinterpret_cast<const float4*>(part(s) + row * kDim)[lane];
+      }
+    }
+    float to = top;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) to = fmaxf(to, ml[k].x);
+    const float keep = exp2_fast(top - to);
+    acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep, sum *= keep;
+    top = to;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (ml[k].y == 0.f) continue;               // (a part that saw nothing)
+      const float w = exp2_fast(ml[k].x - top);
+      acc.x = fmaf(w, o[k].x, acc.x), acc.y = fmaf(w, o[k].y, acc.y), acc.z = fmaf(w, o[k].z, acc.z);
+      acc.w = fmaf(w, o[k].w, acc.w);
+      sum = fmaf(w, ml[k].y, sum);
     }
   }
   acc_s[mine][warp][lane] = acc;
-  if (lane == 0) sum_s[mine][warp] = sum;
+  if (lane == 0) sum_s[mine][warp] = sum, top_s[mine][warp] = top;
   __syncthreads();
   if (warp != 0 || !live) return;
-  for (int w = 1; w < kJoinWarps; ++w) {
+  float to = top;
+  for (int w = 1; w < kJoinWarps; ++w) to = fmaxf(to, top_s[mine][w]);
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
     const float4 o = acc_s[mine][w][lane];
-    acc.x += o.x, acc.y += o.y, acc.z += o.z, acc.w += o.w;
-    sum += sum_s[mine][w];
+    const float f = exp2_fast(top_s[mine][w] - to);
+    acc.x = fmaf(f, o.x, acc.x), acc.y = fmaf(f, o.y, acc.y), acc.z = fmaf(f, o.z, acc.z), acc.w = fmaf(f, o.w, acc.w);
+    sum = fmaf(f, sum_s[mine][w], sum);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / (kWeightScale * sum);
   const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
