@@ -105,7 +105,9 @@ struct RunStart {
   Sequence s;
 };
 
-// A walk over a run's items.
+// A walk over a run's items: a sequence's row tiles, and in each its KV heads,
+// so that the row tiles that read the same keys are worked on by different CTAs
+// at about the same time and find them in L2.
 template <int RT>
 struct Walk {
   int b, kvh, rt;        // sequence, KV head, row tile
@@ -119,9 +121,9 @@ struct Walk {
     s = at.s;
     tiles = key_tiles(s.ctx);
     const long long item = at.rem / (kItemCost + tiles);
-    const int offset = static_cast<int>(at.rem - item * (kItemCost + tiles)), rts = row_tiles(s.n * a.group, RT);
-    kvh = static_cast<int>(item / rts);
-    rt = static_cast<int>(item - static_cast<long long>(kvh) * rts);
+    const int offset = static_cast<int>(at.rem - item * (kItemCost + tiles));
+    rt = static_cast<int>(item / a.c.n_kv);
+    kvh = static_cast<int>(item - static_cast<long long>(rt) * a.c.n_kv);
     tile = max(0, offset - kItemCost);
     pos += max(0, kItemCost - offset);
     return pos < end;
@@ -132,10 +134,10 @@ struct Walk {
   __device__ __forceinline__ bool next(const Fp8AttendArgs& a) {
     pos += (tiles - tile) + kItemCost;
     if (pos >= end) return false;
-    if (++rt >= row_tiles(s.n * a.group, RT)) {
-      rt = 0;
-      if (++kvh >= a.c.n_kv) {
-        kvh = 0;
+    if (++kvh >= a.c.n_kv) {
+      kvh = 0;
+      if (++rt >= row_tiles(s.n * a.group, RT)) {
+        rt = 0;
         do {
           s = load_sequence<RT>(a, ++b);          // (units are left, so there is one with work)
         } while (s.units == 0);
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
       prepare_rows<RT / P::kSoftWarps, RT>(a, walk, warp, P::kSoftWarps, query_s, sh.factor[0], sh.seen[0]);
       if (lane == 0) ptx::mbar_arrive(&bar.q_full[0]);
     }
-    int jt = 0;                                   // key tiles so far
+    int jt = 0, met = 0;                          // key tiles so far, and those that this split's warps met over
     int slot = 1, slot_phase = 0;                 // of the value tile
     for (int seg = 0; more; ++seg, more = walk.next(a)) {
       const int n = walk.s.n, ctx = walk.s.ctx, row0 = walk.s.row0, kvh = walk.kvh, rt = walk.rt;
@@ -467,14 +469,15 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
         // the tile's largest, over the four warps
 #pragma unroll
         for (int r = 0; r < kRowsPerThread; ++r) top[r] = warp_max(x[r]);
-        float4(*const buf)[2] = sh.top[jt & 1][split];
+        float4(*const buf)[2] = sh.top[met & 1][split];
         if (lane == 0) {
           buf[quarter][0] = make_float4(top[0], top[1], top[2], top[3]);
           buf[quarter][1] = make_float4(top[4], top[5], top[6], top[7]);
           ptx::mbar_arrive(&bar.maxima[split]);
         }
-        ok = TQ_WARP_WAIT(bar.maxima[split], jt & 1);
+        ok = TQ_WARP_WAIT(bar.maxima[split], met & 1);
         if (!ok) break;
+        ++met;
         bool raise = false;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

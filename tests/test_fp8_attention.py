@@ -153,6 +153,19 @@ def test_groups_and_ragged_batches(group, n_kv):
     c.check()
 
 
+@pytest.mark.parametrize("group,bs", [(8, 64), (16, 32), (4, 96)])
+@pytest.mark.parametrize("seed", range(3))
+def test_many_short_sequences_of_changing_row_counts(group, bs, seed):
+    # a CTA works on several sequences, one after another, with fewer and more rows and key tiles than the one before
+    rng = np.random.default_rng(seed)
+    batch = 260
+    new = [int(n) for n in rng.choice([0, 1, 1, 2, 3, 4, 6, 9], batch)]
+    ctx = [n + int(c) for n, c in zip(new, rng.integers(0, 500, batch))]
+    c = Case(new, ctx, n_kv=2, group=group, bs=bs, seed=seed)
+    c.run()
+    c.check()
+
+
 @pytest.mark.parametrize("new,ctx", [([1], [20000]), ([2, 5, 1], [9000, 30, 12345]), ([4], [4]), ([33], [5000])])
 def test_few_tokens_on_long_contexts(new, ctx):
     c = Case(new, ctx, n_kv=1, group=8, seed=1)
