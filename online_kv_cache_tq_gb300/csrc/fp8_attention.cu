@@ -55,10 +55,13 @@ struct Shape {
   static constexpr int kSlots = RT == 32 ? 10 : 5;          // ring of key and value tiles in turn
   static constexpr int kQueryCols = 4 * RT;
   static constexpr int kWeightCols = (3 * RT + 15) / 16 * 16;
-  static constexpr int kQueryBytes = kQueryCols * kDim, kWeightBytes = kWeightCols * kTile;
+  // (64 bytes more than the rows between sixteen tokens and the next, so that a
+  // warp's byte stores to both meet different banks)
+  static constexpr int kWeightStride = kWeightCols * 16 + 64;
+  static constexpr int kQueryBytes = kQueryCols * kDim, kWeightBytes = kWeightStride * kTile / 16;
   static constexpr int kTmem = RT == 8 ? 128 : RT == 16 ? 256 : 512;
   static constexpr int kSmem = kSlots * kSlotBytes + 2 * kQueryBytes + 2 * kWeightBytes + 128;   // (128: alignment)
-  static_assert(2 * kQueryCols + 2 * kWeightCols <= kTmem, "two buffers of scores and of outputs");
+  static_assert(2 * kQueryCols + kWeightCols <= kTmem, "two buffers of scores, one of outputs");
 };
 
 struct TileInfo {
@@ -231,13 +234,18 @@ __device__ __forceinline__ void arrive_copies(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr)
-               : "memory");
+__device__ __forceinline__ void tmem_ld24(uint32_t taddr, uint32_t (&r)[24]) {
+#pragma unroll
+  for (int i = 0; i < 24; i += 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]),
+                   "=r"(r[i + 7])
+                 : "r"(taddr + i)
+                 : "memory");
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23])
                :
                : "memory");
 }
@@ -255,7 +263,7 @@ template <int RT>
 struct Shared {
   Barriers<RT> bar;
   TileInfo info[kMetaRing];
-  float factor[2][RT];           // scale log2(e) over the query's piece scale
+  __align__(16) float factor[2][RT];           // scale log2(e) over the query's piece scale
   int seen[2][RT];               // positions a row sees
   float4 top[2][Shape<RT>::kSplit][4][2];   // largest scores of a tile, by warp: eight rows
   float sum[2][Shape<RT>::kSoftWarps][kRowsPerThread];
@@ -334,7 +342,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
   using P = Shape<RT>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared<RT> sh;
-  static_assert(offsetof(Shared<RT>, top) % 16 == 0 && alignof(Shared<RT>) >= 16, "16-byte stores");
+  static_assert(offsetof(Shared<RT>, top) % 16 == 0 && offsetof(Shared<RT>, factor) % 16 == 0 && alignof(Shared<RT>) >= 16, "16-byte stores");
   uint8_t* const smem = smem_raw + ((128u - (ptx::smem_u32(smem_raw) & 127u)) & 127u);
   uint8_t* const query_s = smem + P::kSlots * kSlotBytes;
   uint8_t* const weight_s = query_s + 2 * P::kQueryBytes;
@@ -385,7 +393,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t my_scores = scores_t + lanes + 4 * kRowsPerThread * split;
     const uint32_t my_outputs = outputs_t + lanes + 3 * kRowsPerThread * split;
-    uint8_t* const my_weights = weight_s + (token >> 4) * (P::kWeightCols * 16) + 3 * kRowsPerThread * split * 16 + (token & 15);
+    uint8_t* const my_weights = weight_s + (token >> 4) * P::kWeightStride + 3 * kRowsPerThread * split * 16 + (token & 15);
     if (more) {                                   // the first queries, which everything waits for
       prepare_rows<RT / P::kSoftWarps, RT>(a, walk, warp, P::kSoftWarps, query_s, sh.factor[0], sh.seen[0]);
       if (lane == 0) ptx::mbar_arrive(&bar.q_full[0]);
@@ -415,7 +423,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
       }
       ok = TQ_WARP_WAIT(bar.q_full[seg & 1], (seg >> 1) & 1);
       if (!ok) break;
-      const float* const factor = sh.factor[seg & 1] + split * kRowsPerThread;
+      const float4* const factor4 = reinterpret_cast<const float4*>(sh.factor[seg & 1] + split * kRowsPerThread);
       const int* const seen = sh.seen[seg & 1] + split * kRowsPerThread;
       const int plain_tiles = sh.seen[seg & 1][0] / kTile;    // those before are seen by every row
       float acc[kRowsPerThread], sum[kRowsPerThread], ref[kRowsPerThread];
@@ -424,17 +432,13 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
       auto add_output = [&](int j) {              // tile j's product
         if (!TQ_WARP_WAIT(bar.o_full[j & 1], (j >> 1) & 1)) return false;
         ptx::tc_fence_after();
-        uint32_t d[3][8];
-        const uint32_t at = my_outputs + (j & 1) * P::kWeightCols;
-        tmem_ld8(at, d[0]);
-        tmem_ld8(at + 8, d[1]);
-        tmem_ld8(at + 16, d[2]);
+        uint32_t d[24];
+        tmem_ld24(my_outputs, d);
+        ptx::tc_fence_before();
         if (sh.info[j & (kMetaRing - 1)].groups == 0) return true;   // (nothing was multiplied)
 #pragma unroll
         for (int r = 0; r < kRowsPerThread; ++r) {
-          const float d0 = __uint_as_float(d[(3 * r) >> 3][(3 * r) & 7]);
-          const float d1 = __uint_as_float(d[(3 * r + 1) >> 3][(3 * r + 1) & 7]);
-          const float d2 = __uint_as_float(d[(3 * r + 2) >> 3][(3 * r + 2) & 7]);
+          const float d0 = __uint_as_float(d[3 * r]), d1 = __uint_as_float(d[3 * r + 1]), d2 = __uint_as_float(d[3 * r + 2]);
           acc[r] = fmaf(fmaf(d2, 0.0625f, d1), 0.0625f, acc[r] + d0);
         }
         return true;
@@ -455,6 +459,8 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
         const bool here = groups >> quarter & 1u;
         const int pos = t * kTile + token;
         float x[kRowsPerThread], top[kRowsPerThread];
+        const float4 f0 = factor4[0], f1 = factor4[1];
+        const float factor[kRowsPerThread] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
         for (int r = 0; r < kRowsPerThread; ++r) {
           const float d = fmaf(fmaf(fmaf(__uint_as_float(s[4 * r + 3]), 0.0625f, __uint_as_float(s[4 * r + 2])), 0.0625f,
@@ -475,6 +481,10 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
           buf[quarter][1] = make_float4(top[4], top[5], top[6], top[7]);
           ptx::mbar_arrive(&bar.maxima[split]);
         }
+        if (t > tile0) {                          // the tile before, while the warps meet
+          ok = add_output(jt - 1);
+          if (!ok) break;
+        }
         ok = TQ_WARP_WAIT(bar.maxima[split], met & 1);
         if (!ok) break;
         ++met;
@@ -489,13 +499,12 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
         }
 #pragma unroll
         for (int r = 0; r < kRowsPerThread; ++r) raise = raise || top[r] > ref[r];
-        float keep[kRowsPerThread];
         if (raise) {                              // (the same for all four warps)
 #pragma unroll
           for (int r = 0; r < kRowsPerThread; ++r) {
-            const float to = fmaxf(ref[r], top[r]);
-            keep[r] = exp2_fast(ref[r] - to);
-            sum[r] *= keep[r];
+            const float to = fmaxf(ref[r], top[r]), keep = exp2_fast(ref[r] - to);
+            sum[r] *= keep;
+            acc[r] *= keep;
             ref[r] = to;
           }
         }
@@ -534,20 +543,10 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
         if (lane == 0) ptx::mbar_arrive(&bar.p_full[jt & 1]);
         slot += 2;
         if (slot >= P::kSlots) slot -= P::kSlots, slot_phase ^= 1;
-        if (t > tile0) {                          // the product before runs meanwhile
-          ok = add_output(jt - 1);
-          if (!ok) break;
-          ptx::tc_fence_before();
-        }
-        if (raise) {
-#pragma unroll
-          for (int r = 0; r < kRowsPerThread; ++r) acc[r] *= keep[r];
-        }
       }
       if (!ok) break;
       ok = add_output(jt - 1);
       if (!ok) break;
-      ptx::tc_fence_before();
       // the rows' sums over the four warps
 #pragma unroll
       for (int r = 0; r < kRowsPerThread; ++r) {
@@ -592,7 +591,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
     const uint32_t ring = ptx::smem_u32(smem);
     const uint64_t key_desc = ptx::desc_k_plain(ring, 128, 1024), value_desc = ptx::desc_k_plain(ring, 2048, 128);
     const uint64_t query_desc = ptx::desc_k_plain(ptx::smem_u32(query_s), P::kQueryCols * 16, 128);
-    const uint64_t weight_desc = ptx::desc_k_plain(ptx::smem_u32(weight_s), P::kWeightCols * 16, 128);
+    const uint64_t weight_desc = ptx::desc_k_plain(ptx::smem_u32(weight_s), P::kWeightStride, 128);
     constexpr uint32_t kScores = ptx::idesc_e4m3_f32(kTile, P::kQueryCols), kOutput = ptx::idesc_e4m3_f32(kDim, P::kWeightCols);
     int seg = 0, left = more ? walk.span() : 0;   // of the next scores: segment, its tiles to come
     int k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0;
@@ -637,7 +636,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           if (!(groups >> g & 1u)) continue;
-          ptx::mma_e4m3(outputs_t + (j & 1) * P::kWeightCols, v + g * (kGroupBytes / 16), w + g * 2 * P::kWeightCols,
+          ptx::mma_e4m3(outputs_t, v + g * (kGroupBytes / 16), w + g * 2 * (P::kWeightStride / 16),
                         kOutput, added);
           added = true;
         }
