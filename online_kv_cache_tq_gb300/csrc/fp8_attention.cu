@@ -42,24 +42,24 @@ constexpr int kGroupBytes = 32 * kDim; // keys or values of 32 tokens: one copy
 constexpr int kRowsPerThread = 8;
 constexpr int kMetaRing = 16;          // more tiles than can be on their way
 constexpr int kItemCost = 2;
+constexpr int kCtasPerSm = 2;
 constexpr float kNothing = -3e38f;     // a row's reference before it sees a token
 constexpr float kWeightScale = 256.f;  // weights are at most 1: times this in e4m3
 
-// RT rows a tile: 8 (two CTAs an SM), 16 (two), 32 (one).
+// RT rows a tile, 8 or 16; two CTAs an SM.
 template <int RT>
 struct Shape {
   static constexpr int kSplit = RT / kRowsPerThread;        // threads per token
   static constexpr int kSoftWarps = 4 * kSplit;
   static constexpr int kThreads = 32 * (kSoftWarps + 3);
-  static constexpr int kCtas = RT == 32 ? 1 : 2;            // per SM
-  static constexpr int kSlots = RT == 32 ? 10 : 5;          // ring of key and value tiles in turn
+  static constexpr int kSlots = 5;                          // ring of key and value tiles in turn
   static constexpr int kQueryCols = 4 * RT;
   static constexpr int kWeightCols = (3 * RT + 15) / 16 * 16;
   // (64 bytes more than the rows between sixteen tokens and the next, so that a
   // warp's byte stores to both meet different banks)
   static constexpr int kWeightStride = kWeightCols * 16 + 64;
   static constexpr int kQueryBytes = kQueryCols * kDim, kWeightBytes = kWeightStride * kTile / 16;
-  static constexpr int kTmem = RT == 8 ? 128 : RT == 16 ? 256 : 512;
+  static constexpr int kTmem = RT == 8 ? 128 : 256;
   static constexpr int kSmem = kSlots * kSlotBytes + 2 * kQueryBytes + 2 * kWeightBytes + 128;   // (128: alignment)
   static_assert(2 * kQueryCols + kWeightCols <= kTmem, "two buffers of scores, one of outputs");
 };
@@ -217,6 +217,20 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Two halves as e4m3 codes, and back; a byte to shared memory.
+__device__ __forceinline__ uint16_t fp8_pair_of_halves(__half2 h) {
+  uint16_t p;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(p) : "r"(*reinterpret_cast<const uint32_t*>(&h)));
+  return p;
+}
+__device__ __forceinline__ __half2 halves_of_fp8_pair(uint16_t p) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(p));
+  return *reinterpret_cast<const __half2*>(&h);
+}
+__device__ __forceinline__ void store_byte(uint32_t saddr, uint16_t b) {
+  asm volatile("st.shared.b8 [%0], %1;" ::"r"(saddr), "h"(b) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_many(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(ptx::smem_u32(bar)), "r"(count) : "memory");
 }
@@ -338,7 +352,7 @@ __device__ __forceinline__ void prepare_rows(const Fp8AttendArgs& a, const Walk<
 }
 
 template <int RT>
-__global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_attend_kernel(Fp8AttendArgs a) {
+__global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_kernel(Fp8AttendArgs a) {
   using P = Shape<RT>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared<RT> sh;
@@ -393,7 +407,9 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t my_scores = scores_t + lanes + 4 * kRowsPerThread * split;
     const uint32_t my_outputs = outputs_t + lanes + 3 * kRowsPerThread * split;
-    uint8_t* const my_weights = weight_s + (token >> 4) * P::kWeightStride + 3 * kRowsPerThread * split * 16 + (token & 15);
+    const uint32_t my_weights =
+        ptx::smem_u32(weight_s) + (token >> 4) * P::kWeightStride + 3 * kRowsPerThread * split * 16 + (token & 15);
+    const __half2 weight_scale = __float2half2_rn(kWeightScale), sixteen = __float2half2_rn(16.f);
     if (more) {                                   // the first queries, which everything waits for
       prepare_rows<RT / P::kSoftWarps, RT>(a, walk, warp, P::kSoftWarps, query_s, sh.factor[0], sh.seen[0]);
       if (lane == 0) ptx::mbar_arrive(&bar.q_full[0]);
@@ -509,19 +525,20 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kCtas) fp8_att
           }
         }
         // weights: at most 1, of the block's codes
-        uint8_t* const dst = my_weights + (jt & 1) * P::kWeightBytes;
+        const uint32_t dst = my_weights + (jt & 1) * P::kWeightBytes;
 #pragma unroll
         for (int r = 0; r < kRowsPerThread; r += 2) {
-          const float2 w = make_float2(exp2_fast(x[r] - ref[r]), exp2_fast(x[r + 1] - ref[r + 1]));
-          sum[r] = fmaf(w.x, down, sum[r]);
-          sum[r + 1] = fmaf(w.y, down, sum[r + 1]);
-          float2 y = __fmul2_rn(w, make_float2(kWeightScale, kWeightScale));
+          const float w0 = exp2_fast(x[r] - ref[r]), w1 = exp2_fast(x[r + 1] - ref[r + 1]);
+          sum[r] = fmaf(w0, down, sum[r]);
+          sum[r + 1] = fmaf(w1, down, sum[r + 1]);
+          // (fp16 holds 2^-12 of a weight too, and what pieces leave of it exactly)
+          __half2 y = __hmul2(__floats2half2_rn(w0, w1), weight_scale);
 #pragma unroll
           for (int i = 0; i < 3; ++i) {
-            const uint32_t p = fp8_pair(y.x, y.y);
-            dst[(3 * r + i) * 16] = static_cast<uint8_t>(p);
-            dst[(3 * r + 3 + i) * 16] = static_cast<uint8_t>(p >> 8);
-            if (i < 2) y = __fmul2_rn(__ffma2_rn(fp8_floats(p), make_float2(-1.f, -1.f), y), make_float2(16.f, 16.f));
+            const uint16_t p = fp8_pair_of_halves(y);
+            store_byte(dst + (3 * r + i) * 16, p);
+            store_byte(dst + (3 * r + 3 + i) * 16, static_cast<uint16_t>(p >> 8));
+            if (i < 2) y = __hmul2(__hsub2(y, halves_of_fp8_pair(p)), sixteen);
           }
         }
         if (split == 0 && here) {
@@ -822,14 +839,28 @@ __global__ void __launch_bounds__(32 * kJoinWarps * kJoinRows, 8) fp8_join_kerne
 
 constexpr size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Rows of a row tile: as many as the average sequence of the call has, 8 to 32.
+// Rows of a row tile: 16 where the average sequence of the call has more than
+// eight.  (16 sequences on 8192 tokens, 64/8 heads, 8 rows each: 52 us with
+// eight a tile, 58 with 16; 16 rows: 91 and 66; 32 rows: 165 and 112, and 109
+// with tiles of 32 rows and one CTA an SM, which take 78 us for 8 rows.)
 int tile_rows(int n_tokens, int batch, int group) {
-  const long long rows = (static_cast<long long>(n_tokens) + batch - 1) / batch * group;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  return (static_cast<long long>(n_tokens) + batch - 1) / batch * group <= 8 ? 8 : 16;
 }
+
 // Rows from which a sequence takes the wide form (extend_wide.cu over tiles
-// that fp8_wide.cu expands).
-constexpr int kWideFrom = 256;
+// that fp8_wide.cu expands).  (Wide | few, us: 16 sequences on 8192 tokens, 64/8
+// heads, 64 rows 381 | 206, 128 rows 385 | 387, 256 rows 396 | 800; one on 32000,
+// 128 rows 130 | 100; 8 on 2000, 32/8 heads, 128 rows 82 | 78.)
+constexpr int kWideFrom = 144;
+// Whether a call has the wide form's launches: only if one sequence can have
+// the rows (all tokens beyond one for each of the others), and if it then would
+// lose more without them than the 12 us that they take: products of tokens,
+// query heads and context, of which this form does 0.4 million in a microsecond.
+constexpr long long kWideWork = 1 << 22;
+bool wide_possible(int n_tokens, int batch, int n_q, int n_kv, int max_context) {
+  const long long most = static_cast<long long>(n_tokens) - batch + 1;
+  return most * (n_q / n_kv) >= kWideFrom && most * n_q >= kWideWork / (max_context > 0 ? max_context : 1);
+}
 
 template <typename Kernel, typename... Args>
 cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
@@ -852,7 +883,7 @@ cudaError_t attend(const Fp8AttendArgs& a, bool planned, cudaStream_t stream) {
   using P = Shape<RT>;
   cudaError_t err = cudaFuncSetAttribute(fp8_attend_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (err != cudaSuccess) return err;
-  const int ctas = P::kCtas * a.num_sms;
+  const int ctas = kCtasPerSm * a.num_sms;
   if (planned) {
     err = launch_dependent(fp8_attend_kernel<RT>, dim3(ctas), P::kThreads, P::kSmem, stream, a);
   } else {
@@ -867,11 +898,13 @@ struct Layout {
   size_t part, wide, total;
 };
 Layout layout(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms) {
-  const int rt = tile_rows(n_tokens, batch, n_q / n_kv), ctas = num_sms * (rt == 32 ? 1 : 2);
+  const int rt = tile_rows(n_tokens, batch, n_q / n_kv), ctas = num_sms * kCtasPerSm;
   Layout l;
   l.part = align256(ctas * sizeof(CutItem));
   l.wide = l.part + align256(2ull * ctas * part_floats(rt) * sizeof(float));
-  l.total = l.wide + extend_wide_workspace_bytes(n_tokens, batch, n_q, n_kv, max_context, num_sms, kWideFrom);
+  l.total = l.wide;
+  if (wide_possible(n_tokens, batch, n_q, n_kv, max_context))
+    l.total += extend_wide_workspace_bytes(n_tokens, batch, n_q, n_kv, max_context, num_sms, kWideFrom);
   return l;
 }
 
@@ -918,8 +951,7 @@ cudaError_t launch_fp8_attention(const Fp8AttendArgs& args, void* workspace, cud
     a.seq = e.ws_seq;
   }
   const bool planned = a.seq != nullptr;
-  const int rt = tile_rows(c.n_tokens, c.batch, a.group);
-  return rt == 8 ? attend<8>(a, planned, stream) : rt == 16 ? attend<16>(a, planned, stream) : attend<32>(a, planned, stream);
+  return tile_rows(c.n_tokens, c.batch, a.group) == 8 ? attend<8>(a, planned, stream) : attend<16>(a, planned, stream);
 }
 
 }  // namespace tq
