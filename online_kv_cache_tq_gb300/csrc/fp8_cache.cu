@@ -9,25 +9,23 @@
 // loses nothing but codes that leave e4m3's normal range.
 //
 // Read.  x = code 2^e, exact in either type.
+#include <algorithm>
+
 #include "fp8_common.cuh"
+#include "tc_ptx.cuh"
 
 namespace tq {
 namespace {
 
 constexpr int kShortRun = 8;      // tokens that one warp appends alone
+constexpr int kReadCtas = 32 * 152;
 
 template <bool BF16>
 struct Eight {                    // eight neighbouring coordinates of a row as they lie in memory
   uint4 w[BF16 ? 1 : 2];
-  __device__ __forceinline__ void load(const void* rows, long long at) {
-    const uint4* const p = BF16 ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(rows) + at)
-                                : reinterpret_cast<const uint4*>(static_cast<const float*>(rows) + at);
-    w[0] = __ldg(p);
-    if constexpr (!BF16) w[1] = __ldg(p + 1);
-  }
-  __device__ __forceinline__ void clear() {
-    w[0] = make_uint4(0, 0, 0, 0);
-    if constexpr (!BF16) w[1] = w[0];
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    w[0] = *reinterpret_cast<const uint4*>(p);
+    if constexpr (!BF16) w[1] = *reinterpret_cast<const uint4*>(p + 16);
   }
   __device__ __forceinline__ void floats(float (&v)[8]) const {
     if constexpr (BF16) {
@@ -127,7 +125,7 @@ __device__ __forceinline__ void append_short(const Fp8Run& r, const void* rows, 
   for (int i = 0; i < kShortRun; ++i) {
     if (i >= r.len) break;
     const bool nan = __any_sync(0xffffffffu, x[i][0] != x[i][0] || x[i][1] != x[i][1] || x[i][2] != x[i][2] || x[i][3] != x[i][3]);
-    const uint32_t w = nan ? kFp8NaN4 : fp8_four(x[i][0] * down, x[i][1] * down, x[i][2] * down, x[i][3] * down);
+    const uint32_t w = nan ? kFp8NaN4 : fp8_four_scaled(x[i][0], x[i][1], x[i][2], x[i][3], down);
     const int token = r.off + i;
     if (!values) {
       *reinterpret_cast<uint32_t*>(block + key_byte(token, 4 * lane)) = w;
@@ -138,141 +136,294 @@ __device__ __forceinline__ void append_short(const Fp8Run& r, const void* rows, 
   }
 }
 
-// A longer run, by the CTA: WARPS groups of sixteen tokens at a time.  A thread
-// has eight coordinates of four tokens twice.  Keys: tokens 4 i + (lane & 3) of
-// the warp's sixteen, coordinates 16 (lane / 4) and the eight behind them, so
-// that a row is read and a core matrix written in whole lines.  Values: tokens
-// 4 (lane & 3) + i, coordinates 8 (lane / 4) and those 64 on; four lanes
-// exchange their words to have sixteen tokens of a coordinate each.
-template <bool BF16, int WARPS>
-__device__ __forceinline__ void append_long(const Fp8Run& r, const void* rows, long long stride, int head,
-                                            uint8_t* block, float* scale, bool values, float* amax_s) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane & 3, piece = lane >> 2;
-  const float old = r.off > 0 ? *scale : 0.f;
-  const int first = r.off & ~15, end = r.off + r.len, step = 16 * WARPS;
-  Eight<BF16> x[8];
-  auto token_of = [&](int base, int i) { return base + 16 * warp + (values ? 4 * quad + i : 4 * i + quad); };
-  auto load = [&](int base) {
+// ---- longer runs ---------------------------------------------------------------
+//
+// A CTA takes 64 tokens of a (run, tensor, KV head) at a time: their rows come
+// into shared memory by asynchronous copies, a stage ahead of the work on them.  Runs of
+// one stage are searched for their largest magnitude and converted where they
+// lie; longer ones (blocks of more than 64 tokens) come twice.
+constexpr int kStageTokens = 64;
+template <bool BF16>
+struct Stage {
+  static constexpr int kThreads = BF16 ? 128 : 256, kWarps = kThreads / 32;
+  static constexpr int kPieces = kDim * (BF16 ? 2 : 4) / 16;   // of a row, 16 bytes each
+  static constexpr int kRows = kThreads / kPieces;             // that the threads take at a time
+  static constexpr int kRow = kDim * (BF16 ? 2 : 4), kPitch = kRow + 16;   // (16: rows in different banks)
+  static constexpr int kBytes = kStageTokens * kPitch;
+};
+
+// One pass over a stage's tokens.
+struct Step {
+  Fp8Run r;
+  int field;                     // tensor and KV head
+  int base;                      // block offset of the stage's first token
+  bool search, write;
+  bool valid;
+};
+
+// The largest magnitude among rows [lo, hi) of a stage over a thread's share of
+// them, as bits; a NaN does not count, but sets *nan.
+template <bool BF16>
+__device__ __forceinline__ uint32_t largest_bits(const uint8_t* stage, int lo, int hi, bool* nan) {
+  using S = Stage<BF16>;
+  const int row = lo + threadIdx.x / S::kPieces;
+  const uint8_t* const mine = stage + row * S::kPitch + threadIdx.x % S::kPieces * 16;
+  uint32_t top = 0;
+  float odd = 0.f;                                // NaN after a NaN (or infinity)
+  {
+    const uint8_t* p = mine;
+#pragma unroll 4
+    for (int r = row; r < hi; r += S::kRows, p += S::kRows * S::kPitch) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      const int token = token_of(base, m >> 1);
-      const int coord = values ? 8 * piece + 64 * (m & 1) : 16 * piece + 8 * (m & 1);
-      if (token >= r.off && token < end)
-        x[m].load(rows, (static_cast<long long>(r.row) + token - r.off) * stride + head * kDim + coord);
-      else x[m].clear();
-    }
-  };
-  float amax = 0.f;
-  for (int base = first; base < end; base += step) {
-    load(base);
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      float v[8];
-      x[m].floats(v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (BF16) {
+          top = __vmaxu2(top, u[j] & 0x7fff7fffu);
+        } else {
+          const float x = __uint_as_float(u[j]);
+          top = __float_as_uint(fmaxf(__uint_as_float(top), fabsf(x)));
+          odd = fmaf(x, 0.f, odd);
+        }
+      }
     }
   }
-  const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
-  if (lane == 0) amax_s[warp] = __uint_as_float(bits);
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) amax = fmaxf(amax, amax_s[w]);
-  int grown;
-  const int e = run_exponent(amax, r.off, old, &grown);
-  if (grown > 0) rescale_block(block, values, r.off, grown, threadIdx.x, 32 * WARPS);
-  __syncthreads();                                // (also: amax_s is read, the next run may write it)
-  if (threadIdx.x == 0 && (r.off == 0 || grown > 0)) *scale = fp8_power(e);
-  const float down = fp8_power(-e);
-  for (int base = first; base < end; base += step) {
-    if (end - first > step) load(base);           // (else the one pass is still here)
-    uint32_t nan = 0;                             // by i: whether the token's vector has a NaN
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float a[8], b[8];
-      x[2 * i].floats(a);
-      x[2 * i + 1].floats(b);
-      bool here = false;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) here = here || a[j] != a[j] || b[j] != b[j];
-      // (a token's eight lanes have the same quad)
-      nan |= (__ballot_sync(0xffffffffu, here) & (0x11111111u << quad)) != 0 ? 1u << i : 0u;
+  if (BF16) top = max(top << 16, top & 0xffff0000u);
+  if (BF16 ? top <= 0x7f800000u : odd == odd) return top;
+  float most = 0.f;                               // once more, without them
+  const uint8_t* p = mine;
+#pragma unroll 1
+  for (int r = row; r < hi; r += S::kRows, p += S::kRows * S::kPitch)
+#pragma unroll 1
+    for (int j = 0; j < (BF16 ? 8 : 4); ++j) {
+      const float x = BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[j]) : reinterpret_cast<const float*>(p)[j];
+      *nan = *nan || x != x;
+      most = fmaxf(most, fabsf(x));
     }
-    if (!values) {
+  return __float_as_uint(most);
+}
+
+// Codes of a stage's tokens that are in the run.  A warp has sixteen
+// tokens (float32: a half of their coordinates).
+// Keys: eight tokens by four chunks of sixteen coordinates a round, a core matrix
+// (128 bytes) per eight lanes.  Values: a lane has four tokens (lane / 8) of eight
+// coordinates (lane % 8) twice; lanes eight apart exchange their words to have
+// sixteen tokens of a coordinate each.  nan: the run's tokens by bit, or null.
+template <bool BF16>
+__device__ __forceinline__ void write_codes(const uint8_t* stage, const Step& s, uint8_t* block, bool values, float down,
+                                            const uint8_t* nan) {
+  constexpr int kParts = Stage<BF16>::kWarps / 4, kEach = 2 / kParts;   // warps of sixteen tokens, halves of the coordinates each
+  const int warp = threadIdx.x >> 5 & 3, part = threadIdx.x >> 7, lane = threadIdx.x & 31;
+  const int end = s.r.off + s.r.len, unit = s.base + 16 * warp;     // the warp's first token
+  if (unit >= end || unit + 16 <= s.r.off) return;
+  const uint8_t* const rows = stage + 16 * warp * Stage<BF16>::kPitch;
+  constexpr int kEight = 8 * (BF16 ? 2 : 4);      // bytes of eight coordinates
+  if (!values) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int token = token_of(base, i);
-        uint32_t w[4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float v[8];
-          x[2 * i + h].floats(v);
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            w[2 * h + j] = nan & (1u << i) ? kFp8NaN4
-                                           : fp8_four(v[4 * j] * down, v[4 * j + 1] * down, v[4 * j + 2] * down, v[4 * j + 3] * down);
-        }
-        if (token >= r.off && token < end)
-          *reinterpret_cast<uint4*>(block + key_byte(token, 16 * piece)) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    } else {
-      const int unit = base + 16 * warp;          // the warp's sixteen tokens
-      uint32_t fix = 0;                           // bytes of the lane's four tokens that are NaN
-#pragma unroll
-      for (int i = 0; i < 4; ++i) fix |= nan & (1u << i) ? 0xffu << (8 * i) : 0u;
+    for (int k = 0; k < 2 * kEach; ++k) {
+      const int i = k + 2 * kEach * part;
+      const int at = 8 * (i & 1) + (lane & 7), chunk = 4 * (i >> 1) + (lane >> 3), token = unit + at;
+      uint32_t w[4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float v[4][8];
+        Eight<BF16> x;
+        float v[8];
+        x.load(rows + at * Stage<BF16>::kPitch + (2 * chunk + h) * kEight);
+        x.floats(v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[2 * i + h].floats(v[i]);
+        for (int j = 0; j < 2; ++j)
+          w[2 * h + j] = fp8_four_scaled(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], down);
+      }
+      if (nan != nullptr && nan[16 * warp + at]) w[0] = w[1] = w[2] = w[3] = kFp8NaN4;
+      if (token >= s.r.off && token < end)
+        *reinterpret_cast<uint4*>(block + key_byte(token, 16 * chunk)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return;
+  }
+  const int quad = lane >> 3, piece = lane & 7;
+  uint32_t fix = 0;                               // bytes of the lane's four tokens that are NaN
+  if (nan != nullptr)
+    for (int i = 0; i < 4; ++i) fix |= nan[16 * warp + 4 * quad + i] ? 0xffu << (8 * i) : 0u;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w[4];
+  for (int g = 0; g < kEach; ++g) {
+    const int h = g + kEach * part;
+    float v[4][8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int k = 4 * c + j;
-            w[j] = (fp8_four(v[0][k] * down, v[1][k] * down, v[2][k] * down, v[3][k] * down) & ~fix) | (kFp8NaN4 & fix);
-          }
-          transpose4(w);
-          uint8_t* const dst = block + value_byte(unit, 8 * piece + 64 * h + 4 * c + quad);
-          if (unit >= r.off && unit + 16 <= end) {
-            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-          } else {
+    for (int i = 0; i < 4; ++i) {
+      Eight<BF16> x;
+      x.load(rows + (4 * quad + i) * Stage<BF16>::kPitch + (piece + 8 * h) * kEight);
+      x.floats(v[i]);
+    }
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (unit + i >= r.off && unit + i < end) dst[i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
-          }
-        }
+    for (int c = 0; c < 2; ++c) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = 4 * c + j;
+        w[j] = (fp8_four_scaled(v[0][k], v[1][k], v[2][k], v[3][k], down) & ~fix) | (kFp8NaN4 & fix);
+      }
+      transpose4<8>(w);
+      uint8_t* const dst = block + value_byte(unit, 8 * piece + 64 * h + 4 * c + quad);
+      if (unit >= s.r.off && unit + 16 <= end) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (unit + i >= s.r.off && unit + i < end) dst[i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
       }
     }
   }
 }
 
-template <bool BF16, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) fp8_append_kernel(Fp8RowsArgs a) {
-  __shared__ Fp8Run runs[kFp8Window];
-  __shared__ int scratch[3];
-  __shared__ float amax_s[WARPS];
+// Items are (run, tensor, KV head), the heads of a run side by side as in memory;
+// the CTAs take every gridDim.x-th.  Where the call's runs are short on average a
+// warp takes an item, and the CTA those among its warps' that are not.
+template <bool BF16>
+constexpr int kAppendCtas = BF16 ? 6 : 3;         // of an SM, by their stages
+
+template <bool BF16>
+__global__ void __launch_bounds__(Stage<BF16>::kThreads, kAppendCtas<BF16>) fp8_append_kernel(Fp8RowsArgs a) {
+  constexpr int kThreads = Stage<BF16>::kThreads, kWarps = Stage<BF16>::kWarps;
+  extern __shared__ __align__(128) uint8_t stages[];
+  __shared__ Fp8Runs<kThreads> runs;
+  __shared__ long long warp_s[kWarps];
+  __shared__ uint32_t top_s[kWarps];
+  __shared__ uint8_t nan_s[kStageTokens];
   const Fp8Cache& c = a.c;
-  const int warp = threadIdx.x >> 5;
-  const bool values = a.rows[0] == nullptr || blockIdx.z == 1;
-  const int head = blockIdx.y;
-  const void* const rows = values ? a.rows[1] : a.rows[0];
-  const long long stride = values ? a.stride[1] : a.stride[0];
-  const int count = fp8_find_runs(c, blockIdx.x * a.window, a.window, runs, scratch);
-  auto block_of = [&](const Fp8Run& r) {
-    return (values ? c.v : c.k) + (static_cast<long long>(r.block) * c.n_kv + head) * c.block_size * kDim;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  runs.find(c, warp_s);
+  const bool shorts = runs.tokens <= static_cast<long long>(kShortRun) * runs.total();
+  auto values_of = [&](int field) { return a.rows[0] == nullptr || field >= c.n_kv; };
+  auto head_of = [&](int field) { return field >= c.n_kv ? field - c.n_kv : field; };
+  auto vector_of = [&](const Fp8Run& r, int field) { return static_cast<long long>(r.block) * c.n_kv + head_of(field); };
+
+  // an item's run and field, moved on by a number of items
+  struct Item {
+    int g, field;
   };
-  auto scale_of = [&](const Fp8Run& r) {
-    return (values ? c.v_scale : c.k_scale) + static_cast<long long>(r.block) * c.n_kv + head;
+  auto move = [&](Item& it, unsigned by) {
+    const unsigned f = it.field + by, over = f / a.fields;
+    it.g += over;
+    it.field = f - over * a.fields;
   };
-  for (int i = warp; i < count; i += WARPS) {
-    const Fp8Run r = runs[i];
-    if (r.len <= kShortRun) append_short<BF16>(r, rows, stride, head, block_of(r), scale_of(r), values);
+  const int total = runs.total();
+  int from = 0;
+  if (shorts) {
+    Item it{0, 0};
+    move(it, blockIdx.x * kWarps + warp);
+    for (; it.g < total; move(it, gridDim.x * kWarps)) {
+      const Fp8Run r = runs.get(c, it.g, &from);
+      if (r.block < 0 || r.len > kShortRun) continue;
+      const bool values = values_of(it.field);
+      append_short<BF16>(r, a.rows[values], a.stride[values], head_of(it.field),
+                         (values ? c.v : c.k) + vector_of(r, it.field) * c.block_size * kDim,
+                         (values ? c.v_scale : c.k_scale) + vector_of(r, it.field), values);
+    }
+    if (runs.most <= kShortRun) return;           // (there are no others)
+    from = 0;
   }
-  for (int i = 0; i < count; ++i) {
-    const Fp8Run r = runs[i];
-    if (r.len > kShortRun) append_long<BF16, WARPS>(r, rows, stride, head, block_of(r), scale_of(r), values, amax_s);
+  // The steps over the CTA's (longer) runs, one after another.
+  Item at{0, 0};
+  move(at, blockIdx.x);
+  auto first_step = [&]() {                       // of the item or those behind it
+    Step s;
+    s.valid = false;
+    for (; at.g < total && !s.valid; move(at, gridDim.x)) {
+      s.field = at.field;
+      s.r = runs.get(c, at.g, &from);
+      if (s.r.block < 0 || (shorts && s.r.len <= kShortRun)) continue;
+      s.base = s.r.off & ~15;
+      s.search = s.valid = true;
+      s.write = s.r.off + s.r.len - s.base <= kStageTokens;
+    }
+    return s;
+  };
+  auto step_after = [&](const Step& s) {
+    Step n = s;
+    const int first = s.r.off & ~15, end = s.r.off + s.r.len;
+    n.base += kStageTokens;
+    if (n.base < end) return n;                   // more of the run in this pass
+    if (s.write) return first_step();
+    n.base = first;                               // found the largest: now the codes
+    n.search = false;
+    n.write = true;
+    return n;
+  };
+  auto copy = [&](const Step& s, int k) {         // its rows, sixteen bytes a thread at a time
+    if (s.valid) {
+      constexpr int kPieces = Stage<BF16>::kPieces, kElem = BF16 ? 2 : 4;
+      const bool values = values_of(s.field);
+      const int lo = max(s.r.off, s.base), hi = min(s.r.off + s.r.len, s.base + kStageTokens);
+      const long long pitch = a.stride[values] * kElem;
+      const uint8_t* src = static_cast<const uint8_t*>(a.rows[values]) + head_of(s.field) * Stage<BF16>::kRow +
+                           (s.r.row + static_cast<long long>(lo + tid / kPieces - s.r.off)) * pitch + tid % kPieces * 16;
+      uint8_t* dst = stages + (k & 1) * Stage<BF16>::kBytes + (lo + tid / kPieces - s.base) * Stage<BF16>::kPitch + tid % kPieces * 16;
+      constexpr int kRows = Stage<BF16>::kRows;
+#pragma unroll 8
+      for (int t = lo + tid / kPieces; t < hi; t += kRows) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+        src += kRows * pitch;
+        dst += kRows * Stage<BF16>::kPitch;
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  Step now = first_step();
+  copy(now, 0);
+  uint32_t top = 0;
+  bool nan = false;
+  float down = 1.f;
+  for (int k = 0; now.valid; ++k) {
+    const Step next = step_after(now);
+    copy(next, k + 1);
+    const uint8_t* const stage = stages + (k & 1) * Stage<BF16>::kBytes;
+    const bool values = values_of(now.field);
+    const long long vec = vector_of(now.r, now.field);
+    uint8_t* const block = (values ? c.v : c.k) + vec * c.block_size * kDim;
+    float* const scale = (values ? c.v_scale : c.k_scale) + vec;
+    const float old = now.search && now.r.off > 0 ? *scale : 0.f;
+    const int lo = max(now.r.off, now.base) - now.base, hi = min(now.r.off + now.r.len, now.base + kStageTokens) - now.base;
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();
+    if (now.search) {
+      if (now.base == (now.r.off & ~15)) top = 0, nan = false;
+      top = max(top, largest_bits<BF16>(stage, lo, hi, &nan));
+      if (now.base + kStageTokens >= now.r.off + now.r.len) {
+        // the run's scale
+        const uint32_t most = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) top_s[warp] = most;
+        nan = __syncthreads_or(nan);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = max(top, top_s[w]);
+        int grown;
+        const int e = run_exponent(__uint_as_float(top), now.r.off, old, &grown);
+        if (grown > 0) {
+          rescale_block(block, values, now.r.off, grown, tid, kThreads);
+          __syncthreads();
+        }
+        if (tid == 0 && (now.r.off == 0 || grown > 0)) *scale = fp8_power(e);
+        down = fp8_power(-e);
+      }
+    }
+    if (now.write) {
+      if (nan) {                                  // which tokens have one (the same for the whole CTA)
+        if (tid < kStageTokens) {
+          bool here = false;
+          if (tid >= lo && tid < hi)
+            for (int d = 0; d < kDim; ++d) {
+              const uint8_t* const p = stage + tid * Stage<BF16>::kPitch;
+              const float v = BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[d])
+                                   : reinterpret_cast<const float*>(p)[d];
+              here = here || v != v;
+            }
+          nan_s[tid] = here;
+        }
+        __syncthreads();
+      }
+      write_codes<BF16>(stage, now, block, values, down, nan ? nan_s : nullptr);
+    }
+    __syncthreads();                              // (the stage may be filled again)
+    now = next;
   }
 }
 
@@ -306,21 +457,23 @@ __device__ __forceinline__ void eight_values(uint32_t lo, uint32_t hi, float sca
   }
 }
 
-// A warp takes sixteen tokens at a time, with the append's shares of lanes.
+// A CTA has the tokens of a window for one (tensor, KV head), its neighbours the
+// others.  A warp takes sixteen tokens at a time, with the append's shares of
+// lanes.
 template <bool BF16>
 __global__ void __launch_bounds__(32 * kReadWarps) fp8_read_kernel(Fp8RowsArgs a) {
-  __shared__ Fp8Run runs[kFp8Window];
-  __shared__ int scratch[3];
+  __shared__ Fp8Finder found;
   const Fp8Cache& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane & 3, piece = lane >> 2;
-  const bool values = a.rows[0] == nullptr || blockIdx.z == 1;
-  const int head = blockIdx.y;
+  const int field = blockIdx.x % a.fields;
+  const int count = fp8_find_runs(c, blockIdx.x / a.fields * a.window, a.window, found);
+  int turn = 0;
+  const bool values = a.rows[0] == nullptr || field >= c.n_kv;
+  const int head = field >= c.n_kv ? field - c.n_kv : field;
   void* const rows = values ? a.rows[1] : a.rows[0];
   const long long stride = values ? a.stride[1] : a.stride[0];
-  const int count = fp8_find_runs(c, blockIdx.x * a.window, a.window, runs, scratch);
-  int turn = 0;
   for (int i = 0; i < count; ++i) {
-    const Fp8Run r = runs[i];
+    const Fp8Run r = found.runs[i];
     const long long vec = static_cast<long long>(r.block) * c.n_kv + head;
     const uint8_t* const block = (values ? c.v : c.k) + vec * c.block_size * kDim;
     const float scale = __ldg((values ? c.v_scale : c.k_scale) + vec);
@@ -353,7 +506,7 @@ __global__ void __launch_bounds__(32 * kReadWarps) fp8_read_kernel(Fp8RowsArgs a
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             uint32_t u[4] = {w[2 * h + k].x, w[2 * h + k].y, w[2 * h + k].z, w[2 * h + k].w};
-            transpose4(u);
+            transpose4<1>(u);
             transpose_bytes(u, four[k]);
           }
 #pragma unroll
@@ -370,40 +523,45 @@ __global__ void __launch_bounds__(32 * kReadWarps) fp8_read_kernel(Fp8RowsArgs a
   }
 }
 
-// Tokens of a window: as few as leave the grid at about 8192 CTAs, so that the
-// runs of a decode step spread over many.
-int window_of(const Fp8RowsArgs& a, int tensors) {
-  int w = 4;
-  while (w < kFp8Window && (static_cast<long long>(a.c.n_tokens) + w - 1) / w * a.c.n_kv * tensors > 8192) w *= 2;
-  return w;
-}
-
+// As many CTAs as the SMs have room for, or as there can be items.
 template <bool BF16>
-cudaError_t append(const Fp8RowsArgs& a, dim3 grid, cudaStream_t stream) {
-  if (a.c.block_size <= 64) fp8_append_kernel<BF16, 4><<<grid, 128, 0, stream>>>(a);
-  else fp8_append_kernel<BF16, 8><<<grid, 256, 0, stream>>>(a);
+cudaError_t append(const Fp8RowsArgs& a, cudaStream_t stream) {
+  constexpr int kSmem = 2 * Stage<BF16>::kBytes;
+  const cudaError_t err = cudaFuncSetAttribute(fp8_append_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (err != cudaSuccess) return err;
+  const long long runs = std::min<long long>(a.c.n_tokens, a.c.n_tokens / a.c.block_size + 2ll * a.c.batch);
+  const long long ctas = std::min<long long>(runs * a.fields, kAppendCtas<BF16> * a.num_sms);
+  fp8_append_kernel<BF16><<<static_cast<unsigned>(ctas), Stage<BF16>::kThreads, kSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
-dim3 grid_of(Fp8RowsArgs& a) {
-  const int tensors = (a.rows[0] != nullptr) + (a.rows[1] != nullptr);
-  a.window = window_of(a, tensors);
-  return dim3((a.c.n_tokens + a.window - 1) / a.window, a.c.n_kv, tensors);
+long long windows_of(const Fp8RowsArgs& a) {
+  return (static_cast<long long>(a.c.n_tokens) + a.window - 1) / a.window;
+}
+
+// Read: windows of 16 tokens, or of 64 where that leaves 32 CTAs an SM (fewer
+// searches for the runs).
+long long read_grid(Fp8RowsArgs& a) {
+  a.fields = ((a.rows[0] != nullptr) + (a.rows[1] != nullptr)) * a.c.n_kv;
+  a.window = kFp8Window;
+  if (windows_of(a) * a.fields < kReadCtas) a.window = 16;
+  return windows_of(a) * a.fields;
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_append(const Fp8RowsArgs& args, bool bf16, cudaStream_t stream) {
   Fp8RowsArgs a = args;
-  const dim3 grid = grid_of(a);
-  return bf16 ? append<true>(a, grid, stream) : append<false>(a, grid, stream);
+  a.fields = ((a.rows[0] != nullptr) + (a.rows[1] != nullptr)) * a.c.n_kv;
+  return bf16 ? append<true>(a, stream) : append<false>(a, stream);
 }
 
 cudaError_t launch_fp8_read(const Fp8RowsArgs& args, bool bf16, cudaStream_t stream) {
   Fp8RowsArgs a = args;
-  const dim3 grid = grid_of(a);
-  if (bf16) fp8_read_kernel<true><<<grid, 32 * kReadWarps, 0, stream>>>(a);
-  else fp8_read_kernel<false><<<grid, 32 * kReadWarps, 0, stream>>>(a);
+  const long long grid = read_grid(a);
+  if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  if (bf16) fp8_read_kernel<true><<<static_cast<unsigned>(grid), 32 * kReadWarps, 0, stream>>>(a);
+  else fp8_read_kernel<false><<<static_cast<unsigned>(grid), 32 * kReadWarps, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

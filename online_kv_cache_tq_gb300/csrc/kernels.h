@@ -349,7 +349,8 @@ struct Fp8RowsArgs {
   Fp8Cache c;
   void* rows[2];              // keys and values (null: not this call's): read by the append, written by the read
   long long stride[2];        // elements from token to token
-  int window;                 // tokens per CTA (set by the launcher)
+  int num_sms;
+  int window, fields;         // set by the launcher: tokens per CTA of the read, (tensor, KV head) pairs
 };
 cudaError_t launch_fp8_append(const Fp8RowsArgs& args, bool bf16, cudaStream_t stream);
 cudaError_t launch_fp8_read(const Fp8RowsArgs& args, bool bf16, cudaStream_t stream);
