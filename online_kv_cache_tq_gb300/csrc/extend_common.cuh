@@ -632,6 +632,55 @@ __device__ __forceinline__ void weigh_usual(uint32_t s, const float* kf, const f
   ptx::tmem_st8(s + 32, rest[0], rest[1], rest[2], rest[3], rest[4], rest[5], rest[6], rest[7]);
 }
 
+// As weigh_usual where a group's 32 columns have one key factor and one power of
+// two 2^e as value factor (the 8-bit cache): the exponent takes it, the sum gives
+// it back once a group.
+__device__ __forceinline__ void weigh_grouped(uint32_t s, const float* kf, const float* vf, float ref, uint64_t& sum2) {
+  uint32_t x[2][16], rest[8];
+  tmem_ld16_start(s, x[0]);
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const float f = kf[32 * g];
+    const int e = exponent_of(vf[32 * g]);
+    const uint64_t factor = pair(f, f), shift = pair(e - ref, e - ref);
+    uint64_t part = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = 2 * g + h;
+      tmem_ld16_wait(x[c & 1]);
+      if (c < 3) tmem_ld16_start(s + 16 * (c + 1), x[(c + 1) & 1]);
+      const uint32_t(&y)[16] = x[c & 1];
+      uint32_t w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 z = unpair(fma2(pair(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), factor, shift));
+        const float p0 = exp2_fast(z.x), p1 = exp2_fast(z.y);
+        part = add2(part, pair(p0, p1));
+        w[k] = pack_bf16(p0, p1);
+        if (c == 3) rest[k] = remainder_bf16(p0, p1, w[k]);
+      }
+      ptx::tmem_st8(s + 8 * c, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+    }
+    sum2 = fma2(part, pair(exp2_int(-e), exp2_int(-e)), sum2);
+  }
+  ptx::tmem_st8(s + 32, rest[0], rest[1], rest[2], rest[3], rest[4], rest[5], rest[6], rest[7]);
+}
+// As plain_top for such columns (their key factors are not negative).
+__device__ __forceinline__ float grouped_top(uint32_t s, const float* kf) {
+  float top[2] = {-INFINITY, -INFINITY};
+  uint32_t x[2][16];
+  tmem_ld16_start(s, x[0]);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    tmem_ld16_wait(x[c & 1]);
+    if (c < 3) tmem_ld16_start(s + 16 * (c + 1), x[(c + 1) & 1]);
+    const uint32_t(&y)[16] = x[c & 1];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) top[c >> 1] = fmaxf(top[c >> 1], __uint_as_float(y[k]));
+  }
+  return fmaxf(top[0] * kf[0], top[1] * kf[32]);
+}
+
 // Visible tokens of group g (32 bits by token) when `here` of the tile's are
 // behind the row's position limit.
 __device__ __forceinline__ uint32_t visible(const uint32_t* valid, int here, int g) {

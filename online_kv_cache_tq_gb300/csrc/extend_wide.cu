@@ -281,6 +281,8 @@ struct WideBarriers {
 };
 
 // TURN: values are in the rotated space, and an output is turned back by R^T.
+// Otherwise the tiles are the 8-bit cache's (TileMeta::grouped says whether a
+// tile's factors go by groups of 32 columns).
 template <bool TURN>
 __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -449,11 +451,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         const uint32_t all = there.x & there.y & there.z & there.w, any = there.x | there.y | there.z | there.w;
         // (both the same for the two threads of a row, and so for their warps)
         bool mask = __any_sync(0xffffffffu, e != 0 || seen < (t + 1) * kTile || all != 0xffffffffu);
+        if constexpr (!TURN) mask = mask || meta->grouped == 0;
         const bool search = __any_sync(0xffffffffu, !(len * meta->reach <= (ref == -INFINITY ? 0.f : ref) + kRaise));
         const int here = min(kTile, max(0, seen - t * kTile));
         if (search) {
           // scores that may pass the reference: the tile's maximum first
-          const float top = mask ? masked_top(s_addr, kf, factor, meta->valid, here, half) : plain_top(s_addr, kf);
+          const float top = mask    ? masked_top(s_addr, kf, factor, meta->valid, here, half)
+                            : TURN ? plain_top(s_addr, kf)
+                                   : grouped_top(s_addr, kf);
           ok = swap(top, &other);
           if (!ok) break;
           const float to = raised(ref, fmaxf(top, other));
@@ -476,7 +481,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         }
         const float shift = ref == -INFINITY ? 0.f : ref;
         if (mask) sum2 = add2(sum2, pair(weigh_masked(s_addr, kf, vf, factor, shift, meta->valid, here, half), 0.f));
-        else weigh_usual(s_addr, kf, vf, shift, sum2);
+        else if constexpr (TURN) weigh_usual(s_addr, kf, vf, shift, sum2);
+        else weigh_grouped(s_addr, kf, vf, shift, sum2);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar.p_full[x]);

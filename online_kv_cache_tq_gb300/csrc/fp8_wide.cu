@@ -166,6 +166,9 @@ __global__ void __launch_bounds__(kExpandThreads) fp8_expand_kernel(Fp8Cache c, 
       uint32_t bits = 0;
       for (int w = 0; w < 4; ++w) bits = max(bits, __float_as_uint(reach_s[w]));
       meta->reach = __uint_as_float(bits);
+      uint32_t odd = 0;                           // tokens whose factors are not their block's
+      for (int g = 0; g < 4; ++g) odd |= nan_s[0][g] | nan_s[1][g] | ~there_s[g];
+      meta->grouped = odd == 0;
     }
   }
   if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // nothing is in flight when the CTA ends

@@ -291,7 +291,8 @@ struct __align__(16) TileMeta {
   float value_factor[kDim];   // what a weight is multiplied by: the value's norm and the levels' scale
   uint32_t valid[4];          // tokens there are, by group of 32
   float reach;                // largest |factor key|
-  float pad[3];
+  uint32_t grouped;           // 1: the factors are the same for the 32 columns of a group (value factors a power of two)
+  float pad[2];
 };
 
 struct ExtendArgs {
