@@ -623,8 +623,8 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           ptx::mma_e4m3(scores_t + (j & 1) * P::kQueryCols, k + ks * 16, q + ks * 2 * P::kQueryCols, kScores, ks > 0);
-        // (a test of the bounded waits: the first tile)
-        if (!(a.debug_withhold && blockIdx.x == 0 && j == 0)) ptx::mma_commit(&bar.s_full[j & 1]);
+        // (a test of the bounded waits: the CTA with the first key tile)
+        if (!(a.debug_withhold && blockIdx.x == kItemCost / per && j == 0)) ptx::mma_commit(&bar.s_full[j & 1]);
         ptx::mma_commit(&bar.empty[k_slot]);
         if (fresh) ptx::mma_commit(&bar.q_empty[seg & 1]);
       }

@@ -427,3 +427,18 @@ def test_any_device_handle_serves(kw):
     c.run()
     torch.cuda.synchronize()
     assert torch.equal(first, c.out)
+
+
+@pytest.mark.parametrize("new", [[1, 1], [2, 5], [300, 200]])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_correct(new, dtype):
+    # the test aid withholds one product's completion in the first CTA of each launch: its waits run out after a second,
+    # what it has in flight is drained, the call ends with device error 4 and the handle works on
+    c = Case(new, [n + 700 for n in new], n_kv=2, group=4, seed=24, dtype=dtype)
+    B.tq_debug_withhold_commit(c.book, True)
+    c.run()
+    torch.cuda.synchronize()
+    assert B.tq_get_last_device_error(c.book) == 4
+    B.tq_debug_withhold_commit(c.book, False)
+    c.run()
+    c.check(tokens=40)
