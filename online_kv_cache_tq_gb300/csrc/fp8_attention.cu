@@ -51,7 +51,7 @@ template <int RT>
 struct Shape {
   static constexpr int kSplit = RT / kRowsPerThread;        // threads per token
   static constexpr int kSoftWarps = 4 * kSplit;
-  static constexpr int kThreads = 32 * (kSoftWarps + 3);
+  static constexpr int kThreads = 32 * (kSoftWarps + 2);
   static constexpr int kSlots = 5;                          // ring of key and value tiles in turn
   static constexpr int kQueryCols = 4 * RT;
   static constexpr int kWeightCols = (3 * RT + 15) / 16 * 16;
@@ -231,9 +231,6 @@ __device__ __forceinline__ __half2 halves_of_fp8_pair(uint16_t p) {
 __device__ __forceinline__ void store_byte(uint32_t saddr, uint16_t b) {
   asm volatile("st.shared.b8 [%0], %1;" ::"r"(saddr), "h"(b) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_many(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(ptx::smem_u32(bar)), "r"(count) : "memory");
-}
 // The warp's largest (NaN does not count).
 __device__ __forceinline__ float warp_max(float x) {
   float y;
@@ -268,7 +265,7 @@ template <int RT>
 struct Barriers {
   uint64_t full[Shape<RT>::kSlots], empty[Shape<RT>::kSlots];
   uint64_t s_full[2], p_full[2], o_full[2];   // scores, weights and output product of a tile
-  uint64_t q_full[2], q_empty[2];             // queries of a segment
+  uint64_t q_full[2];                         // queries of a segment
   uint64_t maxima[Shape<RT>::kSplit], sums;   // the softmax warps of a row split, and all of them
   uint64_t drain;
 };
@@ -380,7 +377,6 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
       ptx::mbar_init(&bar.p_full[s], P::kSoftWarps);
       ptx::mbar_init(&bar.o_full[s], 1);
       ptx::mbar_init(&bar.q_full[s], P::kSoftWarps);
-      ptx::mbar_init(&bar.q_empty[s], 1 + P::kSoftWarps);   // the scores' products, and who reads the factors
     }
     for (int s = 0; s < P::kSplit; ++s) ptx::mbar_init(&bar.maxima[s], 4);
     ptx::mbar_init(&bar.sums, P::kSoftWarps);
@@ -410,16 +406,15 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
     const uint32_t my_weights =
         ptx::smem_u32(weight_s) + (token >> 4) * P::kWeightStride + 3 * kRowsPerThread * split * 16 + (token & 15);
     const __half2 weight_scale = __float2half2_rn(kWeightScale), sixteen = __float2half2_rn(16.f);
-    if (more) {                                   // the first queries, which everything waits for
-      prepare_rows<RT / P::kSoftWarps, RT>(a, walk, warp, P::kSoftWarps, query_s, sh.factor[0], sh.seen[0]);
-      if (lane == 0) ptx::mbar_arrive(&bar.q_full[0]);
-    }
     int jt = 0, met = 0;                          // key tiles so far, and those that this split's warps met over
     int slot = 1, slot_phase = 0;                 // of the value tile
     for (int seg = 0; more; ++seg, more = walk.next(a)) {
       const int n = walk.s.n, ctx = walk.s.ctx, row0 = walk.s.row0, kvh = walk.kvh, rt = walk.rt;
       const int first = rt * RT + split * kRowsPerThread;     // my first row of the sequence
       const int tile0 = walk.tile, tiles = walk.tiles, reached = tile0 + walk.span();
+      prepare_rows<RT / P::kSoftWarps, RT>(a, walk, warp, P::kSoftWarps, query_s + (seg & 1) * P::kQueryBytes, sh.factor[seg & 1],
+                                           sh.seen[seg & 1]);
+      if (lane == 0) ptx::mbar_arrive(&bar.q_full[seg & 1]);
       if (first >= n * a.group) {
         // no such rows: only keep in step
         for (int t = tile0; ok && t < reached; ++t, ++jt) {
@@ -429,10 +424,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
           if (slot >= P::kSlots) slot -= P::kSlots, slot_phase ^= 1;
         }
         if (!ok) break;
-        if (lane == 0) {
-          ptx::mbar_arrive(&bar.sums);
-          ptx::mbar_arrive(&bar.q_empty[seg & 1]);
-        }
+        if (lane == 0) ptx::mbar_arrive(&bar.sums);
         ok = TQ_WARP_WAIT(bar.sums, seg & 1);
         if (!ok) break;
         continue;
@@ -572,10 +564,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
         if (lane == 0) sh.sum[seg & 1][warp][r] = sum[r];
       }
       __syncwarp();
-      if (lane == 0) {
-        ptx::mbar_arrive(&bar.sums);
-        ptx::mbar_arrive(&bar.q_empty[seg & 1]);  // (factors and limits are read)
-      }
+      if (lane == 0) ptx::mbar_arrive(&bar.sums);
       ok = TQ_WARP_WAIT(bar.sums, seg & 1);
       if (!ok) break;
       if (tid < RT) sh.poison[(seg + 2) % 3][tid] = 0;        // (read by all before they came here)
@@ -626,7 +615,6 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
         // (a test of the bounded waits: the CTA with the first key tile)
         if (!(a.debug_withhold && blockIdx.x == kItemCost / per && j == 0)) ptx::mma_commit(&bar.s_full[j & 1]);
         ptx::mma_commit(&bar.empty[k_slot]);
-        if (fresh) ptx::mma_commit(&bar.q_empty[seg & 1]);
       }
       __syncwarp();
       k_slot += 2;
@@ -642,7 +630,8 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
     bool work = left > 0 || seg > 0;              // (a run without work has no tile)
     for (int j = 0; work && ok; ++j) {
       work = more;
-      if (work) ok = scores(j + 1);
+      const bool later = fresh;                   // (a segment's queries come after the one before is done)
+      if (work && !later) ok = scores(j + 1);
       ok = ok && TQ_WARP_WAIT(bar.full[v_slot], v_phase) && TQ_WARP_WAIT(bar.p_full[j & 1], (j >> 1) & 1);
       if (!ok) break;
       const uint32_t groups = sh.info[j & (kMetaRing - 1)].groups;
@@ -663,12 +652,13 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
       __syncwarp();
       v_slot += 2;
       if (v_slot >= P::kSlots) v_slot -= P::kSlots, v_phase ^= 1;
+      if (work && later) ok = scores(j + 1);
     }
     if (ptx::elect_one()) {
       ptx::mma_commit(&bar.drain);                // nothing is in flight when the CTA ends
       ptx::drain_bar(&bar.drain, 0);
     }
-  } else if (warp == P::kSoftWarps + 1) {
+  } else {
     // ---------------- copies ----------------
     // lane g < 4 has the tile's group g; its block id is read a tile ahead
     int slot = 0, phase = 1, issued = 0;
@@ -700,11 +690,25 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
       ++issued;
       if (++slot == P::kSlots) slot = 0, phase ^= 1;
     };
+    CutItem cut{0, 0, 0, 0, 0};
+    auto begin = [&]() {                          // of an item
+      // (the queries come from far memory, and a segment begins with them)
+      const int rows = min(RT, walk.s.n * a.group - walk.rt * RT), lines = a.q_bf16 ? 2 : 4;   // of 128 bytes
+      for (int k = lane; k < rows * lines; k += 32) {
+        const long long vec = row_vector(a, walk.s.row0, walk.kvh, walk.rt * RT + k / lines);
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.q) + (vec * lines + k % lines) * 128));
+      }
+      // what the run begins and does not end, for the join
+      if (walk.tile == 0 && walk.span() < walk.tiles)
+        cut = CutItem{walk.s.row0, walk.kvh, walk.rt, rows,
+                      static_cast<int>((walk.pos + walk.tiles - 1) / per)};
+    };
     Group now{};
-    if (more) now = read_id();
+    if (more) now = read_id(), begin();
     for (int j = 0; more; ++j) {
       if (++t == reached) {
         more = walk.next(a);
+        if (more) begin();
         if (more) t = walk.tile, reached = t + walk.span();
       }
       Group ahead{};
@@ -735,28 +739,10 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
       step();
       now = ahead;
     }
+    if (lane == 0) a.cuts[blockIdx.x] = cut;
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (*abort && lane == 0)                      // copies in flight land before the CTA ends
       for (int i = max(0, issued - P::kSlots); i < issued; ++i) ptx::drain_bar(&bar.full[i % P::kSlots], (i / P::kSlots) & 1);
-  } else {
-    // ---------------- queries ----------------
-    // one segment ahead of the others
-    CutItem cut{0, 0, 0, 0, 0};
-    for (int seg = 0; more; ++seg, more = walk.next(a)) {
-      ok = TQ_WARP_WAIT(bar.q_empty[seg & 1], ((seg >> 1) & 1) ^ 1);
-      if (!ok) break;
-      const int rows = walk.s.n * a.group, first = walk.rt * RT;
-      if (seg > 0) {                              // (the softmax warps prepare the run's first)
-#pragma unroll 1
-        for (int r0 = 0; r0 < RT; r0 += 4)
-          prepare_rows<4, RT>(a, walk, r0, 1, query_s + (seg & 1) * P::kQueryBytes, sh.factor[seg & 1], sh.seen[seg & 1]);
-        if (lane == 0) mbar_arrive_many(&bar.q_full[seg & 1], P::kSoftWarps);
-      }
-      if (walk.tile == 0 && walk.span() < walk.tiles)
-        cut = CutItem{walk.s.row0, walk.kvh, walk.rt, min(RT, rows - first),
-                      static_cast<int>((walk.pos + walk.tiles - 1) / per)};
-    }
-    if (lane == 0) a.cuts[blockIdx.x] = cut;
   }
   __syncwarp();
   ptx::tc_fence_before();
@@ -841,8 +827,10 @@ constexpr size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Rows of a row tile: 16 where the average sequence of the call has more than
 // eight.  (16 sequences on 8192 tokens, 64/8 heads, 8 rows each: 52 us with
-// eight a tile, 58 with 16; 16 rows: 91 and 66; 32 rows: 165 and 112, and 109
-// with tiles of 32 rows and one CTA an SM, which take 78 us for 8 rows.)
+// eight a tile, 59 with 16; 16 rows: 91 and 62; 32 rows: 165 and 118.  With 32
+// rows a tile and one CTA an SM 16 rows take 87 us and 32 rows 109; with four
+// warps that turn the tiles into fp16 operands, which need no pieces, 105 and
+// 135: then one chain of waits, exponentials and stores is all an SM has to do.)
 int tile_rows(int n_tokens, int batch, int group) {
   return (static_cast<long long>(n_tokens) + batch - 1) / batch * group <= 8 ? 8 : 16;
 }
