@@ -408,13 +408,21 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
     const __half2 weight_scale = __float2half2_rn(kWeightScale), sixteen = __float2half2_rn(16.f);
     int jt = 0, met = 0;                          // key tiles so far, and those that this split's warps met over
     int slot = 1, slot_phase = 0;                 // of the value tile
-    for (int seg = 0; more; ++seg, more = walk.next(a)) {
+    auto prepare = [&](const Walk<RT>& w, int seg) {          // a segment's queries
+      prepare_rows<RT / P::kSoftWarps, RT>(a, w, warp, P::kSoftWarps, query_s + (seg & 1) * P::kQueryBytes, sh.factor[seg & 1],
+                                           sh.seen[seg & 1]);
+      if (lane == 0) ptx::mbar_arrive(&bar.q_full[seg & 1]);
+    };
+    if (more) prepare(walk, 0);
+    for (int seg = 0; more; ++seg) {
       const int n = walk.s.n, ctx = walk.s.ctx, row0 = walk.s.row0, kvh = walk.kvh, rt = walk.rt;
       const int first = rt * RT + split * kRowsPerThread;     // my first row of the sequence
       const int tile0 = walk.tile, tiles = walk.tiles, reached = tile0 + walk.span();
-      prepare_rows<RT / P::kSoftWarps, RT>(a, walk, warp, P::kSoftWarps, query_s + (seg & 1) * P::kQueryBytes, sh.factor[seg & 1],
-                                           sh.seen[seg & 1]);
-      if (lane == 0) ptx::mbar_arrive(&bar.q_full[seg & 1]);
+      // (called after the last weights: the next queries, while the last product runs)
+      auto move_on = [&]() {
+        more = walk.next(a);
+        if (more) prepare(walk, seg + 1);
+      };
       if (first >= n * a.group) {
         // no such rows: only keep in step
         for (int t = tile0; ok && t < reached; ++t, ++jt) {
@@ -424,6 +432,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
           if (slot >= P::kSlots) slot -= P::kSlots, slot_phase ^= 1;
         }
         if (!ok) break;
+        move_on();
         if (lane == 0) ptx::mbar_arrive(&bar.sums);
         ok = TQ_WARP_WAIT(bar.sums, seg & 1);
         if (!ok) break;
@@ -554,6 +563,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
         if (slot >= P::kSlots) slot -= P::kSlots, slot_phase ^= 1;
       }
       if (!ok) break;
+      move_on();
       ok = add_output(jt - 1);
       if (!ok) break;
       // the rows' sums over the four warps
