@@ -566,13 +566,19 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
       move_on();
       ok = add_output(jt - 1);
       if (!ok) break;
-      // the rows' sums over the four warps
+      // the rows' sums over the four warps: halves of the rows are exchanged until
+      // a lane has one
 #pragma unroll
-      for (int r = 0; r < kRowsPerThread; ++r) {
+      for (int o = 16, k = kRowsPerThread / 2; o >= 4; o >>= 1, k >>= 1)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], o);
-        if (lane == 0) sh.sum[seg & 1][warp][r] = sum[r];
-      }
+        for (int r = 0; r < k; ++r) {
+          const bool upper = lane & o;
+          const float theirs = __shfl_xor_sync(0xffffffffu, upper ? sum[r] : sum[r + k], o);
+          sum[r] = (upper ? sum[r + k] : sum[r]) + theirs;
+        }
+      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
+      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
+      if ((lane & 3) == 0) sh.sum[seg & 1][warp][(lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1)] = sum[0];
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&bar.sums);
       ok = TQ_WARP_WAIT(bar.sums, seg & 1);
@@ -581,6 +587,11 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
       // (a run's first item may have begun in the run before, its last may go on)
       const bool whole = tile0 == 0 && reached == tiles;
       float* const part = a.part + (2ll * blockIdx.x + (tile0 == 0 ? 1 : 0)) * part_floats(RT);
+      // vector (token x query head) of my first row; the next row's is one on, or
+      // the next token's first of the group
+      const int tok = first / a.group;
+      int head = first - tok * a.group;
+      long long vec = (static_cast<long long>(row0) + tok) * a.n_q + kvh * a.group + head;
 #pragma unroll
       for (int r = 0; r < kRowsPerThread; ++r) {
         const int row = split * kRowsPerThread + r;
@@ -590,8 +601,10 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
         for (int w = 0; w < 4; ++w) all += sh.sum[seg & 1][4 * split + w][r];
         if (sh.poison[seg % 3][row] != 0) all = __int_as_float(0x7fc00000);
         if (whole) {
-          static_cast<__nv_bfloat16*>(a.out)[row_vector(a, row0, kvh, first + r) * kDim + token] =
-              __float2bfloat16_rn(all == 0.f ? 0.f : acc[r] / (kWeightScale * all));
+          static_cast<__nv_bfloat16*>(a.out)[vec * kDim + token] =
+              __float2bfloat16_rn(all == 0.f ? 0.f : __fdividef(acc[r], kWeightScale * all));
+          vec += ++head == a.group ? a.n_q - a.group + 1 : 1;
+          if (head == a.group) head = 0;
         } else {
           part[row * kDim + token] = acc[r];
           if (token == 0) {
