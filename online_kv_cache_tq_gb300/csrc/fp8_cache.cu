@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(Stage<BF16>::kThreads, kAppendCtas<BF16>) fp8_
   constexpr int kThreads = Stage<BF16>::kThreads, kWarps = Stage<BF16>::kWarps;
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ Fp8Runs<kThreads> runs;
-  __shared__ long long warp_s[kWarps];
+  __shared__ long long warp_s[kWarps][2];
   __shared__ uint32_t top_s[kWarps];
   __shared__ uint8_t nan_s[kStageTokens];
   const Fp8Cache& c = a.c;

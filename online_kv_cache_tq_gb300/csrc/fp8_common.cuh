@@ -86,11 +86,12 @@ struct Fp8Runs {
   static __device__ __forceinline__ int count(const Fp8Cache& c, const int3& s) {
     return s.y == 0 ? 0 : ((s.z - s.y) % c.block_size + s.y - 1) / c.block_size + 1;
   }
-  // By the whole CTA.
-  __device__ __forceinline__ void find(const Fp8Cache& c, long long* warp_s) {
+  // By the whole CTA.  Rows that overlap (query_start goes down) are recorded, and
+  // then there are no runs.
+  __device__ __forceinline__ void find(const Fp8Cache& c, long long (*warp_s)[2]) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, per = (c.batch + THREADS - 1) / THREADS;
-    int runs = 0, top = 0;
-    long long rows = 0;
+    int top = 0;
+    long long runs = 0, rows = 0;
     if (tid == 0) most = 0;
     for (int i = 0; i < per; ++i) {
       const int b = tid * per + i;
@@ -102,28 +103,29 @@ struct Fp8Runs {
       top = max(top, s.y);
     }
     top = __reduce_max_sync(0xffffffffu, top);
-    int upto = runs;
+    long long upto = runs;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, upto, d);
+      const long long o = __shfl_up_sync(0xffffffffu, upto, d);
       if (lane >= d) upto += o;
       rows += __shfl_xor_sync(0xffffffffu, rows, d);
     }
-    if (lane == 31) warp_s[warp] = rows << 32 | upto;    // (both below 2^31)
+    if (lane == 31) warp_s[warp][0] = upto, warp_s[warp][1] = rows;
     __syncthreads();
     long long before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
-      const long long v = warp_s[w];
-      if (w < warp) before += v;
-      all += v;
+      if (w < warp) before += warp_s[w][0];
+      all += warp_s[w][1];
     }
-    first[tid + 1] = static_cast<int>(before & 0xffffffff) + upto;
+    const bool ok = all <= c.n_tokens;            // (a run has a row at least: the sums below are ints)
+    if (!ok && tid == 0 && blockIdx.x == 0) atomicCAS(c.error, 0, kErrContext);
+    first[tid + 1] = ok ? static_cast<int>(before + upto) : 0;
     if (lane == 0) atomicMax(&most, top);
     if (tid == 0) {
       first[0] = 0;
       chunk = per;
-      tokens = all >> 32;
+      tokens = all;
     }
     __syncthreads();
   }

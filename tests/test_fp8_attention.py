@@ -442,3 +442,60 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_correct(new, dtyp
     B.tq_debug_withhold_commit(c.book, False)
     c.run()
     c.check(tokens=40)
+
+
+@pytest.mark.parametrize("group,new", [(4, [1]), (4, [4, 3, 0, 5]), (2, [1, 0, 90])])
+def test_more_sequences_than_threads(group, new):
+    rng = np.random.default_rng(group + len(new))
+    batch = 900
+    new = [new[i % len(new)] for i in range(batch)]
+    ctx = [max(n, 1) + int(c) for n, c in zip(new, rng.integers(0, 140, batch))]
+    c = Case(new, ctx, n_kv=1, group=group, bs=32, seed=20)
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("new,ctx", [([1, 1], [0, 40]), ([5, 2], [0, 1]), ([200, 1], [0, 30]), ([300], [3])])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_empty_contexts(new, ctx, dtype):
+    c = Case(new, ctx, group=4, dtype=dtype, seed=21)
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("new", [2, 6, 200])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_query_that_is_not_finite_spoils_its_own_row_only(new, bad):
+    c = Case([new, 1], [300, 90], n_kv=1, group=4, seed=22)
+    c.run()
+    torch.cuda.synchronize()
+    first = c.out.clone()
+    c.q[1, 2, 17] = bad
+    c.run()
+    torch.cuda.synchronize()
+    keep = torch.ones_like(first[..., 0], dtype=torch.bool)
+    keep[1, 2] = False
+    assert torch.equal(first[keep], c.out[keep])
+    if bad != bad:
+        assert bool(torch.isnan(c.out[1, 2]).all())
+
+
+@pytest.mark.parametrize("new", [1, 4, 200])
+def test_blocks_beyond_four_gigabytes(new):
+    # the same tokens in a small cache and at the end of one of 4.6 GB of keys and as much of values
+    c = Case([new, 2], [300, 90], n_kv=8, group=1, seed=23)
+    c.run()
+    torch.cuda.synchronize()
+    first = c.out.clone()
+    num_blocks, used = 70000, np.unique(c.table[c.table >= 0])
+    big = {name: torch.empty((num_blocks,) + tuple(t.shape[1:]), dtype=t.dtype, device="cuda") for name, t in c.cache.items()}
+    far = {int(b): num_blocks - 1 - i for i, b in enumerate(used)}
+    for name in big:
+        big[name][torch.tensor([far[int(b)] for b in used], device="cuda")] = c.cache[name][ints(used).long()]
+    c.table_t = ints(np.vectorize(lambda b: far.get(int(b), -1))(c.table))
+    c.view = C.fp8_view(c.book, big)
+    c.out.fill_(5.0)
+    c.run()
+    torch.cuda.synchronize()
+    assert B.tq_get_last_device_error(c.book) == 0
+    assert torch.equal(first, c.out)

@@ -419,3 +419,51 @@ def test_streams_and_graphs():
     for i, name in enumerate("kv"):
         model.append(name, x[:, i], c.table, c.new, c.ctx)
     model.check(c.cache)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,dtype", [(300, torch.float32), (1500, torch.bfloat16), (900, torch.float32)])
+def test_more_sequences_than_threads(batch, dtype):
+    # single tokens, and a few long runs among them
+    rng = np.random.default_rng(batch)
+    new = rng.choice([0, 1, 1, 1, 1, 1, 3], batch)
+    new[[5, batch // 2, batch - 1]] = [130, 70, 40]
+    c = Case([int(n) for n in new], [int(p) for p in rng.integers(0, 60, batch)], bs=32, n_kv=2, dtype=dtype, seed=15)
+    c.check_read(c.check_append())
+
+
+@pytest.mark.gpu
+def test_rows_that_overlap_are_recorded():
+    # query_start goes down: every other sequence would have all rows
+    c = Case([40] * 6, [100] * 6, seed=16)
+    before = {k: v.clone() for k, v in c.cache.items()}
+    c.start.copy_(ints([0, 240, 0, 240, 0, 240, 240]))
+    c.ctx_t.fill_(240)
+    c.append()
+    assert B.tq_get_last_device_error(c.book) == 3
+    assert all(torch.equal(before[k], c.cache[k]) for k in before)
+
+
+@pytest.mark.gpu
+def test_blocks_beyond_four_gigabytes():
+    # the same tokens in a small cache and at the end of one of 4.6 GB of keys and as much of values
+    bs, n_kv, num_blocks = 64, 8, 70000
+    small = Case([150, 1, 9], [0, 70, 120], bs=bs, n_kv=n_kv, identity=False, seed=17)
+    ids = np.unique(small.table)
+    far = {int(b): num_blocks - 1 - i for i, b in enumerate(ids)}
+    keys = torch.empty((num_blocks, n_kv, bs // 8, 8, 8, 16), dtype=torch.uint8, device="cuda")
+    values = torch.empty((num_blocks, n_kv, bs // 16, 128, 16), dtype=torch.uint8, device="cuda")
+    scales = torch.ones((2, num_blocks, n_kv), device="cuda")
+    big = dict(k_codes=keys, v_codes=values, k_scale=scales[0], v_scale=scales[1])
+    near_t, far_t = ints(ids).long(), torch.tensor([far[int(b)] for b in ids], device="cuda")
+    for name in big:
+        big[name][far_t] = small.cache[name][near_t]
+    small.append()
+    out = small.read()
+    small.table_t = ints(np.vectorize(far.get)(small.table))
+    small.view = C.fp8_view(small.book, big)
+    small.append()
+    assert B.tq_get_last_device_error(small.book) == 0
+    for name in big:
+        assert torch.equal(big[name][far_t], small.cache[name][near_t]), name
+    assert torch.equal(out, small.read())
