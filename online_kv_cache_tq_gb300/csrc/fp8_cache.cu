@@ -7,8 +7,17 @@
 // its first offset).  The codes are rn_e4m3(x 2^-e); where the scale grew, the
 // earlier tokens' codes become rn_e4m3(code 2^(e_old - e)).  A power of two
 // loses nothing but codes that leave e4m3's normal range.
+// The bound is HBM, 2 x 128 x (element + 1) bytes a token and KV head, and the
+// latency of a chain (run, table entry, rows, largest, codes) that a stage ahead
+// hides: a prompt of 32768 tokens x 8 heads takes 39.4 us in bf16 (5.1 TB/s, 0.76
+// of the measured copy; 800 warp instructions for a warp's 16 tokens x 128, 57 %
+// of issue), a decode step of 64 sequences 4 us.  Rows kept in registers between
+// the two passes took 45 us, read twice from memory 55, staged by bulk copies of
+// a row each 55; windows of tokens per CTA instead of runs 28 us in place of 21
+// for a mixed float32 step, because a window's runs come one after another.
 //
-// Read.  x = code 2^e, exact in either type.
+// Read.  x = code 2^e, exact in either type.  The bound is HBM: 131072 tokens x 8
+// heads to bf16 122 us (6.6 TB/s, 0.99), 65536 to float32 103 us (0.97).
 #include <algorithm>
 
 #include "fp8_common.cuh"

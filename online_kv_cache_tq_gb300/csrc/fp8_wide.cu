@@ -4,7 +4,10 @@
 // codes, in the swizzled layout that its products read, with the blocks' scales
 // as the columns' factors.  Then a tile serves every row tile of 256 rows.
 //
-// The bound is memory: 32 KB in and 64.5 KB out a tile.
+// The bound is memory: 32 KB in and 64.5 KB out a tile; 1008 tiles take 31 us
+// (3.1 TB/s).  A chunk of 2048 tokens on 14001, 64/8 heads, takes 870 us with it,
+// 1.16 PFLOP/s, where keys with large channels have every tile searched for its
+// maximum, and 793 us (1.27) where not.
 #include "fp8_common.cuh"
 #include "tc_ptx.cuh"
 
