@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(ExtendArgs a)
     a.wide.first[a.d.batch] = base.wide;
     a.ws_expand[a.d.batch] = base.expand;
   }
+  wait_prerequisites();                           // (of a launch beside it, where there is one)
 }
 
 // Joins the partial outputs of a split row tile: sum_s l_s 2^{m_s - M} o_s / sum_s l_s 2^{m_s - M}.
@@ -211,8 +212,9 @@ Layout layout(int n_tokens, int batch, int group, int n_kv, int max_context, int
   return l;
 }
 
-// Workspace regions and row arithmetic, then the launch of the plan.
-cudaError_t launch_plan(ExtendArgs& a, const Layout& l, char* ws, int ctas, cudaStream_t stream) {
+// Workspace regions and row arithmetic, then the launch of the plan (`beside` the
+// launch before it, which does not touch these regions).
+cudaError_t launch_plan(ExtendArgs& a, const Layout& l, char* ws, int ctas, bool beside, cudaStream_t stream) {
   a.narrow = ExtendForm{kNarrowRows, kNarrowCost, reinterpret_cast<long long*>(ws + l.first),
                         reinterpret_cast<float*>(ws + l.part), reinterpret_cast<CutItem*>(ws + l.cuts)};
   a.wide = ExtendForm{kWideRows, kWideCost, reinterpret_cast<long long*>(ws + l.wide_first),
@@ -226,6 +228,7 @@ cudaError_t launch_plan(ExtendArgs& a, const Layout& l, char* ws, int ctas, cuda
   while ((1 << a.group_shift) < a.d.group) ++a.group_shift;
   a.group_mul = static_cast<uint32_t>(((1ull << (31 + a.group_shift)) + a.d.group - 1) / a.d.group);
   const int plan_threads = a.d.batch >= kPlanThreads ? kPlanThreads : (a.d.batch + 255) / 256 * 256;
+  if (beside) return launch_dependent(extend_plan_kernel, dim3(1), plan_threads, 0, stream, a);
   extend_plan_kernel<<<1, plan_threads, 0, stream>>>(a);
   return cudaGetLastError();
 }
@@ -241,7 +244,7 @@ cudaError_t launch_extend(const ExtendArgs& args, void* workspace, cudaStream_t 
   const int ctas = a.d.num_sms;
   a.wide_from = kWideFrom;
   const Layout l = layout(a.n_tokens, a.d.batch, a.d.group, a.d.n_kv, a.d.max_context, ctas, kWideFrom, kNarrowRows);
-  cudaError_t err = launch_plan(a, l, static_cast<char*>(workspace), ctas, stream);
+  cudaError_t err = launch_plan(a, l, static_cast<char*>(workspace), ctas, false, stream);
   if (err == cudaSuccess && a.tile_cap > 0) err = launch_extend_expand(a, ctas, stream);
   if (err == cudaSuccess && a.tile_cap > 0) err = launch_extend_wide(a, true, ctas, stream);
   if (err == cudaSuccess) err = launch_extend_narrow(a, ctas, stream);
@@ -255,10 +258,14 @@ size_t extend_wide_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, i
   return l.tile_cap > 0 ? l.total : 0;
 }
 
-cudaError_t launch_extend_wide_plan(ExtendArgs& a, void* workspace, cudaStream_t stream) {
+bool extend_wide_fits(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms, int wide_from) {
+  return layout(n_tokens, batch, n_q / n_kv, n_kv, max_context, num_sms, wide_from, 0).tile_cap < kTileCap;
+}
+
+cudaError_t launch_extend_wide_plan(ExtendArgs& a, void* workspace, bool beside, cudaStream_t stream) {
   const int ctas = a.d.num_sms;
   const Layout l = layout(a.n_tokens, a.d.batch, a.d.group, a.d.n_kv, a.d.max_context, ctas, a.wide_from, 0);
-  return launch_plan(a, l, static_cast<char*>(workspace), ctas, stream);
+  return launch_plan(a, l, static_cast<char*>(workspace), ctas, beside, stream);
 }
 
 cudaError_t launch_extend_wide_join(const ExtendArgs& args, cudaStream_t stream) {

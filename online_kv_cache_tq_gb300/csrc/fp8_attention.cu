@@ -103,6 +103,7 @@ __device__ __forceinline__ Sequence load_sequence(const Fp8AttendArgs& a, int b)
   s.n = rows_ok ? s1 - s0 : 0;
   s.ctx = ctx_ok ? ctx : 0;
   s.ok = rows_ok && ctx_ok;
+  if (a.wide_from > 0 && s.n * a.group >= a.wide_from) s.n = 0;   // (the wide form's)
   s.units = s.n == 0 ? 0 : static_cast<long long>(c.n_kv) * row_tiles(s.n * a.group, RT) * (kItemCost + key_tiles(s.ctx));
   return s;
 }
@@ -898,17 +899,12 @@ cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem,
 template <int RT>
 cudaError_t attend(const Fp8AttendArgs& a, bool planned, cudaStream_t stream) {
   using P = Shape<RT>;
-  cudaError_t err = cudaFuncSetAttribute(fp8_attend_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  const cudaError_t err = cudaFuncSetAttribute(fp8_attend_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (err != cudaSuccess) return err;
   const int ctas = kCtasPerSm * a.num_sms;
-  if (planned) {
-    err = launch_dependent(fp8_attend_kernel<RT>, dim3(ctas), P::kThreads, P::kSmem, stream, a);
-  } else {
-    fp8_attend_kernel<RT><<<ctas, P::kThreads, P::kSmem, stream>>>(a);
-    err = cudaGetLastError();
-  }
-  if (err != cudaSuccess) return err;
-  return launch_dependent(fp8_join_kernel, dim3(ctas, RT / kJoinRows), 32 * kJoinWarps * kJoinRows, 0, stream, a, RT);
+  if (planned) return launch_dependent(fp8_attend_kernel<RT>, dim3(ctas), P::kThreads, P::kSmem, stream, a);
+  fp8_attend_kernel<RT><<<ctas, P::kThreads, P::kSmem, stream>>>(a);
+  return cudaGetLastError();
 }
 
 struct Layout {
@@ -938,9 +934,15 @@ cudaError_t launch_fp8_attention(const Fp8AttendArgs& args, void* workspace, cud
   const Layout l = layout(c.n_tokens, c.batch, a.n_q, c.n_kv, a.max_context, a.num_sms);
   a.cuts = reinterpret_cast<CutItem*>(ws);
   a.part = reinterpret_cast<float*>(ws + l.part);
+  const int rt = tile_rows(c.n_tokens, c.batch, a.group);
+  auto few = [&](bool planned) { return rt == 8 ? attend<8>(a, planned, stream) : attend<16>(a, planned, stream); };
+  auto join = [&]() {
+    return launch_dependent(fp8_join_kernel, dim3(kCtasPerSm * a.num_sms, rt / kJoinRows), 32 * kJoinWarps * kJoinRows, 0, stream, a,
+                            rt);
+  };
   cudaError_t err = cudaSuccess;
   if (l.total > l.wide) {
-    // some sequence may have the rows for the wide form: the plan says which
+    // some sequence may have the rows for the wide form
     ExtendArgs e{};
     e.d.q = a.q;
     e.d.batch = c.batch;
@@ -960,15 +962,25 @@ cudaError_t launch_fp8_attention(const Fp8AttendArgs& args, void* workspace, cud
     e.q_bf16 = a.q_bf16;
     e.query_top = 15;                             // coordinates below 2^15 are fp16 numbers as they are
     e.wide_from = kWideFrom;
-    err = launch_extend_wide_plan(e, ws + l.wide, stream);
+    // Where the rows alone say which sequences those are, the others go first and
+    // the plan runs beside them (24 sequences of 1 to 8 tokens: 109 us after it).
+    const bool first = extend_wide_fits(c.n_tokens, c.batch, a.n_q, c.n_kv, a.max_context, a.num_sms, kWideFrom);
+    if (first) {
+      a.wide_from = kWideFrom;
+      err = few(false);
+    }
+    if (err == cudaSuccess) err = launch_extend_wide_plan(e, ws + l.wide, first, stream);
     if (err == cudaSuccess) err = launch_fp8_expand(c, e, a.scale, stream);
     if (err == cudaSuccess) err = launch_extend_wide(e, false, a.num_sms, stream);
     if (err == cudaSuccess) err = launch_extend_wide_join(e, stream);
-    if (err != cudaSuccess) return err;
-    a.seq = e.ws_seq;
+    if (err == cudaSuccess && !first) {
+      a.seq = e.ws_seq;
+      err = few(true);
+    }
+  } else {
+    err = few(false);
   }
-  const bool planned = a.seq != nullptr;
-  return tile_rows(c.n_tokens, c.batch, a.group) == 8 ? attend<8>(a, planned, stream) : attend<16>(a, planned, stream);
+  return err == cudaSuccess ? join() : err;
 }
 
 }  // namespace tq

@@ -323,7 +323,11 @@ cudaError_t launch_extend_wide(const ExtendArgs& args, bool turn, int ctas, cuda
 // The wide form over tiles that another cache's kernel expands: the plan (sets
 // the workspace regions of `args`) and the join around it (extend.cu).
 size_t extend_wide_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms, int wide_from);
-cudaError_t launch_extend_wide_plan(ExtendArgs& args, void* workspace, cudaStream_t stream);
+// Whether the expanded tiles of every sequence with the rows have room, so that
+// the rows alone say which sequences are wide.
+bool extend_wide_fits(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms, int wide_from);
+// beside: the plan may run with the launch before it.
+cudaError_t launch_extend_wide_plan(ExtendArgs& args, void* workspace, bool beside, cudaStream_t stream);
 cudaError_t launch_extend_wide_join(const ExtendArgs& args, cudaStream_t stream);
 
 // The 8-bit cache (fp8_cache.cu, fp8_attention.cu): e4m3 codes with one power
@@ -369,7 +373,10 @@ struct Fp8AttendArgs {
   // workspace regions
   float* part;                // partial outputs of the row tiles that runs cut
   CutItem* cuts;              // [ctas]: what run c begins and does not end
-  const int4* seq;            // the plan's sequences (ExtendArgs::ws_seq), where some take the wide form; or null
+  // Sequences of the wide form: those that the plan says (ExtendArgs::ws_seq), or
+  // those with `wide_from` rows; or none.
+  const int4* seq;
+  int wide_from;
 };
 cudaError_t launch_fp8_expand(const Fp8Cache& cache, const ExtendArgs& args, float scale, cudaStream_t stream);   // (fp8_wide.cu)
 size_t fp8_workspace_bytes(int n_tokens, int batch, int n_q, int n_kv, int max_context, int num_sms);
