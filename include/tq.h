@@ -562,12 +562,13 @@ size_t tq_fp8_workspace_bytes(const tq_codebook* book, int n_tokens, int batch, 
  * Accuracy: a sequence with fewer than 144 rows (new tokens x n_q_heads /
  * n_kv_heads) has queries held to 2^-16 of a coordinate, keys exactly and
  * weights to 2^-11; with ordinary scores the result is off by 0.0017 in the root
- * mean square, the rounding of the output.  One with more has queries as fp16
+ * mean square, the rounding of the output.  One with more may have queries as fp16
  * numbers, weights as bf16 (a quarter of them with the remainder): 0.0022.
  * workspace: device scratch of tq_fp8_workspace_bytes bytes (up to 5 MB, and
  * where sequences can have those rows as tq_extend_attention's), 256-byte
- * aligned, not used by any concurrent call.  The same call gives the same bits.
- * Device errors as tq_extend_attention's.  Asynchronous on `stream`. */
+ * aligned, not used by any concurrent call; more tokens or a longer context of
+ * as many sequences need no less, fewer sequences may need more.  The same call
+ * gives the same bits.  Device errors as tq_extend_attention's.  Asynchronous on `stream`. */
 tq_status tq_fp8_attention(const tq_codebook* book, const void* q, tq_dtype dtype, int n_tokens, int batch,
                            int n_q_heads, int n_kv_heads, const tq_fp8_view* cache, const int32_t* block_table,
                            int max_blocks, const int32_t* query_start, const int32_t* context_lens, int max_context,

@@ -1208,7 +1208,6 @@ static tq_status fp8_cache_args(const tq_codebook* book, const tq_fp8_view* cach
   }
   if (n_tokens > 0 && batch > 0 && (!query_start || !context_lens)) return TQ_ERR_INVALID_ARG;
   if (!aligned4(query_start) || !aligned4(context_lens) || !aligned4(block_table)) return TQ_ERR_INVALID_ARG;
-  if (n_kv_heads > 32767) return TQ_ERR_UNSUPPORTED;   // (keys and values of a head are a grid dimension)
   *c = tq::Fp8Cache{static_cast<uint8_t*>(cache->k_codes), static_cast<uint8_t*>(cache->v_codes), cache->k_scale,
                     cache->v_scale, cache->num_blocks, n_kv_heads, cache->block_size, block_table, max_blocks, batch,
                     n_tokens, query_start, context_lens, book->d_error};

@@ -10,8 +10,8 @@
 // product, coordinates those of the output product; rows are its columns:
 //   scores [128 tokens x 4 RT]  = keys x (four e4m3 pieces of each query)^T,
 //   output [128 coordinates x 3 RT] = values^T x (three pieces of each weight)^T,
-// pieces as in e4m3_pieces.cuh (queries to 2^-16 of a coordinate, weights to
-// 2^-12).  A thread owns a token for the softmax and a coordinate for the
+// each piece what those before leave times sixteen (queries to 2^-16 of a
+// coordinate; weights to 2^-11: fp16 and three pieces, half a step of 2^-11 each).  A thread owns a token for the softmax and a coordinate for the
 // output, of eight rows; it keeps the output in registers and adds a tile's
 // product to it, so nothing is rescaled in tensor memory.
 //
@@ -32,7 +32,6 @@
 // 32 short ones of 16 rows 18.8, 18.9, 22.3 us.)
 #include <cstddef>
 
-#include "e4m3_pieces.cuh"
 #include "fp8_common.cuh"
 #include "tc_ptx.cuh"
 

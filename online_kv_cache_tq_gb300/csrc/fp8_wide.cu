@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kExpandThreads) fp8_expand_kernel(Fp8Cache c, 
       for (int g = 0; g < 4; ++g) odd |= nan_s[0][g] | nan_s[1][g] | ~there_s[g];
       meta->grouped = odd == 0;
     }
+    __syncwarp();                                 // (thread 0's neighbours write there_s next)
   }
   if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // nothing is in flight when the CTA ends
 }

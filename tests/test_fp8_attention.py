@@ -6,7 +6,8 @@ weights) and V = 2^-8 (half a step of bf16, relative).
 Few rows: a query coordinate is held to 2^-16 of itself, keys exactly, and a
 score is summed and shifted in float32, so |delta s_t| <= D = 2^-15 scale |q| |k_t|
 (Cauchy-Schwarz), which changes p-weighted means by at most (e^{2 D} - 1) a_j.
-Weights are held to 2^-12 of themselves and 2^-26 of the largest weight times
+Weights are held to 2^-11 of themselves (an fp16 rounding, then three e4m3
+pieces of it) and 2^-26 of the largest weight times
 the largest scale.  The output is rounded to bf16 once: V |o_j|.
 Many rows (from WIDE rows of a sequence and KV head): queries are fp16 numbers
 (u = 2^-11), D = 1.5 u scale |q| |k|; weights bf16 (V); the output passes once
@@ -151,6 +152,13 @@ def test_groups_and_ragged_batches(group, n_kv):
     c = Case(new, [5, 700, 129, 7, 1, 300, 0, 64, 3], n_kv=n_kv, group=group, seed=group, pad=4)
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("n_kv,group,new,ctx", [(33000, 1, [2], [3]), (700, 3, [1, 4], [130, 5]), (300, 1, [200, 2], [260, 40])])
+def test_many_kv_heads(n_kv, group, new, ctx):
+    c = Case(new, ctx, bs=32, n_kv=n_kv, group=group, seed=n_kv)
+    c.run()
+    c.check(tokens=2)
 
 
 @pytest.mark.parametrize("group,bs", [(8, 64), (16, 32), (4, 96)])
