@@ -13,8 +13,9 @@
 // of the measured copy; 800 warp instructions for a warp's 16 tokens x 128, 57 %
 // of issue), a decode step of 64 sequences 4 us.  Rows kept in registers between
 // the two passes took 45 us, read twice from memory 55, staged by bulk copies of
-// a row each 55; windows of tokens per CTA instead of runs 28 us in place of 21
-// for a mixed float32 step, because a window's runs come one after another.
+// a row each 55.  A mixed step of 24 sequences x 4 heads, float32, blocks of 96
+// tokens: 15.7 us; 20.7 where a run longer than a stage came twice, 28 with windows
+// of tokens per CTA instead of runs, because a window's runs come one after another.
 //
 // Read.  x = code 2^e, exact in either type.  The bound is HBM: 131072 tokens x 8
 // heads to bf16 122 us (6.6 TB/s, 0.99), 65536 to float32 103 us (0.97).
@@ -150,7 +151,9 @@ __device__ __forceinline__ void append_short(const Fp8Run& r, const void* rows, 
 // A CTA takes 64 tokens of a (run, tensor, KV head) at a time: their rows come
 // into shared memory by asynchronous copies, a stage ahead of the work on them.  Runs of
 // one stage are searched for their largest magnitude and converted where they
-// lie; longer ones (blocks of more than 64 tokens) come twice.
+// lie.  With blocks of up to 128 tokens the two stages are one, without copies
+// ahead (prefetching the next rows to L2 gains nothing); with longer ones a run's
+// rows come twice.
 constexpr int kStageTokens = 64;
 template <bool BF16>
 struct Stage {
@@ -219,12 +222,12 @@ __device__ __forceinline__ uint32_t largest_bits(const uint8_t* stage, int lo, i
 // coordinates (lane % 8) twice; lanes eight apart exchange their words to have
 // sixteen tokens of a coordinate each.  nan: the run's tokens by bit, or null.
 template <bool BF16>
-__device__ __forceinline__ void write_codes(const uint8_t* stage, const Step& s, uint8_t* block, bool values, float down,
-                                            const uint8_t* nan) {
+__device__ __forceinline__ void write_codes(const uint8_t* stage, const Fp8Run& r, int base, uint8_t* block, bool values,
+                                            float down, const uint8_t* nan) {
   constexpr int kParts = Stage<BF16>::kWarps / 4, kEach = 2 / kParts;   // warps of sixteen tokens, halves of the coordinates each
   const int warp = threadIdx.x >> 5 & 3, part = threadIdx.x >> 7, lane = threadIdx.x & 31;
-  const int end = s.r.off + s.r.len, unit = s.base + 16 * warp;     // the warp's first token
-  if (unit >= end || unit + 16 <= s.r.off) return;
+  const int end = r.off + r.len, unit = base + 16 * warp;     // the warp's first token
+  if (unit >= end || unit + 16 <= r.off) return;
   const uint8_t* const rows = stage + 16 * warp * Stage<BF16>::kPitch;
   constexpr int kEight = 8 * (BF16 ? 2 : 4);      // bytes of eight coordinates
   if (!values) {
@@ -244,7 +247,7 @@ __device__ __forceinline__ void write_codes(const uint8_t* stage, const Step& s,
           w[2 * h + j] = fp8_four_scaled(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], down);
       }
       if (nan != nullptr && nan[16 * warp + at]) w[0] = w[1] = w[2] = w[3] = kFp8NaN4;
-      if (token >= s.r.off && token < end)
+      if (token >= r.off && token < end)
         *reinterpret_cast<uint4*>(block + key_byte(token, 16 * chunk)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     return;
@@ -273,12 +276,12 @@ __device__ __forceinline__ void write_codes(const uint8_t* stage, const Step& s,
       }
       transpose4<8>(w);
       uint8_t* const dst = block + value_byte(unit, 8 * piece + 64 * h + 4 * c + quad);
-      if (unit >= s.r.off && unit + 16 <= end) {
+      if (unit >= r.off && unit + 16 <= end) {
         *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (unit + i >= s.r.off && unit + i < end) dst[i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
+          if (unit + i >= r.off && unit + i < end) dst[i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
       }
     }
   }
@@ -287,17 +290,18 @@ __device__ __forceinline__ void write_codes(const uint8_t* stage, const Step& s,
 // Items are (run, tensor, KV head), the heads of a run side by side as in memory;
 // the CTAs take every gridDim.x-th.  Where the call's runs are short on average a
 // warp takes an item, and the CTA those among its warps' that are not.
-template <bool BF16>
-constexpr int kAppendCtas = BF16 ? 6 : 3;         // of an SM, by their stages
+template <bool BF16, bool WHOLE>
+constexpr int kAppendCtas = BF16 ? 6 : WHOLE ? 4 : 3;   // of an SM, by their stages (float32, blocks of 96: four 15.9 us, three 16.9)
 
-template <bool BF16>
-__global__ void __launch_bounds__(Stage<BF16>::kThreads, kAppendCtas<BF16>) fp8_append_kernel(Fp8RowsArgs a) {
+// WHOLE: the two stages are one (blocks of 65 to 128 tokens).
+template <bool BF16, bool WHOLE>
+__global__ void __launch_bounds__(Stage<BF16>::kThreads, kAppendCtas<BF16, WHOLE>) fp8_append_kernel(Fp8RowsArgs a) {
   constexpr int kThreads = Stage<BF16>::kThreads, kWarps = Stage<BF16>::kWarps;
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ Fp8Runs<kThreads> runs;
   __shared__ long long warp_s[kWarps][2];
   __shared__ uint32_t top_s[kWarps];
-  __shared__ uint8_t nan_s[kStageTokens];
+  __shared__ uint8_t nan_s[2 * kStageTokens];
   const Fp8Cache& c = a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   runs.find(c, warp_s);
@@ -332,6 +336,7 @@ __global__ void __launch_bounds__(Stage<BF16>::kThreads, kAppendCtas<BF16>) fp8_
     from = 0;
   }
   // The steps over the CTA's (longer) runs, one after another.
+  constexpr int span = WHOLE ? 2 * kStageTokens : kStageTokens;
   Item at{0, 0};
   move(at, blockIdx.x);
   auto first_step = [&]() {                       // of the item or those behind it
@@ -343,14 +348,14 @@ __global__ void __launch_bounds__(Stage<BF16>::kThreads, kAppendCtas<BF16>) fp8_
       if (s.r.block < 0 || (shorts && s.r.len <= kShortRun)) continue;
       s.base = s.r.off & ~15;
       s.search = s.valid = true;
-      s.write = s.r.off + s.r.len - s.base <= kStageTokens;
+      s.write = s.r.off + s.r.len - s.base <= span;
     }
     return s;
   };
   auto step_after = [&](const Step& s) {
     Step n = s;
     const int first = s.r.off & ~15, end = s.r.off + s.r.len;
-    n.base += kStageTokens;
+    n.base += span;
     if (n.base < end) return n;                   // more of the run in this pass
     if (s.write) return first_step();
     n.base = first;                               // found the largest: now the codes
@@ -362,7 +367,7 @@ __global__ void __launch_bounds__(Stage<BF16>::kThreads, kAppendCtas<BF16>) fp8_
     if (s.valid) {
       constexpr int kPieces = Stage<BF16>::kPieces, kElem = BF16 ? 2 : 4;
       const bool values = values_of(s.field);
-      const int lo = max(s.r.off, s.base), hi = min(s.r.off + s.r.len, s.base + kStageTokens);
+      const int lo = max(s.r.off, s.base), hi = min(s.r.off + s.r.len, s.base + span);
       const long long pitch = a.stride[values] * kElem;
       const uint8_t* src = static_cast<const uint8_t*>(a.rows[values]) + head_of(s.field) * Stage<BF16>::kRow +
                            (s.r.row + static_cast<long long>(lo + tid / kPieces - s.r.off)) * pitch + tid % kPieces * 16;
@@ -384,20 +389,21 @@ __global__ void __launch_bounds__(Stage<BF16>::kThreads, kAppendCtas<BF16>) fp8_
   float down = 1.f;
   for (int k = 0; now.valid; ++k) {
     const Step next = step_after(now);
-    copy(next, k + 1);
-    const uint8_t* const stage = stages + (k & 1) * Stage<BF16>::kBytes;
+    if (!WHOLE) copy(next, k + 1);
+    const uint8_t* const stage = stages + (WHOLE ? 0 : k & 1) * Stage<BF16>::kBytes;
     const bool values = values_of(now.field);
     const long long vec = vector_of(now.r, now.field);
     uint8_t* const block = (values ? c.v : c.k) + vec * c.block_size * kDim;
     float* const scale = (values ? c.v_scale : c.k_scale) + vec;
     const float old = now.search && now.r.off > 0 ? *scale : 0.f;
-    const int lo = max(now.r.off, now.base) - now.base, hi = min(now.r.off + now.r.len, now.base + kStageTokens) - now.base;
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const int lo = max(now.r.off, now.base) - now.base, hi = min(now.r.off + now.r.len, now.base + span) - now.base;
+    if (WHOLE) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();
     if (now.search) {
       if (now.base == (now.r.off & ~15)) top = 0, nan = false;
       top = max(top, largest_bits<BF16>(stage, lo, hi, &nan));
-      if (now.base + kStageTokens >= now.r.off + now.r.len) {
+      if (now.base + span >= now.r.off + now.r.len) {
         // the run's scale
         const uint32_t most = __reduce_max_sync(0xffffffffu, top);
         if (lane == 0) top_s[warp] = most;
@@ -416,7 +422,7 @@ __global__ void __launch_bounds__(Stage<BF16>::kThreads, kAppendCtas<BF16>) fp8_
     }
     if (now.write) {
       if (nan) {                                  // which tokens have one (the same for the whole CTA)
-        if (tid < kStageTokens) {
+        if (tid < span) {
           bool here = false;
           if (tid >= lo && tid < hi)
             for (int d = 0; d < kDim; ++d) {
@@ -429,9 +435,11 @@ __global__ void __launch_bounds__(Stage<BF16>::kThreads, kAppendCtas<BF16>) fp8_
         }
         __syncthreads();
       }
-      write_codes<BF16>(stage, now, block, values, down, nan ? nan_s : nullptr);
+      for (int t = 0; t < span; t += kStageTokens)
+        write_codes<BF16>(stage + t * Stage<BF16>::kPitch, now.r, now.base + t, block, values, down, nan ? nan_s + t : nullptr);
     }
     __syncthreads();                              // (the stage may be filled again)
+    if (WHOLE) copy(next, 0);
     now = next;
   }
 }
@@ -563,14 +571,18 @@ __global__ void __launch_bounds__(32 * kReadWarps<BF16>) fp8_read_kernel(Fp8Rows
 }
 
 // As many CTAs as the SMs have room for, or as there can be items.
-template <bool BF16>
+template <bool BF16, bool WHOLE>
 cudaError_t append(const Fp8RowsArgs& a, cudaStream_t stream) {
-  constexpr int kSmem = 2 * Stage<BF16>::kBytes;
-  const cudaError_t err = cudaFuncSetAttribute(fp8_append_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  using S = Stage<BF16>;
+  const int smem = WHOLE ? a.c.block_size * S::kPitch : 2 * S::kBytes;
+  const cudaError_t err =
+      cudaFuncSetAttribute(fp8_append_kernel<BF16, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * S::kBytes);
   if (err != cudaSuccess) return err;
+  // (an SM has 228 KB; a CTA takes 1 KB more than it asks for)
+  const int fit = std::min<int>(kAppendCtas<BF16, WHOLE>, (228 << 10) / (smem + static_cast<int>(sizeof(Fp8Runs<S::kThreads>)) + 1536));
   const long long runs = std::min<long long>(a.c.n_tokens, a.c.n_tokens / a.c.block_size + 2ll * a.c.batch);
-  const long long ctas = std::min<long long>(runs * a.fields, kAppendCtas<BF16> * a.num_sms);
-  fp8_append_kernel<BF16><<<static_cast<unsigned>(ctas), Stage<BF16>::kThreads, kSmem, stream>>>(a);
+  const long long ctas = std::min<long long>(runs * a.fields, fit * a.num_sms);
+  fp8_append_kernel<BF16, WHOLE><<<static_cast<unsigned>(ctas), S::kThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -592,7 +604,9 @@ long long read_grid(Fp8RowsArgs& a) {
 cudaError_t launch_fp8_append(const Fp8RowsArgs& args, bool bf16, cudaStream_t stream) {
   Fp8RowsArgs a = args;
   a.fields = ((a.rows[0] != nullptr) + (a.rows[1] != nullptr)) * a.c.n_kv;
-  return bf16 ? append<true>(a, stream) : append<false>(a, stream);
+  const bool whole = a.c.block_size > kStageTokens && a.c.block_size <= 2 * kStageTokens;
+  if (whole) return bf16 ? append<true, true>(a, stream) : append<false, true>(a, stream);
+  return bf16 ? append<true, false>(a, stream) : append<false, false>(a, stream);
 }
 
 cudaError_t launch_fp8_read(const Fp8RowsArgs& args, bool bf16, cudaStream_t stream) {
