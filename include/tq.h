@@ -560,10 +560,11 @@ size_t tq_fp8_workspace_bytes(const tq_codebook* book, int n_tokens, int batch, 
  * were.  max_context bounds every context_lens[b] and is at most 2^30 (else
  * TQ_ERR_UNSUPPORTED).  scale: 0 selects 1/sqrt(d).
  * Accuracy: a sequence with fewer than 144 rows (new tokens x n_q_heads /
- * n_kv_heads) has queries held to 2^-16 of a coordinate, keys exactly and
+ * n_kv_heads) has keys exactly, bf16 queries exactly (coordinates below 2^-12 of
+ * a vector's largest to 2^-21 of it), float32 ones to 2^-16 of a coordinate and
  * weights to 2^-11; with ordinary scores the result is off by 0.0017 in the root
- * mean square, the rounding of the output.  One with more may have queries as fp16
- * numbers, weights as bf16 (a quarter of them with the remainder): 0.0022.
+ * mean square, the rounding of the output.  One with more may have queries as
+ * fp16 numbers, weights as bf16 (a quarter of them with the remainder): 0.0022.
  * workspace: device scratch of tq_fp8_workspace_bytes bytes (up to 5 MB, and
  * where sequences can have those rows as tq_extend_attention's), 256-byte
  * aligned, not used by any concurrent call; more tokens or a longer context of

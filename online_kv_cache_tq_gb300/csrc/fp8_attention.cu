@@ -8,12 +8,16 @@
 // or value tile (128 tokens) is four bulk copies of 32 tokens and no
 // instruction touches its bytes.  Cached tokens are the lanes of the score
 // product, coordinates those of the output product; rows are its columns:
-//   scores [128 tokens x 4 RT]  = keys x (four e4m3 pieces of each query)^T,
+//   scores [128 tokens x 2 RT or 4 RT] = keys x (two or four e4m3 pieces of each query)^T,
 //   output [128 coordinates x 3 RT] = values^T x (three pieces of each weight)^T,
-// each piece what those before leave times sixteen (queries to 2^-16 of a
-// coordinate; weights to 2^-11: fp16 and three pieces, half a step of 2^-11 each).  A thread owns a token for the softmax and a coordinate for the
-// output, of eight rows; it keeps the output in registers and adds a tile's
-// product to it, so nothing is rescaled in tensor memory.
+// each piece what those before leave, times a power of two.  Two pieces of four
+// bits are a bf16 coordinate exactly, where it is 2^-12 of the query's largest or
+// more, and hold it to 2^-21 of the largest below that; four hold a float32 one to
+// 2^-16 of itself.  (bf16 with two | with four: 16 rows on 8192 tokens 58.5 | 60.3
+// us, on 2000 99 | 105.)  Weights are held to 2^-11: rounded to fp16, then three
+// pieces.  A thread owns a token for the softmax and a coordinate for the output,
+// of eight rows; it keeps the output in registers and adds a tile's product to it,
+// so nothing is rescaled in tensor memory.
 //
 // The bound is HBM: 256 bytes per token and KV head.  A tile of 32 KB takes an
 // SM 1490 cycles at the copy rate; one chain of softmax on a tile (four warps:
@@ -22,7 +26,7 @@
 // tokens, 64/8 heads, 340 us (6.9 TB/s); 16 of 8192, 32/8 heads, 49 us, and one of
 // 131072, 64/8, 49 us (5.4 TB/s): 2.5 us until the first copies, 3 us in which
 // some CTAs are done and others not, 4 us for the join.  Sixteen rows a tile are
-// issue bound: 62 us for 16 sequences of 8192 with 16 rows.
+// issue bound: 58.5 us for 16 sequences of 8192 with 16 rows.
 //
 // Work is split as in extend.cu: an item is a row tile of a sequence and KV
 // head, worth kItemCost units and one per key tile; every CTA takes an equal
@@ -51,20 +55,21 @@ constexpr int kCtasPerSm = 2;
 constexpr float kNothing = -3e38f;     // a row's reference before it sees a token
 constexpr float kWeightScale = 256.f;  // weights are at most 1: times this in e4m3
 
-// RT rows a tile, 8 or 16; two CTAs an SM.
-template <int RT>
+// RT rows a tile, 8 or 16, with queries of QP pieces; two CTAs an SM.
+template <int RT, int QP>
 struct Shape {
   static constexpr int kSplit = RT / kRowsPerThread;        // threads per token
   static constexpr int kSoftWarps = 4 * kSplit;
   static constexpr int kThreads = 32 * (kSoftWarps + 2);
   static constexpr int kSlots = 5;                          // ring of key and value tiles in turn
-  static constexpr int kQueryCols = 4 * RT;
+  static constexpr float kPiece = QP == 2 ? 64.f : 16.f;    // a query's piece over the one before
+  static constexpr int kQueryCols = QP * RT;
   static constexpr int kWeightCols = (3 * RT + 15) / 16 * 16;
   // (64 bytes more than the rows between sixteen tokens and the next, so that a
   // warp's byte stores to both meet different banks)
   static constexpr int kWeightStride = kWeightCols * 16 + 64;
   static constexpr int kQueryBytes = kQueryCols * kDim, kWeightBytes = kWeightStride * kTile / 16;
-  static constexpr int kTmem = RT == 8 ? 128 : 256;
+  static constexpr int kTmem = RT == 8 || QP == 2 ? 128 : 256;
   static constexpr int kSmem = kSlots * kSlotBytes + 2 * kQueryBytes + 2 * kWeightBytes + 128;   // (128: alignment)
   static_assert(2 * kQueryCols + kWeightCols <= kTmem, "two buffers of scores, one of outputs");
 };
@@ -159,9 +164,8 @@ struct Walk {
 };
 
 // The run's start, by the whole CTA.
-template <int RT>
+template <int RT, int kWarps>
 __device__ __forceinline__ void find_run(const Fp8AttendArgs& a, RunStart* out, long long* warp_s) {
-  constexpr int kWarps = Shape<RT>::kThreads / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int batch = a.c.batch;
   // all units: in one round while the batch has no more sequences than the CTA threads
@@ -251,41 +255,39 @@ __device__ __forceinline__ void arrive_copies(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld24(uint32_t taddr, uint32_t (&r)[24]) {
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[N]) {
 #pragma unroll
-  for (int i = 0; i < 24; i += 8)
+  for (int i = 0; i < N; i += 8)
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]),
                    "=r"(r[i + 7])
                  : "r"(taddr + i)
                  : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
-                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23])
-               :
-               : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));   // (nothing that uses them goes before the wait)
 }
 
-template <int RT>
+template <int RT, int QP>
 struct Barriers {
-  uint64_t full[Shape<RT>::kSlots], empty[Shape<RT>::kSlots];
+  uint64_t full[Shape<RT, QP>::kSlots], empty[Shape<RT, QP>::kSlots];
   uint64_t s_full[2], p_full[2], o_full[2];   // scores, weights and output product of a tile
   uint64_t q_full[2];                         // queries of a segment
-  uint64_t maxima[Shape<RT>::kSplit], sums;   // the softmax warps of a row split, and all of them
+  uint64_t maxima[Shape<RT, QP>::kSplit], sums;   // the softmax warps of a row split, and all of them
   uint64_t drain;
 };
 
-template <int RT>
+template <int RT, int QP>
 struct Shared {
-  Barriers<RT> bar;
+  Barriers<RT, QP> bar;
   TileInfo info[kMetaRing];
   __align__(16) float factor[2][RT];           // scale log2(e) over the query's piece scale
   int seen[2][RT];               // positions a row sees
-  float4 top[2][Shape<RT>::kSplit][4][2];   // largest scores of a tile, by warp: eight rows
-  float sum[2][Shape<RT>::kSoftWarps][kRowsPerThread];
+  float4 top[2][Shape<RT, QP>::kSplit][4][2];   // largest scores of a tile, by warp: eight rows
+  float sum[2][Shape<RT, QP>::kSoftWarps][kRowsPerThread];
   uint32_t poison[3][RT];        // rows that see a value that is NaN
-  long long warp_s[Shape<RT>::kThreads / 32];
+  long long warp_s[Shape<RT, QP>::kThreads / 32];
   RunStart start;
   uint32_t tmem;
   int abort;
@@ -303,11 +305,11 @@ __device__ __forceinline__ long long row_vector(const Fp8AttendArgs& a, int row0
 // Rows r0, r0 + step, .. (N of them) of the walk's item as operand rows of the
 // score product, by a warp: four coordinates a lane, as e4m3 pieces of the
 // query times a power of two.
-template <int N, int RT>
+template <int N, int RT, int QP>
 __device__ __forceinline__ void prepare_rows(const Fp8AttendArgs& a, const Walk<RT>& walk, int r0, int step, uint8_t* operand,
                                              float* factor, int* seen) {
   const int lane = threadIdx.x & 31, rows = walk.s.n * a.group, first = walk.rt * RT;
-  uint8_t* const dst = operand + (lane >> 2) * (Shape<RT>::kQueryCols * 16) + (lane & 3) * 4;
+  uint8_t* const dst = operand + (lane >> 2) * (Shape<RT, QP>::kQueryCols * 16) + (lane & 3) * 4;
   float v[N][4];
   int token[N];
 #pragma unroll
@@ -318,7 +320,7 @@ __device__ __forceinline__ void prepare_rows(const Fp8AttendArgs& a, const Walk<
     if (row < rows) {
       const long long vec = (static_cast<long long>(walk.s.row0) + token[i]) * a.n_q + walk.kvh * a.group + row - token[i] * a.group;
       const long long at = vec * kDim + 4 * lane;
-      if (a.q_bf16) {
+      if constexpr (QP == 2) {                    // (bf16)
         const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + at));
         v[i][0] = __uint_as_float(u.x << 16), v[i][1] = __uint_as_float(u.x & 0xffff0000u);
         v[i][2] = __uint_as_float(u.y << 16), v[i][3] = __uint_as_float(u.y & 0xffff0000u);
@@ -338,11 +340,12 @@ __device__ __forceinline__ void prepare_rows(const Fp8AttendArgs& a, const Walk<
     const float up = e > 126 ? __int_as_float(0x7fc00000) : fp8_power(6 - e);   // (infinite: the row is NaN)
     float4 y = make_float4(v[i][0] * up, v[i][1] * up, v[i][2] * up, v[i][3] * up);
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
+    for (int p = 0; p < QP; ++p) {
       const uint32_t w = fp8_four(y.x, y.y, y.z, y.w);
-      *reinterpret_cast<uint32_t*>(dst + (4 * r + p) * 16) = w;
+      *reinterpret_cast<uint32_t*>(dst + (QP * r + p) * 16) = w;
       const float2 lo = fp8_floats(w), hi = fp8_floats(w >> 16);
-      y = make_float4((y.x - lo.x) * 16.f, (y.y - lo.y) * 16.f, (y.z - hi.x) * 16.f, (y.w - hi.y) * 16.f);
+      constexpr float up = Shape<RT, QP>::kPiece;
+      y = make_float4((y.x - lo.x) * up, (y.y - lo.y) * up, (y.z - hi.x) * up, (y.w - hi.y) * up);
     }
     if (lane == 0) {
       const bool live = first + r < rows;
@@ -354,17 +357,18 @@ __device__ __forceinline__ void prepare_rows(const Fp8AttendArgs& a, const Walk<
   __syncwarp();
 }
 
-template <int RT>
-__global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_kernel(Fp8AttendArgs a) {
-  using P = Shape<RT>;
+template <int RT, int QP>
+__global__ void __launch_bounds__(Shape<RT, QP>::kThreads, kCtasPerSm) fp8_attend_kernel(Fp8AttendArgs a) {
+  using P = Shape<RT, QP>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Shared<RT> sh;
-  static_assert(offsetof(Shared<RT>, top) % 16 == 0 && offsetof(Shared<RT>, factor) % 16 == 0 && alignof(Shared<RT>) >= 16, "16-byte stores");
+  __shared__ Shared<RT, QP> sh;
+  using Sh = Shared<RT, QP>;
+  static_assert(offsetof(Sh, top) % 16 == 0 && offsetof(Sh, factor) % 16 == 0 && alignof(Sh) >= 16, "16-byte stores");
   uint8_t* const smem = smem_raw + ((128u - (ptx::smem_u32(smem_raw) & 127u)) & 127u);
   uint8_t* const query_s = smem + P::kSlots * kSlotBytes;
   uint8_t* const weight_s = query_s + 2 * P::kQueryBytes;
   const Fp8Cache& c = a.c;
-  Barriers<RT>& bar = sh.bar;
+  Barriers<RT, QP>& bar = sh.bar;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* const abort = &sh.abort;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -392,7 +396,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
   for (int i = tid; i < 3 * RT; i += P::kThreads) (&sh.poison[0][0])[i] = 0;
   ptx::tc_fence_before();
   asm volatile("griddepcontrol.wait;" ::: "memory");        // (for the plan, where there is one)
-  find_run<RT>(a, &sh.start, sh.warp_s);
+  find_run<RT, P::kThreads / 32>(a, &sh.start, sh.warp_s);
   ptx::tc_fence_after();
   const long long total = sh.start.total, per = (total + gridDim.x - 1) / gridDim.x;
   Walk<RT> walk;
@@ -407,7 +411,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
     // ---------------- softmax and output ----------------
     const int quarter = warp & 3, split = warp >> 2, token = 32 * quarter + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
-    const uint32_t my_scores = scores_t + lanes + 4 * kRowsPerThread * split;
+    const uint32_t my_scores = scores_t + lanes + QP * kRowsPerThread * split;
     const uint32_t my_outputs = outputs_t + lanes + 3 * kRowsPerThread * split;
     const uint32_t my_weights =
         ptx::smem_u32(weight_s) + (token >> 4) * P::kWeightStride + 3 * kRowsPerThread * split * 16 + (token & 15);
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
     int jt = 0, met = 0;                          // key tiles so far, and those that this split's warps met over
     int slot = 1, slot_phase = 0;                 // of the value tile
     auto prepare = [&](const Walk<RT>& w, int seg) {          // a segment's queries
-      prepare_rows<RT / P::kSoftWarps, RT>(a, w, warp, P::kSoftWarps, query_s + (seg & 1) * P::kQueryBytes, sh.factor[seg & 1],
+      prepare_rows<RT / P::kSoftWarps, RT, QP>(a, w, warp, P::kSoftWarps, query_s + (seg & 1) * P::kQueryBytes, sh.factor[seg & 1],
                                            sh.seen[seg & 1]);
       if (lane == 0) ptx::mbar_arrive(&bar.q_full[seg & 1]);
     };
@@ -456,7 +460,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
         if (!TQ_WARP_WAIT(bar.o_full[j & 1], (j >> 1) & 1)) return false;
         ptx::tc_fence_after();
         uint32_t d[24];
-        tmem_ld24(my_outputs, d);
+        tmem_load(my_outputs, d);
         ptx::tc_fence_before();
         if (sh.info[j & (kMetaRing - 1)].groups == 0) return true;   // (nothing was multiplied)
 #pragma unroll
@@ -470,8 +474,8 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
         ok = TQ_WARP_WAIT(bar.s_full[jt & 1], (jt >> 1) & 1);
         if (!ok) break;
         ptx::tc_fence_after();
-        uint32_t s[32];
-        ptx::tmem_ld32(my_scores + (jt & 1) * P::kQueryCols, s);
+        uint32_t s[QP * kRowsPerThread];
+        tmem_load(my_scores + (jt & 1) * P::kQueryCols, s);
         ok = TQ_WARP_WAIT(bar.full[slot], slot_phase);
         if (!ok) break;
         const TileInfo& info = sh.info[jt & (kMetaRing - 1)];
@@ -486,8 +490,9 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
         const float factor[kRowsPerThread] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
         for (int r = 0; r < kRowsPerThread; ++r) {
-          const float d = fmaf(fmaf(fmaf(__uint_as_float(s[4 * r + 3]), 0.0625f, __uint_as_float(s[4 * r + 2])), 0.0625f,
-                                    __uint_as_float(s[4 * r + 1])), 0.0625f, __uint_as_float(s[4 * r]));
+          float d = __uint_as_float(s[QP * r + QP - 1]);
+#pragma unroll
+          for (int p = QP - 2; p >= 0; --p) d = fmaf(d, 1.f / P::kPiece, __uint_as_float(s[QP * r + p]));
           // (with the value's scale: what the weight is of the block's codes)
           x[r] = fmaf(d * ks, factor[r], up);
         }
@@ -722,7 +727,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, kCtasPerSm) fp8_attend_ke
     CutItem cut{0, 0, 0, 0, 0};
     auto begin = [&]() {                          // of an item
       // (the queries come from far memory, and a segment begins with them)
-      const int rows = min(RT, walk.s.n * a.group - walk.rt * RT), lines = a.q_bf16 ? 2 : 4;   // of 128 bytes
+      const int rows = min(RT, walk.s.n * a.group - walk.rt * RT), lines = QP == 2 ? 2 : 4;   // of 128 bytes
       for (int k = lane; k < rows * lines; k += 32) {
         const long long vec = row_vector(a, walk.s.row0, walk.kvh, walk.rt * RT + k / lines);
         asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.q) + (vec * lines + k % lines) * 128));
@@ -856,7 +861,7 @@ constexpr size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Rows of a row tile: 16 where the average sequence of the call has more than
 // eight.  (16 sequences on 8192 tokens, 64/8 heads, 8 rows each: 52 us with
-// eight a tile, 59 with 16; 16 rows: 91 and 62; 32 rows: 165 and 118.  With 32
+// eight a tile, 59 with 16; 16 rows: 91 and 58; 32 rows: 165 and 109.  With 32
 // rows a tile and one CTA an SM 16 rows take 87 us and 32 rows 109; with four
 // warps that turn the tiles into fp16 operands, which need no pieces, 105 and
 // 135: then one chain of waits, exponentials and stores is all an SM has to do.)
@@ -866,7 +871,7 @@ int tile_rows(int n_tokens, int batch, int group) {
 
 // Rows from which a sequence takes the wide form (extend_wide.cu over tiles
 // that fp8_wide.cu expands).  (Wide | few, us: 16 sequences on 8192 tokens, 64/8
-// heads, 64 rows 381 | 206, 128 rows 385 | 387, 256 rows 396 | 800; one on 32000,
+// heads, 64 rows 381 | 190, 128 rows 385 | 351 (387 in float32), 256 rows 396 | 800; one on 32000,
 // 128 rows 130 | 100; 8 on 2000, 32/8 heads, 128 rows 82 | 78.)
 constexpr int kWideFrom = 144;
 // Whether a call has the wide form's launches: only if one sequence can have
@@ -895,14 +900,14 @@ cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem,
 }
 
 // `planned`: launches of the same call come before.
-template <int RT>
+template <int RT, int QP>
 cudaError_t attend(const Fp8AttendArgs& a, bool planned, cudaStream_t stream) {
-  using P = Shape<RT>;
-  const cudaError_t err = cudaFuncSetAttribute(fp8_attend_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  using P = Shape<RT, QP>;
+  const cudaError_t err = cudaFuncSetAttribute(fp8_attend_kernel<RT, QP>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (err != cudaSuccess) return err;
   const int ctas = kCtasPerSm * a.num_sms;
-  if (planned) return launch_dependent(fp8_attend_kernel<RT>, dim3(ctas), P::kThreads, P::kSmem, stream, a);
-  fp8_attend_kernel<RT><<<ctas, P::kThreads, P::kSmem, stream>>>(a);
+  if (planned) return launch_dependent(fp8_attend_kernel<RT, QP>, dim3(ctas), P::kThreads, P::kSmem, stream, a);
+  fp8_attend_kernel<RT, QP><<<ctas, P::kThreads, P::kSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -934,7 +939,10 @@ cudaError_t launch_fp8_attention(const Fp8AttendArgs& args, void* workspace, cud
   a.cuts = reinterpret_cast<CutItem*>(ws);
   a.part = reinterpret_cast<float*>(ws + l.part);
   const int rt = tile_rows(c.n_tokens, c.batch, a.group);
-  auto few = [&](bool planned) { return rt == 8 ? attend<8>(a, planned, stream) : attend<16>(a, planned, stream); };
+  auto few = [&](bool planned) { 
+    if (a.q_bf16) return rt == 8 ? attend<8, 2>(a, planned, stream) : attend<16, 2>(a, planned, stream);
+    return rt == 8 ? attend<8, 4>(a, planned, stream) : attend<16, 4>(a, planned, stream);
+  };
   auto join = [&]() {
     return launch_dependent(fp8_join_kernel, dim3(kCtasPerSm * a.num_sms, rt / kJoinRows), 32 * kJoinWarps * kJoinRows, 0, stream, a,
                             rt);
