@@ -241,6 +241,10 @@ __device__ __forceinline__ __half2 halves_of_fp8_pair(uint16_t p) {
 __device__ __forceinline__ void store_byte(uint32_t saddr, uint16_t b) {
   asm volatile("st.shared.b8 [%0], %1;" ::"r"(saddr), "h"(b) : "memory");
 }
+// All but the bytes whose bits are set (four of them).
+__device__ __forceinline__ uint32_t bytes_without(uint32_t bits) {
+  return ~(((bits & 1u) | (bits & 2u) << 7 | (bits & 4u) << 14 | (bits & 8u) << 21) * 255u);
+}
 // The warp's largest (NaN does not count).
 __device__ __forceinline__ float warp_max(float x) {
   float y;
@@ -285,8 +289,8 @@ struct Shared {
   __align__(16) float factor[2][RT];           // scale log2(e) over the query's piece scale
   int seen[2][RT];               // positions a row sees
   float4 top[2][Shape<RT, QP>::kSplit][4][2];   // largest scores of a tile, by warp: eight rows
-  float sum[2][Shape<RT, QP>::kSoftWarps][kRowsPerThread];
-  uint32_t poison[3][RT];        // rows that see a value that is NaN
+  __align__(16) float sum[2][Shape<RT, QP>::kSoftWarps][kRowsPerThread];
+  __align__(16) uint32_t poison[3][RT];        // rows that see a value that is NaN
   long long warp_s[Shape<RT, QP>::kThreads / 32];
   RunStart start;
   uint32_t tmem;
@@ -363,7 +367,8 @@ __global__ void __launch_bounds__(Shape<RT, QP>::kThreads, kCtasPerSm) fp8_atten
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared<RT, QP> sh;
   using Sh = Shared<RT, QP>;
-  static_assert(offsetof(Sh, top) % 16 == 0 && offsetof(Sh, factor) % 16 == 0 && alignof(Sh) >= 16, "16-byte stores");
+  static_assert(offsetof(Sh, top) % 16 == 0 && offsetof(Sh, factor) % 16 == 0 && offsetof(Sh, sum) % 16 == 0 &&
+                    offsetof(Sh, poison) % 16 == 0 && alignof(Sh) >= 16, "16-byte stores");
   uint8_t* const smem = smem_raw + ((128u - (ptx::smem_u32(smem_raw) & 127u)) & 127u);
   uint8_t* const query_s = smem + P::kSlots * kSlotBytes;
   uint8_t* const weight_s = query_s + 2 * P::kQueryBytes;
@@ -556,14 +561,22 @@ __global__ void __launch_bounds__(Shape<RT, QP>::kThreads, kCtasPerSm) fp8_atten
         if (split == 0 && here) {
           // values that no weight may meet: slots behind the context, whatever
           // they hold, and vectors that are NaN (whose rows are marked)
-          uint8_t* const value = smem + slot * kSlotBytes + (token >> 4) * 2048 + (token & 15);
-          const bool nan = (value[0] & 0x7fu) == 0x7fu;
-          if (pos >= ctx || nan) {
-            if (pos < ctx)
+          uint8_t* const value = smem + slot * kSlotBytes + quarter * kGroupBytes;
+          const bool nan = (value[(lane >> 4) * 2048 + (lane & 15)] & 0x7fu) == 0x7fu;
+          const uint32_t gone = __ballot_sync(0xffffffffu, pos >= ctx || nan);
+          if (gone != 0) {
+            if (pos < ctx && nan)
               for (int r = 0; r < RT; ++r)
                 if (pos < sh.seen[seg & 1][r]) sh.poison[seg % 3][r] = 1;
 #pragma unroll 4
-            for (int d = 0; d < kDim; ++d) value[d * 16] = 0;
+            for (int i = lane; i < 2 * kDim; i += 32) {       // sixteen tokens of a coordinate
+              const uint32_t tokens = gone >> (i >= kDim ? 16 : 0);
+              uint4* const p = reinterpret_cast<uint4*>(value + i * 16);
+              uint4 u = *p;
+              u.x &= bytes_without(tokens), u.y &= bytes_without(tokens >> 4);
+              u.z &= bytes_without(tokens >> 8), u.w &= bytes_without(tokens >> 12);
+              *p = u;
+            }
           }
         }
         ptx::fence_async_shared();
@@ -598,30 +611,30 @@ __global__ void __launch_bounds__(Shape<RT, QP>::kThreads, kCtasPerSm) fp8_atten
       // (a run's first item may have begun in the run before, its last may go on)
       const bool whole = tile0 == 0 && reached == tiles;
       float* const part = a.part + (2ll * blockIdx.x + (tile0 == 0 ? 1 : 0)) * part_floats(RT);
-      // vector (token x query head) of my first row; the next row's is one on, or
-      // the next token's first of the group
-      const int tok = first / a.group;
-      int head = first - tok * a.group;
-      long long vec = (static_cast<long long>(row0) + tok) * a.n_q + kvh * a.group + head;
+      // a lane has a row's sum and vector (token x query head), and gives them to all
+      const int mine = lane & (kRowsPerThread - 1);
+      float all = 0.f;
 #pragma unroll
-      for (int r = 0; r < kRowsPerThread; ++r) {
-        const int row = split * kRowsPerThread + r;
-        if (first + r >= n * a.group) break;
-        float all = 0.f;
+      for (int w = 0; w < 4; ++w) all += sh.sum[seg & 1][4 * split + w][mine];
+      if (sh.poison[seg % 3][split * kRowsPerThread + mine] != 0) all = __int_as_float(0x7fc00000);
+      const int live = min(kRowsPerThread, n * a.group - first);
+      if (whole) {
+        const float inv = all == 0.f ? 0.f : __fdividef(1.f, kWeightScale * all);
+        const int vec = static_cast<int>(row_vector(a, row0, kvh, first + mine));   // (n_tokens x n_q is an int)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) all += sh.sum[seg & 1][4 * split + w][r];
-        if (sh.poison[seg % 3][row] != 0) all = __int_as_float(0x7fc00000);
-        if (whole) {
-          static_cast<__nv_bfloat16*>(a.out)[vec * kDim + token] =
-              __float2bfloat16_rn(all == 0.f ? 0.f : __fdividef(acc[r], kWeightScale * all));
-          vec += ++head == a.group ? a.n_q - a.group + 1 : 1;
-          if (head == a.group) head = 0;
-        } else {
-          part[row * kDim + token] = acc[r];
-          if (token == 0) {
-            part[RT * kDim + 2 * row] = ref[r];
-            part[RT * kDim + 2 * row + 1] = all;
-          }
+        for (int r = 0; r < kRowsPerThread; ++r) {
+          const float by = __shfl_sync(0xffffffffu, inv, r);
+          const int to = __shfl_sync(0xffffffffu, vec, r);
+          if (r < live) static_cast<__nv_bfloat16*>(a.out)[static_cast<long long>(to) * kDim + token] = __float2bfloat16_rn(acc[r] * by);
+        }
+      } else {
+        float* const rows = part + split * kRowsPerThread * kDim + token;
+        float2* const stats = reinterpret_cast<float2*>(part + RT * kDim) + split * kRowsPerThread;
+#pragma unroll
+        for (int r = 0; r < kRowsPerThread; ++r) {
+          const float total = __shfl_sync(0xffffffffu, all, r);
+          if (r < live) rows[r * kDim] = acc[r];
+          if (r < live && token == 0) stats[r] = make_float2(ref[r], total);
         }
       }
     }
