@@ -23,10 +23,10 @@
 // SM 1490 cycles at the copy rate; one chain of softmax on a tile (four warps:
 // scores, a meeting over the tile's maximum, weights, the product before) takes
 // 2400, so two CTAs an SM work side by side.  Measured: 64 sequences of 1 to 32 K
-// tokens, 64/8 heads, 340 us (6.9 TB/s); 16 of 8192, 32/8 heads, 49 us, and one of
+// tokens, 64/8 heads, 342 us (6.8 TB/s); 16 of 8192, 32/8 heads, 49 us, and one of
 // 131072, 64/8, 49 us (5.4 TB/s): 2.5 us until the first copies, 3 us in which
 // some CTAs are done and others not, 4 us for the join.  Sixteen rows a tile are
-// issue bound: 58.5 us for 16 sequences of 8192 with 16 rows.
+// issue bound: 57 us for 16 sequences of 8192 with 16 rows.
 //
 // Work is split as in extend.cu: an item is a row tile of a sequence and KV
 // head, worth kItemCost units and one per key tile; every CTA takes an equal
