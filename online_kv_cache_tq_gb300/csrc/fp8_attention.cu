@@ -34,6 +34,7 @@
 // Every CTA forms the sums over the batch itself, which costs less than a
 // launch before it.  (An item cost of 1, 2, 3: the 64 sequences 353, 346, 345 us,
 // 32 short ones of 16 rows 18.8, 18.9, 22.3 us.)
+#include <algorithm>
 #include <cstddef>
 
 #include "fp8_common.cuh"
@@ -801,11 +802,15 @@ __global__ void __launch_bounds__(Shape<RT, QP>::kThreads, kCtasPerSm) fp8_atten
 }
 
 // Joins the partial outputs of a row tile: sum_s 2^{m_s - M} o_s over
-// sum_s 2^{m_s - M} l_s.  Block (x, y) joins kJoinRows rows of the item that
-// run x begins and does not end; four warps a row take every fourth part, four
-// coordinates a lane.
-constexpr int kJoinWarps = 4, kJoinRows = 1;
-__global__ void __launch_bounds__(32 * kJoinWarps * kJoinRows, 8) fp8_join_kernel(Fp8AttendArgs a, int rt_rows) {
+// sum_s 2^{m_s - M} l_s.  Block (x, y) joins four rows, or one, of the item that
+// run x begins and does not end: a warp a row, or four of which each takes every
+// fourth part; four coordinates a lane.  (One warp, four warps: eight items of 38
+// parts 51.3, 49.1 us; 24 sequences of drafted tokens, up to four parts each, 100.5,
+// 103; one short context 7.8, 8.2.)
+constexpr int kJoinThreads = 128, kJoinAtOnce = 8;   // parts that a warp reads at a time
+template <int kJoinWarps>
+__global__ void __launch_bounds__(kJoinThreads, 8) fp8_join_kernel(Fp8AttendArgs a, int rt_rows) {
+  constexpr int kJoinRows = kJoinThreads / 32 / kJoinWarps;
   __shared__ float4 acc_s[kJoinRows][kJoinWarps][32];
   __shared__ float sum_s[kJoinRows][kJoinWarps], top_s[kJoinRows][kJoinWarps];
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % kJoinWarps, mine = (threadIdx.x >> 5) / kJoinWarps;
@@ -820,11 +825,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps * kJoinRows, 8) fp8_join_kerne
   // one pass: eight parts' reads at once, the reference raised as they come
   float top = kNothing, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = c0 + warp; live && s0 <= cut.last; s0 += 8 * kJoinWarps) {
-    float2 ml[8];
-    float4 o[8];
+  for (int s0 = c0 + warp; live && s0 <= cut.last; s0 += kJoinAtOnce * kJoinWarps) {
+    float2 ml[kJoinAtOnce];
+    float4 o[kJoinAtOnce];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kJoinAtOnce; ++k) {
       const int s = s0 + k * kJoinWarps;
       ml[k] = make_float2(kNothing, 0.f);
       o[k] = acc;
@@ -835,12 +840,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps * kJoinRows, 8) fp8_join_kerne
     }
     float to = top;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) to = fmaxf(to, ml[k].x);
+    for (int k = 0; k < kJoinAtOnce; ++k) to = fmaxf(to, ml[k].x);
     const float keep = exp2_fast(top - to);
     acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep, sum *= keep;
     top = to;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kJoinAtOnce; ++k) {
       if (ml[k].y == 0.f) continue;               // (a part that saw nothing)
       const float w = exp2_fast(ml[k].x - top);
       acc.x = fmaf(w, o[k].x, acc.x), acc.y = fmaf(w, o[k].y, acc.y), acc.z = fmaf(w, o[k].z, acc.z);
@@ -957,8 +962,11 @@ cudaError_t launch_fp8_attention(const Fp8AttendArgs& args, void* workspace, cud
     return rt == 8 ? attend<8, 4>(a, planned, stream) : attend<16, 4>(a, planned, stream);
   };
   auto join = [&]() {
-    return launch_dependent(fp8_join_kernel, dim3(kCtasPerSm * a.num_sms, rt / kJoinRows), 32 * kJoinWarps * kJoinRows, 0, stream, a,
-                            rt);
+    // parts of an item: as many as it has CTAs on average, or key tiles
+    const long long ctas = kCtasPerSm * a.num_sms, items = static_cast<long long>(c.batch) * c.n_kv;
+    const bool one = std::min(ctas / items, static_cast<long long>(a.max_context / kTile)) < kJoinAtOnce;
+    return one ? launch_dependent(fp8_join_kernel<1>, dim3(ctas, rt / 4), kJoinThreads, 0, stream, a, rt)
+               : launch_dependent(fp8_join_kernel<4>, dim3(ctas, rt), kJoinThreads, 0, stream, a, rt);
   };
   cudaError_t err = cudaSuccess;
   if (l.total > l.wide) {
