@@ -23,10 +23,10 @@
 // SM 1490 cycles at the copy rate; one chain of softmax on a tile (four warps:
 // scores, a meeting over the tile's maximum, weights, the product before) takes
 // 2400, so two CTAs an SM work side by side.  Measured: 64 sequences of 1 to 32 K
-// tokens, 64/8 heads, 342 us (6.8 TB/s); 16 of 8192, 32/8 heads, 49 us, and one of
-// 131072, 64/8, 49 us (5.4 TB/s): 2.5 us until the first copies, 3 us in which
-// some CTAs are done and others not, 4 us for the join.  Sixteen rows a tile are
-// issue bound: 57 us for 16 sequences of 8192 with 16 rows.
+// tokens, 64/8 heads, 341 us (6.9 TB/s); 16 of 8192, 32/8 heads, 48.4 us, and one of
+// 131072, 64/8, 48.6 us (5.5 TB/s): 2.5 us until the first copies, 3 us in which
+// some CTAs are done and others not, 3 us for the join.  Sixteen rows a tile are
+// issue bound: 53 us for 16 sequences of 8192 with 16 rows.
 //
 // Work is split as in extend.cu: an item is a row tile of a sequence and KV
 // head, worth kItemCost units and one per key tile; every CTA takes an equal
@@ -806,8 +806,9 @@ __global__ void __launch_bounds__(Shape<RT, QP>::kThreads, kCtasPerSm) fp8_atten
 // run x begins and does not end: a warp a row, or four of which each takes every
 // fourth part; four coordinates a lane.  (One warp, four warps: eight items of 38
 // parts 51.3, 49.1 us; 24 sequences of drafted tokens, up to four parts each, 100.5,
-// 103; one short context 7.8, 8.2.)
-constexpr int kJoinThreads = 128, kJoinAtOnce = 8;   // parts that a warp reads at a time
+// 103; one short context 7.8, 8.2.  Eight parts at once, which spill, in place of
+// four: 49.0 us for 48.4, 99.8 for 99.0.)
+constexpr int kJoinThreads = 128, kJoinAtOnce = 4;   // parts that a warp reads at a time
 template <int kJoinWarps>
 __global__ void __launch_bounds__(kJoinThreads, 8) fp8_join_kernel(Fp8AttendArgs a, int rt_rows) {
   constexpr int kJoinRows = kJoinThreads / 32 / kJoinWarps;
@@ -822,7 +823,7 @@ __global__ void __launch_bounds__(kJoinThreads, 8) fp8_join_kernel(Fp8AttendArgs
   // (the run that holds key tile 0 wrote its second slot, the others their first)
   auto part = [&](int s) { return a.part + (2ll * s + (s == c0 ? 1 : 0)) * part_floats(rt_rows); };
   const int stats = rt_rows * kDim + 2 * row;
-  // one pass: eight parts' reads at once, the reference raised as they come
+  // one pass: four parts' reads at once, the reference raised as they come
   float top = kNothing, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = c0 + warp; live && s0 <= cut.last; s0 += kJoinAtOnce * kJoinWarps) {
@@ -889,7 +890,7 @@ int tile_rows(int n_tokens, int batch, int group) {
 
 // Rows from which a sequence takes the wide form (extend_wide.cu over tiles
 // that fp8_wide.cu expands).  (Wide | few, us: 16 sequences on 8192 tokens, 64/8
-// heads, 64 rows 381 | 190, 128 rows 385 | 351 (387 in float32), 256 rows 396 | 800; one on 32000,
+// heads, 64 rows 381 | 184, 128 rows 385 | 344 (380 in float32), 256 rows 396 | 800; one on 32000,
 // 128 rows 130 | 100; 8 on 2000, 32/8 heads, 128 rows 82 | 78.)
 constexpr int kWideFrom = 144;
 // Whether a call has the wide form's launches: only if one sequence can have
@@ -964,7 +965,7 @@ cudaError_t launch_fp8_attention(const Fp8AttendArgs& args, void* workspace, cud
   auto join = [&]() {
     // parts of an item: as many as it has CTAs on average, or key tiles
     const long long ctas = kCtasPerSm * a.num_sms, items = static_cast<long long>(c.batch) * c.n_kv;
-    const bool one = std::min(ctas / items, static_cast<long long>(a.max_context / kTile)) < kJoinAtOnce;
+    const bool one = std::min(ctas / items, static_cast<long long>(a.max_context / kTile)) < 2 * kJoinAtOnce;
     return one ? launch_dependent(fp8_join_kernel<1>, dim3(ctas, rt / 4), kJoinThreads, 0, stream, a, rt)
                : launch_dependent(fp8_join_kernel<4>, dim3(ctas, rt), kJoinThreads, 0, stream, a, rt);
   };
