@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(ExtendArgs a) {
           const float top = mask ? masked_top(s_addr, kf, factor, valid_s[rg], here, half) : plain_top(s_addr, kf);
           ok = swap(top, &other);
           if (!ok) break;
-          const float to = raised(ref, fmaxf(top, other));
+          const float to = raised(ref, fmaxf(top, other), kRaise);
           if (__any_sync(0xffffffffu, to != ref)) {
             const float scale = to != ref ? exp2_fast(ref - to) : 1.f;
             if (t > t0) {
