@@ -116,11 +116,16 @@ __device__ __forceinline__ void append_short(const Fp8Run& r, const void* rows, 
       x[i][0] = u.x, x[i][1] = u.y, x[i][2] = u.z, x[i][3] = u.w;
     }
   }
+  uint32_t nans = 0;                              // tokens with a NaN, by bit: they do not count
 #pragma unroll
   for (int i = 0; i < kShortRun; ++i)
     if (i < r.len) {
+      // (a sum of magnitudes is NaN only if one of them is)
+      const float all = (fabsf(x[i][0]) + fabsf(x[i][1])) + (fabsf(x[i][2]) + fabsf(x[i][3]));
+      const bool nan = __any_sync(0xffffffffu, all != all);
+      nans |= nan ? 1u << i : 0u;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fabsf(x[i][j]));   // (a NaN is no magnitude)
+      for (int j = 0; j < 4; ++j) amax = nan ? amax : fmaxf(amax, fabsf(x[i][j]));
     }
   amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
   int grown;
@@ -134,8 +139,7 @@ __device__ __forceinline__ void append_short(const Fp8Run& r, const void* rows, 
 #pragma unroll
   for (int i = 0; i < kShortRun; ++i) {
     if (i >= r.len) break;
-    const bool nan = __any_sync(0xffffffffu, x[i][0] != x[i][0] || x[i][1] != x[i][1] || x[i][2] != x[i][2] || x[i][3] != x[i][3]);
-    const uint32_t w = nan ? kFp8NaN4 : fp8_four_scaled(x[i][0], x[i][1], x[i][2], x[i][3], down);
+    const uint32_t w = nans >> i & 1u ? kFp8NaN4 : fp8_four_scaled(x[i][0], x[i][1], x[i][2], x[i][3], down);
     const int token = r.off + i;
     if (!values) {
       *reinterpret_cast<uint32_t*>(block + key_byte(token, 4 * lane)) = w;
@@ -174,7 +178,8 @@ struct Step {
 };
 
 // The largest magnitude among rows [lo, hi) of a stage over a thread's share of
-// them, as bits; a NaN does not count, but sets *nan.
+// them, as bits; vectors with a NaN do not count, but set *nan.  By whole warps:
+// one has a row, or two side by side (bf16).
 template <bool BF16>
 __device__ __forceinline__ uint32_t largest_bits(const uint8_t* stage, int lo, int hi, bool* nan) {
   using S = Stage<BF16>;
@@ -201,17 +206,27 @@ __device__ __forceinline__ uint32_t largest_bits(const uint8_t* stage, int lo, i
     }
   }
   if (BF16) top = max(top << 16, top & 0xffff0000u);
-  if (BF16 ? top <= 0x7f800000u : odd == odd) return top;
-  float most = 0.f;                               // once more, without them
+  if (!__any_sync(0xffffffffu, BF16 ? top > 0x7f800000u : odd != odd)) return top;
+  float most = 0.f;                               // once more, row by row
   const uint8_t* p = mine;
+  const int first = lo + threadIdx.x / 32 * (32 / S::kPieces);   // (the same for the warp)
+  const uint32_t neighbours = (S::kPieces == 32 ? 0xffffffffu : 0xffffu) << (threadIdx.x & 31 & ~(S::kPieces - 1));
 #pragma unroll 1
-  for (int r = row; r < hi; r += S::kRows, p += S::kRows * S::kPitch)
+  for (int r = first; r < hi; r += S::kRows, p += S::kRows * S::kPitch) {
+    float own = 0.f;
+    bool bad = false;
+    if (r + row - first < hi) {
 #pragma unroll 1
-    for (int j = 0; j < (BF16 ? 8 : 4); ++j) {
-      const float x = BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[j]) : reinterpret_cast<const float*>(p)[j];
-      *nan = *nan || x != x;
-      most = fmaxf(most, fabsf(x));
+      for (int j = 0; j < (BF16 ? 8 : 4); ++j) {
+        const float x = BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[j]) : reinterpret_cast<const float*>(p)[j];
+        bad = bad || x != x;
+        own = fmaxf(own, fabsf(x));
+      }
     }
+    bad = (__ballot_sync(0xffffffffu, bad) & neighbours) != 0;
+    *nan = *nan || bad;
+    if (!bad) most = fmaxf(most, own);
+  }
   return __float_as_uint(most);
 }
 

@@ -467,3 +467,31 @@ def test_blocks_beyond_four_gigabytes():
     for name in big:
         assert torch.equal(big[name][far_t], small.cache[name][near_t]), name
     assert torch.equal(out, small.read())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bs,new,past", [(64, [3], [50]), (64, [40], [10]), (64, [60], [0]), (96, [90], [3]), (128, [100], [28]),
+                                         (256, [200], [40]), (256, [256], [0])])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_vector_with_a_nan_leaves_its_block_alone(bs, new, past, dtype):
+    # its other coordinates, however large, do not count for the scale: the other tokens, earlier ones among them, are stored
+    # as if it were a vector of zeros
+    spoilt = [(1, 0, 5, 1e4), (new[0] - 1, 1, 127, float("inf")), (new[0] // 2, 0, 64, -1e4)]
+    first = Case(new, past, bs=bs, dtype=dtype, seed=20)
+    for t, head, at, _ in spoilt:
+        first.kv[t, :, head] = 0.0
+    model = first.check_append()
+    for values in (1, 8, 128):                            # huge coordinates: beside the NaN, in its eighth, all
+        c = Case(new, past, bs=bs, dtype=dtype, seed=20)
+        for t, head, at, huge in spoilt:
+            lo = at // values * values
+            c.kv[t, :, head, lo:lo + values] = huge
+            c.kv[t, 0, head, (at + 1) % 128] = c.kv[t, 1, head, at] = float("nan")
+            c.kv[t, 0, head, at] = huge
+        c.append()
+        assert B.tq_get_last_device_error(c.book) == 0
+        for t, head, _, _ in spoilt:
+            pos = past[0] + t
+            for name in "kv":
+                model.codes[name][c.table[0, pos // bs], head, pos % bs] = 127
+        model.check(c.cache)
