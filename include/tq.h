@@ -526,8 +526,8 @@ typedef struct {
  * stands once in the tables of its sequences.  The same call on the same cache
  * gives the same bits.  Device errors: 2 a block id out of range (its tokens are
  * skipped), 3 a query_start or context out of range, or more rows than context
- * (the sequence is skipped; where query_start goes down so that rows overlap,
- * the whole call).  Asynchronous on `stream`. */
+ * (the sequence is skipped; where query_start goes down anywhere, the whole
+ * call).  Asynchronous on `stream`. */
 tq_status tq_fp8_append(const tq_codebook* book, const void* k, const void* v, tq_dtype dtype, int n_tokens, int batch,
                         int n_kv_heads, int64_t k_stride, int64_t v_stride, const tq_fp8_view* cache,
                         const int32_t* block_table, int max_blocks, const int32_t* query_start,

@@ -86,17 +86,19 @@ struct Fp8Runs {
   static __device__ __forceinline__ int count(const Fp8Cache& c, const int3& s) {
     return s.y == 0 ? 0 : ((s.z - s.y) % c.block_size + s.y - 1) / c.block_size + 1;
   }
-  // By the whole CTA.  Rows that overlap (query_start goes down) are recorded, and
-  // then there are no runs.
+  // By the whole CTA.  Where query_start goes down anywhere (rows could overlap),
+  // that is recorded and there are no runs.
   __device__ __forceinline__ void find(const Fp8Cache& c, long long (*warp_s)[2]) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, per = (c.batch + THREADS - 1) / THREADS;
     int top = 0;
+    bool down = false;
     long long runs = 0, rows = 0;
     if (tid == 0) most = 0;
     for (int i = 0; i < per; ++i) {
       const int b = tid * per + i;
       if (b >= c.batch) break;
       const int3 s = fp8_sequence(c, b, blockIdx.x == 0);
+      down = down || c.query_start[b + 1] < c.query_start[b];
       if (i == 0) seq[tid] = s;
       runs += count(c, s);
       rows += s.y;
@@ -111,15 +113,13 @@ struct Fp8Runs {
       rows += __shfl_xor_sync(0xffffffffu, rows, d);
     }
     if (lane == 31) warp_s[warp][0] = upto, warp_s[warp][1] = rows;
-    __syncthreads();
+    const bool ok = !__syncthreads_or(down);      // (then rows are at most n_tokens, and a run has one: the sums below are ints)
     long long before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
       if (w < warp) before += warp_s[w][0];
       all += warp_s[w][1];
     }
-    const bool ok = all <= c.n_tokens;            // (a run has a row at least: the sums below are ints)
-    if (!ok && tid == 0 && blockIdx.x == 0) atomicCAS(c.error, 0, kErrContext);
     first[tid + 1] = ok ? static_cast<int>(before + upto) : 0;
     if (lane == 0) atomicMax(&most, top);
     if (tid == 0) {

@@ -495,3 +495,16 @@ def test_a_vector_with_a_nan_leaves_its_block_alone(bs, new, past, dtype):
             for name in "kv":
                 model.codes[name][c.table[0, pos // bs], head, pos % bs] = 127
         model.check(c.cache)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("start", [[0, 20, 10, 30], [0, 20, 20, 19], [5, 3, 20, 30], [0, 60, 59, 59], [0, 10, -1, 30]])
+@pytest.mark.parametrize("batch", [3, 400])
+def test_an_append_whose_query_start_goes_down_writes_nothing(start, batch):
+    # rows to spare: the sum of the sequences' rows is no more than there are
+    c = Case([20, 0, 20] + [0] * (batch - 3), [100] * batch, seed=21, pad=24)
+    before = {k: v.clone() for k, v in c.cache.items()}
+    c.start.copy_(ints(start + [start[-1]] * (batch - 3)))
+    c.append()
+    assert B.tq_get_last_device_error(c.book) == 3
+    assert all(torch.equal(before[k], c.cache[k]) for k in before)
