@@ -537,8 +537,9 @@ tq_status tq_fp8_append(const tq_codebook* book, const void* k, const void* v, t
  * sequence's context (any range: context_lens need not be the sequence's whole
  * length): code * scale, exact in `dtype`, to k_out and v_out, device rows laid
  * out as the append's k and v (either may be NULL).  Rows behind
- * query_start[batch] and rows with a device error (as the append's) are left as
- * they were.  No output may overlap the cache.  Asynchronous on `stream`. */
+ * query_start[batch] and rows with a device error (as the append's, the whole
+ * call's where query_start goes down) are left as they were.  No output may
+ * overlap the cache.  Asynchronous on `stream`. */
 tq_status tq_fp8_read(const tq_codebook* book, const tq_fp8_view* cache, const int32_t* block_table, int max_blocks,
                       int n_tokens, int batch, int n_kv_heads, const int32_t* query_start, const int32_t* context_lens,
                       tq_dtype dtype, void* k_out, void* v_out, int64_t k_stride, int64_t v_stride, void* stream);

@@ -175,7 +175,8 @@ struct Fp8Finder {
 // The parts of runs that lie among tokens w0 .. w0 + window - 1 of the call, into
 // `f.runs` (at most a run per token), in no order; returns how many.  Called by
 // the whole CTA; a sequence whose rows or length are out of range, and a block
-// id outside the cache, are recorded and left out.
+// id outside the cache, are recorded and left out.  Where query_start goes down
+// anywhere, that is recorded and there are no runs.
 //
 // The sequences of the window's first and last token come from counts over
 // query_start; a token's own sequence is then searched between those two.  A
@@ -187,8 +188,10 @@ __device__ __forceinline__ int fp8_find_runs(const Fp8Cache& c, int w0, int wind
   if (tid < 3) f.count[tid] = 0;
   __syncthreads();
   int before = 0, upto = 0;
+  bool down = false;
   for (int b = tid; b < c.batch; b += blockDim.x) {
     const int s = c.query_start[b];
+    down |= c.query_start[b + 1] < s;
     before += s <= w0;
     upto += s <= w0 + window - 1;
     if (held) f.start[b] = s, f.ctx[b] = c.context_lens[b];
@@ -200,7 +203,10 @@ __device__ __forceinline__ int fp8_find_runs(const Fp8Cache& c, int w0, int wind
     atomicAdd(&f.count[0], before);
     atomicAdd(&f.count[1], upto);
   }
-  __syncthreads();
+  if (__syncthreads_or(down)) {
+    if (tid == 0) atomicCAS(c.error, 0, kErrContext);
+    return 0;
+  }
   const int t = w0 + tid;
   if (tid < window && t < c.n_tokens) {
     const int* const start = held ? f.start : c.query_start;

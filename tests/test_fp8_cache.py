@@ -508,3 +508,13 @@ def test_an_append_whose_query_start_goes_down_writes_nothing(start, batch):
     c.append()
     assert B.tq_get_last_device_error(c.book) == 3
     assert all(torch.equal(before[k], c.cache[k]) for k in before)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("start", [[0, 20, 10, 30], [0, 20, 20, 19], [5, 3, 20, 30], [0, 60, 59, 59], [0, 10, -1, 30]])
+@pytest.mark.parametrize("batch", [3, 400])
+def test_a_read_whose_query_start_goes_down_writes_nothing(start, batch):
+    c = Case([20, 0, 20] + [0] * (batch - 3), [100] * batch, seed=22, pad=24)
+    out = c.read(start=ints(start + [start[-1]] * (batch - 3)))
+    assert B.tq_get_last_device_error(c.book) == 3
+    assert bool((out == 7.0).all())
