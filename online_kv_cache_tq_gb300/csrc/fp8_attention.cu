@@ -342,7 +342,7 @@ __device__ __forceinline__ void prepare_rows(const Fp8AttendArgs& a, const Walk<
     const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
     // 2^e <= most < 2^(e+1) goes to [64, 128); tiny queries stay tiny
     const int e = max(-100, static_cast<int>(bits >> 23) - 127);
-    const float up = e > 126 ? __int_as_float(0x7fc00000) : fp8_power(6 - e);   // (infinite: the row is NaN)
+    const float up = e > 127 ? __int_as_float(0x7fc00000) : fp8_power(6 - e);   // (infinite: the row is NaN)
     float4 y = make_float4(v[i][0] * up, v[i][1] * up, v[i][2] * up, v[i][3] * up);
 #pragma unroll
     for (int p = 0; p < QP; ++p) {
