@@ -1,7 +1,6 @@
 """Attention over the 8-bit cache at the ends of its numbers: queries up to the
 largest finite one.  Tolerances as in test_fp8_attention.py.
 """
-import numpy as np
 import pytest
 import torch
 
