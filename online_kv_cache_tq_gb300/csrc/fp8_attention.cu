@@ -893,14 +893,22 @@ int tile_rows(int n_tokens, int batch, int group) {
 // heads, 64 rows 381 | 184, 128 rows 385 | 344 (380 in float32), 256 rows 396 | 800; one on 32000,
 // 128 rows 130 | 100; 8 on 2000, 32/8 heads, 128 rows 82 | 78.)
 constexpr int kWideFrom = 144;
-// Whether a call has the wide form's launches: only if one sequence can have
-// the rows (all tokens beyond one for each of the others), and if it then would
-// lose more without them than the 12 us that they take: products of tokens,
-// query heads and context, of which this form does 0.4 million in a microsecond.
-constexpr long long kWideWork = 1 << 22;
+// Whether a call has the wide form's launches: if one sequence can have the rows,
+// and if the call would lose more without them than they take, 9 us where there
+// is no such sequence.  What it can lose goes with the products of tokens, query
+// heads and context: this form does 0.3 to 0.4 million of them in a microsecond.
+// A sequence has the rows if the others have a token each; or, as sequences
+// may be empty, if it has all tokens.  A call that can have it only so is nearly
+// always a decode step, and takes the launches from where they are 1 % of one.
+// (64/8 heads, us, with the launches | without.  A sequence of 2048 tokens on 16 K
+// among 2048 854 | 7326, one of 256 on 32 K among 256 308 | 1821, one of 64 on
+// 8192 among 64 77 | 125.  Decode steps: 64 on 1 K to 32 K 321 | 312, 256 on 8192
+// 630 | 621, 128 on 700 54 | 47.)
+constexpr long long kWideWork = 1 << 22, kWideWorkIdle = 1 << 28;
 bool wide_possible(int n_tokens, int batch, int n_q, int n_kv, int max_context) {
-  const long long most = static_cast<long long>(n_tokens) - batch + 1;
-  return most * (n_q / n_kv) >= kWideFrom && most * n_q >= kWideWork / (max_context > 0 ? max_context : 1);
+  const long long context = max_context > 0 ? max_context : 1;
+  auto gains = [&](long long most, long long work) { return most * (n_q / n_kv) >= kWideFrom && most * n_q >= work / context; };
+  return gains(static_cast<long long>(n_tokens) - batch + 1, kWideWork) || gains(n_tokens, kWideWorkIdle);
 }
 
 template <typename Kernel, typename... Args>

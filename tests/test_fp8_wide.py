@@ -46,3 +46,20 @@ def test_scores_far_below_zero_beside_blocks_of_tiny_scale(near):
     c.q.fill_(2.125 if near else 3.875)
     c.run()
     c.check(tokens=300)
+
+
+def test_one_chunk_among_many_empty_sequences():
+    # a sequence has all tokens of the call, which has as many tokens as sequences: before, behind and among empty ones
+    ctx = 16384
+    for at in (0, 100, 255):
+        new, lengths = [0] * 256, [1] * 256
+        new[at], lengths[at] = 256, ctx
+        c = Case(new, lengths, group=64, seed=2)
+        c.run()
+        c.check([at], tokens=3)
+
+
+def test_decode_steps_have_no_workspace_for_it():
+    book = B.Codebook(block_size=64)
+    for batch, n_q, n_kv, ctx in ((64, 64, 8, 32768), (256, 64, 8, 8192), (1, 64, 8, 1 << 20), (128, 64, 8, 700)):
+        assert B.tq_fp8_workspace_bytes(book, batch, batch, n_q, n_kv, ctx) < WIDE_BYTES
