@@ -562,10 +562,14 @@ size_t tq_fp8_workspace_bytes(const tq_codebook* book, int n_tokens, int batch, 
  * TQ_ERR_UNSUPPORTED).  scale: 0 selects 1/sqrt(d).
  * Accuracy: a sequence with fewer than 144 rows (new tokens x n_q_heads /
  * n_kv_heads) has keys exactly, bf16 queries exactly (coordinates below 2^-12 of
- * a vector's largest to 2^-21 of it), float32 ones to 2^-16 of a coordinate and
- * weights to 2^-11; with ordinary scores the result is off by 0.0017 in the root
- * mean square, the rounding of the output.  One with more may have queries as
- * fp16 numbers, weights as bf16 (a quarter of them with the remainder): 0.0022.
+ * a vector's largest to 2^-21 of it), float32 ones to 2^-16 of a coordinate, and
+ * weights to 2^-11 of themselves or to 2^-26 of the row's largest product of
+ * weight and value scale, whichever is more (tokens below that count in the
+ * softmax sum only).  With ordinary scores the result is off by 0.0017 in the
+ * root mean square, the rounding of the output.  A sequence with more rows may
+ * have queries (float32 ones too) as fp16 numbers and weights as bf16, a quarter
+ * of them with the remainder (tokens below 2^-30 of the row's largest weight may
+ * not count): 0.0022.
  * workspace: device scratch of tq_fp8_workspace_bytes bytes (up to 5 MB, and
  * where sequences can have those rows as tq_extend_attention's), 256-byte
  * aligned, not used by any concurrent call; more tokens or a longer context of
