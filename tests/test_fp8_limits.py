@@ -8,7 +8,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_fp8_attention import Case
+import test_fp8_run
+from test_fp8_attention import Case, reference
 from test_fp8_cache import Model
 
 pytestmark = pytest.mark.gpu
@@ -52,3 +53,15 @@ def test_a_long_tail_beside_a_token_with_small_values(depth, dtype):
     held = max(2.0 ** -11, 2.0 ** -26 * p[0] / p[1]) + np.expm1(2.0 ** -14 * d)
     bound = p[1:] @ v[1:] * held + p[0] * v[0] * held + 1.01 * 2.0 ** -8 * (p @ v)
     assert (np.abs(c.out[-1].double().cpu().numpy() - p @ v) <= bound).all()
+
+
+def test_the_serving_loop_within_the_bound_of_few_rows(monkeypatch):
+    # (the loop's calls are too small for the form with the wider one)
+    monkeypatch.setattr(test_fp8_run, "reference", lambda q, k, v, n, scale, wide: reference(q, k, v, n, scale, False))
+    loop = test_fp8_run.Loop()
+    assert loop.nbytes < 16 << 20
+    model, past = Model(loop.cache), [0, 0, 0]
+    for new in ([70, 33, 0], [1, 40, 90], [1, 1, 1], [4, 0, 2], [1, 1, 1], [8, 8, 8]):
+        loop.fill(new)
+        loop.step()
+        past = loop.check(model, new, past)
