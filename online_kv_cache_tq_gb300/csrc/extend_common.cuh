@@ -21,10 +21,11 @@ constexpr int kBlockBytes = kTile * 128;          // a 64-column K block of a 12
 // factor of two, have bounds up to 2^75: 123 us; with 2^72 some tiles are
 // searched, 133 us; with a limit per tile from its largest value, 127 us.)
 constexpr float kRaise = 80.f;
-// The same for the 8-bit cache, whose weights take their value's scale (2^-40 to
-// 2^14) in the exponent before they are summed: tokens down to 2^-30 of a row's
-// largest weight stay normal numbers, 56 + 40 + 30 = 126.
-constexpr float kRaiseScaled = 56.f;
+// log2 by which a row's largest score may lie below a reference of zero for the
+// 8-bit cache, whose weights take their value's scale (2^-40 to 2^14) in the
+// exponent before they are summed: tokens down to 2^-30 of the largest weight stay
+// normal numbers, 56 + 40 + 30 = 126.  A row's first tile decides it.
+constexpr float kBelowScaled = 56.f;
 // References up to which a score may keep its product's low bits while the
 // reference, a rounded product, does not: they differ by 2^-24 of it, 1/16 here.
 // Beyond, both are rounded alike (else 2^32 could leave an exponent of 256).
@@ -597,11 +598,11 @@ __device__ __forceinline__ void load_value(const DecodeArgs& d, const Item& it, 
 
 // The row's reference after a search found `top` (-inf: nothing visible).  A
 // first maximum in bounds leaves zero, as it would be without the search, so
-// that what other rows see does not change a row's bits.  limit: kRaise or
-// kRaiseScaled.
-__device__ __forceinline__ float raised(float ref, float top, float limit) {
-  if (ref == -INFINITY) return top > -INFINITY && fabsf(top) <= limit ? 0.f : top;
-  return top > ref + limit ? top : ref;
+// that what other rows see does not change a row's bits.  below: how far it may
+// lie below that (kRaise or kBelowScaled).
+__device__ __forceinline__ float raised(float ref, float top, float below) {
+  if (ref == -INFINITY) return top >= -below && top <= kRaise ? 0.f : top;
+  return top > ref + kRaise ? top : ref;
 }
 
 // No score hidden, none that may pass the reference by 2^kRaise.
@@ -639,8 +640,7 @@ __device__ __forceinline__ void weigh_usual(uint32_t s, const float* kf, const f
 
 // As weigh_usual where a group's 32 columns have one key factor and one power of
 // two 2^e as value factor (the 8-bit cache): the exponent takes it, the sum gives
-// it back once a group.  (The row's largest score is 2^-kRaiseScaled of the
-// reference or more.)
+// it back once a group.  (A row's largest weight is 2^-kBelowScaled or more.)
 __device__ __forceinline__ void weigh_grouped(uint32_t s, const float* kf, const float* vf, float ref, uint64_t& sum2) {
   uint32_t x[2][16], rest[8];
   tmem_ld16_start(s, x[0]);

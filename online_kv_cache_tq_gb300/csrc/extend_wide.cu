@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
     const int copy_row = 32 * quarter + (lane >> 3), copy_chunk = lane & 7;
     uint8_t* const half_s = smem + kQuery0 + x * kImage + half * kBlockBytes;
     auto swizzled = [&](int qr, int chunk) { return reinterpret_cast<uint4*>(half_s + qr * 128 + (((chunk ^ qr) & 7) << 4)); };
-    constexpr float kLimit = TURN ? kRaise : kRaiseScaled;
+    constexpr float kBelow = TURN ? kRaise : kBelowScaled;
     int jt = 0;                                   // key tiles so far
     for (int seg = 0; next_segment(a, a.wide, run, t0, t1); ++seg) {
       const int n_rows = it.seq.y * d.group;
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
         // (both the same for the two threads of a row, and so for their warps)
         bool mask = __any_sync(0xffffffffu, e != 0 || seen < (t + 1) * kTile || all != 0xffffffffu);
         if constexpr (!TURN) mask = mask || meta->grouped == 0;
-        const bool search = __any_sync(0xffffffffu, !(len * meta->reach <= (ref == -INFINITY ? 0.f : ref) + kLimit));
+        const bool search = __any_sync(0xffffffffu, !(len * meta->reach <= (ref == -INFINITY ? kBelow : ref + kRaise)));
         const int here = min(kTile, max(0, seen - t * kTile));
         if (search) {
           // scores that may pass the reference: the tile's maximum first
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) extend_wide_kernel(ExtendArgs
                                    : grouped_top(s_addr, kf);
           ok = swap(top, &other);
           if (!ok) break;
-          const float to = raised(ref, fmaxf(top, other), kLimit);
+          const float to = raised(ref, fmaxf(top, other), kBelow);
           if (__any_sync(0xffffffffu, to != ref)) {
             const float scale = to != ref ? exp2_fast(ref - to) : 1.f;
             if (t > t0) {
