@@ -1255,6 +1255,7 @@ tq_status tq_fp8_read(const tq_codebook* book, const tq_fp8_view* cache, const i
                                 context_lens, &a.c);
   if (st == TQ_OK) st = fp8_rows_args(k_out, v_out, dtype, n_tokens, n_kv_heads, k_stride, v_stride, &a);
   if (st != TQ_OK || n_tokens == 0 || batch == 0) return st;
+  a.num_sms = book->num_sms;
   DeviceGuard guard(book->device);
   return launched(tq::launch_fp8_read(a, dtype == TQ_BF16, static_cast<cudaStream_t>(stream)));
 }

@@ -28,7 +28,7 @@ namespace tq {
 namespace {
 
 constexpr int kShortRun = 8;      // tokens that one warp appends alone
-constexpr int kReadCtas = 32 * 152;
+constexpr int kReadCtasPerSm = 32;
 
 template <bool BF16>
 struct Eight {                    // eight neighbouring coordinates of a row as they lie in memory
@@ -610,7 +610,7 @@ long long windows_of(const Fp8RowsArgs& a) {
 long long read_grid(Fp8RowsArgs& a) {
   a.fields = ((a.rows[0] != nullptr) + (a.rows[1] != nullptr)) * a.c.n_kv;
   a.window = kFp8Window;
-  if (windows_of(a) * a.fields < kReadCtas) a.window = 16;
+  if (windows_of(a) * a.fields < static_cast<long long>(kReadCtasPerSm) * a.num_sms) a.window = 16;
   return windows_of(a) * a.fields;
 }
 
