@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "dependent.cuh"
 #include "kernels.h"
 #include "tc_ptx.cuh"
 
@@ -34,28 +35,6 @@ constexpr float kFused = 1048576.f;
 // kind::f16 with fp16 or bf16 operands, fp32 accumulators, 128 x 128.
 constexpr uint32_t kIdescBf16 = ptx::idesc_bf16_f32(128, 128);
 constexpr uint32_t kIdescF16 = kIdescBf16 & ~((7u << 7) | (7u << 10));
-
-// The launches of a call follow one another as programmatic dependents: each
-// starts while the one before runs (or waits for room), sets itself up, and
-// waits here before it reads or writes memory.  Every CTA waits, so that a
-// launch is complete only after all before it are.
-__device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-template <typename Kernel>
-cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const ExtendArgs& a) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
-}
 
 // ptx::wait_bar without its suspension hint: a waiting warp sleeps for the
 // hardware's own short time, which wakes it sooner than the hint does; the
@@ -351,11 +330,6 @@ __device__ __forceinline__ void product(uint32_t d, uint32_t a_tmem, uint64_t b_
                          accumulate || ks > 0);
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t w;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));

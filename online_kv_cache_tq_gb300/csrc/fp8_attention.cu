@@ -37,6 +37,7 @@
 #include <algorithm>
 #include <cstddef>
 
+#include "dependent.cuh"
 #include "fp8_common.cuh"
 #include "tc_ptx.cuh"
 
@@ -223,11 +224,6 @@ __device__ __forceinline__ void find_run(const Fp8AttendArgs& a, RunStart* out, 
   __syncthreads();
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Two halves as e4m3 codes, and back; a byte to shared memory.
 __device__ __forceinline__ uint16_t fp8_pair_of_halves(__half2 h) {
   uint16_t p;
@@ -377,7 +373,7 @@ __global__ void __launch_bounds__(Shape<RT, QP>::kThreads, kCtasPerSm) fp8_atten
   Barriers<RT, QP>& bar = sh.bar;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* const abort = &sh.abort;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  launch_dependents();
   if (warp == P::kSoftWarps) {
     ptx::tmem_alloc(&sh.tmem, P::kTmem);
     ptx::tmem_relinquish();
@@ -401,7 +397,7 @@ __global__ void __launch_bounds__(Shape<RT, QP>::kThreads, kCtasPerSm) fp8_atten
   }
   for (int i = tid; i < 3 * RT; i += P::kThreads) (&sh.poison[0][0])[i] = 0;
   ptx::tc_fence_before();
-  asm volatile("griddepcontrol.wait;" ::: "memory");        // (for the plan, where there is one)
+  wait_prerequisites();                           // (for the plan, where there is one)
   find_run<RT, P::kThreads / 32>(a, &sh.start, sh.warp_s);
   ptx::tc_fence_after();
   const long long total = sh.start.total, per = (total + gridDim.x - 1) / gridDim.x;
@@ -816,7 +812,7 @@ __global__ void __launch_bounds__(kJoinThreads, 8) fp8_join_kernel(Fp8AttendArgs
   __shared__ float sum_s[kJoinRows][kJoinWarps], top_s[kJoinRows][kJoinWarps];
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % kJoinWarps, mine = (threadIdx.x >> 5) / kJoinWarps;
   const int row = blockIdx.y * kJoinRows + mine, c0 = blockIdx.x;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_prerequisites();
   const CutItem cut = a.cuts[c0];
   if (static_cast<int>(blockIdx.y) * kJoinRows >= cut.rows) return;      // (the whole CTA)
   const bool live = row < cut.rows;
@@ -909,21 +905,6 @@ bool wide_possible(int n_tokens, int batch, int n_q, int n_kv, int max_context) 
   const long long context = max_context > 0 ? max_context : 1;
   auto gains = [&](long long most, long long work) { return most * (n_q / n_kv) >= kWideFrom && most * n_q >= work / context; };
   return gains(static_cast<long long>(n_tokens) - batch + 1, kWideWork) || gains(n_tokens, kWideWorkIdle);
-}
-
-template <typename Kernel, typename... Args>
-cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // `planned`: launches of the same call come before.

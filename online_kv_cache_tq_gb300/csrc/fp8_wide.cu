@@ -8,6 +8,7 @@
 // (3.1 TB/s).  A chunk of 2048 tokens on 14001, 64/8 heads, takes 870 us with it,
 // 1.16 PFLOP/s, where keys with large channels have every tile searched for its
 // maximum, and 793 us (1.27) where not.
+#include "dependent.cuh"
 #include "fp8_common.cuh"
 #include "tc_ptx.cuh"
 
@@ -41,8 +42,8 @@ __global__ void __launch_bounds__(kExpandThreads) fp8_expand_kernel(Fp8Cache c, 
   uint8_t* const codes = smem;                    // keys, then values
   uint8_t* const image = smem + 2 * kTile * kDim;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  launch_dependents();
+  wait_prerequisites();
   const long long total = a.ws_expand[c.batch];
   for (long long g = blockIdx.x; g < total; g += gridDim.x) {
     int lo = 0, hi = c.batch;                     // the last sequence whose tiles start at or before g
@@ -183,17 +184,8 @@ __global__ void __launch_bounds__(kExpandThreads) fp8_expand_kernel(Fp8Cache c, 
 cudaError_t launch_fp8_expand(const Fp8Cache& cache, const ExtendArgs& args, float scale, cudaStream_t stream) {
   cudaError_t err = cudaFuncSetAttribute(fp8_expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmem);
   if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * args.d.num_sms);
-  cfg.blockDim = dim3(kExpandThreads);
-  cfg.dynamicSmemBytes = kExpandSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fp8_expand_kernel, cache, args, scale * 1.4426950408889634f);
+  return launch_dependent(fp8_expand_kernel, dim3(2 * args.d.num_sms), kExpandThreads, kExpandSmem, stream, cache, args,
+                          scale * 1.4426950408889634f);
 }
 
 }  // namespace tq
