@@ -9,12 +9,12 @@
 // loses nothing but codes that leave e4m3's normal range.
 // The bound is HBM, 2 x 128 x (element + 1) bytes a token and KV head, and the
 // latency of a chain (run, table entry, rows, largest, codes) that a stage ahead
-// hides: a prompt of 32768 tokens x 8 heads takes 39.4 us in bf16 (5.1 TB/s, 0.76
-// of the measured copy; 800 warp instructions for a warp's 16 tokens x 128, 57 %
+// hides: a prompt of 32768 tokens x 8 heads takes 39.1 us in bf16 (5.1 TB/s, 0.77
+// of the measured copy; 730 warp instructions for a warp's 16 tokens x 128, 57 %
 // of issue), a decode step of 64 sequences 4 us.  Rows kept in registers between
 // the two passes took 45 us, read twice from memory 55, staged by bulk copies of
 // a row each 55.  A mixed step of 24 sequences x 4 heads, float32, blocks of 96
-// tokens: 15.7 us; 20.7 where a run longer than a stage came twice, 28 with windows
+// tokens: 15.6 us; 20.7 where a run longer than a stage came twice, 28 with windows
 // of tokens per CTA instead of runs, because a window's runs come one after another.
 //
 // Read.  x = code 2^e, exact in either type.  The bound is HBM: 131072 tokens x 8

@@ -5,9 +5,9 @@
 // as the columns' factors.  Then a tile serves every row tile of 256 rows.
 //
 // The bound is memory: 32 KB in and 64.5 KB out a tile; 1008 tiles take 31 us
-// (3.1 TB/s).  A chunk of 2048 tokens on 14001, 64/8 heads, takes 870 us with it,
+// (3.1 TB/s).  A chunk of 2048 tokens on 14001, 64/8 heads, takes 867 us with it,
 // 1.16 PFLOP/s, where keys with large channels have every tile searched for its
-// maximum, and 793 us (1.27) where not.
+// maximum, and 795 us (1.27) where not.
 #include "dependent.cuh"
 #include "fp8_common.cuh"
 #include "tc_ptx.cuh"

@@ -280,7 +280,10 @@ struct ExtendForm {
 };
 constexpr int kNarrowRows = 128, kWideRows = 256;
 // (ragged prompts take 305, 300, 318, 339 us at a wide cost of 3, 4, 6, 9; a ragged
-// step of few rows 412, 405, 391, 394 us at a narrow cost of 2, 3, 5, 7)
+// step of few rows 412, 405, 391, 394 us at a narrow cost of 2, 3, 5, 7; over the
+// 8-bit cache, whose wide form turns nothing back, twelve ragged sequences 309,
+// 285, 289, 308 us at a wide cost of 2, 3, 4, 6, eight chunks of 300 tokens 218, 200,
+// 201, 204)
 constexpr int kNarrowCost = 5, kWideCost = 4;
 
 // A key tile expanded for the wide form: the keys (R^T c + rho S^T signs,
