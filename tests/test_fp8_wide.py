@@ -331,3 +331,17 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_correct(new, ctx,
     B.tq_debug_withhold_commit(c.book, False)
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("max_context", [1 << 15, 1 << 20])
+@pytest.mark.parametrize("past", [0, 5])
+def test_a_decode_step_large_enough_for_its_launches(max_context, past):
+    # no sequence takes the form: the others run before its launches, or behind them (where its tiles may have no room)
+    rng = np.random.default_rng(max_context)
+    ctx = [int(x) for x in rng.integers(1, 400, 600)]
+    c = few.Case([1] * 600, ctx, n_kv=2, group=8, seed=17, pad=past)
+    ws, nbytes = C.allocate_fp8_workspace(c.book, c.total, c.batch, c.n_q, c.n_kv, max_context)
+    assert nbytes > WIDE_BYTES
+    B.tq_fp8_attention(c.book, c.q, B.TQ_BF16, c.total, c.batch, c.n_q, c.n_kv, c.view, c.table_t, c.max_blocks, c.start,
+                       c.ctx_t, max_context, 0.0, c.out, ws, nbytes)
+    c.check(wide=False)
