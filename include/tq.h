@@ -559,7 +559,10 @@ size_t tq_fp8_workspace_bytes(const tq_codebook* book, int n_tokens, int batch, 
  * h / (n_q_heads / n_kv_heads), any whole ratio.  out: device bf16
  * [n_tokens][n_q_heads][128]; rows behind query_start[batch] are left as they
  * were.  max_context bounds every context_lens[b] and is at most 2^30 (else
- * TQ_ERR_UNSUPPORTED).  scale: 0 selects 1/sqrt(d).
+ * TQ_ERR_UNSUPPORTED).  scale: 0 selects 1/sqrt(d).  Sequences may be empty; but a
+ * call of no more tokens than sequences, and fewer than 512, is taken for a decode
+ * step, and several hundred rows of one sequence in it take up to six times as
+ * long as in a call without the empty ones.
  * Accuracy: a sequence with fewer than 144 rows (new tokens x n_q_heads /
  * n_kv_heads) has keys exactly, bf16 queries exactly (coordinates below 2^-12 of
  * a vector's largest to 2^-21 of it), float32 ones to 2^-16 of a coordinate, and
@@ -571,10 +574,11 @@ size_t tq_fp8_workspace_bytes(const tq_codebook* book, int n_tokens, int batch, 
  * of them with the remainder (tokens below 2^-30 of the row's largest weight may
  * not count): 0.0022.
  * workspace: device scratch of tq_fp8_workspace_bytes bytes (up to 5 MB, and
- * where sequences can have those rows as tq_extend_attention's), 256-byte
+ * where a sequence can have those rows as tq_extend_attention's), 256-byte
  * aligned, not used by any concurrent call; more tokens or a longer context of
  * as many sequences need no less, fewer sequences may need more.  The same call
- * gives the same bits.  Device errors as tq_extend_attention's.  Asynchronous on `stream`. */
+ * gives the same bits.  Device errors as tq_extend_attention's.  Asynchronous on
+ * `stream`. */
 tq_status tq_fp8_attention(const tq_codebook* book, const void* q, tq_dtype dtype, int n_tokens, int batch,
                            int n_q_heads, int n_kv_heads, const tq_fp8_view* cache, const int32_t* block_table,
                            int max_blocks, const int32_t* query_start, const int32_t* context_lens, int max_context,

@@ -895,16 +895,20 @@ constexpr int kWideFrom = 144;
 // heads and context: this form does 0.3 to 0.4 million of them in a microsecond.
 // A sequence has the rows if the others have a token each; or, as sequences
 // may be empty, if it has all tokens.  A call that can have it only so is nearly
-// always a decode step, and takes the launches from where they are 1 % of one.
+// always a decode step, whose contexts may be far shorter than max_context: such
+// a call has the launches from 512 tokens on, and where they are 1 % of a decode
+// step with contexts of max_context.
 // (64/8 heads, us, with the launches | without.  A sequence of 2048 tokens on 16 K
-// among 2048 854 | 7326, one of 256 on 32 K among 256 308 | 1821, one of 64 on
+// among 2048 854 | 7326, one of 256 on 8192 among 256 117 | 472, one of 64 on
 // 8192 among 64 77 | 125.  Decode steps: 64 on 1 K to 32 K 321 | 312, 256 on 8192
 // 630 | 621, 128 on 700 54 | 47.)
 constexpr long long kWideWork = 1 << 22, kWideWorkIdle = 1 << 28;
+constexpr int kWideTokensIdle = 512;
 bool wide_possible(int n_tokens, int batch, int n_q, int n_kv, int max_context) {
   const long long context = max_context > 0 ? max_context : 1;
   auto gains = [&](long long most, long long work) { return most * (n_q / n_kv) >= kWideFrom && most * n_q >= work / context; };
-  return gains(static_cast<long long>(n_tokens) - batch + 1, kWideWork) || gains(n_tokens, kWideWorkIdle);
+  return gains(static_cast<long long>(n_tokens) - batch + 1, kWideWork) ||
+         (n_tokens >= kWideTokensIdle && gains(n_tokens, kWideWorkIdle));
 }
 
 // `planned`: launches of the same call come before.

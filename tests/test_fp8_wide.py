@@ -53,10 +53,10 @@ def test_scores_far_below_zero_beside_blocks_of_tiny_scale(near):
 
 def test_one_chunk_among_many_empty_sequences():
     # a sequence has all tokens of the call, which has as many tokens as sequences: before, behind and among empty ones
-    ctx = 16384
-    for at in (0, 100, 255):
-        new, lengths = [0] * 256, [1] * 256
-        new[at], lengths[at] = 256, ctx
+    ctx = 8192
+    for at in (0, 200, 511):
+        new, lengths = [0] * 512, [1] * 512
+        new[at], lengths[at] = 512, ctx
         c = Case(new, lengths, group=64, seed=2)
         c.run()
         c.check([at], tokens=3)
@@ -64,7 +64,7 @@ def test_one_chunk_among_many_empty_sequences():
 
 def test_decode_steps_have_no_workspace_for_it():
     book = B.Codebook(block_size=64)
-    for batch, n_q, n_kv, ctx in ((64, 64, 8, 32768), (256, 64, 8, 8192), (1, 64, 8, 1 << 20), (128, 64, 8, 700)):
+    for batch, n_q, n_kv, ctx in ((64, 64, 8, 32768), (256, 64, 8, 1 << 20), (1, 64, 8, 1 << 20), (2048, 64, 8, 700)):
         assert B.tq_fp8_workspace_bytes(book, batch, batch, n_q, n_kv, ctx) < WIDE_BYTES
 
 
